@@ -25,6 +25,7 @@ GLU_ERR_UNSUPPORTED = 6
 GLU_ERR_BAD_STRIDE = 7
 GLU_ERR_WORKSPACE = 8
 GLU_ERR_SCRATCH_LIMIT = 9
+GLU_ERR_BAD_ARGUMENT = 10
 NOALLOC_SCRATCH_BYTES = 48 << 20  # the device array glu_dual_gemv_backward_noalloc works in
 (KERNEL_NONE, KERNEL_ZERO, KERNEL_VALU, KERNEL_MFMA, KERNEL_GENERIC, KERNEL_GEMM, KERNEL_BACKWARD,
  KERNEL_CEILING) = range(8)
@@ -57,6 +58,19 @@ EXPORTED_SYMBOLS = (
     "glu_unit_ceiling",
     "glu_unit_ceiling_work",
     "glu_copy_ceiling",
+    # include/glu_fp8.h; declared and called in fp8.py
+    "glu_add_rms_norm",
+    "glu_add_rms_norm_fp8",
+    "glu_add_rms_norm_backward",
+    "glu_add_rms_norm_backward_workspace",
+    "glu_fp8_quantize",
+    "glu_fp8_quantize_weight",
+    "glu_fp8_linear",
+    "glu_fp8_dual_glu",
+    "glu_fp8_product_plan",
+    "glu_fp8_workspace",
+    "glu_fp8_product_tuned",
+    "glu_fp8_product_workspace",
 )
 
 
@@ -159,6 +173,8 @@ def library() -> ctypes.CDLL:
     lib.glu_unit_ceiling_work.restype = ctypes.c_int
     lib.glu_copy_ceiling.argtypes = [vp, vp, vp, vp, i64, i64, ctypes.POINTER(Tuning), vp]
     lib.glu_copy_ceiling.restype = ctypes.c_int
+    from . import fp8
+    fp8._declare(lib)
     _LIB = lib
     return lib
 

@@ -14,10 +14,21 @@
 #include "glu_ceiling.h"
 #include "glu_grouped.h"
 #include "glu_launch.h"
+#include "glu_status.h"
 
 namespace {
 
 thread_local int g_last_hip_error = 0;
+
+}  // namespace
+
+glu_status glu::fail_launch(hipError_t e)
+{
+    g_last_hip_error = (int)e;
+    return GLU_ERR_LAUNCH;
+}
+
+namespace {
 
 constexpr int64_t kMaxDim = 0x7fffffff;    // N and K index rows and columns in 32 bits
 // the VALU and MFMA kernels address a group's weight rows and the hidden
@@ -387,11 +398,7 @@ bool overlaps(const void* a, int64_t abytes, const void* b, int64_t bbytes)
     return a0 < b0 + (uintptr_t)bbytes && b0 < a0 + (uintptr_t)abytes;
 }
 
-glu_status fail_launch(hipError_t e)
-{
-    g_last_hip_error = (int)e;
-    return GLU_ERR_LAUNCH;
-}
+glu_status fail_launch(hipError_t e) { return glu::fail_launch(e); }
 
 // Elements spanned by `rows` rows of `len` elements at stride `ld`, or -1 if
 // that does not fit in int64 as a byte count.
@@ -1254,6 +1261,8 @@ const char* glu_status_string(int status)
     case GLU_ERR_WORKSPACE: return "GLU_ERR_WORKSPACE: the workspace is NULL, misaligned or too small";
     case GLU_ERR_SCRATCH_LIMIT:
         return "GLU_ERR_SCRATCH_LIMIT: the call needs more scratch than the library's fixed device array holds";
+    case GLU_ERR_BAD_ARGUMENT:
+        return "GLU_ERR_BAD_ARGUMENT: an unknown element type, or an eps that is negative or not finite";
     default: return "unknown glu_status";
     }
 }

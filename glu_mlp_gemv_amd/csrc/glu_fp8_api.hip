@@ -1,0 +1,436 @@
+// C ABI of the 8-bit decoder-MLP path (include/glu_fp8.h): argument
+// validation, the choice of kernel, and launch.  Validation happens before any
+// HIP call; nothing is allocated or cached.
+#include <hip/hip_runtime.h>
+
+#include <math.h>
+#include <stdint.h>
+
+#include "../../include/glu_fp8.h"
+#include "glu_fp8.h"
+#include "glu_norm.h"
+#include "glu_quantize.h"
+#include "glu_status.h"
+
+namespace {
+
+constexpr int64_t kMaxDim = (int64_t)1 << 30;  // rows and columns index in 32 bits, rounded up to tiles
+constexpr int64_t kMaxFastLd = 1 << 23;        // the tile kernel's row offsets: 256 rows * stride < 2^32
+constexpr int kGroup = 128;
+constexpr int kCUs = 256;
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+int type_size(int dtype) { return dtype == GLU_DTYPE_E4M3 ? 1 : dtype == GLU_DTYPE_FP32 ? 4 : 2; }
+bool input_type(int dtype) { return dtype == GLU_DTYPE_BF16 || dtype == GLU_DTYPE_FP16 || dtype == GLU_DTYPE_FP32; }
+
+// An array of `rows` rows of `len` elements at stride `ld`.
+struct Array {
+    const void* p;
+    int64_t rows, len, ld;
+    int size;  // bytes per element
+    bool output;
+};
+
+// bytes from the first to past the last element; -1 if that does not fit
+int64_t extent(const Array& a)
+{
+    if (a.rows == 0 || a.len == 0) return 0;
+    const int64_t limit = INT64_MAX / a.size;
+    if (a.rows > 1 && a.ld > (limit - a.len) / (a.rows - 1)) return -1;
+    return ((a.rows - 1) * a.ld + a.len) * a.size;
+}
+
+// NULL, strides, alignment and overlap of a call's arrays, in that order.  An output may coincide exactly (pointer and
+// stride) with the inputs in `shared`, a bit per array.
+glu_status check_arrays(const Array* a, int n, unsigned shared_out = 0, unsigned shared_in = 0)
+{
+    int64_t bytes[16];
+    for (int i = 0; i < n; ++i) {
+        if (a[i].rows > 1 && a[i].ld < a[i].len) return GLU_ERR_BAD_STRIDE;
+        bytes[i] = extent(a[i]);
+        if (bytes[i] < 0) return GLU_ERR_BAD_STRIDE;
+    }
+    for (int i = 0; i < n; ++i) {
+        if (bytes[i] > 0 && !a[i].p) return GLU_ERR_NULL_POINTER;
+    }
+    for (int i = 0; i < n; ++i) {
+        if (bytes[i] > 0 && ((uintptr_t)a[i].p & (uintptr_t)(a[i].size - 1))) return GLU_ERR_MISALIGNED;
+    }
+    for (int i = 0; i < n; ++i) {
+        if (!a[i].output || bytes[i] == 0) continue;
+        for (int j = 0; j < n; ++j) {
+            if (j == i || bytes[j] == 0 || (a[j].output && j < i)) continue;
+            const bool exact = a[i].p == a[j].p && a[i].len == a[j].len && (a[i].rows <= 1 || a[i].ld == a[j].ld);
+            if (exact && (shared_out >> i & 1) && (shared_in >> j & 1)) continue;
+            const uintptr_t p = (uintptr_t)a[i].p, q = (uintptr_t)a[j].p;
+            if (p < q + (uintptr_t)bytes[j] && q < p + (uintptr_t)bytes[i]) return GLU_ERR_ALIASING;
+        }
+    }
+    return GLU_OK;
+}
+
+glu_status launched(hipError_t e) { return e == hipSuccess ? GLU_OK : glu::fail_launch(e); }
+
+bool bad_dim(int64_t v) { return v < 0 || v > kMaxDim; }
+
+glu_status norm_call(const void* x, int64_t ldx, const void* residual, int64_t ldr, const void* weight, void* sum,
+                     int64_t lds, void* out, int64_t ldo, float* scale, int64_t ld_scale, float* rstd, int64_t M,
+                     int64_t K, float eps, int dtype, bool e4m3, void* stream)
+{
+    if (!input_type(dtype) || !(eps >= 0.0f) || !(eps <= 3.4028234e38f)) return GLU_ERR_BAD_ARGUMENT;
+    if (bad_dim(M) || bad_dim(K) || K == 0) return GLU_ERR_BAD_SHAPE;
+    if (M == 0) return GLU_OK;
+    if ((residual == nullptr) != (sum == nullptr)) return GLU_ERR_NULL_POINTER;
+    const int es = type_size(dtype);
+    const int64_t with = residual ? M : 0;
+    const Array arrays[] = {
+        {x, M, K, ldx, es, false},
+        {residual, with, K, ldr, es, false},
+        {weight, 1, K, K, es, false},
+        {sum, with, K, lds, es, true},
+        {out, M, K, ldo, e4m3 ? 1 : es, true},
+        {scale, e4m3 ? ceil_div(K, kGroup) : 0, M, ld_scale, 4, true},
+        {rstd, rstd ? 1 : 0, M, M, 4, true},
+    };
+    const glu_status st = check_arrays(arrays, 7, 1u << 3, 1u << 0 | 1u << 1);
+    if (st != GLU_OK) return st;
+    const glu::NormArgs a{x, residual, weight, sum, out, scale, rstd, ldx, ldr, lds, ldo, ld_scale, (int)M, (int)K, eps};
+    return launched(glu::norm_launch(dtype, e4m3, a, (hipStream_t)stream));
+}
+
+// ---- products ----------------------------------------------------------------------
+
+struct Operand {
+    const glu_fp8_matrix* m;
+    int64_t rows, scale_rows, blocks;
+};
+
+// 16-row tiles of x per workgroup of the streaming kernel
+int stream_tiles(int64_t M, bool any) { return any || M <= 16 ? 1 : M <= 32 ? 2 : 4; }
+
+// Fills the launch shape for sizes >= 1.  What decides is measured with perf's sizes in DESIGN's table and at the rule.
+void choose(int mats, int64_t M, int64_t N, int64_t K, int out_dtype, bool fast, glu_fp8_plan* p)
+{
+    const int64_t KB = ceil_div(K, kGroup);
+    p->splits = 1;
+    if (!fast) {
+        p->kernel = GLU_FP8_KERNEL_ANY;
+        p->tile = 16;
+        p->width = 4;
+        return;
+    }
+    if (M <= 16 || out_dtype == GLU_DTYPE_FP32) {
+        p->kernel = GLU_FP8_KERNEL_STREAM;
+        p->tile = 16;
+        while (p->tile > 4 && M <= p->tile / 2 && ceil_div(N, p->tile) < 2 * kCUs) p->tile /= 2;
+        const int64_t steps = ceil_div(KB, 16 / p->tile);
+        int64_t w = ceil_div(steps, 4);
+        const int64_t most = M <= 16 ? 16 : 8;
+        p->width = (int)(w > most ? most : w);
+        return;
+    }
+    p->kernel = GLU_FP8_KERNEL_TILE;
+    p->tile = M <= 32 ? 3 : M <= 64 ? 2 : M <= 1024 ? 1 : 0;
+    const glu::TileShape& t = glu::kTileShapes[p->tile];
+    p->width = t.threads;
+    const int64_t tiles = ceil_div(M, t.bm) * ceil_div(N, t.br / mats);
+    int64_t splits = 2 * kCUs / tiles;
+    if (splits > KB / 4) splits = KB / 4;
+    if (splits > 8) splits = 8;
+    p->splits = (int)(splits < 1 ? 1 : splits);
+}
+
+// whether sums go to planes for the second kernel, and what follows from that
+void complete(int mats, int64_t M, int64_t N, int out_dtype, glu_fp8_plan* p)
+{
+    bool planes = p->splits > 1;
+    if (out_dtype == GLU_DTYPE_E4M3) {
+        planes = planes || p->kernel != GLU_FP8_KERNEL_TILE || !glu::fp8_tile_owns_groups(mats, p->tile);
+    }
+    p->launches = planes ? 2 : 1;
+    p->workspace_bytes = planes ? (int64_t)p->splits * mats * M * N * 4 : 0;
+}
+
+glu_status product_plan(int mats, int64_t M, int64_t N, int64_t K, int out_dtype, bool fast,
+                        const glu_fp8_plan* asked, glu_fp8_plan* p)
+{
+    *p = glu_fp8_plan{};
+    if (mats != 1 && mats != 2) return GLU_ERR_BAD_ARGUMENT;
+    if (out_dtype < GLU_DTYPE_BF16 || out_dtype > GLU_DTYPE_E4M3) return GLU_ERR_BAD_ARGUMENT;
+    if (bad_dim(M) || bad_dim(N) || bad_dim(K)) return GLU_ERR_BAD_SHAPE;
+    if (M > 0 && N > INT64_MAX / 64 / M) return GLU_ERR_BAD_SHAPE;
+    if (M == 0 || N == 0) {
+        p->kernel = GLU_FP8_KERNEL_NONE;
+        return GLU_OK;
+    }
+    if (K == 0) {
+        p->kernel = GLU_FP8_KERNEL_ZERO;
+        p->launches = 1;
+        return GLU_OK;
+    }
+    if (asked) {
+        p->kernel = asked->kernel;
+        p->tile = asked->tile;
+        p->width = asked->width;
+        p->splits = asked->splits;
+        if (p->splits < 1 || p->splits > ceil_div(K, kGroup) || p->splits > 64) return GLU_ERR_UNSUPPORTED;
+        if (p->kernel == GLU_FP8_KERNEL_TILE) {
+            if (!fast || p->tile < 0 || p->tile >= glu::kTileShapeCount) return GLU_ERR_UNSUPPORTED;
+            if (out_dtype == GLU_DTYPE_FP32) return GLU_ERR_UNSUPPORTED;  // its sums are coarser than that
+            p->width = glu::kTileShapes[p->tile].threads;
+        } else if (p->kernel == GLU_FP8_KERNEL_STREAM || p->kernel == GLU_FP8_KERNEL_ANY) {
+            const bool any = p->kernel == GLU_FP8_KERNEL_ANY;
+            if (!any && !fast) return GLU_ERR_UNSUPPORTED;
+            const glu::StreamConfig c{p->tile, stream_tiles(M, any), p->width, p->splits, any};
+            if (!glu::fp8_stream_supported(mats, c, (int)M)) return GLU_ERR_UNSUPPORTED;
+        } else {
+            return GLU_ERR_UNSUPPORTED;
+        }
+    } else {
+        choose(mats, M, N, K, out_dtype, fast, p);
+    }
+    // the streaming grid: one row tile's threads below 2^32
+    if (p->kernel != GLU_FP8_KERNEL_TILE && ceil_div(N, p->tile) * p->splits > 0xffffffffLL / (64 * p->width)) {
+        return GLU_ERR_UNSUPPORTED;
+    }
+    complete(mats, M, N, out_dtype, p);
+    return GLU_OK;
+}
+
+glu_status product_call(const glu_fp8_matrix* x, const glu_fp8_matrix* w0, const glu_fp8_matrix* w1, int mats,
+                        void* out, int64_t ldo, float* out_scale, int64_t ld_scale, int64_t M, int64_t N, int64_t K,
+                        int out_dtype, const glu_fp8_plan* asked, void* ws, int64_t ws_bytes, void* stream)
+{
+    glu_fp8_plan p;
+    glu_status st = product_plan(mats, M, N, K, out_dtype, true, nullptr, &p);  // sizes and types
+    if (st != GLU_OK) return st;
+    if (M == 0 || N == 0) return GLU_OK;
+    if (!x || !w0 || (mats == 2 && !w1)) return GLU_ERR_NULL_POINTER;
+    const glu_fp8_matrix* w[2] = {w0, w1};
+    const int64_t KB = ceil_div(K, kGroup), NB = ceil_div(N, kGroup);
+    // scales: x's by two strides of any order, a weight's rows contiguous
+    if (KB > 0 && (x->scale_row < 0 || x->scale_block < 0)) return GLU_ERR_BAD_STRIDE;
+    if (KB > 0 && ((M > 1 && x->scale_row > INT64_MAX / 8 / M) || (KB > 1 && x->scale_block > INT64_MAX / 8 / KB))) {
+        return GLU_ERR_BAD_STRIDE;
+    }
+    for (int i = 0; i < mats; ++i) {
+        if (KB > 1 && w[i]->scale_block != 1) return GLU_ERR_BAD_STRIDE;
+    }
+    const int64_t sx_span = KB > 0 ? (M - 1) * x->scale_row + (KB - 1) * x->scale_block + 1 : 0;
+    const int64_t on = K > 0 ? 1 : 0;  // with K == 0 no operand is read
+    const bool e4m3 = out_dtype == GLU_DTYPE_E4M3;
+    uintptr_t bits = 0;
+    bool fast = K % 16 == 0;
+    if (on) {
+        bits = (uintptr_t)x->data | (M > 1 ? (uintptr_t)x->ld : 0);
+        fast = fast && (M <= 1 || x->ld <= kMaxFastLd);
+        for (int i = 0; i < mats; ++i) {
+            bits |= (uintptr_t)w[i]->data | (N > 1 ? (uintptr_t)w[i]->ld : 0);
+            fast = fast && (N <= 1 || w[i]->ld <= kMaxFastLd);
+        }
+        fast = fast && (bits & 15) == 0;
+    }
+    st = product_plan(mats, M, N, K, out_dtype, fast, asked, &p);
+    if (st != GLU_OK) return st;
+    const Array arrays[] = {
+        {x->data, M * on, K, x->ld, 1, false},
+        {x->scale, on, sx_span, sx_span, 4, false},
+        {w0->data, N * on, K, w0->ld, 1, false},
+        {w0->scale, NB * on, KB, w0->scale_row, 4, false},
+        {w1 ? w1->data : nullptr, mats == 2 ? N * on : 0, K, w1 ? w1->ld : K, 1, false},
+        {w1 ? w1->scale : nullptr, mats == 2 ? NB * on : 0, KB, w1 ? w1->scale_row : KB, 4, false},
+        {out, M, N, ldo, type_size(out_dtype), true},
+        {out_scale, e4m3 ? NB : 0, M, ld_scale, 4, true},
+        {ws, p.workspace_bytes && ws ? 1 : 0, p.workspace_bytes, p.workspace_bytes, 1, true},
+    };
+    st = check_arrays(arrays, 9);
+    if (st != GLU_OK) return st;
+    if (p.workspace_bytes > 0 && (!ws || ((uintptr_t)ws & 15) || ws_bytes < p.workspace_bytes)) return GLU_ERR_WORKSPACE;
+
+    hipStream_t s = (hipStream_t)stream;
+    const glu::FinishArgs fin{static_cast<const float*>(ws), out, out_scale, ldo, ld_scale, (int)M, (int)N, p.splits,
+                              mats};
+    if (p.kernel == GLU_FP8_KERNEL_ZERO) return launched(glu::finish_launch(out_dtype, fin, s));
+    glu::Fp8Args a{};
+    a.x = x->data;
+    a.sx = x->scale;
+    a.ldx = x->ld;
+    a.sxm = x->scale_row;
+    a.sxg = x->scale_block;
+    for (int i = 0; i < mats; ++i) {
+        a.w[i] = w[i]->data;
+        a.sw[i] = w[i]->scale;
+        a.ldw[i] = w[i]->ld;
+        a.ldsw[i] = w[i]->scale_row;
+    }
+    a.out = out;
+    a.scale = out_scale;
+    a.ldo = ldo;
+    a.lds = ld_scale;
+    a.part = static_cast<float*>(ws);
+    a.M = (int)M;
+    a.N = (int)N;
+    a.K = (int)K;
+    a.out_dtype = p.launches == 2 ? glu::kPartial : out_dtype;
+    hipError_t e;
+    if (p.kernel == GLU_FP8_KERNEL_TILE) {
+        e = glu::fp8_tile_launch(mats, glu::TileConfig{p.tile, p.splits}, a, s);
+    } else {
+        const bool any = p.kernel == GLU_FP8_KERNEL_ANY;
+        const glu::StreamConfig c{p.tile, stream_tiles(M, any), p.width, p.splits, any};
+        e = glu::fp8_stream_launch(mats, c, a, s);
+    }
+    if (e == hipSuccess && p.launches == 2) e = glu::finish_launch(out_dtype, fin, s);
+    return launched(e);
+}
+
+}  // namespace
+
+extern "C" {
+
+glu_status glu_add_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t ldr, const void* weight,
+                            void* sum, int64_t lds, void* out, int64_t ldo, float* rstd, int64_t M, int64_t K,
+                            float eps, int dtype, void* stream)
+{
+    return norm_call(x, ldx, residual, ldr, weight, sum, lds, out, ldo, nullptr, 0, rstd, M, K, eps, dtype, false,
+                     stream);
+}
+
+glu_status glu_add_rms_norm_fp8(const void* x, int64_t ldx, const void* residual, int64_t ldr, const void* weight,
+                                void* sum, int64_t lds, uint8_t* q, int64_t ldq, float* scale, int64_t ld_scale,
+                                float* rstd, int64_t M, int64_t K, float eps, int dtype, void* stream)
+{
+    return norm_call(x, ldx, residual, ldr, weight, sum, lds, q, ldq, scale, ld_scale, rstd, M, K, eps, dtype, true,
+                     stream);
+}
+
+glu_status glu_add_rms_norm_backward_workspace(int64_t M, int64_t K, int64_t* bytes)
+{
+    if (!bytes) return GLU_ERR_NULL_POINTER;
+    *bytes = 0;
+    if (bad_dim(M) || bad_dim(K) || K == 0) return GLU_ERR_BAD_SHAPE;
+    *bytes = glu::norm_grad_part_floats((int)M, (int)K) * 4;
+    return GLU_OK;
+}
+
+glu_status glu_add_rms_norm_backward(const void* dy, int64_t lddy, const void* h, int64_t ldh, const void* weight,
+                                     const float* rstd, const void* dresidual, int64_t lddr, void* dx, int64_t lddx,
+                                     void* dweight, int64_t M, int64_t K, int dtype, void* workspace,
+                                     int64_t workspace_bytes, void* stream)
+{
+    if (!input_type(dtype)) return GLU_ERR_BAD_ARGUMENT;
+    int64_t need = 0;
+    const glu_status size = glu_add_rms_norm_backward_workspace(M, K, &need);
+    if (size != GLU_OK) return size;
+    const int es = type_size(dtype);
+    const Array arrays[] = {
+        {dy, M, K, lddy, es, false},
+        {h, M, K, ldh, es, false},
+        {weight, M > 0 ? 1 : 0, K, K, es, false},
+        {rstd, M > 0 ? 1 : 0, M, M, 4, false},
+        {dresidual, dresidual ? M : 0, K, lddr, es, false},
+        {dx, M, K, lddx, es, true},
+        {dweight, 1, K, K, es, true},
+        {workspace, need && workspace ? 1 : 0, need, need, 1, true},
+    };
+    const glu_status st = check_arrays(arrays, 8, 1u << 5, 1u << 4);
+    if (st != GLU_OK) return st;
+    if (need > 0 && (!workspace || ((uintptr_t)workspace & 15) || workspace_bytes < need)) return GLU_ERR_WORKSPACE;
+    const glu::NormGradArgs a{dy, h, dresidual, weight, rstd, dx, dweight, static_cast<float*>(workspace),
+                              lddy, ldh, lddr, lddx, (int)M, (int)K};
+    return launched(glu::norm_grad_launch(dtype, a, (hipStream_t)stream));
+}
+
+glu_status glu_fp8_quantize(const void* x, int64_t ldx, uint8_t* q, int64_t ldq, float* scale, int64_t ld_scale,
+                            int64_t M, int64_t K, int dtype, void* stream)
+{
+    if (!input_type(dtype)) return GLU_ERR_BAD_ARGUMENT;
+    if (bad_dim(M) || bad_dim(K)) return GLU_ERR_BAD_SHAPE;
+    if (M == 0 || K == 0) return GLU_OK;
+    const Array arrays[] = {
+        {x, M, K, ldx, type_size(dtype), false},
+        {q, M, K, ldq, 1, true},
+        {scale, ceil_div(K, kGroup), M, ld_scale, 4, true},
+    };
+    const glu_status st = check_arrays(arrays, 3);
+    if (st != GLU_OK) return st;
+    return launched(glu::quantize_rows_launch(dtype, x, ldx, q, ldq, scale, ld_scale, (int)M, (int)K,
+                                              (hipStream_t)stream));
+}
+
+glu_status glu_fp8_quantize_weight(const void* w, int64_t ldw, uint8_t* q, int64_t ldq, float* scale,
+                                   int64_t ld_scale, int64_t N, int64_t K, int dtype, void* stream)
+{
+    if (!input_type(dtype)) return GLU_ERR_BAD_ARGUMENT;
+    if (bad_dim(N) || bad_dim(K)) return GLU_ERR_BAD_SHAPE;
+    if (N == 0 || K == 0) return GLU_OK;
+    const Array arrays[] = {
+        {w, N, K, ldw, type_size(dtype), false},
+        {q, N, K, ldq, 1, true},
+        {scale, ceil_div(N, kGroup), ceil_div(K, kGroup), ld_scale, 4, true},
+    };
+    const glu_status st = check_arrays(arrays, 3);
+    if (st != GLU_OK) return st;
+    return launched(glu::quantize_blocks_launch(dtype, w, ldw, q, ldq, scale, ld_scale, (int)N, (int)K,
+                                                (hipStream_t)stream));
+}
+
+glu_status glu_fp8_linear(const glu_fp8_matrix* x, const glu_fp8_matrix* w, void* out, int64_t ldo, float* out_scale,
+                          int64_t ld_scale, int64_t M, int64_t N, int64_t K, int out_dtype, void* workspace,
+                          int64_t workspace_bytes, void* stream)
+{
+    return product_call(x, w, nullptr, 1, out, ldo, out_scale, ld_scale, M, N, K, out_dtype, nullptr, workspace,
+                        workspace_bytes, stream);
+}
+
+glu_status glu_fp8_dual_glu(const glu_fp8_matrix* x, const glu_fp8_matrix* gate, const glu_fp8_matrix* up, void* out,
+                            int64_t ldo, float* out_scale, int64_t ld_scale, int64_t M, int64_t N, int64_t K,
+                            int out_dtype, void* workspace, int64_t workspace_bytes, void* stream)
+{
+    return product_call(x, gate, up, 2, out, ldo, out_scale, ld_scale, M, N, K, out_dtype, nullptr, workspace,
+                        workspace_bytes, stream);
+}
+
+glu_status glu_fp8_product_tuned(const glu_fp8_matrix* x, const glu_fp8_matrix* w, const glu_fp8_matrix* up,
+                                 void* out, int64_t ldo, float* out_scale, int64_t ld_scale, int64_t M, int64_t N,
+                                 int64_t K, int out_dtype, const glu_fp8_plan* plan, void* workspace,
+                                 int64_t workspace_bytes, void* stream)
+{
+    return product_call(x, w, up, up ? 2 : 1, out, ldo, out_scale, ld_scale, M, N, K, out_dtype, plan, workspace,
+                        workspace_bytes, stream);
+}
+
+glu_status glu_fp8_product_plan(int mats, int64_t M, int64_t N, int64_t K, int out_dtype, int fast,
+                                glu_fp8_plan* plan)
+{
+    if (!plan) return GLU_ERR_NULL_POINTER;
+    return product_plan(mats, M, N, K, out_dtype, fast != 0, nullptr, plan);
+}
+
+glu_status glu_fp8_product_workspace(int mats, int64_t M, int64_t N, int64_t K, int out_dtype,
+                                     const glu_fp8_plan* plan, int64_t* bytes)
+{
+    if (!bytes) return GLU_ERR_NULL_POINTER;
+    *bytes = 0;
+    glu_fp8_plan p;
+    const glu_status st = product_plan(mats, M, N, K, out_dtype, true, plan, &p);
+    if (st == GLU_OK) *bytes = p.workspace_bytes;
+    return st;
+}
+
+glu_status glu_fp8_workspace(int mats, int64_t M, int64_t N, int64_t K, int out_dtype, int64_t* bytes)
+{
+    if (!bytes) return GLU_ERR_NULL_POINTER;
+    *bytes = 0;
+    for (int fast = 0; fast < 2; ++fast) {
+        glu_fp8_plan p;
+        const glu_status st = product_plan(mats, M, N, K, out_dtype, fast != 0, nullptr, &p);
+        if (fast == 0 && st == GLU_ERR_UNSUPPORTED) continue;  // too large for the other layouts' kernel
+        if (st != GLU_OK) return st;
+        if (p.workspace_bytes > *bytes) *bytes = p.workspace_bytes;
+    }
+    return GLU_OK;
+}
+
+}  // extern "C"

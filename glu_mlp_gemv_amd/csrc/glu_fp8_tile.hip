@@ -1,0 +1,334 @@
+// Block-scaled e4m3 products tiled through LDS, for more rows of x than the
+// streaming kernels take.
+//
+// A workgroup of WM x WN waves owns BM = 16 TM WM rows of x and BR = 16 TN WN weight rows (with two matrices
+// half of each, so that gate and up of one output meet in one lane).  K is walked one block of 128 at a time: a stage
+// is BM + BR rows of 128 bytes, brought straight from memory into LDS, STAGES - 1 stages ahead of their use, with one
+// barrier per stage.  The matrix instruction sums exactly one K-block, so its result is multiplied by the two scales
+// and added to the accumulator on the vector unit: 4 fused multiply-adds per lane against 32 cycles of the
+// matrix unit, which another wave uses meanwhile.
+//
+// In LDS, 16-byte chunk c of row r lies at c ^ ((r >> 1) & 7): every group of 16 lanes that a ds_read_b128 serves together
+// then touches 16 different slots of the 256-byte bank line.  A wave's direct load writes 64 consecutive
+// slots (8 rows), so the exchange is made in the source addresses.
+#include "glu_fp8_mfma.h"
+
+namespace glu {
+
+const TileShape kTileShapes[kTileShapeCount] = {
+    {256, 256, 512, 2},
+    {128, 128, 256, 2},
+    {64, 256, 256, 3},
+    {32, 128, 256, 4},
+};
+
+namespace {
+
+// 16 bytes per lane from base + off into LDS at lds_base + 16 lane
+__device__ __forceinline__ void lds_load16(const uint8_t* base, uint32_t off, uint8_t* lds)
+{
+    __builtin_amdgcn_global_load_lds(
+        (const __attribute__((address_space(1))) void*)(base + off),
+        (__attribute__((address_space(3))) void*)lds, 16, 0, 0);
+}
+
+template <int N>
+__device__ __forceinline__ void wait_vm()
+{
+    // vmcnt in bits 3:0 and 15:14, everything else not waited for
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
+}
+
+}  // namespace
+
+template <int NM, int TM, int TN, int WM, int WN, int STAGES, bool E4M3>
+__global__ void __launch_bounds__(64 * WM * WN)
+fp8_tile_kernel(Fp8Args a, int nbm, int nbn, int splits)
+{
+    constexpr int WAVES = WM * WN;
+    constexpr int BM = 16 * TM * WM, BR = 16 * TN * WN, BN = BR / NM;
+    constexpr int TNM = TN / NM;                      // 16-row tiles of each matrix per wave
+    constexpr int LPW = (BM + BR) / 8 / WAVES;        // direct loads (8 rows each) per wave and stage
+    constexpr int XPW = BM / 8 / WAVES;               // ... of which rows of x
+    constexpr int SXW = (BM + 63) / 64;               // waves that load scales of x
+    constexpr int STAGE = (BM + BR) * kGroup + 4 * SXW * 64;
+    static_assert(BM % (8 * WAVES) == 0 && BR % (8 * NM * WAVES) == 0 && TN % NM == 0, "whole loads per wave");
+
+    extern __shared__ __attribute__((aligned(256))) uint8_t smem[];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave % WM, wn = wave / WM;
+    const int i16 = lane & 15, q = lane >> 4;
+
+    // an XCD takes a run of tiles, rows of x varying fastest: they share their weights in its L2
+    const int tile = xcd_run(blockIdx.x, nbm * nbn);
+    const int nb = tile / nbm, mb = tile - nb * nbm;
+    const int m0 = mb * BM, n0 = nb * BN;
+    const int KB = (a.K + kGroup - 1) / kGroup;
+    const int split = blockIdx.y;
+    const int kb0 = (int)((int64_t)KB * split / splits), kb1 = (int)((int64_t)KB * (split + 1) / splits);
+    const int stages = kb1 - kb0;
+
+    // sources of this wave's direct loads: lane l fills slot l % 8 of row l / 8, with chunk (l % 8) ^ swizzle
+    const int lr = lane >> 3, lc = lane & 7;
+    const uint8_t* base[1 + NM];
+    base[0] = a.x + (int64_t)m0 * a.ldx;
+#pragma unroll
+    for (int m = 0; m < NM; ++m) base[1 + m] = a.w[m] + (int64_t)n0 * a.ldw[m];
+    uint32_t off[LPW];
+    int chunk[LPW];
+#pragma unroll
+    for (int i = 0; i < LPW; ++i) {
+        // rows of the stage in LDS: x, then each matrix
+        const int r = i < XPW ? (i * WAVES + wave) * 8 + lr : BM + ((i - XPW) * WAVES + wave) * 8 + lr;
+        chunk[i] = lc ^ ((r >> 1) & 7);
+        if (i < XPW) {
+            off[i] = (uint32_t)min(r, a.M - 1 - m0) * (uint32_t)a.ldx;
+        } else {
+            const int m = (i - XPW) / ((LPW - XPW) / NM);
+            off[i] = (uint32_t)min(r - BM - m * BN, a.N - 1 - n0) * (uint32_t)a.ldw[m];
+        }
+        off[i] += 16 * chunk[i];
+    }
+    const int sxrow = min(m0 + (wave % SXW) * 64 + lane, a.M - 1);
+    const float* sxp = a.sx + (int64_t)sxrow * a.sxm;
+    const bool ktail = (a.K & (kGroup - 1)) != 0;
+
+    auto issue = [&](int kb, int buf) __attribute__((always_inline)) {
+        uint8_t* st = smem + buf * STAGE;
+        const bool tail = ktail && kb == KB - 1;
+#pragma unroll
+        for (int i = 0; i < LPW; ++i) {
+            const int b = i < XPW ? 0 : 1 + (i - XPW) / ((LPW - XPW) / NM);
+            const int r8 = i < XPW ? i * WAVES + wave : BM / 8 + (i - XPW) * WAVES + wave;
+            // past the row's end the row's own first chunk is read instead; it is overwritten with zeros below
+            const bool out = tail && kb * kGroup + 16 * chunk[i] >= a.K;
+            lds_load16(base[b] + (int64_t)kb * kGroup, out ? off[i] - 16 * chunk[i] : off[i], st + r8 * 1024);
+        }
+        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(sxp + kb * a.sxg),
+                                         (__attribute__((address_space(3))) void*)(st + (BM + BR) * kGroup +
+                                                                                   (wave % SXW) * 256),
+                                         4, 0, 0);
+    };
+
+    f32x4 acc[TN][TM];
+#pragma unroll
+    for (int i = 0; i < TN; ++i) {
+#pragma unroll
+        for (int j = 0; j < TM; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    // this wave's weight rows within a matrix, and the scale row they share (a wave's rows lie in one block of 128)
+    const int wr0 = wn * (TNM * 16);
+    const float* swp[NM];
+#pragma unroll
+    for (int m = 0; m < NM; ++m) swp[m] = a.sw[m] + (int64_t)min((n0 + wr0) / kGroup, (a.N - 1) / kGroup) * a.ldsw[m];
+
+    // slots of the operand reads: rows 16 t + l % 16 share the swizzle of l % 16
+    const int swz = (i16 >> 1) & 7;
+    const int rd0 = i16 * kGroup + ((q ^ swz) << 4), rd1 = i16 * kGroup + (((q + 4) ^ swz) << 4);
+
+    auto compute = [&](int kb, int buf) __attribute__((always_inline)) {
+        const uint8_t* st = smem + buf * STAGE;
+        const uint8_t* xs = st + wm * (TM * 16) * kGroup;
+        raw4_t b[TM][2];
+        float sc[NM][TM];
+#pragma unroll
+        for (int j = 0; j < TM; ++j) {
+            b[j][0] = *reinterpret_cast<const raw4_t*>(xs + j * 16 * kGroup + rd0);
+            b[j][1] = *reinterpret_cast<const raw4_t*>(xs + j * 16 * kGroup + rd1);
+        }
+        const float* sx = reinterpret_cast<const float*>(st + (BM + BR) * kGroup) + wm * (TM * 16);
+#pragma unroll
+        for (int m = 0; m < NM; ++m) {
+            const float sw = scalar_load(swp[m] + kb);
+#pragma unroll
+            for (int j = 0; j < TM; ++j) sc[m][j] = sx[16 * j + i16] * sw;
+        }
+#pragma unroll
+        for (int i = 0; i < TN; ++i) {
+            const int m = i / TNM;
+            const uint8_t* ws = st + (BM + m * BN + wr0 + (i - m * TNM) * 16) * kGroup;
+            const raw4_t a0 = *reinterpret_cast<const raw4_t*>(ws + rd0);
+            const raw4_t a1 = *reinterpret_cast<const raw4_t*>(ws + rd1);
+#pragma unroll
+            for (int j = 0; j < TM; ++j) {
+                const f32x4 p = mfma_e4m3(a0, a1, b[j][0], b[j][1]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(p[e], sc[m][j], acc[i][j][e]);
+            }
+        }
+    };
+
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s) {
+        if (s < stages) issue(kb0 + s, s);
+    }
+    int buf = 0;
+    for (int s = 0; s < stages; ++s) {
+        // this wave's loads of stage s have landed; past the barrier everyone's have, and everyone is
+        // done with the buffer that the next issue overwrites
+        if (s + STAGES - 1 <= stages) wait_vm<(STAGES - 2) * (LPW + 1)>();
+        else wait_vm<0>();
+        if (ktail && kb0 + s == KB - 1) {
+#pragma unroll
+            for (int i = 0; i < LPW; ++i) {
+                const int r8 = i < XPW ? i * WAVES + wave : BM / 8 + (i - XPW) * WAVES + wave;
+                if ((KB - 1) * kGroup + 16 * chunk[i] >= a.K) {
+                    *reinterpret_cast<raw4_t*>(smem + buf * STAGE + r8 * 1024 + lane * 16) = raw4_t{0u, 0u, 0u, 0u};
+                }
+            }
+            __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): the zeros are in LDS
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        if (s + STAGES - 1 < stages) issue(kb0 + s + STAGES - 1, buf == 0 ? STAGES - 1 : buf - 1);
+        compute(kb0 + s, buf);
+        buf = buf + 1 == STAGES ? 0 : buf + 1;
+    }
+
+    // lane l holds weight rows 4 (l / 16) + e of each tile, for row l % 16 of x
+    const int mrow = m0 + wm * (TM * 16) + i16;
+    const int ncol = n0 + wr0 + 4 * q;
+    if (!E4M3 && a.out_dtype == kPartial) {
+#pragma unroll
+        for (int i = 0; i < TN; ++i) {
+            const int m = i / TNM, n = ncol + (i - m * TNM) * 16;
+#pragma unroll
+            for (int j = 0; j < TM; ++j) {
+                const int row = mrow + 16 * j;
+                if (row < a.M && n < a.N) {
+                    store_values4(a.part, GLU_DTYPE_FP32, ((int64_t)(split * NM + m) * a.M + row) * a.N + n, acc[i][j],
+                                  a.N - n);
+                }
+            }
+        }
+        return;
+    }
+    if constexpr (NM == 2) {
+#pragma unroll
+        for (int i = 0; i < TNM; ++i) {
+#pragma unroll
+            for (int j = 0; j < TM; ++j) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[i][j][e] = silu_mul(acc[i][j][e], acc[TNM + i][j][e]);
+            }
+        }
+    }
+    if constexpr (E4M3) {
+        // rows past N hold copies of row N - 1 and may not count towards the maximum
+        constexpr int GW = TNM * 16 >= kGroup ? 1 : kGroup / (TNM * 16);  // waves that share a group
+        uint32_t* gmax = reinterpret_cast<uint32_t*>(smem);               // [WN][BM]
+        __syncthreads();
+        uint32_t am[TM];
+#pragma unroll
+        for (int j = 0; j < TM; ++j) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < TNM; ++i) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (ncol + 16 * i + e < a.N) m = max(m, abs_bits(acc[i][j][e]));
+                }
+            }
+            m = max(m, (uint32_t)__builtin_amdgcn_ds_swizzle((int)m, 0x401F));  // lane ^ 16
+            auto pr = __builtin_amdgcn_permlane32_swap(m, m, false, false);
+            am[j] = max((uint32_t)pr[0], (uint32_t)pr[1]);
+        }
+        if constexpr (GW > 1) {
+            if (lane < 16) {
+#pragma unroll
+                for (int j = 0; j < TM; ++j) gmax[wn * BM + wm * (TM * 16) + 16 * j + i16] = am[j];
+            }
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < TM; ++j) {
+                const int g0 = wn / GW * GW;
+#pragma unroll
+                for (int w = 0; w < GW; ++w) am[j] = max(am[j], gmax[(g0 + w) * BM + wm * (TM * 16) + 16 * j + i16]);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < TM; ++j) {
+            const int row = mrow + 16 * j;
+            const Scale s = scale_of(am[j]);
+            if (row >= a.M) continue;
+#pragma unroll
+            for (int i = 0; i < TNM; ++i) {
+                const int n = ncol + 16 * i;
+                if (n >= a.N) continue;
+                int d = 0;
+                d = __builtin_amdgcn_cvt_pk_fp8_f32(quotient(acc[i][j][0], s), quotient(acc[i][j][1], s), d, false);
+                d = __builtin_amdgcn_cvt_pk_fp8_f32(quotient(acc[i][j][2], s), quotient(acc[i][j][3], s), d, true);
+                uint8_t* o = static_cast<uint8_t*>(a.out) + row * a.ldo + n;
+                if (n + 3 < a.N) {
+                    __builtin_memcpy(o, &d, 4);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 3; ++e) {
+                        if (n + e < a.N) o[e] = (uint8_t)(d >> (8 * e));
+                    }
+                }
+            }
+            if (q == 0 && wn % GW == 0 && n0 + wr0 < a.N) a.scale[(int64_t)((n0 + wr0) / kGroup) * a.lds + row] = s.s;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < TNM; ++i) {
+#pragma unroll
+            for (int j = 0; j < TM; ++j) {
+                const int row = mrow + 16 * j, n = ncol + 16 * i;
+                if (row < a.M && n < a.N) store_values4(a.out, a.out_dtype, row * a.ldo + n, acc[i][j], a.N - n);
+            }
+        }
+    }
+}
+
+namespace {
+
+using TileFn = void (*)(Fp8Args, int, int, int);
+
+template <int NM>
+TileFn pick_tile(int shape, bool e4m3)
+{
+    switch (shape) {
+    case 0: return e4m3 ? fp8_tile_kernel<NM, 4, 8, 4, 2, 2, true> : fp8_tile_kernel<NM, 4, 8, 4, 2, 2, false>;
+    case 1:
+        if (e4m3) return NM == 1 ? fp8_tile_kernel<1, 4, 4, 2, 2, 2, true> : nullptr;
+        return fp8_tile_kernel<NM, 4, 4, 2, 2, 2, false>;
+    case 2: return e4m3 ? fp8_tile_kernel<NM, 4, 4, 1, 4, 3, true> : fp8_tile_kernel<NM, 4, 4, 1, 4, 3, false>;
+    case 3:
+        if (e4m3) return NM == 1 ? fp8_tile_kernel<1, 2, 2, 1, 4, 4, true> : nullptr;
+        return fp8_tile_kernel<NM, 2, 2, 1, 4, 4, false>;
+    }
+    return nullptr;
+}
+
+size_t tile_lds(int shape)
+{
+    const TileShape& t = kTileShapes[shape];
+    return (size_t)t.stages * ((t.bm + t.br) * kGroup + 4 * ((t.bm + 63) / 64) * 64);
+}
+
+}  // namespace
+
+bool fp8_tile_owns_groups(int mats, int shape) { return kTileShapes[shape].br / mats % kGroup == 0; }
+
+hipError_t fp8_tile_launch(int mats, const TileConfig& c, const Fp8Args& a, hipStream_t stream)
+{
+    const TileShape& t = kTileShapes[c.shape];
+    const bool e4m3 = a.out_dtype == GLU_DTYPE_E4M3;
+    const TileFn f = mats == 1 ? pick_tile<1>(c.shape, e4m3) : pick_tile<2>(c.shape, e4m3);
+    if (!f) return hipErrorInvalidValue;
+    const size_t lds = tile_lds(c.shape);
+    hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(f), hipFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)lds);
+    if (e != hipSuccess) return e;
+    const int bn = t.br / mats;
+    const int nbm = (int)(((int64_t)a.M + t.bm - 1) / t.bm), nbn = (int)(((int64_t)a.N + bn - 1) / bn);
+    hipLaunchKernelGGL(f, dim3((unsigned)(nbm * nbn), (unsigned)c.splits), dim3(t.threads), lds, stream, a, nbm, nbn,
+                       c.splits);
+    return hipGetLastError();
+}
+
+}  // namespace glu

@@ -1,0 +1,211 @@
+// Conversions to e4m3 with scales: activations with one scale per row and 128
+// columns, weights with one per block of 128 x 128; and the end of the products
+// whose partial sums are joined outside their kernel.
+//
+//   s = max(amax |v| / 448, 2^-126)      q = e4m3(v / s)
+//
+// One pass, bound by memory: a lane holds chunks of 8 values, 16 lanes one group of
+// 128 columns, whose maximum is a DPP reduction.
+#include "../../include/glu_fp8.h"
+#include "glu_fp8_device.h"
+#include "glu_quantize.h"
+
+namespace glu {
+
+namespace {
+
+constexpr int kRowsPerWave = 4;  // rows a wave takes through its 512 columns, all loaded before the first is used
+
+// sources of 8 values at (row, chunk c), the first n of them present
+template <class T>
+struct RowSource {
+    const T* x;
+    int64_t ld;
+    __device__ __forceinline__ void load(int row, int c, int n, float (&v)[8]) const
+    {
+        const Chunk<T> ch = load_chunk(x + row * ld + 8 * (int64_t)c, n);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = widen(ch.e[e]);
+    }
+};
+
+struct PartSource {
+    const float* part;
+    int64_t plane;  // M * N
+    int N, splits, mats;
+    __device__ __forceinline__ void sum(const float* p, int64_t step, int n, float (&v)[8]) const
+    {
+        if (splits == 0) {  // an empty contraction
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+            return;
+        }
+        const Chunk<Fp32> first = load_chunk(reinterpret_cast<const Fp32*>(p), n);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = first.e[e].v;
+        for (int s = 1; s < splits; ++s) {
+            const Chunk<Fp32> ch = load_chunk(reinterpret_cast<const Fp32*>(p + s * step), n);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] += ch.e[e].v;
+        }
+    }
+    __device__ __forceinline__ void load(int row, int c, int n, float (&v)[8]) const
+    {
+        const float* p = part + (int64_t)row * N + 8 * (int64_t)c;
+        if (mats == 2) {
+            float u[8];
+            sum(p, 2 * plane, n, v);
+            sum(p + plane, 2 * plane, n, u);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = silu_mul(v[e], u[e]);
+        } else {
+            sum(p, plane, n, v);
+        }
+    }
+};
+
+// 4 waves; a wave takes 512 columns (4 groups) of `R` rows
+template <class Src, class Out, int R>
+__global__ void __launch_bounds__(256)
+convert_rows_kernel(Src src, void* out, int64_t ldo, float* scale, int64_t lds, int M, int K, int col_blocks)
+{
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int rb = blockIdx.x / col_blocks, cb = blockIdx.x - rb * col_blocks;
+    const int c = cb * 64 + lane;
+    const int n = K - 8 * c;
+    const int row0 = (rb * 4 + wave) * R;
+    float v[R][8];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        if (n > 0 && row0 + i < M) {
+            src.load(row0 + i, c, n, v[i]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[i][e] = 0.0f;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int row = row0 + i;
+        const bool live = n > 0 && row < M;
+        if constexpr (sizeof(Out) == 1) {
+            const Scale s = scale_of(max16(abs_max8(v[i])));
+            if (live) {
+                store_e4m3x8(static_cast<uint8_t*>(out) + row * ldo + 8 * (int64_t)c, e4m3x8(v[i], s), n);
+                if ((lane & 15) == 0) scale[(c >> 4) * lds + row] = s.s;
+            }
+        } else {
+            if (live) store_chunk(static_cast<Out*>(out) + row * ldo + 8 * (int64_t)c, narrow8<Out>(v[i]), n);
+        }
+    }
+}
+
+// A workgroup of 256 holds one 128 x 128 block in registers: 16 lanes a row, 16 rows a step, 8 steps.
+template <class T>
+__global__ void __launch_bounds__(256)
+quantize_blocks_kernel(const T* __restrict__ w, int64_t ldw, uint8_t* __restrict__ q, int64_t ldq,
+                       float* __restrict__ scale, int64_t lds, int N, int K, int col_blocks)
+{
+    __shared__ uint32_t red[4];
+    const int rb = blockIdx.x / col_blocks, cb = blockIdx.x - rb * col_blocks;
+    const int c = cb * 16 + (threadIdx.x & 15);
+    const int n = K - 8 * c;
+    const int row0 = rb * kGroup + (threadIdx.x >> 4);
+    Chunk<T> v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int row = row0 + 16 * i;
+        if (n > 0 && row < N) v[i] = load_chunk(w + row * ldw + 8 * (int64_t)c, n);
+        else v[i] = Chunk<T>{};
+    }
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = max(m, abs_bits(widen(v[i].e[e])));
+    }
+    m = max16(m);
+    m = max(m, (uint32_t)__builtin_amdgcn_ds_swizzle((int)m, 0x401F));  // lane ^ 16
+    auto pr = __builtin_amdgcn_permlane32_swap(m, m, false, false);
+    m = max((uint32_t)pr[0], (uint32_t)pr[1]);
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
+    __syncthreads();
+    const Scale s = scale_of(max(max(red[0], red[1]), max(red[2], red[3])));
+    if (threadIdx.x == 0) scale[rb * lds + cb] = s.s;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int row = row0 + 16 * i;
+        if (n > 0 && row < N) {
+            float f[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = widen(v[i].e[e]);
+            store_e4m3x8(q + row * ldq + 8 * (int64_t)c, e4m3x8(f, s), n);
+        }
+    }
+}
+
+// rows per wave: one while the rows would not fill the card otherwise
+template <class Out, class Src>
+hipError_t convert_rows(const Src& src, void* out, int64_t ldo, float* scale, int64_t lds, int M, int K,
+                        hipStream_t stream)
+{
+    const int col_blocks = (K + 511) / 512;
+    const auto blocks = [&](int r) { return (int64_t)((M + 4 * r - 1) / (4 * r)) * col_blocks; };
+    if (blocks(kRowsPerWave) >= 1024) {
+        hipLaunchKernelGGL((convert_rows_kernel<Src, Out, kRowsPerWave>), dim3((unsigned)blocks(kRowsPerWave)),
+                           dim3(256), 0, stream, src, out, ldo, scale, lds, M, K, col_blocks);
+    } else {
+        hipLaunchKernelGGL((convert_rows_kernel<Src, Out, 1>), dim3((unsigned)blocks(1)), dim3(256), 0, stream, src,
+                           out, ldo, scale, lds, M, K, col_blocks);
+    }
+    return hipGetLastError();
+}
+
+template <class T>
+hipError_t blocks_t(const void* w, int64_t ldw, uint8_t* q, int64_t ldq, float* scale, int64_t lds, int N, int K,
+                    hipStream_t stream)
+{
+    const int col_blocks = (K + kGroup - 1) / kGroup, row_blocks = (N + kGroup - 1) / kGroup;
+    hipLaunchKernelGGL((quantize_blocks_kernel<T>), dim3((unsigned)(col_blocks * row_blocks)), dim3(256), 0, stream,
+                       static_cast<const T*>(w), ldw, q, ldq, scale, lds, N, K, col_blocks);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t quantize_rows_launch(int dtype, const void* x, int64_t ldx, uint8_t* q, int64_t ldq, float* scale,
+                                int64_t lds, int M, int K, hipStream_t stream)
+{
+    switch (dtype) {
+    case GLU_DTYPE_BF16:
+        return convert_rows<uint8_t>(RowSource<Bf16>{static_cast<const Bf16*>(x), ldx}, q, ldq, scale, lds, M, K, stream);
+    case GLU_DTYPE_FP16:
+        return convert_rows<uint8_t>(RowSource<Fp16>{static_cast<const Fp16*>(x), ldx}, q, ldq, scale, lds, M, K, stream);
+    default:
+        return convert_rows<uint8_t>(RowSource<Fp32>{static_cast<const Fp32*>(x), ldx}, q, ldq, scale, lds, M, K, stream);
+    }
+}
+
+hipError_t quantize_blocks_launch(int dtype, const void* w, int64_t ldw, uint8_t* q, int64_t ldq, float* scale,
+                                  int64_t lds, int N, int K, hipStream_t stream)
+{
+    switch (dtype) {
+    case GLU_DTYPE_BF16: return blocks_t<Bf16>(w, ldw, q, ldq, scale, lds, N, K, stream);
+    case GLU_DTYPE_FP16: return blocks_t<Fp16>(w, ldw, q, ldq, scale, lds, N, K, stream);
+    default: return blocks_t<Fp32>(w, ldw, q, ldq, scale, lds, N, K, stream);
+    }
+}
+
+hipError_t finish_launch(int out_dtype, const FinishArgs& a, hipStream_t stream)
+{
+    const PartSource src{a.part, (int64_t)a.M * a.N, a.N, a.splits, a.mats};
+    switch (out_dtype) {
+    case GLU_DTYPE_BF16: return convert_rows<Bf16>(src, a.out, a.ldo, a.scale, a.lds, a.M, a.N, stream);
+    case GLU_DTYPE_FP16: return convert_rows<Fp16>(src, a.out, a.ldo, a.scale, a.lds, a.M, a.N, stream);
+    case GLU_DTYPE_FP32: return convert_rows<Fp32>(src, a.out, a.ldo, a.scale, a.lds, a.M, a.N, stream);
+    default: return convert_rows<uint8_t>(src, a.out, a.ldo, a.scale, a.lds, a.M, a.N, stream);
+    }
+}
+
+}  // namespace glu

@@ -59,8 +59,9 @@ typedef enum glu_status {
                                  rows whose extent overflows int64 */
     GLU_ERR_WORKSPACE = 8,    /* glu_dual_gemv_backward: workspace NULL, not 256-byte aligned
                                  or smaller than glu_dual_gemv_backward_workspace asks */
-    GLU_ERR_SCRATCH_LIMIT = 9 /* glu_dual_gemv_backward_noalloc: the call needs more scratch than
+    GLU_ERR_SCRATCH_LIMIT = 9, /* glu_dual_gemv_backward_noalloc: the call needs more scratch than
                                  the library's fixed device array holds */
+    GLU_ERR_BAD_ARGUMENT = 10 /* glu_fp8.h: an unknown element type, or an eps that is negative or not finite */
 } glu_status;
 
 /*

@@ -1,0 +1,191 @@
+"""The C ABI of include/glu_fp8.h on the host: refusals before any HIP call, and launch plans (CPU only).
+
+The addresses are made up: a call that got past its checks would launch, so every call here must be
+refused or be empty."""
+import ctypes
+
+import pytest
+
+from glu_mlp_gemv_amd import api, fp8
+
+OK, NULLP, SHAPE, ALIGN, ALIAS, LAUNCH, UNSUP, STRIDE, WORKSPACE = range(9)
+ARG = 10
+BF16, FP16, FP32, E4M3 = range(4)
+# disjoint made-up arrays, 256 MiB apart
+P = [0x100000000 + i * 0x10000000 for i in range(12)]
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return api.library()
+
+
+def norm(lib, **kw):
+    a = dict(x=P[0], ldx=256, res=P[1], ldr=256, w=P[2], sum=P[3], lds=256, out=P[4], ldo=256, rstd=P[5], M=4, K=256,
+             eps=1e-6, dtype=BF16)
+    a.update(kw)
+    return lib.glu_add_rms_norm(a["x"], a["ldx"], a["res"], a["ldr"], a["w"], a["sum"], a["lds"], a["out"], a["ldo"],
+                                a["rstd"], a["M"], a["K"], a["eps"], a["dtype"], None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(dtype=3), ARG), (dict(dtype=-1), ARG), (dict(dtype=7), ARG),
+    (dict(eps=-1.0), ARG), (dict(eps=float("nan")), ARG), (dict(eps=float("inf")), ARG),
+    (dict(M=-1), SHAPE), (dict(K=-1), SHAPE), (dict(K=0), SHAPE), (dict(M=1 << 31), SHAPE), (dict(K=1 << 31), SHAPE),
+    (dict(M=0), OK), (dict(M=0, x=None, w=None, out=None), OK),
+    (dict(sum=None), NULLP), (dict(res=None), NULLP), (dict(x=None), NULLP), (dict(w=None), NULLP), (dict(out=None), NULLP),
+    (dict(ldx=255), STRIDE), (dict(ldr=0), STRIDE), (dict(lds=-256), STRIDE), (dict(ldo=255), STRIDE),
+    (dict(ldx=1 << 62), STRIDE),
+    (dict(x=P[0] + 1), ALIGN), (dict(out=P[4] + 1), ALIGN), (dict(rstd=P[5] + 2), ALIGN),
+    (dict(dtype=FP32, w=P[2] + 2), ALIGN),
+    (dict(out=P[0]), ALIAS), (dict(out=P[1] + 512), ALIAS), (dict(out=P[2]), ALIAS), (dict(out=P[3]), ALIAS),
+    (dict(sum=P[1] + 2), ALIAS), (dict(sum=P[1], lds=300), ALIAS), (dict(sum=P[2]), ALIAS), (dict(rstd=P[4]), ALIAS),
+])
+def test_norm_refusals(lib, kw, status):
+    assert norm(lib, **kw) == status
+
+
+def test_norm_fp8_refusals(lib):
+    def call(q=P[4], ldq=256, scale=P[5], lds=4, M=4):
+        return lib.glu_add_rms_norm_fp8(P[0], 256, None, 0, P[2], None, 0, q, ldq, scale, lds, None, M, 256, 1e-6, BF16,
+                                        None)
+    assert call(q=None) == NULLP and call(scale=None) == NULLP
+    assert call(ldq=255) == STRIDE and call(lds=3) == STRIDE
+    assert call(scale=P[5] + 2) == ALIGN
+    assert call(q=P[5]) == ALIAS and call(scale=P[0]) == ALIAS
+    assert call(M=0) == OK
+
+
+def test_norm_backward_refusals(lib):
+    need = ctypes.c_int64()
+    assert lib.glu_add_rms_norm_backward_workspace(100, 512, ctypes.byref(need)) == OK
+    assert need.value % 4 == 0 and need.value >= 2 * 512 * 4
+    assert lib.glu_add_rms_norm_backward_workspace(1, 512, ctypes.byref(need)) == OK and need.value == 0
+    assert lib.glu_add_rms_norm_backward_workspace(0, 512, ctypes.byref(need)) == OK and need.value == 0
+    assert lib.glu_add_rms_norm_backward_workspace(5, 0, ctypes.byref(need)) == SHAPE
+    assert lib.glu_add_rms_norm_backward_workspace(5, 5, None) == NULLP
+    lib.glu_add_rms_norm_backward_workspace(100, 512, ctypes.byref(need))
+
+    def call(dy=P[0], lddy=512, h=P[1], w=P[2], rstd=P[3], dr=P[4], dx=P[5], dw=P[6], M=100, K=512, dtype=BF16,
+             ws=P[7], n=need.value):
+        return lib.glu_add_rms_norm_backward(dy, lddy, h, 512, w, rstd, dr, 512, dx, 512, dw, M, K, dtype, ws, n, None)
+    for name in ("dy", "h", "w", "rstd", "dx", "dw"):
+        assert call(**{name: None}) == NULLP
+    assert call(dtype=E4M3) == ARG and call(M=-1) == SHAPE and call(K=0) == SHAPE
+    assert call(lddy=511) == STRIDE and call(dx=P[5] + 1) == ALIGN
+    assert call(dx=P[0]) == ALIAS and call(dx=P[4] + 2) == ALIAS and call(dw=P[2]) == ALIAS and call(dw=P[5]) == ALIAS
+    assert call(ws=P[1]) == ALIAS
+    assert call(ws=None) == WORKSPACE and call(ws=P[7] + 4) == WORKSPACE and call(n=need.value - 1) == WORKSPACE
+
+
+def test_quantize_refusals(lib):
+    for f, scale_ld in ((lib.glu_fp8_quantize, 4), (lib.glu_fp8_quantize_weight, 2)):
+        def call(x=P[0], ldx=256, q=P[1], ldq=256, s=P[2], lds=scale_ld, M=4, K=256, dtype=BF16):
+            return f(x, ldx, q, ldq, s, lds, M, K, dtype, None)
+        assert call(dtype=E4M3) == ARG and call(M=-1) == SHAPE and call(K=1 << 31) == SHAPE
+        assert call(M=0) == OK and call(K=0) == OK
+        assert call(x=None) == NULLP and call(q=None) == NULLP and call(s=None) == NULLP
+        assert call(ldx=255) == STRIDE and call(ldq=255) == STRIDE and call(M=400, lds=1) == STRIDE
+        assert call(x=P[0] + 1) == ALIGN and call(s=P[2] + 1) == ALIGN
+        assert call(q=P[0]) == ALIAS and call(s=P[1]) == ALIAS
+
+
+def product(lib, mats=1, x=P[0], sx=P[1], ldx=256, sxr=1, sxb=4, w=P[2], sw=P[3], ldw=256, swr=2, swb=1, up=P[4],
+            su=P[5], out=P[6], ldo=256, os=None, lds=0, M=4, N=256, K=256, dtype=BF16, ws=P[8], n=1 << 20, plan=None):
+    xm, wm = fp8.Matrix(x, sx, ldx, sxr, sxb), fp8.Matrix(w, sw, ldw, swr, swb)
+    um = fp8.Matrix(up, su, ldw, swr, swb)
+    r = ctypes.byref
+    if plan is not None:
+        return lib.glu_fp8_product_tuned(r(xm), r(wm), r(um) if mats == 2 else None, out, ldo, os, lds, M, N, K, dtype,
+                                         r(plan), ws, n, None)
+    if mats == 2:
+        return lib.glu_fp8_dual_glu(r(xm), r(wm), r(um), out, ldo, os, lds, M, N, K, dtype, ws, n, None)
+    return lib.glu_fp8_linear(r(xm), r(wm), out, ldo, os, lds, M, N, K, dtype, ws, n, None)
+
+
+@pytest.mark.parametrize("mats", [1, 2])
+@pytest.mark.parametrize("kw,status", [
+    (dict(dtype=4), ARG), (dict(dtype=-1), ARG),
+    (dict(M=-1), SHAPE), (dict(N=-1), SHAPE), (dict(K=-1), SHAPE), (dict(N=1 << 31), SHAPE),
+    (dict(M=0), OK), (dict(N=0), OK), (dict(M=0, x=None, w=None, out=None), OK),
+    (dict(x=None), NULLP), (dict(sx=None), NULLP), (dict(w=None), NULLP), (dict(sw=None), NULLP), (dict(out=None), NULLP),
+    (dict(dtype=E4M3, os=None, lds=4), NULLP),
+    (dict(ldx=255), STRIDE), (dict(ldw=0), STRIDE), (dict(ldo=255), STRIDE), (dict(swr=1), STRIDE), (dict(swb=2), STRIDE),
+    (dict(sxr=-1), STRIDE), (dict(sxb=-4), STRIDE), (dict(sxr=1 << 62), STRIDE), (dict(dtype=E4M3, os=P[7], lds=3), STRIDE),
+    (dict(sx=P[1] + 1), ALIGN), (dict(sw=P[3] + 2), ALIGN), (dict(out=P[6] + 1), ALIGN),
+    (dict(out=P[0]), ALIAS), (dict(out=P[1]), ALIAS), (dict(out=P[2] + 1024), ALIAS), (dict(out=P[3]), ALIAS),
+    (dict(dtype=E4M3, os=P[6], lds=4), ALIAS),
+    (dict(dtype=E4M3, os=P[7], lds=4, ws=P[0]), ALIAS),
+    (dict(dtype=E4M3, os=P[7], lds=4, ws=None), WORKSPACE), (dict(dtype=E4M3, os=P[7], lds=4, n=16), WORKSPACE),
+    (dict(dtype=E4M3, os=P[7], lds=4, ws=P[8] + 8), WORKSPACE),
+])
+def test_product_refusals(lib, kw, status, mats):
+    assert product(lib, mats, **kw) == status
+
+
+def test_dual_refusals(lib):
+    assert product(lib, 2, up=None) == NULLP and product(lib, 2, su=None) == NULLP
+    assert product(lib, 2, out=P[4]) == ALIAS and product(lib, 2, out=P[5]) == ALIAS
+    assert lib.glu_fp8_linear(None, None, P[0], 256, None, 0, 4, 256, 256, BF16, None, 0, None) == NULLP
+
+
+@pytest.mark.parametrize("plan", [(0, 0, 0, 1), (5, 0, 0, 1), (3, -1, 0, 1), (3, 99, 0, 1), (3, 0, 0, 0), (3, 0, 0, 3),
+                                  (2, 5, 4, 1), (2, 16, 0, 1), (2, 16, 17, 1), (2, 16, 4, -1), (2, 32, 4, 1), (4, 8, 4, 1)])
+def test_unsupported_plans(lib, plan):
+    assert product(lib, plan=fp8.ProductPlan(*plan)) == UNSUP
+
+
+def test_layouts_that_are_not_fast_refuse_the_fast_kernels(lib):
+    for kw in (dict(x=P[0] + 1), dict(ldx=264), dict(w=P[2] + 8), dict(K=250, ldw=256)):
+        for kernel, tile in ((2, 16), (3, 1)):
+            assert product(lib, plan=fp8.ProductPlan(kernel, tile, 4, 1), **kw) == UNSUP
+    assert product(lib, plan=fp8.ProductPlan(2, 4, 4, 1), M=5, sxb=5) == UNSUP, "4 rows of weights serve 4 rows of x"
+
+
+def test_plans_cover_every_size():
+    """Every size gets a plan whose parts fit it; e4m3 output and split sums ask for the workspace they use."""
+    import torch
+    for mats in (1, 2):
+        for M in (1, 2, 4, 5, 8, 9, 16, 17, 32, 33, 64, 65, 128, 203, 257, 1024, 1025, 4096, 8192, 70000):
+            for N in (1, 100, 256, 2560, 17408, 100000):
+                for K in (1, 16, 128, 144, 2560, 9216, 17408):
+                    for t in (torch.bfloat16, fp8.E4M3):
+                        for fast in (True, False):
+                            p = fp8.product_plan(mats, M, N, K, t, fast)
+                            blocks = -(-K // 128)
+                            assert p["kernel_name"] in (("stream", "tile") if fast else ("any",))
+                            assert 1 <= p["splits"] <= blocks and p["launches"] in (1, 2)
+                            want = p["splits"] * mats * M * N * 4 if p["launches"] == 2 else 0
+                            assert p["workspace_bytes"] == want
+                            assert p["splits"] == 1 or p["launches"] == 2
+    assert fp8.product_plan(1, 0, 5, 5)["kernel_name"] == "none"
+    assert fp8.product_plan(1, 5, 5, 0)["kernel_name"] == "zero"
+
+
+def test_workspace_covers_either_layout(lib):
+    import torch
+    need = ctypes.c_int64()
+    for mats in (1, 2):
+        for M, N, K in ((1, 9216, 2560), (37, 12288, 4096), (203, 4096, 12288), (4096, 17408, 5120)):
+            for t in (torch.bfloat16, fp8.E4M3):
+                assert lib.glu_fp8_workspace(mats, M, N, K, fp8.DTYPES[t], ctypes.byref(need)) == OK
+                for fast in (True, False):
+                    assert need.value >= fp8.product_plan(mats, M, N, K, t, fast)["workspace_bytes"]
+    assert lib.glu_fp8_workspace(3, 1, 1, 1, BF16, ctypes.byref(need)) == ARG
+    assert lib.glu_fp8_workspace(1, 1, 1, 1, BF16, None) == NULLP
+    assert lib.glu_fp8_product_plan(1, 1, 1, 1, BF16, 1, None) == NULLP
+
+
+def test_python_refuses_cpu_tensors():
+    import torch
+
+    import glu_mlp_gemv_amd as glu
+    x = torch.zeros(2, 128, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        glu.add_rms_norm(x, x[0], 1e-6)
+    with pytest.raises(ValueError):
+        glu.fp8_quantize(x)
+    with pytest.raises(ValueError):
+        glu.fp8_linear(x.to(fp8.E4M3), torch.ones(2, 1), x.to(fp8.E4M3), torch.ones(1, 1))
+    with pytest.raises(TypeError):
+        glu.add_rms_norm([1.0], x[0], 1e-6)
