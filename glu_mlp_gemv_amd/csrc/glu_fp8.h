@@ -22,10 +22,10 @@ struct Fp8Args {
 constexpr int kPartial = -1;
 
 // Weights straight from memory to the matrix cores; a workgroup of `waves` waves splits the K-blocks of
-// `rows` weight rows (4, 8, 16) among them.  tiles: 16-row tiles of x per workgroup (1, 2, 4; 1 below 16 rows).
+// `rows` weight rows (4, 8, 16) among them.
 struct StreamConfig {
-    int rows, tiles, waves, splits;
-    bool any;  // K or an address not a multiple of 16: byte-aligned loads (rows 16, tiles 1)
+    int rows, waves, splits;
+    bool any;  // K or an address not a multiple of 16: byte-aligned loads (rows 16)
 };
 hipError_t fp8_stream_launch(int mats, const StreamConfig& c, const Fp8Args& a, hipStream_t stream);
 bool fp8_stream_supported(int mats, const StreamConfig& c, int M);
@@ -41,6 +41,7 @@ constexpr int kTileShapeCount = 4;
 extern const TileShape kTileShapes[kTileShapeCount];
 struct TileConfig {
     int shape, splits;
+    bool wide;  // fp32 sums on the bf16 unit, else the 8-bit unit's (glu_fp8_mfma.h); e4m3 out: always
 };
 // whether the kernel can finish e4m3 by itself: a workgroup holds whole groups of 128 columns
 bool fp8_tile_owns_groups(int mats, int shape);

@@ -106,11 +106,11 @@ struct Operand {
     int64_t rows, scale_rows, blocks;
 };
 
-// 16-row tiles of x per workgroup of the streaming kernel
-int stream_tiles(int64_t M, bool any) { return any || M <= 16 ? 1 : M <= 32 ? 2 : 4; }
+// outputs that show more than the 8-bit matrix unit's sums hold (glu_fp8_mfma.h)
+bool needs_wide(int out_dtype) { return out_dtype == GLU_DTYPE_FP32 || out_dtype == GLU_DTYPE_E4M3; }
 
 // Fills the launch shape for sizes >= 1.  What decides is measured with perf's sizes in DESIGN's table and at the rule.
-void choose(int mats, int64_t M, int64_t N, int64_t K, int out_dtype, bool fast, glu_fp8_plan* p)
+void choose(int mats, int64_t M, int64_t N, int64_t K, bool fast, glu_fp8_plan* p)
 {
     const int64_t KB = ceil_div(K, kGroup);
     p->splits = 1;
@@ -120,14 +120,13 @@ void choose(int mats, int64_t M, int64_t N, int64_t K, int out_dtype, bool fast,
         p->width = 4;
         return;
     }
-    if (M <= 16 || out_dtype == GLU_DTYPE_FP32) {
+    if (M <= 16) {
         p->kernel = GLU_FP8_KERNEL_STREAM;
         p->tile = 16;
         while (p->tile > 4 && M <= p->tile / 2 && ceil_div(N, p->tile) < 2 * kCUs) p->tile /= 2;
         const int64_t steps = ceil_div(KB, 16 / p->tile);
         int64_t w = ceil_div(steps, 4);
-        const int64_t most = M <= 16 ? 16 : 8;
-        p->width = (int)(w > most ? most : w);
+        p->width = (int)(w > 16 ? 16 : w);
         return;
     }
     p->kernel = GLU_FP8_KERNEL_TILE;
@@ -177,18 +176,17 @@ glu_status product_plan(int mats, int64_t M, int64_t N, int64_t K, int out_dtype
         if (p->splits < 1 || p->splits > ceil_div(K, kGroup) || p->splits > 64) return GLU_ERR_UNSUPPORTED;
         if (p->kernel == GLU_FP8_KERNEL_TILE) {
             if (!fast || p->tile < 0 || p->tile >= glu::kTileShapeCount) return GLU_ERR_UNSUPPORTED;
-            if (out_dtype == GLU_DTYPE_FP32) return GLU_ERR_UNSUPPORTED;  // its sums are coarser than that
             p->width = glu::kTileShapes[p->tile].threads;
         } else if (p->kernel == GLU_FP8_KERNEL_STREAM || p->kernel == GLU_FP8_KERNEL_ANY) {
             const bool any = p->kernel == GLU_FP8_KERNEL_ANY;
             if (!any && !fast) return GLU_ERR_UNSUPPORTED;
-            const glu::StreamConfig c{p->tile, stream_tiles(M, any), p->width, p->splits, any};
+            const glu::StreamConfig c{p->tile, p->width, p->splits, any};
             if (!glu::fp8_stream_supported(mats, c, (int)M)) return GLU_ERR_UNSUPPORTED;
         } else {
             return GLU_ERR_UNSUPPORTED;
         }
     } else {
-        choose(mats, M, N, K, out_dtype, fast, p);
+        choose(mats, M, N, K, fast, p);
     }
     // the streaming grid: one row tile's threads below 2^32
     if (p->kernel != GLU_FP8_KERNEL_TILE && ceil_div(N, p->tile) * p->splits > 0xffffffffLL / (64 * p->width)) {
@@ -275,10 +273,10 @@ glu_status product_call(const glu_fp8_matrix* x, const glu_fp8_matrix* w0, const
     a.out_dtype = p.launches == 2 ? glu::kPartial : out_dtype;
     hipError_t e;
     if (p.kernel == GLU_FP8_KERNEL_TILE) {
-        e = glu::fp8_tile_launch(mats, glu::TileConfig{p.tile, p.splits}, a, s);
+        e = glu::fp8_tile_launch(mats, glu::TileConfig{p.tile, p.splits, needs_wide(out_dtype)}, a, s);
     } else {
         const bool any = p.kernel == GLU_FP8_KERNEL_ANY;
-        const glu::StreamConfig c{p.tile, stream_tiles(M, any), p.width, p.splits, any};
+        const glu::StreamConfig c{p.tile, p.width, p.splits, any};
         e = glu::fp8_stream_launch(mats, c, a, s);
     }
     if (e == hipSuccess && p.launches == 2) e = glu::finish_launch(out_dtype, fin, s);

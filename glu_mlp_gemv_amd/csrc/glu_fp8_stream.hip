@@ -7,15 +7,14 @@
 // K-blocks, the B operand holds x at those K-blocks in the same order, and of the 16 x 16 results the
 // blocks on the diagonal are the products wanted.  That gives narrow matrices 2 and 4 times the workgroups, for x of
 // up to R rows.  The waves' sums meet in LDS in wave order.  The products run on the bf16 unit, whose sums are fp32
-// (glu_fp8_mfma.h), so this is also the kernel of fp32 results for any number of rows, 64 at a time.
+// (glu_fp8_mfma.h).
 #include "glu_fp8_mfma.h"
 
 namespace glu {
 
 namespace {
 
-// more tiles of x per wave take more registers
-constexpr int stream_max_waves(int tiles) { return tiles == 1 ? 16 : 8; }
+constexpr int kStreamMaxWaves = 16;
 
 template <bool ANY>
 __device__ __forceinline__ raw4_t chunk16(const uint8_t* row, int64_t off, int K)
@@ -39,21 +38,20 @@ __device__ __forceinline__ raw4_t chunk16(const uint8_t* row, int64_t off, int K
 
 }  // namespace
 
-template <int NM, int T, int R, bool ANY>
-__global__ void __launch_bounds__(64 * stream_max_waves(T))
+template <int NM, int R, bool ANY>
+__global__ void __launch_bounds__(64 * kStreamMaxWaves)
 fp8_stream_kernel(Fp8Args a, int waves, int splits, int nbn, int m_base)
 {
-    static_assert(R == 16 || T == 1, "several K-blocks per instruction: one tile of x");
     constexpr int S = 16 / R;          // K-blocks per instruction
-    constexpr int U = T > 1 ? 1 : NM == 2 ? 2 : 4;  // steps whose loads are issued together
-    extern __shared__ float red[];     // [waves][NM][T][4][64]
+    constexpr int U = NM == 2 ? 2 : 4;  // steps whose loads are issued together
+    extern __shared__ float red[];     // [waves][NM][4][64]
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int i16 = lane & 15, q = lane >> 4;
     const int sel = i16 / R;  // this lane's K-block within the instruction (both operands)
     const int mb = blockIdx.x / nbn;
     const int n0 = (blockIdx.x - mb * nbn) * R;
-    const int m0 = m_base + mb * 16 * T;
+    const int m0 = m_base + mb * 16;
     const int split = blockIdx.y;
     const int KB = (a.K + kGroup - 1) / kGroup;
     const int steps = (KB + S - 1) / S;
@@ -65,25 +63,17 @@ fp8_stream_kernel(Fp8Args a, int waves, int splits, int nbn, int m_base)
         wr[m] = a.w[m] + (int64_t)min(n0 + i16 % R, a.N - 1) * a.ldw[m];
         ws[m] = a.sw[m] + (int64_t)(n0 / kGroup) * a.ldsw[m];
     }
-    const uint8_t* xr[T];
-    const float* xs[T];
-#pragma unroll
-    for (int t = 0; t < T; ++t) {
-        const int row = min(m0 + 16 * t + i16 % R, a.M - 1);
-        xr[t] = a.x + (int64_t)row * a.ldx;
-        xs[t] = a.sx + (int64_t)row * a.sxm;
-    }
+    const int xrow = min(m0 + i16 % R, a.M - 1);
+    const uint8_t* xr = a.x + (int64_t)xrow * a.ldx;
+    const float* xs = a.sx + (int64_t)xrow * a.sxm;
 
-    f32x4 acc[NM][T];
+    f32x4 acc[NM];
 #pragma unroll
-    for (int m = 0; m < NM; ++m) {
-#pragma unroll
-        for (int t = 0; t < T; ++t) acc[m][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    }
+    for (int m = 0; m < NM; ++m) acc[m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     const int stride = waves * splits;
     for (int s0 = split * waves + wave; s0 < steps; s0 += U * stride) {
-        raw4_t wv[U][NM][2], xv[U][T][2];
-        float sc[U][NM][T];
+        raw4_t wv[U][NM][2], xv[U][2];
+        float sc[U][NM];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int s = s0 + u * stride;
@@ -96,30 +86,21 @@ fp8_stream_kernel(Fp8Args a, int waves, int splits, int nbn, int m_base)
                 wv[u][m][1] = chunk16<ANY>(wr[m], off + 64, a.K);
             }
             const int kbs = min(kb, KB - 1);
+            xv[u][0] = chunk16<ANY>(xr, off, a.K);
+            xv[u][1] = chunk16<ANY>(xr, off + 64, a.K);
+            const float sx = xs[kbs * a.sxg];
 #pragma unroll
-            for (int t = 0; t < T; ++t) {
-                xv[u][t][0] = chunk16<ANY>(xr[t], off, a.K);
-                xv[u][t][1] = chunk16<ANY>(xr[t], off + 64, a.K);
-                const float sx = xs[t][kbs * a.sxg];
-#pragma unroll
-                for (int m = 0; m < NM; ++m) sc[u][m][t] = sx * ws[m][kbs];
-            }
+            for (int m = 0; m < NM; ++m) sc[u][m] = sx * ws[m][kbs];
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (s0 + u * stride >= steps) break;
-            Wide x[T];
-#pragma unroll
-            for (int t = 0; t < T; ++t) x[t] = widen32(xv[u][t][0], xv[u][t][1]);
+            const Wide x = widen32(xv[u][0], xv[u][1]);
 #pragma unroll
             for (int m = 0; m < NM; ++m) {
-                const Wide w = widen32(wv[u][m][0], wv[u][m][1]);
+                const f32x4 p = mfma_wide(widen32(wv[u][m][0], wv[u][m][1]), x);
 #pragma unroll
-                for (int t = 0; t < T; ++t) {
-                    const f32x4 p = mfma_wide(w, x[t]);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[m][t][e] = fmaf(p[e], sc[u][m][t], acc[m][t][e]);
-                }
+                for (int e = 0; e < 4; ++e) acc[m][e] = fmaf(p[e], sc[u][m], acc[m][e]);
             }
         }
     }
@@ -127,16 +108,13 @@ fp8_stream_kernel(Fp8Args a, int waves, int splits, int nbn, int m_base)
 #pragma unroll
     for (int m = 0; m < NM; ++m) {
 #pragma unroll
-        for (int t = 0; t < T; ++t) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) red[(((wave * NM + m) * T + t) * 4 + e) * 64 + lane] = acc[m][t][e];
-        }
+        for (int e = 0; e < 4; ++e) red[((wave * NM + m) * 4 + e) * 64 + lane] = acc[m][e];
     }
     __syncthreads();
     // one output a thread: weight row r, row j of x; its sums are D[sel R + r][sel R + j] of every wave
-    for (int idx = threadIdx.x; idx < T * R * R; idx += 64 * waves) {
-        const int r = idx % R, j = (idx / R) % R, t = idx / (R * R);
-        const int n = n0 + r, row = m0 + 16 * t + j;
+    for (int idx = threadIdx.x; idx < R * R; idx += 64 * waves) {
+        const int r = idx % R, j = idx / R;
+        const int n = n0 + r, row = m0 + j;
         if (n >= a.N || row >= a.M) continue;
         float v[NM];
 #pragma unroll
@@ -146,7 +124,7 @@ fp8_stream_kernel(Fp8Args a, int waves, int splits, int nbn, int m_base)
 #pragma unroll
                 for (int b = 0; b < S; ++b) {
                     const int i = b * R + r;
-                    v[m] += red[(((w * NM + m) * T + t) * 4 + (i & 3)) * 64 + (i >> 2) * 16 + b * R + j];
+                    v[m] += red[((w * NM + m) * 4 + (i & 3)) * 64 + (i >> 2) * 16 + b * R + j];
                 }
             }
         }
@@ -168,31 +146,27 @@ using StreamFn = void (*)(Fp8Args, int, int, int, int);
 template <int NM>
 StreamFn pick_stream(const StreamConfig& c)
 {
-    if (c.any) return c.rows == 16 && c.tiles == 1 ? fp8_stream_kernel<NM, 1, 16, true> : nullptr;
-    if (c.tiles == 1 && c.rows == 4) return fp8_stream_kernel<NM, 1, 4, false>;
-    if (c.tiles == 1 && c.rows == 8) return fp8_stream_kernel<NM, 1, 8, false>;
-    if (c.rows != 16) return nullptr;
-    if (c.tiles == 1) return fp8_stream_kernel<NM, 1, 16, false>;
-    if (c.tiles == 2) return fp8_stream_kernel<NM, 2, 16, false>;
-    if (c.tiles == 4) return fp8_stream_kernel<NM, 4, 16, false>;
-    return nullptr;
+    if (c.any) return c.rows == 16 ? fp8_stream_kernel<NM, 16, true> : nullptr;
+    if (c.rows == 4) return fp8_stream_kernel<NM, 4, false>;
+    if (c.rows == 8) return fp8_stream_kernel<NM, 8, false>;
+    return c.rows == 16 ? fp8_stream_kernel<NM, 16, false> : nullptr;
 }
 
-size_t stream_lds(int mats, const StreamConfig& c) { return (size_t)c.waves * mats * c.tiles * 1024; }
+size_t stream_lds(int mats, const StreamConfig& c) { return (size_t)c.waves * mats * 1024; }
 
 }  // namespace
 
 bool fp8_stream_supported(int mats, const StreamConfig& c, int M)
 {
-    if (c.waves < 1 || c.waves > stream_max_waves(c.tiles) || c.splits < 1) return false;
+    if (c.waves < 1 || c.waves > kStreamMaxWaves || c.splits < 1) return false;
     if ((mats == 1 ? pick_stream<1>(c) : pick_stream<2>(c)) == nullptr) return false;
-    return (c.rows == 16 || M <= c.rows) && stream_lds(mats, c) <= 64 * 1024;
+    return c.rows == 16 || M <= c.rows;
 }
 
 hipError_t fp8_stream_launch(int mats, const StreamConfig& c, const Fp8Args& a, hipStream_t stream)
 {
     const StreamFn f = mats == 1 ? pick_stream<1>(c) : pick_stream<2>(c);
-    const int rows_x = c.rows == 16 ? 16 * c.tiles : c.rows;
+    const int rows_x = c.rows;
     const int nbn = (int)(((int64_t)a.N + c.rows - 1) / c.rows);
     // slices of x's rows that keep a grid below 2^32 threads (one launch for anything but vast outputs)
     const int64_t tiles = ((int64_t)a.M + rows_x - 1) / rows_x;

@@ -32,6 +32,37 @@ __device__ __forceinline__ void lds_load16(const uint8_t* base, uint32_t off, ui
         (__attribute__((address_space(3))) void*)lds, 16, 0, 0);
 }
 
+struct Narrow { raw4_t c0, c1; };
+template <bool WIDE> struct Form { using type = Narrow; };
+template <> struct Form<true> { using type = Wide; };
+
+template <bool WIDE>
+__device__ __forceinline__ typename Form<WIDE>::type operand(raw4_t c0, raw4_t c1)
+{
+    if constexpr (WIDE) return widen32(c0, c1);
+    else return Narrow{c0, c1};
+}
+
+// p[j] = the K-block's product of a with b[j]
+template <int TM>
+__device__ __forceinline__ void multiply(const Narrow& a, const Narrow (&b)[TM], f32x4 (&p)[TM])
+{
+#pragma unroll
+    for (int j = 0; j < TM; ++j) p[j] = mfma_e4m3(a.c0, a.c1, b[j].c0, b[j].c1);
+}
+template <int TM>
+__device__ __forceinline__ void multiply(const Wide& a, const Wide (&b)[TM], f32x4 (&p)[TM])
+{
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+#pragma unroll
+        for (int j = 0; j < TM; ++j) {
+            const f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
+            p[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v[k], b[j].v[k], k == 0 ? z : p[j], 0, 0, 0);
+        }
+    }
+}
+
 template <int N>
 __device__ __forceinline__ void wait_vm()
 {
@@ -41,7 +72,9 @@ __device__ __forceinline__ void wait_vm()
 
 }  // namespace
 
-template <int NM, int TM, int TN, int WM, int WN, int STAGES, bool E4M3>
+// WIDE: products on the bf16 unit, for outputs that show more than the 8-bit unit's sums hold: e4m3, whose fp32
+// scales are the largest sums themselves, and fp32.  E4M3: the kernel converts by itself (a workgroup holds whole groups).
+template <int NM, int TM, int TN, int WM, int WN, int STAGES, bool WIDE, bool E4M3>
 __global__ void __launch_bounds__(64 * WM * WN)
 fp8_tile_kernel(Fp8Args a, int nbm, int nbn, int splits)
 {
@@ -53,6 +86,7 @@ fp8_tile_kernel(Fp8Args a, int nbm, int nbn, int splits)
     constexpr int SXW = (BM + 63) / 64;               // waves that load scales of x
     constexpr int STAGE = (BM + BR) * kGroup + 4 * SXW * 64;
     static_assert(BM % (8 * WAVES) == 0 && BR % (8 * NM * WAVES) == 0 && TN % NM == 0, "whole loads per wave");
+    static_assert(WAVES % 2 == 0, "a wave's loads lie a multiple of 16 rows apart");
 
     extern __shared__ __attribute__((aligned(256))) uint8_t smem[];
     const int lane = threadIdx.x & 63;
@@ -75,20 +109,20 @@ fp8_tile_kernel(Fp8Args a, int nbm, int nbn, int splits)
     base[0] = a.x + (int64_t)m0 * a.ldx;
 #pragma unroll
     for (int m = 0; m < NM; ++m) base[1 + m] = a.w[m] + (int64_t)n0 * a.ldw[m];
+    // the same chunk in every load: rows of two loads differ by a multiple of 16
+    const int chunk = lc ^ ((wave * 4 + (lr >> 1)) & 7);
     uint32_t off[LPW];
-    int chunk[LPW];
 #pragma unroll
     for (int i = 0; i < LPW; ++i) {
         // rows of the stage in LDS: x, then each matrix
         const int r = i < XPW ? (i * WAVES + wave) * 8 + lr : BM + ((i - XPW) * WAVES + wave) * 8 + lr;
-        chunk[i] = lc ^ ((r >> 1) & 7);
         if (i < XPW) {
             off[i] = (uint32_t)min(r, a.M - 1 - m0) * (uint32_t)a.ldx;
         } else {
             const int m = (i - XPW) / ((LPW - XPW) / NM);
             off[i] = (uint32_t)min(r - BM - m * BN, a.N - 1 - n0) * (uint32_t)a.ldw[m];
         }
-        off[i] += 16 * chunk[i];
+        off[i] += 16 * chunk;
     }
     const int sxrow = min(m0 + (wave % SXW) * 64 + lane, a.M - 1);
     const float* sxp = a.sx + (int64_t)sxrow * a.sxm;
@@ -96,14 +130,13 @@ fp8_tile_kernel(Fp8Args a, int nbm, int nbn, int splits)
 
     auto issue = [&](int kb, int buf) __attribute__((always_inline)) {
         uint8_t* st = smem + buf * STAGE;
-        const bool tail = ktail && kb == KB - 1;
+        // past the row's end the row's own first chunk is read instead; it is overwritten with zeros below
+        const uint32_t back = ktail && kb == KB - 1 && kb * kGroup + 16 * chunk >= a.K ? 16 * chunk : 0;
 #pragma unroll
         for (int i = 0; i < LPW; ++i) {
             const int b = i < XPW ? 0 : 1 + (i - XPW) / ((LPW - XPW) / NM);
             const int r8 = i < XPW ? i * WAVES + wave : BM / 8 + (i - XPW) * WAVES + wave;
-            // past the row's end the row's own first chunk is read instead; it is overwritten with zeros below
-            const bool out = tail && kb * kGroup + 16 * chunk[i] >= a.K;
-            lds_load16(base[b] + (int64_t)kb * kGroup, out ? off[i] - 16 * chunk[i] : off[i], st + r8 * 1024);
+            lds_load16(base[b] + (int64_t)kb * kGroup, off[i] - back, st + r8 * 1024);
         }
         __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(sxp + kb * a.sxg),
                                          (__attribute__((address_space(3))) void*)(st + (BM + BR) * kGroup +
@@ -127,6 +160,7 @@ fp8_tile_kernel(Fp8Args a, int nbm, int nbn, int splits)
     const int swz = (i16 >> 1) & 7;
     const int rd0 = i16 * kGroup + ((q ^ swz) << 4), rd1 = i16 * kGroup + (((q + 4) ^ swz) << 4);
 
+    using Operand = typename Form<WIDE>::type;
     auto compute = [&](int kb, int buf) __attribute__((always_inline)) {
         const uint8_t* st = smem + buf * STAGE;
         const uint8_t* xs = st + wm * (TM * 16) * kGroup;
@@ -144,18 +178,44 @@ fp8_tile_kernel(Fp8Args a, int nbm, int nbn, int splits)
 #pragma unroll
             for (int j = 0; j < TM; ++j) sc[m][j] = sx[16 * j + i16] * sw;
         }
+        Operand bw[TM];
 #pragma unroll
-        for (int i = 0; i < TN; ++i) {
+        for (int j = 0; j < TM; ++j) bw[j] = operand<WIDE>(b[j][0], b[j][1]);
+        raw4_t a0, a1;
+        auto fetch = [&](int i) __attribute__((always_inline)) {
             const int m = i / TNM;
             const uint8_t* ws = st + (BM + m * BN + wr0 + (i - m * TNM) * 16) * kGroup;
-            const raw4_t a0 = *reinterpret_cast<const raw4_t*>(ws + rd0);
-            const raw4_t a1 = *reinterpret_cast<const raw4_t*>(ws + rd1);
+            a0 = *reinterpret_cast<const raw4_t*>(ws + rd0);
+            a1 = *reinterpret_cast<const raw4_t*>(ws + rd1);
+        };
+        auto add = [&](int i, const f32x4 (&p)[TM]) __attribute__((always_inline)) {
 #pragma unroll
             for (int j = 0; j < TM; ++j) {
-                const f32x4 p = mfma_e4m3(a0, a1, b[j][0], b[j][1]);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(p[e], sc[m][j], acc[i][j][e]);
+                for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(p[j][e], sc[i / TNM][j], acc[i][j][e]);
             }
+        };
+        fetch(0);
+        if constexpr (WIDE) {
+#pragma unroll
+            for (int i = 0; i < TN; ++i) {
+                const Operand aw = operand<WIDE>(a0, a1);
+                if (i + 1 < TN) fetch(i + 1);
+                f32x4 p[TM];
+                multiply<TM>(aw, bw, p);
+                add(i, p);
+            }
+        } else {
+            // tile i's products run while tile i - 1's are scaled and added
+            f32x4 p[2][TM];
+#pragma unroll
+            for (int i = 0; i < TN; ++i) {
+                const Operand aw = operand<WIDE>(a0, a1);
+                if (i + 1 < TN) fetch(i + 1);
+                multiply<TM>(aw, bw, p[i & 1]);
+                if (i > 0) add(i - 1, p[(i - 1) & 1]);
+            }
+            add(TN - 1, p[(TN - 1) & 1]);
         }
     };
 
@@ -170,10 +230,10 @@ fp8_tile_kernel(Fp8Args a, int nbm, int nbn, int splits)
         if (s + STAGES - 1 <= stages) wait_vm<(STAGES - 2) * (LPW + 1)>();
         else wait_vm<0>();
         if (ktail && kb0 + s == KB - 1) {
+            if ((KB - 1) * kGroup + 16 * chunk >= a.K) {
 #pragma unroll
-            for (int i = 0; i < LPW; ++i) {
-                const int r8 = i < XPW ? i * WAVES + wave : BM / 8 + (i - XPW) * WAVES + wave;
-                if ((KB - 1) * kGroup + 16 * chunk[i] >= a.K) {
+                for (int i = 0; i < LPW; ++i) {
+                    const int r8 = i < XPW ? i * WAVES + wave : BM / 8 + (i - XPW) * WAVES + wave;
                     *reinterpret_cast<raw4_t*>(smem + buf * STAGE + r8 * 1024 + lane * 16) = raw4_t{0u, 0u, 0u, 0u};
                 }
             }
@@ -288,20 +348,23 @@ namespace {
 
 using TileFn = void (*)(Fp8Args, int, int, int);
 
-template <int NM>
-TileFn pick_tile(int shape, bool e4m3)
+template <int NM, bool WIDE, bool E4M3>
+TileFn pick_tile(int shape)
 {
     switch (shape) {
-    case 0: return e4m3 ? fp8_tile_kernel<NM, 4, 8, 4, 2, 2, true> : fp8_tile_kernel<NM, 4, 8, 4, 2, 2, false>;
-    case 1:
-        if (e4m3) return NM == 1 ? fp8_tile_kernel<1, 4, 4, 2, 2, 2, true> : nullptr;
-        return fp8_tile_kernel<NM, 4, 4, 2, 2, 2, false>;
-    case 2: return e4m3 ? fp8_tile_kernel<NM, 4, 4, 1, 4, 3, true> : fp8_tile_kernel<NM, 4, 4, 1, 4, 3, false>;
-    case 3:
-        if (e4m3) return NM == 1 ? fp8_tile_kernel<1, 2, 2, 1, 4, 4, true> : nullptr;
-        return fp8_tile_kernel<NM, 2, 2, 1, 4, 4, false>;
+    case 0: return fp8_tile_kernel<NM, 4, 8, 4, 2, 2, WIDE, E4M3>;
+    case 1: return E4M3 && NM == 2 ? nullptr : fp8_tile_kernel<NM, 4, 4, 2, 2, 2, WIDE, E4M3 && NM == 1>;
+    case 2: return fp8_tile_kernel<NM, 4, 4, 1, 4, 3, WIDE, E4M3>;
+    case 3: return E4M3 && NM == 2 ? nullptr : fp8_tile_kernel<NM, 2, 2, 1, 4, 4, WIDE, E4M3 && NM == 1>;
     }
     return nullptr;
+}
+
+template <int NM>
+TileFn pick_tile(int shape, bool wide, bool e4m3)
+{
+    if (e4m3) return pick_tile<NM, true, true>(shape);
+    return wide ? pick_tile<NM, true, false>(shape) : pick_tile<NM, false, false>(shape);
 }
 
 size_t tile_lds(int shape)
@@ -318,7 +381,7 @@ hipError_t fp8_tile_launch(int mats, const TileConfig& c, const Fp8Args& a, hipS
 {
     const TileShape& t = kTileShapes[c.shape];
     const bool e4m3 = a.out_dtype == GLU_DTYPE_E4M3;
-    const TileFn f = mats == 1 ? pick_tile<1>(c.shape, e4m3) : pick_tile<2>(c.shape, e4m3);
+    const TileFn f = mats == 1 ? pick_tile<1>(c.shape, c.wide, e4m3) : pick_tile<2>(c.shape, c.wide, e4m3);
     if (!f) return hipErrorInvalidValue;
     const size_t lds = tile_lds(c.shape);
     hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(f), hipFuncAttributeMaxDynamicSharedMemorySize,

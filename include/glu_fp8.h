@@ -17,9 +17,9 @@
  *
  * Products: out[m, n] = sum_b sx[m, b] sw[n / 128, b] sum_{k in block b} x[m, k] w[n, k],
  * glu_fp8_dual_glu gives silu(gate) * up of two such sums, evaluated in fp32
- * and rounded once to the output's type.  The sums are fp32 for up to 16 rows of x and for fp32 output; for
- * more rows and a 16- or 8-bit output they run on the matrix unit's 8-bit path, which within 8 neighbouring products
- * drops what lies 13 to 14 bits below the largest and adds the eighths in fp32.
+ * and rounded once to the output's type.  The sums are fp32, except that with more than 16 rows of x and a 16-bit
+ * output they run on the matrix unit's 8-bit path, which within 8 neighbouring products drops what lies 13
+ * to 14 bits below the largest and adds the eighths in fp32.
  *
  * Ownership, execution, determinism and errors are those of glu_gemv.h: all
  * arrays are device memory of the caller, calls are asynchronous on `stream`,

@@ -165,7 +165,7 @@ def test_product(M, N, K, mats):
     ops = operands(M, N, K, M + N + K, mats)
     for kind in ("bf16", "fp16", "fp32", "e4m3"):
         plan = fp8.product_plan(mats, M, N, K, T[kind])
-        want, err = expected(ops, plan["kernel_name"] == "tile")
+        want, err = expected(ops, plan["kernel_name"] == "tile" and kind in ("bf16", "fp16"))
         print(f"[product] mats={mats} M={M} N={N} K={K} {kind} {plan}", flush=True)
         got = run(ops, T[kind])
         torch.cuda.synchronize()
@@ -205,13 +205,13 @@ def plans():
 @pytest.mark.parametrize("kernel,tile,width,splits,M,N,K", plans())
 def test_every_launch_shape(kernel, tile, width, splits, M, N, K, mats):
     ops = operands(M, N, K, M + N + K, mats)
-    want, err = expected(ops, kernel == 3)
+    strict, loose = expected(ops), expected(ops, kernel == 3)
     plan = fp8.ProductPlan(kernel, tile, width, splits)
-    for kind in ("bf16", "e4m3"):
+    for kind in ("bf16", "fp32", "e4m3"):
         print(f"[plan] mats={mats} {kernel} {tile} {width} {splits} M={M} N={N} K={K} {kind}", flush=True)
         got = run(ops, T[kind], plan=plan)
         torch.cuda.synchronize()
-        check(kind, got, want, err)
+        check(kind, got, *(loose if kind == "bf16" else strict))
         again = run(ops, T[kind], plan=plan)
         for a, b in zip(got if isinstance(got, tuple) else (got,), again if isinstance(again, tuple) else (again,)):
             assert same_bits(a, b), "a second call gives the same bits"
@@ -250,7 +250,7 @@ def test_product_strides(M, mats, shift):
     ss = torch.full((ref.groups(N), M + 1), 2.0, device=DEV)
     got = run(wide, E4M3, out=qs.view(E4M3)[:, 1:1 + N], scale_out=ss[:, :M].t())
     torch.cuda.synchronize()
-    check("e4m3", got, *(loose if shift == 16 and M > 16 else strict))
+    check("e4m3", got, *strict)
     assert (qs[:, :1] == 0x22).all() and (qs[:, 1 + N:] == 0x22).all() and (ss[:, M:] == 2).all()
 
 
@@ -364,7 +364,7 @@ def test_mlp_block(M):
     # each stage against the 64-bit stage on the stored 8-bit operands before it
     q, s, _ = glu.add_rms_norm_fp8(x, nw, 1e-6, residual=r)
     a, sa = glu.fp8_dual_glu(q, s, *mlp.gate, *mlp.up, out_dtype=E4M3)
-    want, err = expected([q, s, *mlp.gate, *mlp.up], M > 16)
+    want, err = expected([q, s, *mlp.gate, *mlp.up])
     ref.check_e4m3("glu", a, sa, want, err)
     want, err = expected([a, sa, *mlp.down], M > 16)
     ref.check_store("down", y, want, err)
@@ -392,7 +392,6 @@ def test_python_refusals():
         (ValueError, lambda: glu.fp8_linear(x, sx, w, sw, out=torch.empty(4, 255, dtype=torch.bfloat16, device=DEV))),
         (GluError, lambda: glu.fp8_linear(x, sx, w, sw, out_dtype=E4M3, out=x)),
         (GluError, lambda: glu.fp8_linear(x, sx, w, sw, plan=fp8.ProductPlan(3, 9, 0, 1))),
-        (GluError, lambda: glu.fp8_linear(x, sx, w, sw, out_dtype=torch.float32, plan=fp8.ProductPlan(3, 1, 0, 1))),
         (GluError, lambda: glu.fp8_linear(x, sx, w, sw, plan=fp8.ProductPlan(2, 16, 17, 1))),
         (GluError, lambda: glu.fp8_linear(x, sx, w, sw, plan=fp8.ProductPlan(3, 1, 0, 3))),
         (TypeError, lambda: glu.fp8_quantize(x)),
