@@ -37,7 +37,7 @@ struct TileShape {
     int threads;
     int stages;
 };
-constexpr int kTileShapeCount = 4;
+constexpr int kTileShapeCount = 6;
 extern const TileShape kTileShapes[kTileShapeCount];
 struct TileConfig {
     int shape, splits;

@@ -11,6 +11,8 @@
 // In LDS, 16-byte chunk c of row r lies at c ^ ((r >> 1) & 7): every group of 16 lanes that a ds_read_b128 serves together
 // then touches 16 different slots of the 256-byte bank line.  A wave's direct load writes 64 consecutive
 // slots (8 rows), so the exchange is made in the source addresses.
+#include <type_traits>
+
 #include "glu_fp8_mfma.h"
 
 namespace glu {
@@ -20,6 +22,8 @@ const TileShape kTileShapes[kTileShapeCount] = {
     {128, 128, 256, 2},
     {64, 256, 256, 3},
     {32, 128, 256, 4},
+    {256, 128, 512, 3},
+    {128, 256, 512, 3},
 };
 
 namespace {
@@ -43,25 +47,12 @@ __device__ __forceinline__ typename Form<WIDE>::type operand(raw4_t c0, raw4_t c
     else return Narrow{c0, c1};
 }
 
-// p[j] = the K-block's product of a with b[j]
-template <int TM>
-__device__ __forceinline__ void multiply(const Narrow& a, const Narrow (&b)[TM], f32x4 (&p)[TM])
+// a K-block's product
+__device__ __forceinline__ f32x4 multiply(const Narrow& a, const Narrow& b)
 {
-#pragma unroll
-    for (int j = 0; j < TM; ++j) p[j] = mfma_e4m3(a.c0, a.c1, b[j].c0, b[j].c1);
+    return mfma_e4m3(a.c0, a.c1, b.c0, b.c1);
 }
-template <int TM>
-__device__ __forceinline__ void multiply(const Wide& a, const Wide (&b)[TM], f32x4 (&p)[TM])
-{
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-#pragma unroll
-        for (int j = 0; j < TM; ++j) {
-            const f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
-            p[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v[k], b[j].v[k], k == 0 ? z : p[j], 0, 0, 0);
-        }
-    }
-}
+__device__ __forceinline__ f32x4 multiply(const Wide& a, const Wide& b) { return mfma_wide(a, b); }
 
 template <int N>
 __device__ __forceinline__ void wait_vm()
@@ -85,7 +76,7 @@ fp8_tile_kernel(Fp8Args a, int nbm, int nbn, int splits)
     constexpr int XPW = BM / 8 / WAVES;               // ... of which rows of x
     constexpr int SXW = (BM + 63) / 64;               // waves that load scales of x
     constexpr int STAGE = (BM + BR) * kGroup + 4 * SXW * 64;
-    static_assert(BM % (8 * WAVES) == 0 && BR % (8 * NM * WAVES) == 0 && TN % NM == 0, "whole loads per wave");
+    static_assert(BM % (8 * WAVES) == 0 && BR % (8 * NM * WAVES) == 0 && TN % 2 == 0 && TN % NM == 0, "whole loads per wave");
     static_assert(WAVES % 2 == 0, "a wave's loads lie a multiple of 16 rows apart");
 
     extern __shared__ __attribute__((aligned(256))) uint8_t smem[];
@@ -94,9 +85,14 @@ fp8_tile_kernel(Fp8Args a, int nbm, int nbn, int splits)
     const int wm = wave % WM, wn = wave / WM;
     const int i16 = lane & 15, q = lane >> 4;
 
-    // an XCD takes a run of tiles, rows of x varying fastest: they share their weights in its L2
-    const int tile = xcd_run(blockIdx.x, nbm * nbn);
-    const int nb = tile / nbm, mb = tile - nb * nbm;
+    // An XCD takes a run of tiles, in blocks 8 tiles of x high: the 32 that it works on at a time then read 8 row blocks of
+    // x and 4 of the weights between them, the least that its L2 has to fetch.
+    constexpr int HIGH = 8;
+    const int t = xcd_run(blockIdx.x, nbm * nbn);
+    const int band = t / (HIGH * nbn);
+    const int high = min(HIGH, nbm - band * HIGH);
+    const int r = t - band * HIGH * nbn;
+    const int nb = r / high, mb = band * HIGH + r - nb * high;
     const int m0 = mb * BM, n0 = nb * BN;
     const int KB = (a.K + kGroup - 1) / kGroup;
     const int split = blockIdx.y;
@@ -126,23 +122,32 @@ fp8_tile_kernel(Fp8Args a, int nbm, int nbn, int splits)
     }
     const int sxrow = min(m0 + (wave % SXW) * 64 + lane, a.M - 1);
     const float* sxp = a.sx + (int64_t)sxrow * a.sxm;
-    const bool ktail = (a.K & (kGroup - 1)) != 0;
 
-    auto issue = [&](int kb, int buf) __attribute__((always_inline)) {
+    // Loads the stage of K-block kb into a buffer; past the last stage the last one again, so that every stage
+    // issues, and waits for, the same number of loads.  Past the row's end its own first chunk is read instead.
+    const uint32_t past_end = (KB - 1) * kGroup + 16 * chunk >= a.K ? 16 * chunk : 0;
+    auto issue = [&](int kb, int buf, int first, int count) __attribute__((always_inline)) {
+        kb = min(kb, kb1 - 1);
         uint8_t* st = smem + buf * STAGE;
-        // past the row's end the row's own first chunk is read instead; it is overwritten with zeros below
-        const uint32_t back = ktail && kb == KB - 1 && kb * kGroup + 16 * chunk >= a.K ? 16 * chunk : 0;
+        const uint32_t back = kb == KB - 1 ? past_end : 0;
 #pragma unroll
-        for (int i = 0; i < LPW; ++i) {
-            const int b = i < XPW ? 0 : 1 + (i - XPW) / ((LPW - XPW) / NM);
-            const int r8 = i < XPW ? i * WAVES + wave : BM / 8 + (i - XPW) * WAVES + wave;
-            lds_load16(base[b] + (int64_t)kb * kGroup, off[i] - back, st + r8 * 1024);
+        for (int i = first; i < first + count; ++i) {
+            if (i < LPW) {
+                const int b = i < XPW ? 0 : 1 + (i - XPW) / ((LPW - XPW) / NM);
+                const int r8 = i < XPW ? i * WAVES + wave : BM / 8 + (i - XPW) * WAVES + wave;
+                lds_load16(base[b] + (int64_t)kb * kGroup, off[i] - back, st + r8 * 1024);
+            } else if (i == LPW) {
+                __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(sxp + kb * a.sxg),
+                                                 (__attribute__((address_space(3))) void*)(st + (BM + BR) * kGroup +
+                                                                                           (wave % SXW) * 256),
+                                                 4, 0, 0);
+            }
         }
-        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(sxp + kb * a.sxg),
-                                         (__attribute__((address_space(3))) void*)(st + (BM + BR) * kGroup +
-                                                                                   (wave % SXW) * 256),
-                                         4, 0, 0);
     };
+    // A stage's loads are issued a few per step (below): all at once they would fill the address units' queue and hold up
+    // the waves' products behind them.
+    constexpr int PER_STEP = (LPW + 1 + TM * TN - 1) / (TM * TN);
+    constexpr int EARLY = TM * PER_STEP < LPW + 1 ? TM * PER_STEP : LPW + 1;  // those in the last row of the stage before
 
     f32x4 acc[TN][TM];
 #pragma unroll
@@ -161,91 +166,122 @@ fp8_tile_kernel(Fp8Args a, int nbm, int nbn, int splits)
     const int rd0 = i16 * kGroup + ((q ^ swz) << 4), rd1 = i16 * kGroup + (((q + 4) ^ swz) << 4);
 
     using Operand = typename Form<WIDE>::type;
-    auto compute = [&](int kb, int buf) __attribute__((always_inline)) {
-        const uint8_t* st = smem + buf * STAGE;
-        const uint8_t* xs = st + wm * (TM * 16) * kGroup;
-        raw4_t b[TM][2];
-        float sc[NM][TM];
-#pragma unroll
-        for (int j = 0; j < TM; ++j) {
-            b[j][0] = *reinterpret_cast<const raw4_t*>(xs + j * 16 * kGroup + rd0);
-            b[j][1] = *reinterpret_cast<const raw4_t*>(xs + j * 16 * kGroup + rd1);
-        }
-        const float* sx = reinterpret_cast<const float*>(st + (BM + BR) * kGroup) + wm * (TM * 16);
-#pragma unroll
-        for (int m = 0; m < NM; ++m) {
-            const float sw = scalar_load(swp[m] + kb);
-#pragma unroll
-            for (int j = 0; j < TM; ++j) sc[m][j] = sx[16 * j + i16] * sw;
-        }
-        Operand bw[TM];
-#pragma unroll
-        for (int j = 0; j < TM; ++j) bw[j] = operand<WIDE>(b[j][0], b[j][1]);
-        raw4_t a0, a1;
-        auto fetch = [&](int i) __attribute__((always_inline)) {
-            const int m = i / TNM;
-            const uint8_t* ws = st + (BM + m * BN + wr0 + (i - m * TNM) * 16) * kGroup;
-            a0 = *reinterpret_cast<const raw4_t*>(ws + rd0);
-            a1 = *reinterpret_cast<const raw4_t*>(ws + rd1);
-        };
-        auto add = [&](int i, const f32x4 (&p)[TM]) __attribute__((always_inline)) {
-#pragma unroll
-            for (int j = 0; j < TM; ++j) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(p[j][e], sc[i / TNM][j], acc[i][j][e]);
-            }
-        };
-        fetch(0);
-        if constexpr (WIDE) {
-#pragma unroll
-            for (int i = 0; i < TN; ++i) {
-                const Operand aw = operand<WIDE>(a0, a1);
-                if (i + 1 < TN) fetch(i + 1);
-                f32x4 p[TM];
-                multiply<TM>(aw, bw, p);
-                add(i, p);
-            }
-        } else {
-            // tile i's products run while tile i - 1's are scaled and added
-            f32x4 p[2][TM];
-#pragma unroll
-            for (int i = 0; i < TN; ++i) {
-                const Operand aw = operand<WIDE>(a0, a1);
-                if (i + 1 < TN) fetch(i + 1);
-                multiply<TM>(aw, bw, p[i & 1]);
-                if (i > 0) add(i - 1, p[(i - 1) & 1]);
-            }
-            add(TN - 1, p[(TN - 1) & 1]);
-        }
+    const int xrd = wm * (TM * 16) * kGroup;
+    auto read_x = [&](int buf, int j, raw4_t (&b)[2]) __attribute__((always_inline)) {
+        const uint8_t* xs = smem + buf * STAGE + xrd + j * 16 * kGroup;
+        b[0] = *reinterpret_cast<const raw4_t*>(xs + rd0);
+        b[1] = *reinterpret_cast<const raw4_t*>(xs + rd1);
     };
-
-#pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s) {
-        if (s < stages) issue(kb0 + s, s);
-    }
-    int buf = 0;
-    for (int s = 0; s < stages; ++s) {
-        // this wave's loads of stage s have landed; past the barrier everyone's have, and everyone is
-        // done with the buffer that the next issue overwrites
-        if (s + STAGES - 1 <= stages) wait_vm<(STAGES - 2) * (LPW + 1)>();
-        else wait_vm<0>();
-        if (ktail && kb0 + s == KB - 1) {
-            if ((KB - 1) * kGroup + 16 * chunk >= a.K) {
-#pragma unroll
-                for (int i = 0; i < LPW; ++i) {
-                    const int r8 = i < XPW ? i * WAVES + wave : BM / 8 + (i - XPW) * WAVES + wave;
-                    *reinterpret_cast<raw4_t*>(smem + buf * STAGE + r8 * 1024 + lane * 16) = raw4_t{0u, 0u, 0u, 0u};
-                }
-            }
-            __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): the zeros are in LDS
-        }
+    auto read_w = [&](int buf, int i, raw4_t (&w)[2]) __attribute__((always_inline)) {
+        const int m = i / TNM;
+        const uint8_t* ws = smem + buf * STAGE + (BM + m * BN + wr0 + (i - m * TNM) * 16) * kGroup;
+        w[0] = *reinterpret_cast<const raw4_t*>(ws + rd0);
+        w[1] = *reinterpret_cast<const raw4_t*>(ws + rd1);
+    };
+    auto meet = [&]() __attribute__((always_inline)) {
+        __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): this wave's reads are in registers
         __builtin_amdgcn_sched_barrier(0);
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
-        if (s + STAGES - 1 < stages) issue(kb0 + s + STAGES - 1, buf == 0 ? STAGES - 1 : buf - 1);
-        compute(kb0 + s, buf);
+    };
+
+#pragma unroll
+    for (int s = 0; s < STAGES; ++s) issue(kb0 + s, s, 0, s < STAGES - 1 ? LPW + 1 : EARLY);
+    wait_vm<(STAGES - 2) * (LPW + 1) + EARLY>();  // all but stage 0's
+    meet();
+    raw4_t b[TM][2], w[2][2];
+    float sx[TM];
+    auto read_first = [&](int buf) __attribute__((always_inline)) {
+        read_w(buf, 0, w[0]);
+        const float* src = reinterpret_cast<const float*>(smem + buf * STAGE + (BM + BR) * kGroup) + wm * (TM * 16);
+#pragma unroll
+        for (int j = 0; j < TM; ++j) sx[j] = src[16 * j + i16];
+    };
+    // past K in the last K-block: zeros for x, so that what was read there instead, of the same rows, adds nothing
+    auto clear = [&](int s, raw4_t (&b)[2]) __attribute__((always_inline)) {
+        const bool in0 = (kb0 + s) * kGroup + 16 * q < a.K, in1 = (kb0 + s) * kGroup + 64 + 16 * q < a.K;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            b[0][e] = in0 ? b[0][e] : 0u;
+            b[1][e] = in1 ? b[1][e] : 0u;
+        }
+    };
+    if constexpr (!WIDE) {
+#pragma unroll
+        for (int j = 0; j < TM; ++j) read_x(0, j, b[j]);
+        read_first(0);
+    }
+
+    // One stage.  Its first operands are in registers already, but for the wide form, which has none left for that and
+    // reads them here.  No branch in it: the compiler would carry the sums past one, in
+    // ever more registers.
+    auto stage = [&](int s, int buf, auto last) __attribute__((always_inline)) {
+        constexpr bool LAST = decltype(last)::value;
+        const int next = buf + 1 == STAGES ? 0 : buf + 1, before = buf == 0 ? STAGES - 1 : buf - 1;
+        if constexpr (WIDE) {
+            read_x(buf, 0, b[0]);
+            read_first(buf);
+        }
+        float sc[NM][TM];
+#pragma unroll
+        for (int m = 0; m < NM; ++m) {
+            const float sw = scalar_load(swp[m] + kb0 + s);
+#pragma unroll
+            for (int j = 0; j < TM; ++j) sc[m][j] = sx[j] * sw;
+        }
+        // One step is one 16 x 16 product, in a fixed order: the sums of the product LAG steps before it, which is done by
+        // now, free the registers that this one takes, and the operands of a step to come are fetched behind it.
+        constexpr int LAG = WIDE ? 1 : TM;
+        Operand aw, bw[TM];
+        f32x4 p[LAG + (WIDE ? 1 : 0)];
+        constexpr int P = sizeof(p) / sizeof(p[0]);
+        auto add = [&](int step) __attribute__((always_inline)) {
+            const int i = step / TM, j = step % TM;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(p[step % P][e], sc[i / TNM][j], acc[i][j][e]);
+        };
+#pragma unroll
+        for (int i = 0; i < TN; ++i) {
+#pragma unroll
+            for (int j = 0; j < TM; ++j) {
+                const int step = i * TM + j;
+                if (!WIDE && step >= LAG) add(step - LAG);
+                if (i == 0) {
+                    if (WIDE && j + 1 < TM) read_x(buf, j + 1, b[j + 1]);
+                    if (LAST) clear(s, b[j]);
+                    bw[j] = operand<WIDE>(b[j][0], b[j][1]);
+                }
+                if (j == 0) aw = operand<WIDE>(w[i & 1][0], w[i & 1][1]);
+                p[step % P] = multiply(aw, bw[j]);
+                if (WIDE && step >= LAG) add(step - LAG);
+                if (j == 0 && i + 1 < TN) read_w(buf, i + 1, w[(i + 1) & 1]);
+                if (!LAST && i == TN - 2 && j == TM - 1) {
+                    // The stage's last operands are in registers, the next stage is in LDS: with a row of products in
+                    // hand the waves meet, begin to refill this buffer and fetch the next stage's first operands.
+                    wait_vm<(STAGES - 2) * (LPW + 1)>();  // all but those after stage s + 1
+                    meet();
+                }
+                if (!LAST && i == TN - 1) issue(kb0 + s + STAGES, buf, j * PER_STEP, PER_STEP);
+                if (!LAST && EARLY + step * PER_STEP < LPW + 1) {
+                    issue(kb0 + s + STAGES - 1, before, EARLY + step * PER_STEP, PER_STEP);
+                }
+                if (!WIDE && !LAST && i == TN - 1) {
+                    read_x(next, j, b[j]);
+                    if (j == 0) read_first(next);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+#pragma unroll
+        for (int step = TN * TM - LAG; step < TN * TM; ++step) add(step);
+    };
+    int buf = 0;
+    for (int s = 0; s + 1 < stages; ++s) {
+        stage(s, buf, std::false_type{});
         buf = buf + 1 == STAGES ? 0 : buf + 1;
     }
+    stage(stages - 1, buf, std::true_type{});
+    wait_vm<0>();  // the repeated loads have landed before LDS is given up or used again
 
     // lane l holds weight rows 4 (l / 16) + e of each tile, for row l % 16 of x
     const int mrow = m0 + wm * (TM * 16) + i16;
@@ -355,6 +391,8 @@ TileFn pick_tile(int shape)
     case 0: return fp8_tile_kernel<NM, 4, 8, 4, 2, 2, WIDE, E4M3>;
     case 1: return E4M3 && NM == 2 ? nullptr : fp8_tile_kernel<NM, 4, 4, 2, 2, 2, WIDE, E4M3 && NM == 1>;
     case 2: return fp8_tile_kernel<NM, 4, 4, 1, 4, 3, WIDE, E4M3>;
+    case 4: return E4M3 && NM == 2 ? nullptr : fp8_tile_kernel<NM, 4, 4, 4, 2, 3, WIDE, E4M3 && NM == 1>;
+    case 5: return fp8_tile_kernel<NM, 4, 4, 2, 4, 3, WIDE, E4M3>;
     case 3: return E4M3 && NM == 2 ? nullptr : fp8_tile_kernel<NM, 2, 2, 1, 4, 4, WIDE, E4M3 && NM == 1>;
     }
     return nullptr;
