@@ -189,10 +189,12 @@ fp8_tile_kernel(Fp8Args a, int nbm, int nbn, int splits)
     for (int s = 0; s < STAGES; ++s) issue(kb0 + s, s, 0, s < STAGES - 1 ? LPW + 1 : EARLY);
     wait_vm<(STAGES - 2) * (LPW + 1) + EARLY>();  // all but stage 0's
     meet();
-    raw4_t b[TM][2], w[2][2];
+    constexpr int AHEAD = !WIDE && TN >= 4 ? 2 : 1, SLOTS = 2 * AHEAD;
+    raw4_t b[TM][2], w[SLOTS][2];
     float sx[TM];
     auto read_first = [&](int buf) __attribute__((always_inline)) {
-        read_w(buf, 0, w[0]);
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) read_w(buf, i, w[i]);
         const float* src = reinterpret_cast<const float*>(smem + buf * STAGE + (BM + BR) * kGroup) + wm * (TM * 16);
 #pragma unroll
         for (int j = 0; j < TM; ++j) sx[j] = src[16 * j + i16];
@@ -251,10 +253,10 @@ fp8_tile_kernel(Fp8Args a, int nbm, int nbn, int splits)
                     if (LAST) clear(s, b[j]);
                     bw[j] = operand<WIDE>(b[j][0], b[j][1]);
                 }
-                if (j == 0) aw = operand<WIDE>(w[i & 1][0], w[i & 1][1]);
+                if (j == 0) aw = operand<WIDE>(w[i % SLOTS][0], w[i % SLOTS][1]);
                 p[step % P] = multiply(aw, bw[j]);
                 if (WIDE && step >= LAG) add(step - LAG);
-                if (j == 0 && i + 1 < TN) read_w(buf, i + 1, w[(i + 1) & 1]);
+                if (j == 0 && i + AHEAD < TN) read_w(buf, i + AHEAD, w[(i + AHEAD) % SLOTS]);
                 if (!LAST && i == TN - 2 && j == TM - 1) {
                     // The stage's last operands are in registers, the next stage is in LDS: with a row of products in
                     // hand the waves meet, begin to refill this buffer and fetch the next stage's first operands.
