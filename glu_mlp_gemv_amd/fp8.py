@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 from typing import Optional
 
 import torch
@@ -48,50 +49,79 @@ def groups(n: int) -> int:
     return -(-n // GROUP)
 
 
-def _tensor(name: str, t, dtypes, ndim: int, dev=None):
+_INPUTS = (torch.bfloat16, torch.float16, torch.float32)
+_raw_stream = torch._C._cuda_getCurrentRawStream  # current_stream().cuda_stream without building a Stream object
+
+
+def _refuse(name: str, t, dtypes, shape, dev):
+    """Says what is wrong with a tensor that is not of these types, this shape (None: any extent) and device."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a GPU, got {t.device}")
-    if t.dim() != ndim:
-        raise ValueError(f"{name} must have {ndim} dims, got {t.dim()}")
+    if t.dim() != len(shape):
+        raise ValueError(f"{name} must have {len(shape)} dims, got {t.dim()}")
+    if any(want is not None and n != want for n, want in zip(t.shape, shape)):
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
     if dev is not None and t.device != dev:
         raise ValueError(f"{name} must be on {dev}, got {t.device}")
 
 
-_INPUTS = (torch.bfloat16, torch.float16, torch.float32)
-_F32 = (torch.float32,)
-_E4M3 = (E4M3,)
+def _matrix(name: str, t, dtypes):
+    """(rows, columns, device) of the tensor that sets a call's sizes."""
+    if not (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.is_cuda and t.dim() == 2):
+        _refuse(name, t, dtypes, (None, None), None)
+    rows, cols = t.shape
+    return rows, cols, t.device
 
 
-def _like(name: str, t, shape, dtype, dev):
-    """An output of this shape: the one given, checked, or a new one."""
+# The checks below are on the path of every call, some microseconds long in all: what is as expected passes one
+# expression, and only what is not is looked at again.
+
+def _rows(name: str, t, dtype, rows: int, cols: int, dev) -> int:
+    """The row stride of a [rows, cols] operand."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == (rows, cols) and t.device == dev):
+        _refuse(name, t, (dtype,), (rows, cols), dev)
+    ld, one = t.stride()
+    return ld if one == 1 and ld >= cols and rows > 1 else _row_stride(name, t)
+
+
+def _vector(name: str, t, dtype, n: int, dev):
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == (n,) and t.device == dev):
+        _refuse(name, t, (dtype,), (n,), dev)
+    if n > 1 and t.stride(0) != 1:
+        raise ValueError(f"{name}: elements must be contiguous, got stride {t.stride(0)}")
+
+
+def _new(rows: int, cols: int, dtype, dev):
+    return torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=dev)
+
+
+def _output(name: str, t, dtype, rows: int, cols: int, dev):
+    """(tensor, row stride) of an output: the one given, checked, or a new one."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    _tensor(name, t, (dtype,), len(shape), dev)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
-    return t
+        return _new(rows, cols, dtype, dev), cols
+    return t, _rows(name, t, dtype, rows, cols, dev)
 
 
 def _row_scales(name: str, t, rows: int, cols: int, dev):
-    """A new [rows, groups] scale tensor stored group by group, or the given one, whose columns must be contiguous."""
+    """(tensor, group stride): a new [rows, groups] scale tensor stored group by group, or the given one, whose
+    columns must be contiguous."""
     if t is None:
-        return torch.empty((groups(cols), rows), dtype=torch.float32, device=dev).t()
-    _tensor(name, t, _F32, 2, dev)
-    if tuple(t.shape) != (rows, groups(cols)):
-        raise ValueError(f"{name} must be {(rows, groups(cols))}, got {tuple(t.shape)}")
+        return torch.empty_strided((rows, groups(cols)), (1, rows), dtype=torch.float32, device=dev), rows
+    _refuse(name, t, (torch.float32,), (rows, groups(cols)), dev)
     _row_stride(name, t.t())
-    return t
+    return t, t.stride(1)
 
 
 def _on(dev, stream, *tensors):
     """(context, stream handle) of a call on ``stream`` or the device's current stream."""
     if stream is None:
-        ctx = _NO_CONTEXT if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
-        return ctx, torch.cuda.current_stream(dev).cuda_stream
+        index = dev.index
+        ctx = _NO_CONTEXT if index == torch.cuda.current_device() else torch.cuda.device(dev)
+        return ctx, _raw_stream(index)
     if stream.device != dev:
         raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
     for t in tensors:
@@ -104,22 +134,33 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _norm_args(x, weight, residual, residual_out):
-    _tensor("x", x, _INPUTS, 2)
-    dev, dt = x.device, x.dtype
-    M, K = x.shape
-    _tensor("weight", weight, (dt,), 1, dev)
-    if weight.shape[0] != K:
-        raise ValueError(f"weight must be ({K},), got {tuple(weight.shape)}")
-    if K > 1 and weight.stride(0) != 1:
-        raise ValueError(f"weight: elements must be contiguous, got stride {weight.stride(0)}")
+def _norm(x, weight, eps, residual, out, scale_out, residual_out, return_rstd, stream, e4m3):
+    M, K, dev = _matrix("x", x, _INPUTS)
+    dt = x.dtype
+    ldx = _rows("x", x, dt, M, K, dev)
+    _vector("weight", weight, dt, K, dev)
+    ldr = 0
     if residual is not None:
-        _tensor("residual", residual, (dt,), 2, dev)
-        if residual.shape != x.shape:
-            raise ValueError(f"residual must be {tuple(x.shape)}, got {tuple(residual.shape)}")
+        ldr = _rows("residual", residual, dt, M, K, dev)
     elif residual_out is not None:
         raise ValueError("residual_out without a residual")
-    return dev, dt, M, K
+    ctx, handle = _on(dev, stream, x, weight, residual, out, scale_out, residual_out)
+    with ctx:
+        h, ldh = (x, 0) if residual is None else _output("residual_out", residual_out, dt, M, K, dev)
+        rstd = torch.empty(M, dtype=torch.float32, device=dev) if return_rstd else None
+        out, ldo = _output("out", out, E4M3 if e4m3 else dt, M, K, dev)
+        head = (x.data_ptr(), ldx, _ptr(residual), ldr, weight.data_ptr(), None if residual is None else h.data_ptr(),
+                ldh, out.data_ptr(), ldo)
+        if e4m3:
+            scale, lds = _row_scales("scale_out", scale_out, M, K, dev)
+            st = library().glu_add_rms_norm_fp8(*head, scale.data_ptr(), lds, _ptr(rstd), M, K, eps, DTYPES[dt],
+                                                handle)
+        else:
+            scale = None
+            st = library().glu_add_rms_norm(*head, _ptr(rstd), M, K, eps, DTYPES[dt], handle)
+    if st:
+        _raise_for(st)
+    return out, scale, h, rstd
 
 
 def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: Optional[torch.Tensor] = None,
@@ -131,18 +172,7 @@ def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: Op
     row, in fp32, and y rounded once.  ``residual_out`` may be ``residual`` or ``x`` (in place).  With
     ``return_rstd`` also 1 / rms [M] in fp32, which ``add_rms_norm_backward`` takes.
     """
-    dev, dt, M, K = _norm_args(x, weight, residual, residual_out)
-    ctx, handle = _on(dev, stream, x, weight, residual, out, residual_out)
-    with ctx:
-        out = _like("out", out, (M, K), dt, dev)
-        h = x if residual is None else _like("residual_out", residual_out, (M, K), dt, dev)
-        rstd = torch.empty(M, dtype=torch.float32, device=dev) if return_rstd else None
-        has = residual is not None
-        st = library().glu_add_rms_norm(
-            x.data_ptr(), _row_stride("x", x), _ptr(residual), _row_stride("residual", residual) if has else 0,
-            weight.data_ptr(), h.data_ptr() if has else None, _row_stride("residual_out", h) if has else 0,
-            out.data_ptr(), _row_stride("out", out), _ptr(rstd), M, K, eps, DTYPES[dt], handle)
-    _raise_for(st)
+    out, _, h, rstd = _norm(x, weight, eps, residual, out, None, residual_out, return_rstd, stream, False)
     return (out, h, rstd) if return_rstd else (out, h)
 
 
@@ -151,21 +181,18 @@ def add_rms_norm_fp8(x: torch.Tensor, weight: torch.Tensor, eps: float, residual
                      residual_out: Optional[torch.Tensor] = None, return_rstd: bool = False,
                      stream: Optional[torch.cuda.Stream] = None):
     """(q, scale, h): ``add_rms_norm`` with y converted to block-scaled e4m3 before any rounding to x's type."""
-    dev, dt, M, K = _norm_args(x, weight, residual, residual_out)
-    ctx, handle = _on(dev, stream, x, weight, residual, out, scale_out, residual_out)
-    with ctx:
-        out = _like("out", out, (M, K), E4M3, dev)
-        scale = _row_scales("scale_out", scale_out, M, K, dev)
-        h = x if residual is None else _like("residual_out", residual_out, (M, K), dt, dev)
-        rstd = torch.empty(M, dtype=torch.float32, device=dev) if return_rstd else None
-        has = residual is not None
-        st = library().glu_add_rms_norm_fp8(
-            x.data_ptr(), _row_stride("x", x), _ptr(residual), _row_stride("residual", residual) if has else 0,
-            weight.data_ptr(), h.data_ptr() if has else None, _row_stride("residual_out", h) if has else 0,
-            out.data_ptr(), _row_stride("out", out), scale.data_ptr(), scale.stride(1), _ptr(rstd), M, K, eps,
-            DTYPES[dt], handle)
-    _raise_for(st)
+    out, scale, h, rstd = _norm(x, weight, eps, residual, out, scale_out, residual_out, return_rstd, stream, True)
     return (out, scale, h, rstd) if return_rstd else (out, scale, h)
+
+
+_grad_workspace = functools.lru_cache(maxsize=256)(lambda M, K: _bytes("glu_add_rms_norm_backward_workspace", M, K))
+
+
+def _bytes(query: str, *args) -> int:
+    """What a workspace query of the library answers (host only)."""
+    need = ctypes.c_int64(0)
+    _raise_for(getattr(library(), query)(*args, ctypes.byref(need)))
+    return need.value
 
 
 def add_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
@@ -176,119 +203,106 @@ def add_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tenso
     h and rstd are the forward's.  dx is the gradient of x and of the residual alike.  dweight sums the
     rows in fp32 in a fixed order.  ``dx`` may be ``dresidual`` (in place).
     """
-    _tensor("h", h, _INPUTS, 2)
-    dev, dt = h.device, h.dtype
-    M, K = h.shape
-    _tensor("dy", dy, (dt,), 2, dev)
-    _tensor("weight", weight, (dt,), 1, dev)
-    _tensor("rstd", rstd, _F32, 1, dev)
-    if dy.shape != h.shape or weight.shape[0] != K or rstd.shape[0] != M:
-        raise ValueError(f"shape mismatch: dy {tuple(dy.shape)}, h {tuple(h.shape)}, weight {tuple(weight.shape)}, "
-                         f"rstd {tuple(rstd.shape)}")
-    for name, t in (("weight", weight), ("rstd", rstd)):
-        if t.shape[0] > 1 and t.stride(0) != 1:
-            raise ValueError(f"{name}: elements must be contiguous, got stride {t.stride(0)}")
-    if dresidual is not None:
-        _tensor("dresidual", dresidual, (dt,), 2, dev)
-        if dresidual.shape != h.shape:
-            raise ValueError(f"dresidual must be {tuple(h.shape)}, got {tuple(dresidual.shape)}")
-    lib = library()
-    need = ctypes.c_int64(0)
-    _raise_for(lib.glu_add_rms_norm_backward_workspace(M, K, ctypes.byref(need)))
+    M, K, dev = _matrix("h", h, _INPUTS)
+    dt = h.dtype
+    ldh = _rows("h", h, dt, M, K, dev)
+    lddy = _rows("dy", dy, dt, M, K, dev)
+    _vector("weight", weight, dt, K, dev)
+    _vector("rstd", rstd, torch.float32, M, dev)
+    lddr = 0 if dresidual is None else _rows("dresidual", dresidual, dt, M, K, dev)
+    need = _grad_workspace(M, K)
     ctx, handle = _on(dev, stream, dy, h, weight, rstd, dresidual, dx, dweight)
     with ctx:
-        dx = _like("dx", dx, (M, K), dt, dev)
-        dweight = _like("dweight", dweight, (K,), dt, dev)
-        if K > 1 and dweight.stride(0) != 1:
-            raise ValueError(f"dweight: elements must be contiguous, got stride {dweight.stride(0)}")
-        ws = torch.empty(need.value // 4, dtype=torch.float32, device=dev) if need.value else None
-        st = lib.glu_add_rms_norm_backward(
-            dy.data_ptr(), _row_stride("dy", dy), h.data_ptr(), _row_stride("h", h), weight.data_ptr(),
-            rstd.data_ptr(), _ptr(dresidual), 0 if dresidual is None else _row_stride("dresidual", dresidual),
-            dx.data_ptr(), _row_stride("dx", dx), dweight.data_ptr(), M, K, DTYPES[dt], _ptr(ws), need.value, handle)
-    _raise_for(st)
+        dx, lddx = _output("dx", dx, dt, M, K, dev)
+        if dweight is None:
+            dweight = torch.empty_like(weight)
+        else:
+            _vector("dweight", dweight, dt, K, dev)
+        ws = torch.empty(need // 4, dtype=torch.float32, device=dev) if need else None
+        st = library().glu_add_rms_norm_backward(
+            dy.data_ptr(), lddy, h.data_ptr(), ldh, weight.data_ptr(), rstd.data_ptr(), _ptr(dresidual), lddr,
+            dx.data_ptr(), lddx, dweight.data_ptr(), M, K, DTYPES[dt], _ptr(ws), need, handle)
+    if st:
+        _raise_for(st)
     return dx, dweight
 
 
 def fp8_quantize(x: torch.Tensor, out: Optional[torch.Tensor] = None, scale_out: Optional[torch.Tensor] = None,
                  stream: Optional[torch.cuda.Stream] = None):
     """(q, scale) of activations x [M, K] (bf16, fp16 or fp32): scale [M, ceil(K / 128)] per row and 128 columns."""
-    _tensor("x", x, _INPUTS, 2)
-    dev = x.device
-    M, K = x.shape
+    M, K, dev = _matrix("x", x, _INPUTS)
+    ldx = _rows("x", x, x.dtype, M, K, dev)
     ctx, handle = _on(dev, stream, x, out, scale_out)
     with ctx:
-        out = _like("out", out, (M, K), E4M3, dev)
-        scale = _row_scales("scale_out", scale_out, M, K, dev)
-        st = library().glu_fp8_quantize(x.data_ptr(), _row_stride("x", x), out.data_ptr(), _row_stride("out", out),
-                                        scale.data_ptr(), scale.stride(1), M, K, DTYPES[x.dtype], handle)
-    _raise_for(st)
+        out, ldo = _output("out", out, E4M3, M, K, dev)
+        scale, lds = _row_scales("scale_out", scale_out, M, K, dev)
+        st = library().glu_fp8_quantize(x.data_ptr(), ldx, out.data_ptr(), ldo, scale.data_ptr(), lds, M, K,
+                                        DTYPES[x.dtype], handle)
+    if st:
+        _raise_for(st)
     return out, scale
 
 
 def fp8_quantize_weight(w: torch.Tensor, out: Optional[torch.Tensor] = None,
                         scale_out: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
     """(q, scale) of a weight w [N, K] (bf16, fp16 or fp32): one scale per 128 x 128 block."""
-    _tensor("w", w, _INPUTS, 2)
-    dev = w.device
-    N, K = w.shape
+    N, K, dev = _matrix("w", w, _INPUTS)
+    ldw = _rows("w", w, w.dtype, N, K, dev)
     ctx, handle = _on(dev, stream, w, out, scale_out)
     with ctx:
-        out = _like("out", out, (N, K), E4M3, dev)
-        scale = _like("scale_out", scale_out, (groups(N), groups(K)), torch.float32, dev)
-        st = library().glu_fp8_quantize_weight(w.data_ptr(), _row_stride("w", w), out.data_ptr(),
-                                               _row_stride("out", out), scale.data_ptr(),
-                                               _row_stride("scale_out", scale), N, K, DTYPES[w.dtype], handle)
-    _raise_for(st)
+        out, ldo = _output("out", out, E4M3, N, K, dev)
+        scale, lds = _output("scale_out", scale_out, torch.float32, groups(N), groups(K), dev)
+        st = library().glu_fp8_quantize_weight(w.data_ptr(), ldw, out.data_ptr(), ldo, scale.data_ptr(), lds, N, K,
+                                               DTYPES[w.dtype], handle)
+    if st:
+        _raise_for(st)
     return out, scale
 
 
+_product_workspace = functools.lru_cache(maxsize=256)(lambda *sizes: _bytes("glu_fp8_workspace", *sizes))
+
+
 def _product(x, x_scale, weights, out_dtype, out, scale_out, plan, stream):
-    _tensor("x", x, _E4M3, 2)
-    dev = x.device
-    M, K = x.shape
-    _tensor("x_scale", x_scale, _F32, 2, dev)
-    if tuple(x_scale.shape) != (M, groups(K)):
-        raise ValueError(f"x_scale must be {(M, groups(K))}, got {tuple(x_scale.shape)}")
-    N = weights[0][1].shape[0] if isinstance(weights[0][1], torch.Tensor) and weights[0][1].dim() == 2 else -1
+    M, K, dev = _matrix("x", x, (E4M3,))
+    G = groups(K)
+    ldx = _rows("x", x, E4M3, M, K, dev)
+    if not (isinstance(x_scale, torch.Tensor) and x_scale.dtype is torch.float32 and x_scale.shape == (M, G)
+            and x_scale.device == dev):
+        _refuse("x_scale", x_scale, (torch.float32,), (M, G), dev)
+    sxm, sxg = x_scale.stride()
+    N, _, _ = _matrix(weights[0][0], weights[0][1], (E4M3,))
+    NG = groups(N)
     mats = []
     for name, w, s in weights:
-        _tensor(name, w, _E4M3, 2, dev)
-        _tensor(name + "_scale", s, _F32, 2, dev)
-        if tuple(w.shape) != (N, K):
-            raise ValueError(f"{name} must be {(N, K)}, got {tuple(w.shape)}")
-        if tuple(s.shape) != (groups(N), groups(K)):
-            raise ValueError(f"{name}_scale must be {(groups(N), groups(K))}, got {tuple(s.shape)}")
-        mats.append(Matrix(w.data_ptr(), s.data_ptr(), _row_stride(name, w), _row_stride(name + "_scale", s), 1))
-    if out_dtype not in DTYPES:
+        ldw, lds = _rows(name, w, E4M3, N, K, dev), _rows(name + "_scale", s, torch.float32, NG, G, dev)
+        mats.append(Matrix(w.data_ptr(), s.data_ptr(), ldw, lds, 1))
+    dt = DTYPES.get(out_dtype)
+    if dt is None:
         raise TypeError(f"out_dtype must be one of {[str(d) for d in DTYPES]}, got {out_dtype}")
     e4m3 = out_dtype is E4M3
     if scale_out is not None and not e4m3:
         raise ValueError("scale_out without an e4m3 output")
-    n, dt = len(mats), DTYPES[out_dtype]
-    lib = library()
-    need = ctypes.c_int64(0)
+    n = len(mats)
     if plan is None:
-        _raise_for(lib.glu_fp8_workspace(n, M, N, K, dt, ctypes.byref(need)))
+        need = _product_workspace(n, M, N, K, dt)
     else:
-        _raise_for(lib.glu_fp8_product_workspace(n, M, N, K, dt, ctypes.byref(plan), ctypes.byref(need)))
-    xm = Matrix(x.data_ptr(), x_scale.data_ptr(), _row_stride("x", x), x_scale.stride(0), x_scale.stride(1))
+        need = _bytes("glu_fp8_product_workspace", n, M, N, K, dt, ctypes.byref(plan))
     ctx, handle = _on(dev, stream, x, x_scale, out, scale_out, *(t for _, w, s in weights for t in (w, s)))
     with ctx:
-        out = _like("out", out, (M, N), out_dtype, dev)
-        scale = _row_scales("scale_out", scale_out, M, N, dev) if e4m3 else None
-        ws = torch.empty(need.value // 4, dtype=torch.float32, device=dev) if need.value else None
-        tail = (out.data_ptr(), _row_stride("out", out), _ptr(scale), scale.stride(1) if e4m3 else 0, M, N, K, dt)
+        out, ldo = _output("out", out, out_dtype, M, N, dev)
+        scale, lds = _row_scales("scale_out", scale_out, M, N, dev) if e4m3 else (None, 0)
+        ws = torch.empty(need // 4, dtype=torch.float32, device=dev) if need else None
+        args = (Matrix(x.data_ptr(), x_scale.data_ptr(), ldx, sxm, sxg), *mats, out.data_ptr(), ldo, _ptr(scale), lds,
+                M, N, K, dt)
         if plan is not None:
-            st = lib.glu_fp8_product_tuned(ctypes.byref(xm), ctypes.byref(mats[0]),
-                                           ctypes.byref(mats[1]) if n == 2 else None, *tail, ctypes.byref(plan),
-                                           _ptr(ws), need.value, handle)
+            up = (None,) if n == 1 else ()
+            st = library().glu_fp8_product_tuned(*args[:2], *up, *args[2:], plan, _ptr(ws), need, handle)
         elif n == 2:
-            st = lib.glu_fp8_dual_glu(ctypes.byref(xm), ctypes.byref(mats[0]), ctypes.byref(mats[1]), *tail, _ptr(ws),
-                                      need.value, handle)
+            st = library().glu_fp8_dual_glu(*args, _ptr(ws), need, handle)
         else:
-            st = lib.glu_fp8_linear(ctypes.byref(xm), ctypes.byref(mats[0]), *tail, _ptr(ws), need.value, handle)
-    _raise_for(st)
+            st = library().glu_fp8_linear(*args, _ptr(ws), need, handle)
+    if st:
+        _raise_for(st)
     return (out, scale) if e4m3 else out
 
 
