@@ -22,13 +22,13 @@ struct Fp8Args {
 constexpr int kPartial = -1;
 
 // Weights straight from memory to the matrix cores; a workgroup of `waves` waves splits the K-blocks of
-// `rows` weight rows (4, 8, 16) among them.
+// `rows` weight rows (4, for x of up to 4 rows, or 16) among them.
 struct StreamConfig {
     int rows, waves, splits;
     bool any;  // K or an address not a multiple of 16: byte-aligned loads (rows 16)
 };
 hipError_t fp8_stream_launch(int mats, const StreamConfig& c, const Fp8Args& a, hipStream_t stream);
-bool fp8_stream_supported(int mats, const StreamConfig& c, int M);
+bool fp8_stream_supported(const StreamConfig& c, int M);
 
 // LDS-tiled product; shape: an index into kTileShapes
 struct TileShape {
@@ -37,7 +37,7 @@ struct TileShape {
     int threads;
     int stages;
 };
-constexpr int kTileShapeCount = 6;
+constexpr int kTileShapeCount = 5;
 extern const TileShape kTileShapes[kTileShapeCount];
 struct TileConfig {
     int shape, splits;

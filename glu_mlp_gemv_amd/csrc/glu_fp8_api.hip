@@ -109,8 +109,56 @@ struct Operand {
 // outputs that show more than the 8-bit matrix unit's sums hold (glu_fp8_mfma.h)
 bool needs_wide(int out_dtype) { return out_dtype == GLU_DTYPE_FP32 || out_dtype == GLU_DTYPE_E4M3; }
 
-// Fills the launch shape for sizes >= 1.  What decides is measured with perf's sizes in DESIGN's table and at the rule.
-void choose(int mats, int64_t M, int64_t N, int64_t K, bool fast, glu_fp8_plan* p)
+// Microseconds that a tiled product is expected to take.  A workgroup takes a constant time per stage (one K-block of
+// its tile), each round of 256 workgroups (one per CU) has a start and an end, and sums that leave the kernel cost their
+// way to memory and back; nothing is faster than reading the operands.  The constants are a fit to 2200 timings of
+// 100 sizes (M = 17 to 4096, K = 128 to 17408, N = 256 to 17408), in which the shape of least expected time is
+// 0.6 % slower than the best in the mean and 9 % at most.  Leaving out one shape costs 1.5 to 6 % in the mean, 19 to 40 % at
+// most; 128 x 128 and 256 x 128 tiles were tried and are worth 0.2 %.
+constexpr double kStage[2][glu::kTileShapeCount] = {{1.7, 0.99, 0.74, 0.44, 0.27}, {3.3, 1.84, 1.28, 0.81, 0.51}};
+constexpr double kRound = 2.4, kLaunch = 2.8, kJoin = 2.5, kJoinSplit = 0.42;  // kJoin: 1.2 and the host's launch
+constexpr double kPlaneBytes = 3.3e6, kReadBytes = 3.6e6;  // per microsecond
+
+bool has_planes(int mats, int out_dtype, int shape, int64_t splits)
+{
+    return splits > 1 || (out_dtype == GLU_DTYPE_E4M3 && !glu::fp8_tile_owns_groups(mats, shape));
+}
+
+double tile_cost(int mats, int64_t M, int64_t N, int64_t K, int out_dtype, int shape, int splits)
+{
+    const glu::TileShape& t = glu::kTileShapes[shape];
+    const int64_t tiles = ceil_div(M, t.bm) * ceil_div(N, t.br / mats);
+    const int stages = ((int)ceil_div(K, kGroup) + splits - 1) / splits;
+    double us = kLaunch + (double)ceil_div(tiles * splits, kCUs) * (stages * kStage[needs_wide(out_dtype)][shape] + kRound);
+    if (has_planes(mats, out_dtype, shape, splits)) {
+        us += kJoin + kJoinSplit * splits + (double)(splits * mats * 4) * (double)M * (double)N / kPlaneBytes;
+    }
+    const double read = kLaunch + ((double)M + (double)mats * (double)N) * (double)K / kReadBytes;
+    return us > read ? us : read;
+}
+
+double best_tile(int mats, int64_t M, int64_t N, int64_t K, int out_dtype, glu_fp8_plan* p)
+{
+    double best = 0.0;
+    p->kernel = GLU_FP8_KERNEL_TILE;
+    p->splits = 0;
+    for (int shape = 0; shape < glu::kTileShapeCount; ++shape) {
+        for (const int splits : {1, 2, 3, 4, 6, 8, 12, 16}) {
+            if (splits > ceil_div(K, kGroup)) break;
+            const double us = tile_cost(mats, M, N, K, out_dtype, shape, splits);
+            if (p->splits == 0 || us < best) {
+                best = us;
+                p->tile = shape;
+                p->width = glu::kTileShapes[shape].threads;
+                p->splits = splits;
+            }
+        }
+    }
+    return best;
+}
+
+// Fills the launch shape for sizes >= 1.
+void choose(int mats, int64_t M, int64_t N, int64_t K, int out_dtype, bool fast, glu_fp8_plan* p)
 {
     const int64_t KB = ceil_div(K, kGroup);
     p->splits = 1;
@@ -122,43 +170,68 @@ void choose(int mats, int64_t M, int64_t N, int64_t K, bool fast, glu_fp8_plan* 
     }
     if (M <= 16) {
         p->kernel = GLU_FP8_KERNEL_STREAM;
-        p->tile = 16;
-        while (p->tile > 4 && M <= p->tile / 2 && ceil_div(N, p->tile) < 2 * kCUs) p->tile /= 2;
-        const int64_t steps = ceil_div(KB, 16 / p->tile);
-        int64_t w = ceil_div(steps, 4);
-        p->width = (int)(w > 16 ? 16 : w);
+        p->tile = M <= 4 ? 4 : 16;
+        // 3 resp. 6 waves keep enough loads in flight; more only lengthen the join (8.1 us against 8.4 with 8 waves at
+        // K = 9216 N = 2560, one row; 12.8 against 12.9 at K = 12288 N = 4096, 8 rows)
+        const int64_t steps = ceil_div(KB, 16 / p->tile), most = p->tile == 4 ? 3 : 6;
+        p->width = (int)(steps < most ? steps : most);
         return;
     }
-    p->kernel = GLU_FP8_KERNEL_TILE;
-    p->tile = M <= 32 ? 3 : M <= 64 ? 2 : M <= 1024 ? 1 : 0;
-    const glu::TileShape& t = glu::kTileShapes[p->tile];
-    p->width = t.threads;
-    const int64_t tiles = ceil_div(M, t.bm) * ceil_div(N, t.br / mats);
-    int64_t splits = 2 * kCUs / tiles;
-    if (splits > KB / 4) splits = KB / 4;
-    if (splits > 8) splits = 8;
-    p->splits = (int)(splits < 1 ? 1 : splits);
+    double best = best_tile(mats, M, N, K, out_dtype, p);
+    // Whole rounds of the largest tile in one launch and the columns left over in another, shaped for themselves, where a
+    // last round would leave most CUs idle
+    const glu::TileShape& t = glu::kTileShapes[0];
+    const int64_t bn = t.br / mats, high = ceil_div(M, t.bm);
+    const int64_t rounds = high * (N / bn) / kCUs, columns = rounds * kCUs / high * bn;
+    if (columns > 0 && columns < N) {
+        glu_fp8_plan rest{};
+        const double us = tile_cost(mats, M, columns, K, out_dtype, 0, 1) +
+                          best_tile(mats, M, N - columns, K, out_dtype, &rest);
+        if (us < best) {
+            best = us;
+            p->tile = 0;
+            p->width = t.threads;
+            p->splits = 1;
+            p->columns = columns;
+        }
+    }
 }
 
-// whether sums go to planes for the second kernel, and what follows from that
-void complete(int mats, int64_t M, int64_t N, int out_dtype, glu_fp8_plan* p)
+// what follows from a launch shape
+void complete(int mats, int64_t M, int64_t N, int64_t K, int out_dtype, glu_fp8_plan* p)
 {
-    bool planes = p->splits > 1;
-    if (out_dtype == GLU_DTYPE_E4M3) {
-        planes = planes || p->kernel != GLU_FP8_KERNEL_TILE || !glu::fp8_tile_owns_groups(mats, p->tile);
+    if (p->columns > 0) {  // the first columns by this shape, the others by their own
+        glu_fp8_plan first = *p, rest{};
+        first.columns = 0;
+        complete(mats, M, p->columns, K, out_dtype, &first);
+        best_tile(mats, M, N - p->columns, K, out_dtype, &rest);
+        complete(mats, M, N - p->columns, K, out_dtype, &rest);
+        p->launches = first.launches + rest.launches;
+        p->workspace_bytes = first.workspace_bytes > rest.workspace_bytes ? first.workspace_bytes : rest.workspace_bytes;
+        return;
     }
+    const bool planes = p->kernel == GLU_FP8_KERNEL_TILE
+                            ? has_planes(mats, out_dtype, p->tile, p->splits)
+                            : p->splits > 1 || out_dtype == GLU_DTYPE_E4M3;
     p->launches = planes ? 2 : 1;
     p->workspace_bytes = planes ? (int64_t)p->splits * mats * M * N * 4 : 0;
+}
+
+glu_status check_sizes(int mats, int64_t M, int64_t N, int64_t K, int out_dtype)
+{
+    if (mats != 1 && mats != 2) return GLU_ERR_BAD_ARGUMENT;
+    if (out_dtype < GLU_DTYPE_BF16 || out_dtype > GLU_DTYPE_E4M3) return GLU_ERR_BAD_ARGUMENT;
+    if (bad_dim(M) || bad_dim(N) || bad_dim(K)) return GLU_ERR_BAD_SHAPE;
+    if (M > 0 && N > INT64_MAX / 64 / M) return GLU_ERR_BAD_SHAPE;
+    return GLU_OK;
 }
 
 glu_status product_plan(int mats, int64_t M, int64_t N, int64_t K, int out_dtype, bool fast,
                         const glu_fp8_plan* asked, glu_fp8_plan* p)
 {
     *p = glu_fp8_plan{};
-    if (mats != 1 && mats != 2) return GLU_ERR_BAD_ARGUMENT;
-    if (out_dtype < GLU_DTYPE_BF16 || out_dtype > GLU_DTYPE_E4M3) return GLU_ERR_BAD_ARGUMENT;
-    if (bad_dim(M) || bad_dim(N) || bad_dim(K)) return GLU_ERR_BAD_SHAPE;
-    if (M > 0 && N > INT64_MAX / 64 / M) return GLU_ERR_BAD_SHAPE;
+    const glu_status st = check_sizes(mats, M, N, K, out_dtype);
+    if (st != GLU_OK) return st;
     if (M == 0 || N == 0) {
         p->kernel = GLU_FP8_KERNEL_NONE;
         return GLU_OK;
@@ -173,6 +246,11 @@ glu_status product_plan(int mats, int64_t M, int64_t N, int64_t K, int out_dtype
         p->tile = asked->tile;
         p->width = asked->width;
         p->splits = asked->splits;
+        p->columns = asked->columns;
+        if (p->columns != 0 && (p->kernel != GLU_FP8_KERNEL_TILE || p->columns < 0 || p->columns >= N ||
+                                p->columns % kGroup != 0)) {
+            return GLU_ERR_UNSUPPORTED;
+        }
         if (p->splits < 1 || p->splits > ceil_div(K, kGroup) || p->splits > 64) return GLU_ERR_UNSUPPORTED;
         if (p->kernel == GLU_FP8_KERNEL_TILE) {
             if (!fast || p->tile < 0 || p->tile >= glu::kTileShapeCount) return GLU_ERR_UNSUPPORTED;
@@ -181,27 +259,42 @@ glu_status product_plan(int mats, int64_t M, int64_t N, int64_t K, int out_dtype
             const bool any = p->kernel == GLU_FP8_KERNEL_ANY;
             if (!any && !fast) return GLU_ERR_UNSUPPORTED;
             const glu::StreamConfig c{p->tile, p->width, p->splits, any};
-            if (!glu::fp8_stream_supported(mats, c, (int)M)) return GLU_ERR_UNSUPPORTED;
+            if (!glu::fp8_stream_supported(c, (int)M)) return GLU_ERR_UNSUPPORTED;
         } else {
             return GLU_ERR_UNSUPPORTED;
         }
     } else {
-        choose(mats, M, N, K, fast, p);
+        choose(mats, M, N, K, out_dtype, fast, p);
     }
     // the streaming grid: one row tile's threads below 2^32
     if (p->kernel != GLU_FP8_KERNEL_TILE && ceil_div(N, p->tile) * p->splits > 0xffffffffLL / (64 * p->width)) {
         return GLU_ERR_UNSUPPORTED;
     }
-    complete(mats, M, N, out_dtype, p);
+    complete(mats, M, N, K, out_dtype, p);
     return GLU_OK;
+}
+
+// One launch shape on checked operands: the product, and the join of its parts
+hipError_t run_product(int mats, const glu_fp8_plan& p, glu::Fp8Args a, int out_dtype, hipStream_t s)
+{
+    a.out_dtype = p.launches == 2 ? glu::kPartial : out_dtype;
+    hipError_t e;
+    if (p.kernel == GLU_FP8_KERNEL_TILE) {
+        e = glu::fp8_tile_launch(mats, glu::TileConfig{p.tile, p.splits, needs_wide(out_dtype)}, a, s);
+    } else {
+        e = glu::fp8_stream_launch(mats, glu::StreamConfig{p.tile, p.width, p.splits, p.kernel == GLU_FP8_KERNEL_ANY}, a,
+                                   s);
+    }
+    if (e != hipSuccess || p.launches == 1) return e;
+    return glu::finish_launch(out_dtype, glu::FinishArgs{a.part, a.out, a.scale, a.ldo, a.lds, a.M, a.N, p.splits, mats},
+                              s);
 }
 
 glu_status product_call(const glu_fp8_matrix* x, const glu_fp8_matrix* w0, const glu_fp8_matrix* w1, int mats,
                         void* out, int64_t ldo, float* out_scale, int64_t ld_scale, int64_t M, int64_t N, int64_t K,
                         int out_dtype, const glu_fp8_plan* asked, void* ws, int64_t ws_bytes, void* stream)
 {
-    glu_fp8_plan p;
-    glu_status st = product_plan(mats, M, N, K, out_dtype, true, nullptr, &p);  // sizes and types
+    glu_status st = check_sizes(mats, M, N, K, out_dtype);
     if (st != GLU_OK) return st;
     if (M == 0 || N == 0) return GLU_OK;
     if (!x || !w0 || (mats == 2 && !w1)) return GLU_ERR_NULL_POINTER;
@@ -229,6 +322,7 @@ glu_status product_call(const glu_fp8_matrix* x, const glu_fp8_matrix* w0, const
         }
         fast = fast && (bits & 15) == 0;
     }
+    glu_fp8_plan p;
     st = product_plan(mats, M, N, K, out_dtype, fast, asked, &p);
     if (st != GLU_OK) return st;
     const Array arrays[] = {
@@ -247,9 +341,10 @@ glu_status product_call(const glu_fp8_matrix* x, const glu_fp8_matrix* w0, const
     if (p.workspace_bytes > 0 && (!ws || ((uintptr_t)ws & 15) || ws_bytes < p.workspace_bytes)) return GLU_ERR_WORKSPACE;
 
     hipStream_t s = (hipStream_t)stream;
-    const glu::FinishArgs fin{static_cast<const float*>(ws), out, out_scale, ldo, ld_scale, (int)M, (int)N, p.splits,
-                              mats};
-    if (p.kernel == GLU_FP8_KERNEL_ZERO) return launched(glu::finish_launch(out_dtype, fin, s));
+    if (p.kernel == GLU_FP8_KERNEL_ZERO) {
+        const glu::FinishArgs zero{nullptr, out, out_scale, ldo, ld_scale, (int)M, (int)N, 0, mats};
+        return launched(glu::finish_launch(out_dtype, zero, s));
+    }
     glu::Fp8Args a{};
     a.x = x->data;
     a.sx = x->scale;
@@ -270,17 +365,26 @@ glu_status product_call(const glu_fp8_matrix* x, const glu_fp8_matrix* w0, const
     a.M = (int)M;
     a.N = (int)N;
     a.K = (int)K;
-    a.out_dtype = p.launches == 2 ? glu::kPartial : out_dtype;
-    hipError_t e;
-    if (p.kernel == GLU_FP8_KERNEL_TILE) {
-        e = glu::fp8_tile_launch(mats, glu::TileConfig{p.tile, p.splits, needs_wide(out_dtype)}, a, s);
-    } else {
-        const bool any = p.kernel == GLU_FP8_KERNEL_ANY;
-        const glu::StreamConfig c{p.tile, p.width, p.splits, any};
-        e = glu::fp8_stream_launch(mats, c, a, s);
+    if (p.columns > 0) {
+        glu_fp8_plan rest{};
+        best_tile(mats, M, N - p.columns, K, out_dtype, &rest);
+        complete(mats, M, N - p.columns, K, out_dtype, &rest);
+        glu_fp8_plan first = p;
+        first.columns = 0;
+        complete(mats, M, p.columns, K, out_dtype, &first);
+        a.N = (int)p.columns;
+        const hipError_t e = run_product(mats, first, a, out_dtype, s);
+        if (e != hipSuccess) return launched(e);
+        for (int i = 0; i < mats; ++i) {
+            a.w[i] += p.columns * a.ldw[i];
+            a.sw[i] += p.columns / kGroup * a.ldsw[i];
+        }
+        a.out = static_cast<char*>(a.out) + p.columns * type_size(out_dtype);
+        if (a.scale) a.scale += p.columns / kGroup * a.lds;
+        a.N = (int)(N - p.columns);
+        return launched(run_product(mats, rest, a, out_dtype, s));
     }
-    if (e == hipSuccess && p.launches == 2) e = glu::finish_launch(out_dtype, fin, s);
-    return launched(e);
+    return launched(run_product(mats, p, a, out_dtype, s));
 }
 
 }  // namespace

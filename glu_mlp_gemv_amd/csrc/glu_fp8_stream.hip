@@ -3,10 +3,12 @@
 //
 // Bound by the weights' bytes.  A workgroup owns R weight rows (of each matrix) and its waves take
 // K-blocks in turn, so that together they read R rows of consecutive 128-byte blocks.  With R = 16 the 16 rows of the
-// matrix instruction's A operand are 16 weight rows; with R = 8 or 4 they are the same rows at 2 or 4 neighbouring
+// matrix instruction's A operand are 16 weight rows; with R = 4 they are the same 4 rows at 4 neighbouring
 // K-blocks, the B operand holds x at those K-blocks in the same order, and of the 16 x 16 results the
-// blocks on the diagonal are the products wanted.  That gives narrow matrices 2 and 4 times the workgroups, for x of
-// up to R rows.  The waves' sums meet in LDS in wave order.  The products run on the bf16 unit, whose sums are fp32
+// blocks on the diagonal are the products wanted.  That gives 4 times the workgroups, each reading 4 times as far along a
+// row, for x of up to 4 rows: at one row 8.1 us against 8.9 (K = 9216 N = 2560), dual 35.0 against 37.4
+// (K = 5120 N = 17408, 178 MB); at 8 rows, which 8 weight rows would serve, 16 is the faster (12.8 against 14.7 us at
+// K = 12288 N = 4096).  The waves' sums meet in LDS in wave order.  The products run on the bf16 unit, whose sums are fp32
 // (glu_fp8_mfma.h).
 #include "glu_fp8_mfma.h"
 
@@ -14,13 +16,22 @@ namespace glu {
 
 namespace {
 
-constexpr int kStreamMaxWaves = 16;
+constexpr int kStreamMaxWaves = 8;
 
-template <bool ANY>
+// Layout of the rows: whole K-blocks in whole instructions; chunks of 16 bytes; or any bytes
+enum { kWhole, kChunks, kBytes };
+
+template <int MODE>
 __device__ __forceinline__ raw4_t chunk16(const uint8_t* row, int64_t off, int K)
 {
-    raw4_t z = {0u, 0u, 0u, 0u};
-    if constexpr (ANY) {
+    if constexpr (MODE == kWhole) {
+        return *reinterpret_cast<const raw4_t*>(row + off);
+    } else if constexpr (MODE == kChunks) {
+        // K is a multiple of 16: the chunk is inside or outside as a whole; outside it is read at 0 and dropped
+        const bool in = off < K;
+        const raw4_t v = *reinterpret_cast<const raw4_t*>(row + (in ? off : 0));
+        return in ? v : raw4_t{0u, 0u, 0u, 0u};
+    } else {
         if (off + 16 <= K) return *reinterpret_cast<const u32x4_any*>(row + off);
         uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
@@ -28,23 +39,18 @@ __device__ __forceinline__ raw4_t chunk16(const uint8_t* row, int64_t off, int K
             if (off + i < K) w[i >> 2] |= (uint32_t)row[off + i] << (8 * (i & 3));
         }
         return raw4_t{w[0], w[1], w[2], w[3]};
-    } else {
-        // K is a multiple of 16: the chunk is inside or outside as a whole; outside it is read at 0 and dropped
-        const bool in = off < K;
-        const raw4_t v = *reinterpret_cast<const raw4_t*>(row + (in ? off : 0));
-        return in ? v : z;
     }
 }
 
 }  // namespace
 
-template <int NM, int R, bool ANY>
+template <int NM, int R, int MODE>
 __global__ void __launch_bounds__(64 * kStreamMaxWaves)
 fp8_stream_kernel(Fp8Args a, int waves, int splits, int nbn, int m_base)
 {
-    constexpr int S = 16 / R;          // K-blocks per instruction
-    constexpr int U = NM == 2 ? 2 : 4;  // steps whose loads are issued together
-    extern __shared__ float red[];     // [waves][NM][4][64]
+    constexpr int S = 16 / R;               // K-blocks per instruction
+    constexpr int U = MODE == kBytes ? 1 : NM == 2 ? 2 : 4;  // steps whose loads are in flight
+    extern __shared__ float red[];          // [waves][NM][4][64]
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int i16 = lane & 15, q = lane >> 4;
@@ -70,38 +76,51 @@ fp8_stream_kernel(Fp8Args a, int waves, int splits, int nbn, int m_base)
     f32x4 acc[NM];
 #pragma unroll
     for (int m = 0; m < NM; ++m) acc[m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    const int stride = waves * splits;
-    for (int s0 = split * waves + wave; s0 < steps; s0 += U * stride) {
-        raw4_t wv[U][NM][2], xv[U][2];
-        float sc[U][NM];
+    raw4_t wv[U][NM][2], xv[U][2];
+    float sc[U][NM + 1];
+    auto load = [&](int u, int s) __attribute__((always_inline)) {
+        const int kb = S * s + sel;
+        const int64_t off = (int64_t)kb * kGroup + 16 * q;
+        const int kbs = min(kb, KB - 1);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int s = s0 + u * stride;
-            if (s >= steps) break;
-            const int kb = S * s + sel;
-            const int64_t off = (int64_t)kb * kGroup + 16 * q;
-#pragma unroll
-            for (int m = 0; m < NM; ++m) {
-                wv[u][m][0] = chunk16<ANY>(wr[m], off, a.K);
-                wv[u][m][1] = chunk16<ANY>(wr[m], off + 64, a.K);
-            }
-            const int kbs = min(kb, KB - 1);
-            xv[u][0] = chunk16<ANY>(xr, off, a.K);
-            xv[u][1] = chunk16<ANY>(xr, off + 64, a.K);
-            const float sx = xs[kbs * a.sxg];
-#pragma unroll
-            for (int m = 0; m < NM; ++m) sc[u][m] = sx * ws[m][kbs];
+        for (int m = 0; m < NM; ++m) {
+            wv[u][m][0] = chunk16<MODE>(wr[m], off, a.K);
+            wv[u][m][1] = chunk16<MODE>(wr[m], off + 64, a.K);
+            sc[u][m] = ws[m][kbs];
         }
+        xv[u][0] = chunk16<MODE>(xr, off, a.K);
+        xv[u][1] = chunk16<MODE>(xr, off + 64, a.K);
+        sc[u][NM] = xs[kbs * a.sxg];
+    };
+    auto use = [&](int u) __attribute__((always_inline)) {
+        const Wide x = widen32(xv[u][0], xv[u][1]);
+#pragma unroll
+        for (int m = 0; m < NM; ++m) {
+            const f32x4 p = mfma_wide(widen32(wv[u][m][0], wv[u][m][1]), x);
+            const float c = sc[u][m] * sc[u][NM];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[m][e] = fmaf(p[e], c, acc[m][e]);
+        }
+    };
+    // a ring of U steps: one is refilled as soon as it is used, so that U - 1 remain in flight
+    const int stride = waves * splits;
+    int s = split * waves + wave;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        if (s + u * stride < steps) load(u, s + u * stride);
+    }
+    for (; s + (2 * U - 1) * stride < steps; s += U * stride) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (s0 + u * stride >= steps) break;
-            const Wide x = widen32(xv[u][0], xv[u][1]);
+            use(u);
+            load(u, s + (u + U) * stride);
+        }
+    }
+    for (; s < steps; s += U * stride) {
 #pragma unroll
-            for (int m = 0; m < NM; ++m) {
-                const f32x4 p = mfma_wide(widen32(wv[u][m][0], wv[u][m][1]), x);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[m][e] = fmaf(p[e], sc[u][m], acc[m][e]);
-            }
+        for (int u = 0; u < U; ++u) {
+            if (s + u * stride < steps) use(u);
+            if (s + (u + U) * stride < steps) load(u, s + (u + U) * stride);
         }
     }
 
@@ -111,23 +130,25 @@ fp8_stream_kernel(Fp8Args a, int waves, int splits, int nbn, int m_base)
         for (int e = 0; e < 4; ++e) red[((wave * NM + m) * 4 + e) * 64 + lane] = acc[m][e];
     }
     __syncthreads();
-    // one output a thread: weight row r, row j of x; its sums are D[sel R + r][sel R + j] of every wave
-    for (int idx = threadIdx.x; idx < R * R; idx += 64 * waves) {
+    // weight row r and row j of x, for matrix m: D[sel R + r][sel R + j] of every wave
+    auto sum = [&](int m, int r, int j) __attribute__((always_inline)) {
+        float v = 0.0f;
+        for (int w = 0; w < waves; ++w) {
+#pragma unroll
+            for (int b = 0; b < S; ++b) {
+                const int i = b * R + r;
+                v += red[((w * NM + m) * 4 + (i & 3)) * 64 + (i >> 2) * 16 + b * R + j];
+            }
+        }
+        return v;
+    };
+    for (int idx = threadIdx.x; idx < R * R; idx += 64 * waves) {  // one output a thread
         const int r = idx % R, j = idx / R;
         const int n = n0 + r, row = m0 + j;
         if (n >= a.N || row >= a.M) continue;
         float v[NM];
 #pragma unroll
-        for (int m = 0; m < NM; ++m) {
-            v[m] = 0.0f;
-            for (int w = 0; w < waves; ++w) {
-#pragma unroll
-                for (int b = 0; b < S; ++b) {
-                    const int i = b * R + r;
-                    v[m] += red[((w * NM + m) * 4 + (i & 3)) * 64 + (i >> 2) * 16 + b * R + j];
-                }
-            }
-        }
+        for (int m = 0; m < NM; ++m) v[m] = sum(m, r, j);
         if (a.out_dtype == kPartial) {
 #pragma unroll
             for (int m = 0; m < NM; ++m) {
@@ -144,29 +165,30 @@ namespace {
 using StreamFn = void (*)(Fp8Args, int, int, int, int);
 
 template <int NM>
-StreamFn pick_stream(const StreamConfig& c)
+StreamFn pick_stream(const StreamConfig& c, int K)
 {
-    if (c.any) return c.rows == 16 ? fp8_stream_kernel<NM, 16, true> : nullptr;
-    if (c.rows == 4) return fp8_stream_kernel<NM, 4, false>;
-    if (c.rows == 8) return fp8_stream_kernel<NM, 8, false>;
-    return c.rows == 16 ? fp8_stream_kernel<NM, 16, false> : nullptr;
+    if (c.any) return c.rows == 16 ? fp8_stream_kernel<NM, 16, kBytes> : nullptr;
+    const bool whole = c.rows > 0 && K % (kGroup * 16 / c.rows) == 0;
+    if (c.rows == 4) return whole ? fp8_stream_kernel<NM, 4, kWhole> : fp8_stream_kernel<NM, 4, kChunks>;
+    if (c.rows == 16) return whole ? fp8_stream_kernel<NM, 16, kWhole> : fp8_stream_kernel<NM, 16, kChunks>;
+    return nullptr;
 }
 
 size_t stream_lds(int mats, const StreamConfig& c) { return (size_t)c.waves * mats * 1024; }
 
 }  // namespace
 
-bool fp8_stream_supported(int mats, const StreamConfig& c, int M)
+bool fp8_stream_supported(const StreamConfig& c, int M)
 {
     if (c.waves < 1 || c.waves > kStreamMaxWaves || c.splits < 1) return false;
-    if ((mats == 1 ? pick_stream<1>(c) : pick_stream<2>(c)) == nullptr) return false;
+    if (c.rows != 16 && (c.any || c.rows != 4)) return false;
     return c.rows == 16 || M <= c.rows;
 }
 
 hipError_t fp8_stream_launch(int mats, const StreamConfig& c, const Fp8Args& a, hipStream_t stream)
 {
-    const StreamFn f = mats == 1 ? pick_stream<1>(c) : pick_stream<2>(c);
-    const int rows_x = c.rows;
+    const StreamFn f = mats == 1 ? pick_stream<1>(c, a.K) : pick_stream<2>(c, a.K);
+    const int rows_x = c.rows;  // rows of x per workgroup
     const int nbn = (int)(((int64_t)a.N + c.rows - 1) / c.rows);
     // slices of x's rows that keep a grid below 2^32 threads (one launch for anything but vast outputs)
     const int64_t tiles = ((int64_t)a.M + rows_x - 1) / rows_x;

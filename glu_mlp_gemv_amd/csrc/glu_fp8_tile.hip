@@ -19,11 +19,10 @@ namespace glu {
 
 const TileShape kTileShapes[kTileShapeCount] = {
     {256, 256, 512, 2},
-    {128, 128, 256, 2},
-    {64, 256, 256, 3},
-    {32, 128, 256, 4},
-    {256, 128, 512, 3},
     {128, 256, 512, 3},
+    {64, 256, 256, 3},
+    {64, 128, 256, 4},
+    {32, 128, 256, 4},
 };
 
 namespace {
@@ -389,13 +388,14 @@ using TileFn = void (*)(Fp8Args, int, int, int);
 template <int NM, bool WIDE, bool E4M3>
 TileFn pick_tile(int shape)
 {
+    // a pair's 128 weight rows are 64 columns: no whole group
+    constexpr bool HALF = E4M3 && NM == 2;
     switch (shape) {
     case 0: return fp8_tile_kernel<NM, 4, 8, 4, 2, 2, WIDE, E4M3>;
-    case 1: return E4M3 && NM == 2 ? nullptr : fp8_tile_kernel<NM, 4, 4, 2, 2, 2, WIDE, E4M3 && NM == 1>;
+    case 1: return fp8_tile_kernel<NM, 4, 4, 2, 4, 3, WIDE, E4M3>;
     case 2: return fp8_tile_kernel<NM, 4, 4, 1, 4, 3, WIDE, E4M3>;
-    case 4: return E4M3 && NM == 2 ? nullptr : fp8_tile_kernel<NM, 4, 4, 4, 2, 3, WIDE, E4M3 && NM == 1>;
-    case 5: return fp8_tile_kernel<NM, 4, 4, 2, 4, 3, WIDE, E4M3>;
-    case 3: return E4M3 && NM == 2 ? nullptr : fp8_tile_kernel<NM, 2, 2, 1, 4, 4, WIDE, E4M3 && NM == 1>;
+    case 3: return HALF ? nullptr : fp8_tile_kernel<NM, 4, 2, 1, 4, 4, WIDE, E4M3 && !HALF>;
+    case 4: return HALF ? nullptr : fp8_tile_kernel<NM, 2, 2, 1, 4, 4, WIDE, E4M3 && !HALF>;
     }
     return nullptr;
 }

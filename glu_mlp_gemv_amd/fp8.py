@@ -36,7 +36,7 @@ class Matrix(ctypes.Structure):
 
 class ProductPlan(ctypes.Structure):
     _fields_ = [("kernel", ctypes.c_int), ("tile", ctypes.c_int), ("width", ctypes.c_int), ("splits", ctypes.c_int),
-                ("launches", ctypes.c_int), ("workspace_bytes", ctypes.c_int64)]
+                ("launches", ctypes.c_int), ("workspace_bytes", ctypes.c_int64), ("columns", ctypes.c_int64)]
 
     def as_dict(self):
         d = {f: getattr(self, f) for f, _ in self._fields_}

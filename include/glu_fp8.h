@@ -127,6 +127,8 @@ typedef struct glu_fp8_plan {
     int splits;                /* parts of K summed by different workgroups */
     int launches;              /* 2: the parts are joined, or e4m3 converted, by a second kernel */
     int64_t workspace_bytes;
+    int64_t columns;           /* TILE: > 0 (a multiple of 128): only the first columns by this shape,
+                                  the others by launches shaped for as many columns; 0: all */
 } glu_fp8_plan;
 
 /* mats: 1 (linear) or 2 (dual GLU); `fast` states whether the layout is fast. */
@@ -137,7 +139,7 @@ glu_status glu_fp8_product_plan(int mats, int64_t M, int64_t N, int64_t K, int o
 glu_status glu_fp8_workspace(int mats, int64_t M, int64_t N, int64_t K, int out_dtype, int64_t* bytes);
 
 /*
- * Either product with the launch shape of `plan` (kernel, tile, width, splits;
+ * Either product with the launch shape of `plan` (kernel, tile, width, splits, columns;
  * launches and workspace_bytes are ignored), for sweeps and tests: up NULL is the linear one.  A shape that the library
  * was not built with or that cannot serve the operands returns GLU_ERR_UNSUPPORTED, before any HIP call.  The
  * workspace is that of glu_fp8_product_workspace for the same plan.

@@ -130,9 +130,15 @@ def test_dual_refusals(lib):
 
 
 @pytest.mark.parametrize("plan", [(0, 0, 0, 1), (5, 0, 0, 1), (3, -1, 0, 1), (3, 99, 0, 1), (3, 0, 0, 0), (3, 0, 0, 3),
-                                  (2, 5, 4, 1), (2, 16, 0, 1), (2, 16, 17, 1), (2, 16, 4, -1), (2, 32, 4, 1), (4, 8, 4, 1)])
+                                  (2, 5, 4, 1), (2, 8, 4, 1), (2, 16, 0, 1), (2, 16, 9, 1), (2, 16, 4, -1), (2, 32, 4, 1), (4, 8, 4, 1)])
 def test_unsupported_plans(lib, plan):
     assert product(lib, plan=fp8.ProductPlan(*plan)) == UNSUP
+
+
+def test_unsupported_columns(lib):
+    for columns in (-128, 100, 256, 384):
+        assert product(lib, plan=fp8.ProductPlan(3, 1, 0, 1, 0, 0, columns)) == UNSUP
+    assert product(lib, plan=fp8.ProductPlan(2, 16, 4, 1, 0, 0, 128)) == UNSUP
 
 
 def test_layouts_that_are_not_fast_refuse_the_fast_kernels(lib):
@@ -154,9 +160,13 @@ def test_plans_cover_every_size():
                             p = fp8.product_plan(mats, M, N, K, t, fast)
                             blocks = -(-K // 128)
                             assert p["kernel_name"] in (("stream", "tile") if fast else ("any",))
-                            assert 1 <= p["splits"] <= blocks and p["launches"] in (1, 2)
+                            assert 1 <= p["splits"] <= blocks
+                            if p["columns"]:
+                                assert fast and 0 < p["columns"] < N and p["columns"] % 128 == 0 and M > 16
+                                assert 2 <= p["launches"] <= 4
+                                continue
                             want = p["splits"] * mats * M * N * 4 if p["launches"] == 2 else 0
-                            assert p["workspace_bytes"] == want
+                            assert p["workspace_bytes"] == want and p["launches"] in (1, 2)
                             assert p["splits"] == 1 or p["launches"] == 2
     assert fp8.product_plan(1, 0, 5, 5)["kernel_name"] == "none"
     assert fp8.product_plan(1, 5, 5, 0)["kernel_name"] == "zero"

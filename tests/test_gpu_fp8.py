@@ -190,14 +190,15 @@ def test_any_contraction_length(M, N, K, mats):
 def plans():
     """Every kernel the library can launch, at sizes past and inside its tiles, with and without split sums."""
     out = []
-    for tile in range(4):
+    for tile in range(5):
         for splits in (1, 3):
             out += [(3, tile, 0, splits, M, N, K) for M, N, K in ((5, 130, 784), (130, 640, 1024), (300, 515, 400))]
-    for rows in (4, 8, 16):
-        for width in (1, 3, 16):
+    for rows in (4, 16):
+        for width in (1, 3, 8):
             out += [(2, rows, width, s, min(4, rows), 260, 1296) for s in (1, 2)]
-    out += [(2, 8, 5, 1, 8, 300, 2000), (2, 16, 4, 1, 16, 300, 2000), (2, 16, 4, 2, 30, 300, 2000),
+    out += [(2, 16, 4, 1, 16, 300, 2000), (2, 16, 4, 2, 30, 300, 2000),
             (2, 16, 4, 1, 61, 300, 2000), (4, 16, 4, 1, 61, 300, 2000), (4, 16, 3, 2, 20, 100, 512)]
+    out += [(2, rows, 4, 1, min(4, rows), 100, 2048) for rows in (4, 16)]
     return out
 
 
@@ -215,6 +216,23 @@ def test_every_launch_shape(kernel, tile, width, splits, M, N, K, mats):
         again = run(ops, T[kind], plan=plan)
         for a, b in zip(got if isinstance(got, tuple) else (got,), again if isinstance(again, tuple) else (again,)):
             assert same_bits(a, b), "a second call gives the same bits"
+
+
+@pytest.mark.parametrize("mats", [1, 2])
+@pytest.mark.parametrize("tile,splits,columns", [(0, 1, 256), (1, 2, 128), (4, 1, 384)])
+def test_columns_in_two_launches(tile, splits, columns, mats):
+    """The first columns by one shape, the others by their own: into strided outputs, with the scales of both."""
+    M, N, K = 150, 515, 784
+    ops = operands(M, N, K, 5, mats)
+    strict, loose = expected(ops), expected(ops, True)
+    plan = fp8.ProductPlan(3, tile, 0, splits, 0, 0, columns)
+    for kind in ("bf16", "fp32", "e4m3"):
+        store = torch.zeros(M, N + 5, dtype=torch.uint8 if kind == "e4m3" else T[kind], device=DEV)
+        out = (store.view(E4M3) if kind == "e4m3" else store)[:, 2:2 + N]
+        got = run(ops, T[kind], plan=plan, out=out)
+        torch.cuda.synchronize()
+        check(kind, got, *(loose if kind == "bf16" else strict))
+        assert (store[:, :2] == 0).all() and (store[:, 2 + N:] == 0).all()
 
 
 @pytest.mark.parametrize("mats", [1, 2])
