@@ -1,7 +1,7 @@
 """Build the HIP library libglu_gemv.so for gfx950, in place.
 
 Each ``csrc/*.hip`` compiles to an object in parallel, then they link into a
-shared library next to this file.  Flags: gfx950 only, -O3, no fast math, no
+shared library next to this file; ``csrc/glu_torch.cpp`` becomes the extension module ``_fast``.  Flags: gfx950 only, -O3, no fast math, no
 FP contraction beyond the explicit fmaf calls, packed-FP32 instructions
 disabled (the compiler forms them from scalar float code on its own), code
 object v5.
@@ -11,12 +11,14 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIBRARY = os.path.join(HERE, "libglu_gemv.so")
+BINDING = os.path.join(HERE, "_fast.so")  # host code only: torch tensors to the C ABI (csrc/glu_torch.cpp)
 ROOT = os.path.dirname(HERE)
 INCLUDE = os.path.join(ROOT, "include")
 
@@ -57,12 +59,35 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def build_binding(verbose: bool = False) -> str:
+    """Compile the torch binding _fast.so (host C++ against torch's headers); returns its path."""
+    import torch
+    from torch.utils import cpp_extension
+
+    tmp = BINDING + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[f for p in cpp_extension.include_paths() for f in ("-isystem", p)], "-isystem",
+           os.path.join(os.path.dirname(os.path.dirname(HIPCC)), "include"), "-I" + sysconfig.get_paths()["include"],
+           os.path.join(CSRC, "glu_torch.cpp"), "-o", tmp, "-L" + cpp_extension.TORCH_LIB_PATH, "-lc10", "-lc10_hip",
+           "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath," + cpp_extension.TORCH_LIB_PATH]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed on glu_torch.cpp:\n{res.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(verbose: bool = False, jobs: int = 8) -> str:
-    """Compile every HIP source and link libglu_gemv.so; returns its path."""
+    """Compile every HIP source, link libglu_gemv.so and compile the torch binding; returns the library's path."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     srcs = sources()
     with ThreadPoolExecutor(max_workers=max(1, min(jobs, len(srcs)))) as ex:
+        binding = ex.submit(build_binding, verbose)
         objs = list(ex.map(lambda s: _compile(s, verbose), srcs))
+        binding.result()
     tmp = LIBRARY + ".tmp"
     cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs]
     if verbose:

@@ -1,7 +1,9 @@
 """Python face of include/glu_fp8.h: RMS norm, conversion to block-scaled e4m3, products on it.
 
 As in ``api``, only argument marshalling happens here: tensors are checked, their device pointers
-and torch's current HIP stream go to ``libglu_gemv.so``, and a non-OK status becomes a ``GluError``.
+and torch's current HIP stream go to ``libglu_gemv.so``, and a non-OK status becomes a ``GluError``.  Calls that
+give no outputs, plan or stream try the extension module ``_fast`` first (csrc/glu_torch.cpp): it does the same for operands in
+the usual form, in a third of the time, and leaves the rest, refusals among them, to the code here.
 
 Block-scaled e4m3: a stored ``torch.float8_e4m3fn`` value q stands for ``q * scale``.  Activations
 [M, K] have an fp32 scale per row and 128 columns, [M, ceil(K / 128)], which the functions here return stored
@@ -16,6 +18,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import functools
+import importlib
 from typing import Optional
 
 import torch
@@ -42,6 +45,34 @@ class ProductPlan(ctypes.Structure):
         d = {f: getattr(self, f) for f, _ in self._fields_}
         d["kernel_name"] = KERNEL_NAMES[self.kernel]
         return d
+
+
+# in the order that _fast.bind takes them
+_BOUND = ("glu_add_rms_norm", "glu_add_rms_norm_fp8", "glu_add_rms_norm_backward",
+          "glu_add_rms_norm_backward_workspace", "glu_fp8_quantize", "glu_fp8_quantize_weight", "glu_fp8_linear",
+          "glu_fp8_dual_glu", "glu_fp8_workspace")
+_fast = None
+
+
+def _load_fast():
+    """The extension module, bound to the library that ``api`` has loaded (raises if it is not built)."""
+    global _fast
+    lib = library()
+    try:
+        module = importlib.import_module("glu_mlp_gemv_amd._fast")
+    except ImportError as e:
+        raise RuntimeError("glu_mlp_gemv_amd/_fast.so is not built; run __graft_entry__.build() "
+                           "(or python -m glu_mlp_gemv_amd.build)") from e
+    module.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in _BOUND))
+    _fast = module
+    return module
+
+
+def _taken(result) -> bool:
+    """Whether the extension module took the call; raises for a status."""
+    if type(result) is int:
+        _raise_for(result)
+    return result is not None
 
 
 def groups(n: int) -> int:
@@ -172,6 +203,10 @@ def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: Op
     row, in fp32, and y rounded once.  ``residual_out`` may be ``residual`` or ``x`` (in place).  With
     ``return_rstd`` also 1 / rms [M] in fp32, which ``add_rms_norm_backward`` takes.
     """
+    if out is None and residual_out is None and stream is None and not return_rstd:
+        r = (_fast or _load_fast()).norm(x, weight, eps, residual, False)
+        if _taken(r):
+            return r[0], x if residual is None else r[1]
     out, _, h, rstd = _norm(x, weight, eps, residual, out, None, residual_out, return_rstd, stream, False)
     return (out, h, rstd) if return_rstd else (out, h)
 
@@ -181,6 +216,10 @@ def add_rms_norm_fp8(x: torch.Tensor, weight: torch.Tensor, eps: float, residual
                      residual_out: Optional[torch.Tensor] = None, return_rstd: bool = False,
                      stream: Optional[torch.cuda.Stream] = None):
     """(q, scale, h): ``add_rms_norm`` with y converted to block-scaled e4m3 before any rounding to x's type."""
+    if out is None and scale_out is None and residual_out is None and stream is None and not return_rstd:
+        r = (_fast or _load_fast()).norm(x, weight, eps, residual, True)
+        if _taken(r):
+            return r[0], r[2], x if residual is None else r[1]
     out, scale, h, rstd = _norm(x, weight, eps, residual, out, scale_out, residual_out, return_rstd, stream, True)
     return (out, scale, h, rstd) if return_rstd else (out, scale, h)
 
@@ -203,6 +242,10 @@ def add_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tenso
     h and rstd are the forward's.  dx is the gradient of x and of the residual alike.  dweight sums the
     rows in fp32 in a fixed order.  ``dx`` may be ``dresidual`` (in place).
     """
+    if dx is None and dweight is None and stream is None:
+        r = (_fast or _load_fast()).norm_grad(dy, h, weight, rstd, dresidual)
+        if _taken(r):
+            return r
     M, K, dev = _matrix("h", h, _INPUTS)
     dt = h.dtype
     ldh = _rows("h", h, dt, M, K, dev)
@@ -230,6 +273,10 @@ def add_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tenso
 def fp8_quantize(x: torch.Tensor, out: Optional[torch.Tensor] = None, scale_out: Optional[torch.Tensor] = None,
                  stream: Optional[torch.cuda.Stream] = None):
     """(q, scale) of activations x [M, K] (bf16, fp16 or fp32): scale [M, ceil(K / 128)] per row and 128 columns."""
+    if out is None and scale_out is None and stream is None:
+        r = (_fast or _load_fast()).quantize(x, False)
+        if _taken(r):
+            return r
     M, K, dev = _matrix("x", x, _INPUTS)
     ldx = _rows("x", x, x.dtype, M, K, dev)
     ctx, handle = _on(dev, stream, x, out, scale_out)
@@ -246,6 +293,10 @@ def fp8_quantize(x: torch.Tensor, out: Optional[torch.Tensor] = None, scale_out:
 def fp8_quantize_weight(w: torch.Tensor, out: Optional[torch.Tensor] = None,
                         scale_out: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
     """(q, scale) of a weight w [N, K] (bf16, fp16 or fp32): one scale per 128 x 128 block."""
+    if out is None and scale_out is None and stream is None:
+        r = (_fast or _load_fast()).quantize(w, True)
+        if _taken(r):
+            return r
     N, K, dev = _matrix("w", w, _INPUTS)
     ldw = _rows("w", w, w.dtype, N, K, dev)
     ctx, handle = _on(dev, stream, w, out, scale_out)
@@ -263,6 +314,11 @@ _product_workspace = functools.lru_cache(maxsize=256)(lambda *sizes: _bytes("glu
 
 
 def _product(x, x_scale, weights, out_dtype, out, scale_out, plan, stream):
+    if out is None and scale_out is None and plan is None and stream is None:
+        r = (_fast or _load_fast()).product(DTYPES.get(out_dtype, -1), x, x_scale, *weights[0][1:],
+                                            *(weights[1][1:] if len(weights) == 2 else ()))
+        if _taken(r):
+            return r if len(r) == 2 else r[0]
     M, K, dev = _matrix("x", x, (E4M3,))
     G = groups(K)
     ldx = _rows("x", x, E4M3, M, K, dev)
