@@ -412,7 +412,10 @@ glu_status glu_add_rms_norm_backward_workspace(int64_t M, int64_t K, int64_t* by
     if (!bytes) return GLU_ERR_NULL_POINTER;
     *bytes = 0;
     if (bad_dim(M) || bad_dim(K) || K == 0) return GLU_ERR_BAD_SHAPE;
-    *bytes = glu::norm_grad_part_floats((int)M, (int)K) * 4;
+    for (int dtype = GLU_DTYPE_BF16; dtype <= GLU_DTYPE_FP32; ++dtype) {  // what serves any of the types
+        const int64_t need = glu::norm_grad_part_floats(dtype, (int)M, (int)K) * 4;
+        if (need > *bytes) *bytes = need;
+    }
     return GLU_OK;
 }
 

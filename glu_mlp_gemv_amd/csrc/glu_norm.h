@@ -33,8 +33,8 @@ struct NormGradArgs {
     int M, K;
 };
 // Teams of waves, each walking its own rows and leaving one fp32 partial of dw; a single team writes dw itself.
-int norm_grad_teams(int M, int K);
-int64_t norm_grad_part_floats(int M, int K);
+int norm_grad_teams(int dtype, int M, int K);
+int64_t norm_grad_part_floats(int dtype, int M, int K);
 hipError_t norm_grad_launch(int dtype, const NormGradArgs& a, hipStream_t stream);
 
 }  // namespace glu
