@@ -101,23 +101,19 @@ glu_status norm_call(const void* x, int64_t ldx, const void* residual, int64_t l
 
 // ---- products ----------------------------------------------------------------------
 
-struct Operand {
-    const glu_fp8_matrix* m;
-    int64_t rows, scale_rows, blocks;
-};
-
 // outputs that show more than the 8-bit matrix unit's sums hold (glu_fp8_mfma.h)
 bool needs_wide(int out_dtype) { return out_dtype == GLU_DTYPE_FP32 || out_dtype == GLU_DTYPE_E4M3; }
 
 // Microseconds that a tiled product is expected to take.  A workgroup takes a constant time per stage (one K-block of
 // its tile), each round of 256 workgroups (one per CU) has a start and an end, and sums that leave the kernel cost their
-// way to memory and back; nothing is faster than reading the operands.  The constants are a fit to 2200 timings of
-// 100 sizes (M = 17 to 4096, K = 128 to 17408, N = 256 to 17408), in which the shape of least expected time is
-// 0.6 % slower than the best in the mean and 9 % at most.  Leaving out one shape costs 1.5 to 6 % in the mean, 19 to 40 % at
-// most; 128 x 128 and 256 x 128 tiles were tried and are worth 0.2 %.
-constexpr double kStage[2][glu::kTileShapeCount] = {{1.7, 0.99, 0.74, 0.44, 0.27}, {3.3, 1.84, 1.28, 0.81, 0.51}};
-constexpr double kRound = 2.4, kLaunch = 2.8, kJoin = 2.5, kJoinSplit = 0.42;  // kJoin: 1.2 and the host's launch
-constexpr double kPlaneBytes = 3.3e6, kReadBytes = 3.6e6;  // per microsecond
+// way to memory and back; that and the time to read the operands join as a fourth-power mean.  The constants are a fit to
+// 2200 timings of 100 sizes (M = 17 to 4096, K = 128 to 17408, N = 256 to 17408), over which the shape of least expected
+// time is 0.5 % slower than the best in the mean and 6 % at most.  Leaving out one shape costs 1.5 to 6 % in the mean, 19 to
+// 40 % at most; 128 x 128 and 256 x 128 tiles were tried and are worth 0.2 %.
+constexpr double kStage[2][glu::kTileShapeCount] = {{1.7, 0.98, 0.74, 0.44, 0.27}, {3.3, 1.8, 1.3, 0.8, 0.51}};
+constexpr double kRound = 2.4, kLaunch = 2.8, kJoinSplit = 0.41;
+constexpr double kJoin = 2.5;                              // 1.2 of it the kernel, the rest the host's launch
+constexpr double kPlaneBytes = 3.3e6, kReadBytes = 4.5e6;  // per microsecond
 
 bool has_planes(int mats, int out_dtype, int shape, int64_t splits)
 {
@@ -129,12 +125,13 @@ double tile_cost(int mats, int64_t M, int64_t N, int64_t K, int out_dtype, int s
     const glu::TileShape& t = glu::kTileShapes[shape];
     const int64_t tiles = ceil_div(M, t.bm) * ceil_div(N, t.br / mats);
     const int stages = ((int)ceil_div(K, kGroup) + splits - 1) / splits;
-    double us = kLaunch + (double)ceil_div(tiles * splits, kCUs) * (stages * kStage[needs_wide(out_dtype)][shape] + kRound);
+    const double round = stages * kStage[needs_wide(out_dtype)][shape] + kRound;
+    double us = kLaunch + (double)ceil_div(tiles * splits, kCUs) * round;
     if (has_planes(mats, out_dtype, shape, splits)) {
         us += kJoin + kJoinSplit * splits + (double)(splits * mats * 4) * (double)M * (double)N / kPlaneBytes;
     }
     const double read = kLaunch + ((double)M + (double)mats * (double)N) * (double)K / kReadBytes;
-    return us > read ? us : read;
+    return sqrt(sqrt(us * us * us * us + read * read * read * read));
 }
 
 double best_tile(int mats, int64_t M, int64_t N, int64_t K, int out_dtype, glu_fp8_plan* p)
