@@ -5,7 +5,8 @@ Dual-Weight GEMV", section "Plan B Design"): the Function keeps hidden, gate_w a
 Parameters in place in both directions, and returns gradients for all three,
 so training and generation share one forward and one set of weights.
 Forward: glu_dual_gemv; backward: glu_dual_gemv_backward (up to 65536 rows
-of hidden per call).  ``rms_norm`` does the same for the residual addition and norm.  Only argument marshalling happens here.
+of hidden per call).  ``rms_norm`` does the same for the residual addition and
+norm.  Only argument marshalling happens here.
 """
 from typing import Optional
 

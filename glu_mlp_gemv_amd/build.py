@@ -1,7 +1,8 @@
 """Build the HIP library libglu_gemv.so for gfx950, in place.
 
 Each ``csrc/*.hip`` compiles to an object in parallel, then they link into a
-shared library next to this file; ``csrc/glu_torch.cpp`` becomes the extension module ``_fast``.  Flags: gfx950 only, -O3, no fast math, no
+shared library next to this file; ``csrc/glu_torch.cpp`` becomes the extension
+module ``_fast``.  Flags: gfx950 only, -O3, no fast math, no
 FP contraction beyond the explicit fmaf calls, packed-FP32 instructions
 disabled (the compiler forms them from scalar float code on its own), code
 object v5.

@@ -6,7 +6,8 @@
 
 namespace glu {
 
-// One or two products of the same rows: sum over K-blocks b of sx[m, b] sw[n / 128, b] sum_{k in b} x[m, k] w[n, k].
+// One or two products of the same rows: sum over K-blocks b of sx[m, b] sw[n / 128, b] sum_{k in b} x[m, k]
+// w[n, k].
 struct Fp8Args {
     const uint8_t* x;       // [M][K] e4m3, row stride ldx
     const float* sx;        // scale of row m, block b at m * sxm + b * sxg

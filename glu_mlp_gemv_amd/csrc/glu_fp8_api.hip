@@ -41,8 +41,8 @@ int64_t extent(const Array& a)
     return ((a.rows - 1) * a.ld + a.len) * a.size;
 }
 
-// NULL, strides, alignment and overlap of a call's arrays, in that order.  An output may coincide exactly (pointer and
-// stride) with the inputs in `shared`, a bit per array.
+// NULL, strides, alignment and overlap of a call's arrays, in that order.  An output may coincide exactly
+// (pointer and stride) with the inputs in `shared`, a bit per array.
 glu_status check_arrays(const Array* a, int n, unsigned shared_out = 0, unsigned shared_in = 0)
 {
     int64_t bytes[16];
@@ -95,7 +95,8 @@ glu_status norm_call(const void* x, int64_t ldx, const void* residual, int64_t l
     };
     const glu_status st = check_arrays(arrays, 7, 1u << 3, 1u << 0 | 1u << 1);
     if (st != GLU_OK) return st;
-    const glu::NormArgs a{x, residual, weight, sum, out, scale, rstd, ldx, ldr, lds, ldo, ld_scale, (int)M, (int)K, eps};
+    const glu::NormArgs a{x,   residual, weight, sum,      out,    scale,  rstd, ldx,
+                          ldr, lds,      ldo,    ld_scale, (int)M, (int)K, eps};
     return launched(glu::norm_launch(dtype, e4m3, a, (hipStream_t)stream));
 }
 
@@ -104,12 +105,13 @@ glu_status norm_call(const void* x, int64_t ldx, const void* residual, int64_t l
 // outputs that show more than the 8-bit matrix unit's sums hold (glu_fp8_mfma.h)
 bool needs_wide(int out_dtype) { return out_dtype == GLU_DTYPE_FP32 || out_dtype == GLU_DTYPE_E4M3; }
 
-// Microseconds that a tiled product is expected to take.  A workgroup takes a constant time per stage (one K-block of
-// its tile), each round of 256 workgroups (one per CU) has a start and an end, and sums that leave the kernel cost their
-// way to memory and back; that and the time to read the operands join as a fourth-power mean.  The constants are a fit to
-// 2200 timings of 100 sizes (M = 17 to 4096, K = 128 to 17408, N = 256 to 17408), over which the shape of least expected
-// time is 0.5 % slower than the best in the mean and 6 % at most.  Leaving out one shape costs 1.5 to 6 % in the mean, 19 to
-// 40 % at most; 128 x 128 and 256 x 128 tiles were tried and are worth 0.2 %.
+// Microseconds that a tiled product is expected to take.  A workgroup takes a constant time per stage (one
+// K-block of its tile), each round of 256 workgroups (one per CU) has a start and an end, and sums that leave
+// the kernel cost their way to memory and back; that and the time to read the operands join as a fourth-power
+// mean.  The constants are a fit to 2200 timings of 100 sizes (M = 17 to 4096, K = 128 to 17408, N = 256 to
+// 17408), over which the shape of least expected time is 0.5 % slower than the best in the mean and 6 % at
+// most.  Leaving out one shape costs 1.5 to 6 % in the mean, 19 to 40 % at most; 128 x 128 and 256 x 128 tiles
+// were tried and are worth 0.2 %.
 constexpr double kStage[2][glu::kTileShapeCount] = {{1.7, 0.98, 0.74, 0.44, 0.27}, {3.3, 1.8, 1.3, 0.8, 0.51}};
 constexpr double kRound = 2.4, kLaunch = 2.8, kJoinSplit = 0.41;
 constexpr double kJoin = 2.5;                              // 1.2 of it the kernel, the rest the host's launch
@@ -168,15 +170,15 @@ void choose(int mats, int64_t M, int64_t N, int64_t K, int out_dtype, bool fast,
     if (M <= 16) {
         p->kernel = GLU_FP8_KERNEL_STREAM;
         p->tile = M <= 4 ? 4 : 16;
-        // 3 resp. 6 waves keep enough loads in flight; more only lengthen the join (8.1 us against 8.4 with 8 waves at
-        // K = 9216 N = 2560, one row; 12.8 against 12.9 at K = 12288 N = 4096, 8 rows)
+        // 3 resp. 6 waves keep enough loads in flight; more only lengthen the join (8.1 us against 8.4 with 8
+        // waves at K = 9216 N = 2560, one row; 12.8 against 12.9 at K = 12288 N = 4096, 8 rows)
         const int64_t steps = ceil_div(KB, 16 / p->tile), most = p->tile == 4 ? 3 : 6;
         p->width = (int)(steps < most ? steps : most);
         return;
     }
     double best = best_tile(mats, M, N, K, out_dtype, p);
-    // Whole rounds of the largest tile in one launch and the columns left over in another, shaped for themselves, where a
-    // last round would leave most CUs idle
+    // Whole rounds of the largest tile in one launch and the columns left over in another, shaped for
+    // themselves, where a last round would leave most CUs idle
     const glu::TileShape& t = glu::kTileShapes[0];
     const int64_t bn = t.br / mats, high = ceil_div(M, t.bm);
     const int64_t rounds = high * (N / bn) / kCUs, columns = rounds * kCUs / high * bn;
@@ -204,7 +206,8 @@ void complete(int mats, int64_t M, int64_t N, int64_t K, int out_dtype, glu_fp8_
         best_tile(mats, M, N - p->columns, K, out_dtype, &rest);
         complete(mats, M, N - p->columns, K, out_dtype, &rest);
         p->launches = first.launches + rest.launches;
-        p->workspace_bytes = first.workspace_bytes > rest.workspace_bytes ? first.workspace_bytes : rest.workspace_bytes;
+        p->workspace_bytes = first.workspace_bytes;
+        if (rest.workspace_bytes > p->workspace_bytes) p->workspace_bytes = rest.workspace_bytes;
         return;
     }
     const bool planes = p->kernel == GLU_FP8_KERNEL_TILE
@@ -279,12 +282,12 @@ hipError_t run_product(int mats, const glu_fp8_plan& p, glu::Fp8Args a, int out_
     if (p.kernel == GLU_FP8_KERNEL_TILE) {
         e = glu::fp8_tile_launch(mats, glu::TileConfig{p.tile, p.splits, needs_wide(out_dtype)}, a, s);
     } else {
-        e = glu::fp8_stream_launch(mats, glu::StreamConfig{p.tile, p.width, p.splits, p.kernel == GLU_FP8_KERNEL_ANY}, a,
-                                   s);
+        const glu::StreamConfig c{p.tile, p.width, p.splits, p.kernel == GLU_FP8_KERNEL_ANY};
+        e = glu::fp8_stream_launch(mats, c, a, s);
     }
     if (e != hipSuccess || p.launches == 1) return e;
-    return glu::finish_launch(out_dtype, glu::FinishArgs{a.part, a.out, a.scale, a.ldo, a.lds, a.M, a.N, p.splits, mats},
-                              s);
+    const glu::FinishArgs fin{a.part, a.out, a.scale, a.ldo, a.lds, a.M, a.N, p.splits, mats};
+    return glu::finish_launch(out_dtype, fin, s);
 }
 
 glu_status product_call(const glu_fp8_matrix* x, const glu_fp8_matrix* w0, const glu_fp8_matrix* w1, int mats,
@@ -335,7 +338,9 @@ glu_status product_call(const glu_fp8_matrix* x, const glu_fp8_matrix* w0, const
     };
     st = check_arrays(arrays, 9);
     if (st != GLU_OK) return st;
-    if (p.workspace_bytes > 0 && (!ws || ((uintptr_t)ws & 15) || ws_bytes < p.workspace_bytes)) return GLU_ERR_WORKSPACE;
+    if (p.workspace_bytes > 0 && (!ws || ((uintptr_t)ws & 15) || ws_bytes < p.workspace_bytes)) {
+        return GLU_ERR_WORKSPACE;
+    }
 
     hipStream_t s = (hipStream_t)stream;
     if (p.kernel == GLU_FP8_KERNEL_ZERO) {

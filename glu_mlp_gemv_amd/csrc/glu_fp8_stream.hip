@@ -1,15 +1,15 @@
 // Block-scaled e4m3 products for few rows of x: weights go from memory
 // straight into matrix instructions, each read once.
 //
-// Bound by the weights' bytes.  A workgroup owns R weight rows (of each matrix) and its waves take
-// K-blocks in turn, so that together they read R rows of consecutive 128-byte blocks.  With R = 16 the 16 rows of the
-// matrix instruction's A operand are 16 weight rows; with R = 4 they are the same 4 rows at 4 neighbouring
-// K-blocks, the B operand holds x at those K-blocks in the same order, and of the 16 x 16 results the
-// blocks on the diagonal are the products wanted.  That gives 4 times the workgroups, each reading 4 times as far along a
-// row, for x of up to 4 rows: at one row 8.1 us against 8.9 (K = 9216 N = 2560), dual 35.0 against 37.4
-// (K = 5120 N = 17408, 178 MB); at 8 rows, which 8 weight rows would serve, 16 is the faster (12.8 against 14.7 us at
-// K = 12288 N = 4096).  The waves' sums meet in LDS in wave order.  The products run on the bf16 unit, whose sums are fp32
-// (glu_fp8_mfma.h).
+// Bound by the weights' bytes.  A workgroup owns R weight rows (of each matrix) and its waves take K-blocks in
+// turn, so that together they read R rows of consecutive 128-byte blocks.  With R = 16 the 16 rows of the matrix
+// instruction's A operand are 16 weight rows; with R = 4 they are the same 4 rows at 4 neighbouring K-blocks,
+// the B operand holds x at those K-blocks in the same order, and of the 16 x 16 results the blocks on the
+// diagonal are the products wanted.  That gives 4 times the workgroups, each reading 4 times as far along a row,
+// for x of up to 4 rows: at one row 8.1 us against 8.9 (K = 9216 N = 2560), dual 35.0 against 37.4 (K = 5120 N
+// = 17408, 178 MB); at 8 rows, which 8 weight rows would serve, 16 is the faster (12.8 against 14.7 us at K =
+// 12288 N = 4096).  The waves' sums meet in LDS in wave order.  The products run on the bf16 unit, whose sums are
+// fp32 (glu_fp8_mfma.h).
 #include "glu_fp8_mfma.h"
 
 namespace glu {

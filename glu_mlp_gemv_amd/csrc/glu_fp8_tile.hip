@@ -2,15 +2,26 @@
 // streaming kernels take.
 //
 // A workgroup of WM x WN waves owns BM = 16 TM WM rows of x and BR = 16 TN WN weight rows (with two matrices
-// half of each, so that gate and up of one output meet in one lane).  K is walked one block of 128 at a time: a stage
-// is BM + BR rows of 128 bytes, brought straight from memory into LDS, STAGES - 1 stages ahead of their use, with one
-// barrier per stage.  The matrix instruction sums exactly one K-block, so its result is multiplied by the two scales
-// and added to the accumulator on the vector unit: 4 fused multiply-adds per lane against 32 cycles of the
-// matrix unit, which another wave uses meanwhile.
+// half of each, so that gate and up of one output meet in one lane).  K is walked one block of 128 at a time: a
+// stage is BM + BR rows of 128 bytes and the scales of x, brought straight from memory into one of STAGES
+// buffers of LDS.  The matrix instruction sums exactly one K-block, so its result is multiplied by the two
+// scales and added to the accumulator on the vector unit, 4 fused multiply-adds per lane against 32 cycles
+// (8-bit) or 64 (bf16) of the matrix unit.
 //
-// In LDS, 16-byte chunk c of row r lies at c ^ ((r >> 1) & 7): every group of 16 lanes that a ds_read_b128 serves together
-// then touches 16 different slots of the 256-byte bank line.  A wave's direct load writes 64 consecutive
-// slots (8 rows), so the exchange is made in the source addresses.
+// What bounds it, at M = 4096 K = 17408 N = 4096 (256 tiles of 256 x 256, one round): 234 us, 2.50 PFLOP/s on
+// the 8-bit unit, where the library's unscaled product at 8192^3 runs at 3.29 in short runs and 2.86 once the
+// card has warmed to its power limit (its clock falls from 1.9 to 1.6 GHz).  The matrix unit is busy 68 % of the
+// cycles; without the loads of the main loop the kernel takes 191 us, without the scaling 217.  On the bf16 unit
+// (dual, K = 17408 N = 2048) 421 us, 1.39 PFLOP/s against the library's 1.65 and 1.5: there conversions,
+// scaling and products together fill 95 % of the issue slots that the products' time has.  Steps that led there,
+// at the first size: operands fetched across the stage's end and one barrier in its middle 262 -> 250, tiles in
+// blocks of 8 x 4 per XCD (a third fewer L2 misses) no change in time, loads spread over the steps 250 -> 243,
+// weights fetched two rows of tiles ahead 243 -> 234.  Half as much again in flight (three buffers of weights,
+// those of x refilled in mid-stage) gave nothing: 244.
+//
+// In LDS, 16-byte chunk c of row r lies at c ^ ((r >> 1) & 7): every group of 16 lanes that a ds_read_b128
+// serves together then touches 16 different slots of the 256-byte bank line (no conflict counted).  A wave's
+// direct load writes 64 consecutive slots (8 rows), so the exchange is made in the source addresses.
 #include <type_traits>
 
 #include "glu_fp8_mfma.h"
@@ -63,7 +74,8 @@ __device__ __forceinline__ void wait_vm()
 }  // namespace
 
 // WIDE: products on the bf16 unit, for outputs that show more than the 8-bit unit's sums hold: e4m3, whose fp32
-// scales are the largest sums themselves, and fp32.  E4M3: the kernel converts by itself (a workgroup holds whole groups).
+// scales are the largest sums themselves, and fp32.  E4M3: the kernel converts by itself (a workgroup holds
+// whole groups).
 template <int NM, int TM, int TN, int WM, int WN, int STAGES, bool WIDE, bool E4M3>
 __global__ void __launch_bounds__(64 * WM * WN)
 fp8_tile_kernel(Fp8Args a, int nbm, int nbn, int splits)
@@ -75,7 +87,8 @@ fp8_tile_kernel(Fp8Args a, int nbm, int nbn, int splits)
     constexpr int XPW = BM / 8 / WAVES;               // ... of which rows of x
     constexpr int SXW = (BM + 63) / 64;               // waves that load scales of x
     constexpr int STAGE = (BM + BR) * kGroup + 4 * SXW * 64;
-    static_assert(BM % (8 * WAVES) == 0 && BR % (8 * NM * WAVES) == 0 && TN % 2 == 0 && TN % NM == 0, "whole loads per wave");
+    static_assert(BM % (8 * WAVES) == 0 && BR % (8 * NM * WAVES) == 0 && TN % 2 == 0 && TN % NM == 0,
+                  "whole loads per wave");
     static_assert(WAVES % 2 == 0, "a wave's loads lie a multiple of 16 rows apart");
 
     extern __shared__ __attribute__((aligned(256))) uint8_t smem[];
@@ -84,8 +97,8 @@ fp8_tile_kernel(Fp8Args a, int nbm, int nbn, int splits)
     const int wm = wave % WM, wn = wave / WM;
     const int i16 = lane & 15, q = lane >> 4;
 
-    // An XCD takes a run of tiles, in blocks 8 tiles of x high: the 32 that it works on at a time then read 8 row blocks of
-    // x and 4 of the weights between them, the least that its L2 has to fetch.
+    // An XCD takes a run of tiles, in blocks 8 tiles of x high: the 32 that it works on at a time then read 8
+    // row blocks of x and 4 of the weights between them, the least that its L2 has to fetch.
     constexpr int HIGH = 8;
     const int t = xcd_run(blockIdx.x, nbm * nbn);
     const int band = t / (HIGH * nbn);
@@ -143,10 +156,11 @@ fp8_tile_kernel(Fp8Args a, int nbm, int nbn, int splits)
             }
         }
     };
-    // A stage's loads are issued a few per step (below): all at once they would fill the address units' queue and hold up
-    // the waves' products behind them.
+    // A stage's loads are issued a few per step (below): all at once they would fill the address units' queue
+    // and hold up the waves' products behind them.
     constexpr int PER_STEP = (LPW + 1 + TM * TN - 1) / (TM * TN);
-    constexpr int EARLY = TM * PER_STEP < LPW + 1 ? TM * PER_STEP : LPW + 1;  // those in the last row of the stage before
+    // those in the last row of the stage before
+    constexpr int EARLY = TM * PER_STEP < LPW + 1 ? TM * PER_STEP : LPW + 1;
 
     f32x4 acc[TN][TM];
 #pragma unroll
@@ -154,7 +168,8 @@ fp8_tile_kernel(Fp8Args a, int nbm, int nbn, int splits)
 #pragma unroll
         for (int j = 0; j < TM; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    // this wave's weight rows within a matrix, and the scale row they share (a wave's rows lie in one block of 128)
+    // this wave's weight rows within a matrix, and the scale row they share (a wave's rows lie in one block of
+    // 128)
     const int wr0 = wn * (TNM * 16);
     const float* swp[NM];
 #pragma unroll
@@ -198,7 +213,8 @@ fp8_tile_kernel(Fp8Args a, int nbm, int nbn, int splits)
 #pragma unroll
         for (int j = 0; j < TM; ++j) sx[j] = src[16 * j + i16];
     };
-    // past K in the last K-block: zeros for x, so that what was read there instead, of the same rows, adds nothing
+    // past K in the last K-block: zeros for x, so that what was read there instead, of the same rows, adds
+    // nothing
     auto clear = [&](int s, raw4_t (&b)[2]) __attribute__((always_inline)) {
         const bool in0 = (kb0 + s) * kGroup + 16 * q < a.K, in1 = (kb0 + s) * kGroup + 64 + 16 * q < a.K;
 #pragma unroll
@@ -213,9 +229,9 @@ fp8_tile_kernel(Fp8Args a, int nbm, int nbn, int splits)
         read_first(0);
     }
 
-    // One stage.  Its first operands are in registers already, but for the wide form, which has none left for that and
-    // reads them here.  No branch in it: the compiler would carry the sums past one, in
-    // ever more registers.
+    // One stage.  Its first operands are in registers already, but for the wide form, which has none left for
+    // that and reads them here.  No branch in it: the compiler would carry the sums past one, in ever more
+    // registers.
     auto stage = [&](int s, int buf, auto last) __attribute__((always_inline)) {
         constexpr bool LAST = decltype(last)::value;
         const int next = buf + 1 == STAGES ? 0 : buf + 1, before = buf == 0 ? STAGES - 1 : buf - 1;
@@ -230,8 +246,9 @@ fp8_tile_kernel(Fp8Args a, int nbm, int nbn, int splits)
 #pragma unroll
             for (int j = 0; j < TM; ++j) sc[m][j] = sx[j] * sw;
         }
-        // One step is one 16 x 16 product, in a fixed order: the sums of the product LAG steps before it, which is done by
-        // now, free the registers that this one takes, and the operands of a step to come are fetched behind it.
+        // One step is one 16 x 16 product, in a fixed order: the sums of the product LAG steps before it, which
+        // is done by now, free the registers that this one takes, and the operands of a step to come are
+        // fetched behind it.
         constexpr int LAG = WIDE ? 1 : TM;
         Operand aw, bw[TM];
         f32x4 p[LAG + (WIDE ? 1 : 0)];
@@ -257,8 +274,9 @@ fp8_tile_kernel(Fp8Args a, int nbm, int nbn, int splits)
                 if (WIDE && step >= LAG) add(step - LAG);
                 if (j == 0 && i + AHEAD < TN) read_w(buf, i + AHEAD, w[(i + AHEAD) % SLOTS]);
                 if (!LAST && i == TN - 2 && j == TM - 1) {
-                    // The stage's last operands are in registers, the next stage is in LDS: with a row of products in
-                    // hand the waves meet, begin to refill this buffer and fetch the next stage's first operands.
+                    // The stage's last operands are in registers, the next stage is in LDS: with a row of
+                    // products in hand the waves meet, begin to refill this buffer and fetch the next stage's
+                    // first operands.
                     wait_vm<(STAGES - 2) * (LPW + 1)>();  // all but those after stage s + 1
                     meet();
                 }
@@ -295,8 +313,8 @@ fp8_tile_kernel(Fp8Args a, int nbm, int nbn, int splits)
             for (int j = 0; j < TM; ++j) {
                 const int row = mrow + 16 * j;
                 if (row < a.M && n < a.N) {
-                    store_values4(a.part, GLU_DTYPE_FP32, ((int64_t)(split * NM + m) * a.M + row) * a.N + n, acc[i][j],
-                                  a.N - n);
+                    const int64_t at = ((int64_t)(split * NM + m) * a.M + row) * a.N + n;
+                    store_values4(a.part, GLU_DTYPE_FP32, at, acc[i][j], a.N - n);
                 }
             }
         }

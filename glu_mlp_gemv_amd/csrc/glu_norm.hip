@@ -158,9 +158,9 @@ norm_long_kernel(NormArgs a)
 //
 //   xhat = h r,  a = dy w,  dx = r (a - xhat mean(a xhat)) + dres,  dw = sum over rows of dy xhat
 //
-// One pass: a team of waves walks a run of rows, keeps w and its columns' dw in registers and loads
-// the next row while the current one's mean is being reduced.  dw's partial sums, one per team, are joined in
-// team order by a second kernel, so the result does not change from run to run.  K past a team's registers walks column
+// One pass: a team of waves walks a run of rows, keeps w and its columns' dw in registers and loads the next
+// row while the current one's mean is being reduced.  dw's partial sums, one per team, are joined in team order
+// by a second kernel, so the result does not change from run to run.  K past a team's registers walks column
 // slices in a first pass for the mean.
 
 namespace {
@@ -326,8 +326,8 @@ norm_grad_long_dw_kernel(NormGradArgs a, int teams)
     store_chunk(reinterpret_cast<Fp32*>(a.part) + (int64_t)team * a.K + 8 * (int64_t)c, narrow8<Fp32>(dw), n);
 }
 
-// dw[k] = T(sum of the teams' partials, lanes of a column striding the teams, then a tree over the lanes); no teams: +0.
-// 32 columns (a 128-byte line of a partial) x 32 lanes per column.
+// dw[k] = T(sum of the teams' partials, lanes of a column striding the teams, then a tree over the lanes); no
+// teams: +0. 32 columns (a 128-byte line of a partial) x 32 lanes per column.
 template <class T>
 __global__ void __launch_bounds__(1024)
 norm_grad_dw_kernel(const float* __restrict__ part, void* dw, int K, int teams)
@@ -365,10 +365,10 @@ namespace {
 constexpr int kNormRows = 1 << 21;  // rows per launch: a grid holds fewer than 2^32 threads
 constexpr int kNormMaxK = 64 * kNormMaxWaves * kNormMaxChunks * 8;  // a row in one workgroup's registers
 
-// Waves per row and chunks per lane.  One chunk while the rows are too few to fill the card (a row then takes the
-// fewest serial steps) and for 4-byte types; else two, which leaves fewer waves per barrier.  8192 x 5120 bf16
-// with residual to e4m3: 59.4 us (4.96 TB/s; a copy reaches 5.2) with two, 65.7 with one, 69.3 with four; 8192 x 8192 fp32: 203 us
-// with one, 219 with two.
+// Waves per row and chunks per lane.  One chunk while the rows are too few to fill the card (a row then takes
+// the fewest serial steps) and for 4-byte types; else two, which leaves fewer waves per barrier.  8192 x 5120
+// bf16 with residual to e4m3: 59.4 us (4.96 TB/s; a copy reaches 5.2) with two, 65.7 with one, 69.3 with four;
+// 8192 x 8192 fp32: 203 us with one, 219 with two.
 struct RowShape {
     int wpr, chunks;
 };
@@ -416,7 +416,8 @@ hipError_t norm_grad_launch_t(int dtype, const NormGradArgs& a, hipStream_t s)
         if (a.K > grad_max_k(dtype)) {
             for (int64_t row = 0; row < a.M; row += kNormRows) {
                 const int rows = (int)(a.M - row < kNormRows ? a.M - row : kNormRows);
-                hipLaunchKernelGGL((norm_grad_long_kernel<T>), dim3(rows), dim3(64 * kNormMaxWaves), 0, s, a, (int)row);
+                hipLaunchKernelGGL((norm_grad_long_kernel<T>), dim3(rows), dim3(64 * kNormMaxWaves), 0, s, a,
+                                   (int)row);
             }
             const int chunks = (a.K + 7) / 8;
             hipLaunchKernelGGL((norm_grad_long_dw_kernel<T>), dim3((chunks + 255) / 256, teams), dim3(256), 0, s, a,
@@ -450,7 +451,8 @@ int norm_grad_teams(int dtype, int M, int K)
     if (M < 1) return 0;
     if (M == 1) return 1;
     if (K > grad_max_k(dtype)) return M < 64 ? M : 64;
-    // 16 waves per CU, all resident at once: at 16384 x 4096 118.5 us, against 132 at half and 119 at twice as many
+    // 16 waves per CU, all resident at once: at 16384 x 4096 118.5 us, against 132 at half and 119 at twice as
+    // many
     const int target = 4096 / grad_shape(K).wpr;
     return M < target ? M : target;
 }

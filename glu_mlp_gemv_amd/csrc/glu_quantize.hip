@@ -5,7 +5,8 @@
 //   s = max(amax |v| / 448, 2^-126)      q = e4m3(v / s)
 //
 // One pass, bound by memory: a lane holds chunks of 8 values, 16 lanes one group of
-// 128 columns, whose maximum is a DPP reduction.
+// 128 columns, whose maximum is a DPP reduction.  Measured: a weight of 17408 x 5120 bf16 in 52 us, 5.1 TB/s (a
+// copy of 1 GiB reaches 5.2); 77 rows of 4096 in 2.8 us, which is a launch.
 #include "../../include/glu_fp8.h"
 #include "glu_fp8_device.h"
 #include "glu_quantize.h"
@@ -177,13 +178,11 @@ hipError_t blocks_t(const void* w, int64_t ldw, uint8_t* q, int64_t ldq, float* 
 hipError_t quantize_rows_launch(int dtype, const void* x, int64_t ldx, uint8_t* q, int64_t ldq, float* scale,
                                 int64_t lds, int M, int K, hipStream_t stream)
 {
+    const auto run = [&](auto src) { return convert_rows<uint8_t>(src, q, ldq, scale, lds, M, K, stream); };
     switch (dtype) {
-    case GLU_DTYPE_BF16:
-        return convert_rows<uint8_t>(RowSource<Bf16>{static_cast<const Bf16*>(x), ldx}, q, ldq, scale, lds, M, K, stream);
-    case GLU_DTYPE_FP16:
-        return convert_rows<uint8_t>(RowSource<Fp16>{static_cast<const Fp16*>(x), ldx}, q, ldq, scale, lds, M, K, stream);
-    default:
-        return convert_rows<uint8_t>(RowSource<Fp32>{static_cast<const Fp32*>(x), ldx}, q, ldq, scale, lds, M, K, stream);
+    case GLU_DTYPE_BF16: return run(RowSource<Bf16>{static_cast<const Bf16*>(x), ldx});
+    case GLU_DTYPE_FP16: return run(RowSource<Fp16>{static_cast<const Fp16*>(x), ldx});
+    default: return run(RowSource<Fp32>{static_cast<const Fp32*>(x), ldx});
     }
 }
 

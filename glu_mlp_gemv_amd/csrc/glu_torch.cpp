@@ -1,8 +1,8 @@
-// The short way from torch tensors to the C ABI, for the calls of fp8.py in their usual form: every operand of the
-// expected type, shape and layout on the current device, outputs to be allocated, the current stream.  Checking,
-// allocating and calling take 2 to 3 us here against 8 in Python, which shows where a kernel takes 3 us.  Whatever
-// is not in that form returns None before anything is allocated, and fp8.py takes the call and says what is wrong.
-// A status other than GLU_OK is returned as an int.
+// The short way from torch tensors to the C ABI, for the calls of fp8.py in their usual form: every operand of
+// the expected type, shape and layout on the current device, outputs to be allocated, the current
+// stream.  Checking, allocating and calling take 2 to 3 us here against 8 in Python, which shows where a kernel
+// takes 3 us.  Whatever is not in that form returns None before anything is allocated, and fp8.py takes the call
+// and says what is wrong. A status other than GLU_OK is returned as an int.
 #include <Python.h>
 
 #include <stdint.h>
@@ -66,7 +66,10 @@ struct Place {
     {
         return at::empty_strided({n}, {1}, at::TensorOptions().dtype(t).device(device));
     }
-    at::Tensor workspace(int64_t bytes) const { return bytes ? empty(bytes / 4, c10::ScalarType::Float) : at::Tensor(); }
+    at::Tensor workspace(int64_t bytes) const
+    {
+        return bytes ? empty(bytes / 4, c10::ScalarType::Float) : at::Tensor();
+    }
 };
 
 // [rows, cols] of type t with contiguous rows that do not overlap; rows or cols < 0: any (returned)
@@ -224,14 +227,15 @@ PyObject* product(PyObject*, PyObject* const* a, Py_ssize_t n)
         if (!at.ok) Py_RETURN_NONE;
         const int mats = n == 7 ? 2 : 1;
         const long dt = PyLong_AsLong(a[0]);
-        const c10::ScalarType types[4] = {c10::ScalarType::BFloat16, c10::ScalarType::Half, c10::ScalarType::Float, kE4m3};
+        const c10::ScalarType types[4] = {c10::ScalarType::BFloat16, c10::ScalarType::Half, c10::ScalarType::Float,
+                                          kE4m3};
         if (dt < 0 || dt > 3) Py_RETURN_NONE;
         const Rows x(a[1], at, -1, -1, kE4m3);
         if (!x.ok || !THPVariable_Check(a[2])) Py_RETURN_NONE;
         const at::Tensor& sx = THPVariable_Unpack(a[2]);
         const int64_t M = x.rows, K = x.cols, G = groups(K);
-        if (sx.layout() != c10::kStrided || sx.dim() != 2 || sx.device() != at.device || sx.scalar_type() != c10::ScalarType::Float || sx.size(0) != M ||
-            sx.size(1) != G) {
+        if (sx.layout() != c10::kStrided || sx.dim() != 2 || sx.device() != at.device ||
+            sx.scalar_type() != c10::ScalarType::Float || sx.size(0) != M || sx.size(1) != G) {
             Py_RETURN_NONE;
         }
         const glu_fp8_matrix xm{(const uint8_t*)x.p, (const float*)sx.data_ptr(), x.ld, sx.stride(0), sx.stride(1)};

@@ -1,9 +1,10 @@
 """Python face of include/glu_fp8.h: RMS norm, conversion to block-scaled e4m3, products on it.
 
 As in ``api``, only argument marshalling happens here: tensors are checked, their device pointers
-and torch's current HIP stream go to ``libglu_gemv.so``, and a non-OK status becomes a ``GluError``.  Calls that
-give no outputs, plan or stream try the extension module ``_fast`` first (csrc/glu_torch.cpp): it does the same for operands in
-the usual form, in a third of the time, and leaves the rest, refusals among them, to the code here.
+and torch's current HIP stream go to ``libglu_gemv.so``, and a non-OK status becomes a ``GluError``.  Calls
+that give no outputs, plan or stream try the extension module ``_fast`` first (csrc/glu_torch.cpp): it does the
+same for operands in the usual form, in a third of the time, and leaves the rest, refusals among them, to the
+code here.
 
 Block-scaled e4m3: a stored ``torch.float8_e4m3fn`` value q stands for ``q * scale``.  Activations
 [M, K] have an fp32 scale per row and 128 columns, [M, ceil(K / 128)], which the functions here return stored
