@@ -11,6 +11,7 @@ norm.  Only argument marshalling happens here.
 from typing import Optional
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import api, fp8
 
@@ -44,7 +45,9 @@ class AddRmsNorm(torch.autograd.Function):
         ctx.set_materialize_grads(False)
         return y if residual is None else (y, h)
 
+    # a gradient of the gradient would pass the library's calls by in silence: once_differentiable refuses it
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dh=None):
         h, weight, rstd = ctx.saved_tensors
         if dy is None:  # only the residual stream was used
@@ -56,6 +59,6 @@ class AddRmsNorm(torch.autograd.Function):
 
 
 def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: Optional[torch.Tensor] = None):
-    """(y, h) of fp8.add_rms_norm, differentiable in x, weight and residual."""
+    """(y, h) of fp8.add_rms_norm, differentiable (once) in x, weight and residual."""
     out = AddRmsNorm.apply(x, weight, eps, residual)
     return (out, x) if residual is None else out

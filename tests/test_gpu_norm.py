@@ -125,6 +125,17 @@ def test_autograd_forms():
     assert torch.equal(x.grad, torch.ones_like(x)) and torch.equal(r.grad, torch.ones_like(x)) and w.grad is None
 
 
+def test_gradient_of_the_gradient_is_refused():
+    from glu_mlp_gemv_amd.autograd import rms_norm
+    x, r = tensors(5, 256, torch.float32, 6, 1.0, 1.0)
+    w = weight(256, torch.float32, 6)
+    x.requires_grad_()
+    y, _ = rms_norm(x, w, EPS, residual=r)
+    dx, = torch.autograd.grad(y.square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        dx.square().sum().backward()
+
+
 @pytest.mark.parametrize("kind", ["bf16", "fp32"])
 def test_strides_and_alignment(kind):
     """Row-strided views that start at odd elements, and outputs into such views: what lies between is untouched."""
