@@ -8,7 +8,12 @@
 // diagonal are the products wanted.  That gives 4 times the workgroups, each reading 4 times as far along a row,
 // for x of up to 4 rows: at one row 8.1 us against 8.9 (K = 9216 N = 2560), dual 35.0 against 37.4 (K = 5120 N
 // = 17408, 178 MB); at 8 rows, which 8 weight rows would serve, 16 is the faster (12.8 against 14.7 us at K =
-// 12288 N = 4096).  The waves' sums meet in LDS in wave order.  The products run on the bf16 unit, whose sums are
+// 12288 N = 4096).  The pair of matrices, read past the caches' keeping, takes whole 128-byte lines per load for
+// it: dual K = 5120 N = 17408 32.3 -> 29.2 us, K = 2560 N = 9216 11.6 -> 11.0 (weights from memory; 11.0 either way
+// where they stay in the last-level cache).  One matrix keeps half lines, cached: K = 17408 N = 5120 18.6 us
+// against 18.0, but 16.8 against 17.6 from the last-level cache.  Longer-lived workgroups that keep x in registers and
+// load one run of rows ahead were slower (one row, K = 9216 N = 2560: 9.6 us).  The waves' sums meet in LDS in
+// wave order.  The products run on the bf16 unit, whose sums are
 // fp32 (glu_fp8_mfma.h).
 #include "glu_fp8_mfma.h"
 
@@ -21,15 +26,23 @@ constexpr int kStreamMaxWaves = 8;
 // Layout of the rows: whole K-blocks in whole instructions; chunks of 16 bytes; or any bytes
 enum { kWhole, kChunks, kBytes };
 
-template <int MODE>
+template <bool ONCE>
+__device__ __forceinline__ raw4_t read16(const uint8_t* p)
+{
+    if constexpr (ONCE) return __builtin_nontemporal_load(reinterpret_cast<const raw4_t*>(p));
+    else return *reinterpret_cast<const raw4_t*>(p);
+}
+
+// ONCE: data that nothing reads again
+template <int MODE, bool ONCE>
 __device__ __forceinline__ raw4_t chunk16(const uint8_t* row, int64_t off, int K)
 {
     if constexpr (MODE == kWhole) {
-        return *reinterpret_cast<const raw4_t*>(row + off);
+        return read16<ONCE>(row + off);
     } else if constexpr (MODE == kChunks) {
         // K is a multiple of 16: the chunk is inside or outside as a whole; outside it is read at 0 and dropped
         const bool in = off < K;
-        const raw4_t v = *reinterpret_cast<const raw4_t*>(row + (in ? off : 0));
+        const raw4_t v = read16<ONCE>(row + (in ? off : 0));
         return in ? v : raw4_t{0u, 0u, 0u, 0u};
     } else {
         if (off + 16 <= K) return *reinterpret_cast<const u32x4_any*>(row + off);
@@ -54,7 +67,11 @@ fp8_stream_kernel(Fp8Args a, int waves, int splits, int nbn, int m_base)
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int i16 = lane & 15, q = lane >> 4;
-    const int sel = i16 / R;  // this lane's K-block within the instruction (both operands)
+    // LINES: the two 16-byte chunks of a lane are of K-blocks sel / 2 and sel / 2 + 2, at half sel % 2, so that 8
+    // neighbouring lanes load a whole 128-byte line; each chunk has its own product and scale then
+    constexpr bool LINES = NM == 2 && R == 4;
+    constexpr int SC = LINES ? 2 : 1;  // scales per step and operand
+    const int sel = i16 / R;  // this lane's place on the diagonal (both operands): a K-block, or half of two
     const int mb = blockIdx.x / nbn;
     const int n0 = (blockIdx.x - mb * nbn) * R;
     const int m0 = m_base + mb * 16;
@@ -77,29 +94,50 @@ fp8_stream_kernel(Fp8Args a, int waves, int splits, int nbn, int m_base)
 #pragma unroll
     for (int m = 0; m < NM; ++m) acc[m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     raw4_t wv[U][NM][2], xv[U][2];
-    float sc[U][NM + 1];
+    float sc[U][NM + 1][SC];
     auto load = [&](int u, int s) __attribute__((always_inline)) {
-        const int kb = S * s + sel;
-        const int64_t off = (int64_t)kb * kGroup + 16 * q;
-        const int kbs = min(kb, KB - 1);
+        const int kb = S * s + (LINES ? sel >> 1 : sel);
+        const int64_t off = (int64_t)kb * kGroup + 16 * q + (LINES ? 64 * (sel & 1) : 0);
+        constexpr int APART = LINES ? 2 * kGroup : 64;
 #pragma unroll
         for (int m = 0; m < NM; ++m) {
-            wv[u][m][0] = chunk16<MODE>(wr[m], off, a.K);
-            wv[u][m][1] = chunk16<MODE>(wr[m], off + 64, a.K);
-            sc[u][m] = ws[m][kbs];
+            wv[u][m][0] = chunk16<MODE, LINES>(wr[m], off, a.K);
+            wv[u][m][1] = chunk16<MODE, LINES>(wr[m], off + APART, a.K);
         }
-        xv[u][0] = chunk16<MODE>(xr, off, a.K);
-        xv[u][1] = chunk16<MODE>(xr, off + 64, a.K);
-        sc[u][NM] = xs[kbs * a.sxg];
+        xv[u][0] = chunk16<MODE, false>(xr, off, a.K);
+        xv[u][1] = chunk16<MODE, false>(xr, off + APART, a.K);
+#pragma unroll
+        for (int c = 0; c < SC; ++c) {
+            const int kbs = min(kb + 2 * c, KB - 1);
+#pragma unroll
+            for (int m = 0; m < NM; ++m) sc[u][m][c] = ws[m][kbs];
+            sc[u][NM][c] = xs[kbs * a.sxg];
+        }
     };
     auto use = [&](int u) __attribute__((always_inline)) {
         const Wide x = widen32(xv[u][0], xv[u][1]);
 #pragma unroll
         for (int m = 0; m < NM; ++m) {
-            const f32x4 p = mfma_wide(widen32(wv[u][m][0], wv[u][m][1]), x);
-            const float c = sc[u][m] * sc[u][NM];
+            const Wide w = widen32(wv[u][m][0], wv[u][m][1]);
+            if constexpr (LINES) {
+                f32x4 p[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[m][e] = fmaf(p[e], c, acc[m][e]);
+                for (int i = 0; i < 4; ++i) {  // the two products' instructions in turn
+                    const int c = i & 1, v = 2 * c + (i >> 1);
+                    p[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.v[v], x.v[v], p[c], 0, 0, 0);
+                }
+#pragma unroll
+                for (int c = 0; c < SC; ++c) {
+                    const float scale = sc[u][m][c] * sc[u][NM][c];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[m][e] = fmaf(p[c][e], scale, acc[m][e]);
+                }
+            } else {
+                const f32x4 p = mfma_wide(w, x);
+                const float scale = sc[u][m][0] * sc[u][NM][0];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[m][e] = fmaf(p[e], scale, acc[m][e]);
+            }
         }
     };
     // a ring of U steps: one is refilled as soon as it is used, so that U - 1 remain in flight

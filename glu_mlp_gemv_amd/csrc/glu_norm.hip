@@ -337,16 +337,14 @@ norm_grad_dw_kernel(const float* __restrict__ part, void* dw, int K, int teams)
     const int k = blockIdx.x * 32 + col;
     float s = 0.0f;
     if (k < K) {
-        const float* p = part + (int64_t)ln * K + k;
-        int t = ln;
-        for (; t + 7 * 32 < teams; t += 8 * 32, p += (int64_t)(8 * 32) * K) {  // 8 loads in flight
+        // 8 loads in flight, those past the last team of the last team's value, which is not added
+        for (int t = ln; t < teams; t += 8 * 32) {
             float v[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = p[(int64_t)(32 * i) * K];
+            for (int i = 0; i < 8; ++i) v[i] = part[(int64_t)min(t + 32 * i, teams - 1) * K + k];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) s += v[i];
+            for (int i = 0; i < 8; ++i) s += t + 32 * i < teams ? v[i] : 0.0f;
         }
-        for (; t < teams; t += 32, p += (int64_t)32 * K) s += *p;
     }
     red[ln][col] = s;
     __syncthreads();
