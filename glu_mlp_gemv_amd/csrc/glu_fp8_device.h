@@ -40,14 +40,16 @@ template <> __device__ __forceinline__ Fp32 narrow<Fp32>(float f) { return Fp32{
 // A chunk: 8 consecutive elements of a row, as stored.
 template <class T> struct Chunk { T e[8]; };
 
-// The chunk at p, of which the first n (>= 1) elements exist; the others read as +0.
-template <class T>
+// The chunk at p, of which the first n (>= 1) elements exist; the others read as +0.  ONCE: whole chunks of 2-byte
+// types are not kept in the caches (a 4-byte type's two halves would each fetch the line).
+template <bool ONCE = false, class T>
 __device__ __forceinline__ Chunk<T> load_chunk(const T* p, int n)
 {
     Chunk<T> c;
     if (n >= 8) {
         if constexpr (sizeof(T) == 2) {
-            const raw4_t v = *reinterpret_cast<const u32x4_any*>(p);
+            const u32x4_any* p4 = reinterpret_cast<const u32x4_any*>(p);
+            const raw4_t v = ONCE ? (raw4_t)__builtin_nontemporal_load(p4) : (raw4_t)*p4;
             __builtin_memcpy(&c, &v, 16);
         } else {
             const raw4_t a = reinterpret_cast<const u32x4_any*>(p)[0];

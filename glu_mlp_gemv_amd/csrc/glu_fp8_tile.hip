@@ -38,12 +38,13 @@ const TileShape kTileShapes[kTileShapeCount] = {
 
 namespace {
 
-// 16 bytes per lane from base + off into LDS at lds_base + 16 lane
+// 16 bytes per lane from base + off into LDS at lds_base + 16 lane; ONCE: not kept in the caches
+template <bool ONCE>
 __device__ __forceinline__ void lds_load16(const uint8_t* base, uint32_t off, uint8_t* lds)
 {
     __builtin_amdgcn_global_load_lds(
         (const __attribute__((address_space(1))) void*)(base + off),
-        (__attribute__((address_space(3))) void*)lds, 16, 0, 0);
+        (__attribute__((address_space(3))) void*)lds, 16, 0, ONCE ? 2 : 0);
 }
 
 struct Narrow { raw4_t c0, c1; };
@@ -75,8 +76,8 @@ __device__ __forceinline__ void wait_vm()
 
 // WIDE: products on the bf16 unit, for outputs that show more than the 8-bit unit's sums hold: e4m3, whose fp32
 // scales are the largest sums themselves, and fp32.  E4M3: the kernel converts by itself (a workgroup holds
-// whole groups).
-template <int NM, int TM, int TN, int WM, int WN, int STAGES, bool WIDE, bool E4M3>
+// whole groups).  ONCE: the weights are not kept in the caches.
+template <int NM, int TM, int TN, int WM, int WN, int STAGES, bool WIDE, bool E4M3, bool ONCE>
 __global__ void __launch_bounds__(64 * WM * WN)
 fp8_tile_kernel(Fp8Args a, int nbm, int nbn, int splits)
 {
@@ -147,7 +148,9 @@ fp8_tile_kernel(Fp8Args a, int nbm, int nbn, int splits)
             if (i < LPW) {
                 const int b = i < XPW ? 0 : 1 + (i - XPW) / ((LPW - XPW) / NM);
                 const int r8 = i < XPW ? i * WAVES + wave : BM / 8 + (i - XPW) * WAVES + wave;
-                lds_load16(base[b] + (int64_t)kb * kGroup, off[i] - back, st + r8 * 1024);
+                const uint8_t* from = base[b] + (int64_t)kb * kGroup;
+                if (i < XPW) lds_load16<false>(from, off[i] - back, st + r8 * 1024);
+                else lds_load16<ONCE>(from, off[i] - back, st + r8 * 1024);
             } else if (i == LPW) {
                 __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(sxp + kb * a.sxg),
                                                  (__attribute__((address_space(3))) void*)(st + (BM + BR) * kGroup +
@@ -403,27 +406,39 @@ namespace {
 
 using TileFn = void (*)(Fp8Args, int, int, int);
 
-template <int NM, bool WIDE, bool E4M3>
-TileFn pick_tile(int shape)
+template <int NM, bool WIDE, bool E4M3, bool ONCE>
+TileFn pick_small(int shape)
 {
     // a pair's 128 weight rows are 64 columns: no whole group
     constexpr bool HALF = E4M3 && NM == 2;
     switch (shape) {
-    case 0: return fp8_tile_kernel<NM, 4, 8, 4, 2, 2, WIDE, E4M3>;
-    case 1: return fp8_tile_kernel<NM, 4, 4, 2, 4, 3, WIDE, E4M3>;
-    case 2: return fp8_tile_kernel<NM, 4, 4, 1, 4, 3, WIDE, E4M3>;
-    case 3: return HALF ? nullptr : fp8_tile_kernel<NM, 4, 2, 1, 4, 4, WIDE, E4M3 && !HALF>;
-    case 4: return HALF ? nullptr : fp8_tile_kernel<NM, 2, 2, 1, 4, 4, WIDE, E4M3 && !HALF>;
+    case 2: return fp8_tile_kernel<NM, 4, 4, 1, 4, 3, WIDE, E4M3, ONCE>;
+    case 3: return HALF ? nullptr : fp8_tile_kernel<NM, 4, 2, 1, 4, 4, WIDE, E4M3 && !HALF, ONCE>;
+    case 4: return HALF ? nullptr : fp8_tile_kernel<NM, 2, 2, 1, 4, 4, WIDE, E4M3 && !HALF, ONCE>;
     }
     return nullptr;
 }
 
-template <int NM>
-TileFn pick_tile(int shape, bool wide, bool e4m3)
+template <int NM, bool WIDE, bool E4M3>
+TileFn pick_tile(int shape, bool once)
 {
-    if (e4m3) return pick_tile<NM, true, true>(shape);
-    return wide ? pick_tile<NM, true, false>(shape) : pick_tile<NM, false, false>(shape);
+    if (shape == 0) return fp8_tile_kernel<NM, 4, 8, 4, 2, 2, WIDE, E4M3, false>;
+    if (shape == 1) return fp8_tile_kernel<NM, 4, 4, 2, 4, 3, WIDE, E4M3, false>;
+    return once ? pick_small<NM, WIDE, E4M3, true>(shape) : pick_small<NM, WIDE, E4M3, false>(shape);
 }
+
+template <int NM>
+TileFn pick_tile(int shape, bool wide, bool e4m3, bool once)
+{
+    if (e4m3) return pick_tile<NM, true, true>(shape, once);
+    return wide ? pick_tile<NM, true, false>(shape, once) : pick_tile<NM, false, false>(shape, once);
+}
+
+// Weights that one row of tiles reads once, and that are too many for the last-level cache (256 MB, which
+// everything between two calls passes through) to hold until the next call, are not kept in the caches: dual M = 37
+// K = 4096 N = 12288 24.0 -> 22.3 us, M = 48 K = 5120 N = 17408 47.2 -> 44.8.  Where they would have stayed it costs:
+// dual M = 64 K = 2560 N = 9216 to e4m3 22.9 -> 25.4.
+constexpr int64_t kOnceBytes = 64 << 20;
 
 size_t tile_lds(int shape)
 {
@@ -439,7 +454,8 @@ hipError_t fp8_tile_launch(int mats, const TileConfig& c, const Fp8Args& a, hipS
 {
     const TileShape& t = kTileShapes[c.shape];
     const bool e4m3 = a.out_dtype == GLU_DTYPE_E4M3;
-    const TileFn f = mats == 1 ? pick_tile<1>(c.shape, c.wide, e4m3) : pick_tile<2>(c.shape, c.wide, e4m3);
+    const bool once = a.M <= t.bm && (int64_t)mats * a.N * a.K > kOnceBytes;
+    const TileFn f = mats == 1 ? pick_tile<1>(c.shape, c.wide, e4m3, once) : pick_tile<2>(c.shape, c.wide, e4m3, once);
     if (!f) return hipErrorInvalidValue;
     const size_t lds = tile_lds(c.shape);
     hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(f), hipFuncAttributeMaxDynamicSharedMemorySize,

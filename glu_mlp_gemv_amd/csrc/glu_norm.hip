@@ -172,7 +172,7 @@ struct GradRow {
 
 }  // namespace
 
-template <class T, int C, int WAVES>
+template <class T, int C, int WAVES, bool ONCE>
 __global__ void __launch_bounds__(64 * WAVES)
 norm_grad_kernel(NormGradArgs a, int wpr, int teams_per_wg, int teams)
 {
@@ -202,9 +202,9 @@ norm_grad_kernel(NormGradArgs a, int wpr, int teams_per_wg, int teams)
             const int c = lane + 64 * (wave + wpr * i);
             const int n = a.K - 8 * c;
             if (n > 0) {
-                g[i].h = load_chunk(static_cast<const T*>(a.h) + row * a.ldh + 8 * c, n);
-                g[i].dy = load_chunk(static_cast<const T*>(a.dy) + row * a.lddy + 8 * c, n);
-                if (a.dres) g[i].dr = load_chunk(static_cast<const T*>(a.dres) + row * a.lddr + 8 * c, n);
+                g[i].h = load_chunk<ONCE>(static_cast<const T*>(a.h) + row * a.ldh + 8 * c, n);
+                g[i].dy = load_chunk<ONCE>(static_cast<const T*>(a.dy) + row * a.lddy + 8 * c, n);
+                if (a.dres) g[i].dr = load_chunk<ONCE>(static_cast<const T*>(a.dres) + row * a.lddr + 8 * c, n);
             } else {
                 g[i] = GradRow<T>{};
             }
@@ -388,6 +388,19 @@ RowShape grad_shape(int K)
     return need <= kNormMaxWaves ? RowShape{need, 1} : RowShape{(need + 1) / 2, 2};
 }
 
+// What the backward reads is dropped from the caches where they could not hold it for the next reader anyway: 16384
+// x 4096 bf16 (403 MB) 117.7 -> 109.6 us; where they hold it that costs: 2048 x 4096 19.7 -> 22.3.
+constexpr int64_t kLastLevelCache = 256 << 20;
+using GradFn = void (*)(NormGradArgs, int, int, int);
+template <class T, int C, int WAVES>
+GradFn grad_kernel(bool once)
+{
+    if constexpr (sizeof(T) == 2) {
+        if (once) return norm_grad_kernel<T, C, WAVES, true>;
+    }
+    return norm_grad_kernel<T, C, WAVES, false>;
+}
+
 template <class T, bool E4M3>
 hipError_t norm_launch_t(const NormArgs& a, hipStream_t s)
 {
@@ -424,14 +437,16 @@ hipError_t norm_grad_launch_t(int dtype, const NormGradArgs& a, hipStream_t s)
             const RowShape p = grad_shape(a.K);
             const int tpw = p.wpr == 1 ? 4 : 1;
             const dim3 grid((teams + tpw - 1) / tpw), block(64 * p.wpr * tpw);
+            const bool once = sizeof(T) == 2 && (int64_t)a.M * a.K * 2 * (a.dres ? 3 : 2) > kLastLevelCache;
+            const auto run = [&](auto kernel) {
+                hipLaunchKernelGGL(kernel, grid, block, 0, s, a, p.wpr, tpw, teams);
+            };
             if (p.chunks == 2) {
-                if constexpr (sizeof(T) == 2) {
-                    hipLaunchKernelGGL((norm_grad_kernel<T, 2, 16>), grid, block, 0, s, a, p.wpr, tpw, teams);
-                }
+                if constexpr (sizeof(T) == 2) run(grad_kernel<T, 2, 16>(once));
             } else if (p.wpr > 8) {
-                hipLaunchKernelGGL((norm_grad_kernel<T, 1, 16>), grid, block, 0, s, a, p.wpr, tpw, teams);
+                run(grad_kernel<T, 1, 16>(once));
             } else {
-                hipLaunchKernelGGL((norm_grad_kernel<T, 1, 8>), grid, block, 0, s, a, p.wpr, tpw, teams);
+                run(grad_kernel<T, 1, 8>(once));
             }
             if (teams == 1) return hipGetLastError();
         }

@@ -219,6 +219,20 @@ def test_every_launch_shape(kernel, tile, width, splits, M, N, K, mats):
 
 
 @pytest.mark.parametrize("mats", [1, 2])
+@pytest.mark.parametrize("tile", [2, 3, 4])
+def test_weights_past_the_cache(tile, mats):
+    """More than 64 MiB of weights under one row of tiles, which are then read past the caches."""
+    M, N, K = 20, 8210 // mats, 8208
+    ops = operands(M, N, K, tile, mats)
+    strict, loose = expected(ops), expected(ops, True)
+    for kind in ("bf16", "fp32", "e4m3"):
+        print(f"[past the cache] mats={mats} tile={tile} {kind}", flush=True)
+        got = run(ops, T[kind], plan=fp8.ProductPlan(3, tile, 0, 1))
+        torch.cuda.synchronize()
+        check(kind, got, *(loose if kind == "bf16" else strict))
+
+
+@pytest.mark.parametrize("mats", [1, 2])
 @pytest.mark.parametrize("tile,splits,columns", [(0, 1, 256), (1, 2, 128), (4, 1, 384)])
 def test_columns_in_two_launches(tile, splits, columns, mats):
     """The first columns by one shape, the others by their own: into strided outputs, with the scales of both."""

@@ -70,6 +70,22 @@ def test_backward(M, K, residual, kind):
     assert torch.equal(gx, gx2) and torch.equal(gw, gw2), "a second call gives the same bits"
 
 
+@pytest.mark.parametrize("M,K,residual", [(16390, 4099, False), (11000, 4099, True), (8300, 8200, False)])
+def test_backward_past_the_cache(M, K, residual):
+    """More than the last-level cache holds, which is then read past it."""
+    t = torch.bfloat16
+    print(f"[norm grad] M={M} K={K} residual={residual}", flush=True)
+    h, dy, dr = tensors(M, K, t, M + K, 3.0, 0.1, 0.1)
+    w = weight(K, t, K)
+    rstd = torch.rsqrt(h.double().square().mean(1) + EPS).float()
+    dres = dr if residual else None
+    dx, edx, dw, edw = ref.grad64(dy, h, w, rstd, dres)
+    gx, gw = glu.add_rms_norm_backward(dy, h, w, rstd, dresidual=dres)
+    torch.cuda.synchronize()
+    ref.check_store("dx", gx, dx, edx)
+    ref.check_store("dweight", gw, dw, edw)
+
+
 def test_gradient_against_differences():
     """The backward's formula against central differences of the 64-bit definition, and the kernels'
     gradient through autograd against the same differences."""
