@@ -71,7 +71,7 @@ def build_binding(verbose: bool = False) -> str:
            *[f for p in cpp_extension.include_paths() for f in ("-isystem", p)], "-isystem",
            os.path.join(os.path.dirname(os.path.dirname(HIPCC)), "include"), "-I" + sysconfig.get_paths()["include"],
            os.path.join(CSRC, "glu_torch.cpp"), "-o", tmp, "-L" + cpp_extension.TORCH_LIB_PATH, "-lc10", "-lc10_hip",
-           "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath," + cpp_extension.TORCH_LIB_PATH]
+           "-ltorch_cpu", "-ltorch_hip", "-ltorch_python", "-Wl,-rpath," + cpp_extension.TORCH_LIB_PATH]
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
