@@ -69,6 +69,7 @@ EXPORTED_SYMBOLS = (
     "glu_fp8_dual_glu",
     "glu_fp8_product_plan",
     "glu_fp8_workspace",
+    "glu_fp8_copy_workspace",
     "glu_fp8_product_tuned",
     "glu_fp8_product_workspace",
 )

@@ -222,7 +222,7 @@ glu_status check_sizes(int mats, int64_t M, int64_t N, int64_t K, int out_dtype)
     if (mats != 1 && mats != 2) return GLU_ERR_BAD_ARGUMENT;
     if (out_dtype < GLU_DTYPE_BF16 || out_dtype > GLU_DTYPE_E4M3) return GLU_ERR_BAD_ARGUMENT;
     if (bad_dim(M) || bad_dim(N) || bad_dim(K)) return GLU_ERR_BAD_SHAPE;
-    if (M > 0 && N > INT64_MAX / 64 / M) return GLU_ERR_BAD_SHAPE;
+    if (M > 0 && N > ((int64_t)1 << 50) / M) return GLU_ERR_BAD_SHAPE;  // bytes of any workspace fit 63 bits
     return GLU_OK;
 }
 
@@ -275,12 +275,12 @@ glu_status product_plan(int mats, int64_t M, int64_t N, int64_t K, int out_dtype
 }
 
 // One launch shape on checked operands: the product, and the join of its parts
-hipError_t run_product(int mats, const glu_fp8_plan& p, glu::Fp8Args a, int out_dtype, hipStream_t s)
+hipError_t run_product(int mats, const glu_fp8_plan& p, glu::Fp8Args a, int out_dtype, bool wide, hipStream_t s)
 {
     a.out_dtype = p.launches == 2 ? glu::kPartial : out_dtype;
     hipError_t e;
     if (p.kernel == GLU_FP8_KERNEL_TILE) {
-        e = glu::fp8_tile_launch(mats, glu::TileConfig{p.tile, p.splits, needs_wide(out_dtype)}, a, s);
+        e = glu::fp8_tile_launch(mats, glu::TileConfig{p.tile, p.splits, wide}, a, s);
     } else {
         const glu::StreamConfig c{p.tile, p.width, p.splits, p.kernel == GLU_FP8_KERNEL_ANY};
         e = glu::fp8_stream_launch(mats, c, a, s);
@@ -288,6 +288,19 @@ hipError_t run_product(int mats, const glu_fp8_plan& p, glu::Fp8Args a, int out_
     if (e != hipSuccess || p.launches == 1) return e;
     const glu::FinishArgs fin{a.part, a.out, a.scale, a.ldo, a.lds, a.M, a.N, p.splits, mats};
     return glu::finish_launch(out_dtype, fin, s);
+}
+
+// A layout that is not fast, above 16 rows: where the workspace has room for them the operands are copied to the
+// fast layout first, behind the product's own part of it: 2048 rows, K = 4100 N = 4096 in 95 us against 470 in
+// place, dual 4096 rows, K = 5125 N = 17408 in 1.29 ms against 21.  The copies run on the bf16 unit, as the kernel in
+// place does.
+int64_t padded(int64_t K) { return (K + 15) / 16 * 16; }
+
+glu_status copy_plan(int mats, int64_t M, int64_t N, int64_t K, int out_dtype, glu_fp8_plan* p, int64_t* bytes)
+{
+    const glu_status st = product_plan(mats, M, N, padded(K), out_dtype, true, nullptr, p);
+    *bytes = padded(p->workspace_bytes) + (M + mats * N) * padded(K);
+    return st;
 }
 
 glu_status product_call(const glu_fp8_matrix* x, const glu_fp8_matrix* w0, const glu_fp8_matrix* w1, int mats,
@@ -323,7 +336,16 @@ glu_status product_call(const glu_fp8_matrix* x, const glu_fp8_matrix* w0, const
         fast = fast && (bits & 15) == 0;
     }
     glu_fp8_plan p;
-    st = product_plan(mats, M, N, K, out_dtype, fast, asked, &p);
+    bool copied = false;
+    int64_t need = 0;
+    if (on && !fast && !asked && M > 16) {
+        st = copy_plan(mats, M, N, K, out_dtype, &p, &need);
+        copied = st == GLU_OK && ws && ((uintptr_t)ws & 15) == 0 && ws_bytes >= need;
+    }
+    if (!copied) {
+        st = product_plan(mats, M, N, K, out_dtype, fast, asked, &p);
+        need = p.workspace_bytes;
+    }
     if (st != GLU_OK) return st;
     const Array arrays[] = {
         {x->data, M * on, K, x->ld, 1, false},
@@ -334,13 +356,11 @@ glu_status product_call(const glu_fp8_matrix* x, const glu_fp8_matrix* w0, const
         {w1 ? w1->scale : nullptr, mats == 2 ? NB * on : 0, KB, w1 ? w1->scale_row : KB, 4, false},
         {out, M, N, ldo, type_size(out_dtype), true},
         {out_scale, e4m3 ? NB : 0, M, ld_scale, 4, true},
-        {ws, p.workspace_bytes && ws ? 1 : 0, p.workspace_bytes, p.workspace_bytes, 1, true},
+        {ws, need && ws ? 1 : 0, need, need, 1, true},
     };
     st = check_arrays(arrays, 9);
     if (st != GLU_OK) return st;
-    if (p.workspace_bytes > 0 && (!ws || ((uintptr_t)ws & 15) || ws_bytes < p.workspace_bytes)) {
-        return GLU_ERR_WORKSPACE;
-    }
+    if (need > 0 && (!ws || ((uintptr_t)ws & 15) || ws_bytes < need)) return GLU_ERR_WORKSPACE;
 
     hipStream_t s = (hipStream_t)stream;
     if (p.kernel == GLU_FP8_KERNEL_ZERO) {
@@ -367,6 +387,24 @@ glu_status product_call(const glu_fp8_matrix* x, const glu_fp8_matrix* w0, const
     a.M = (int)M;
     a.N = (int)N;
     a.K = (int)K;
+    const bool wide = copied || needs_wide(out_dtype);
+    if (copied) {
+        const int kp = (int)padded(K);
+        uint8_t* to = static_cast<uint8_t*>(ws) + padded(p.workspace_bytes);
+        hipError_t e = glu::copy_rows_launch(a.x, a.ldx, to, kp, a.M, a.K, s);
+        a.x = to;
+        a.ldx = kp;
+        to += (int64_t)M * kp;
+        for (int i = 0; i < mats && e == hipSuccess; ++i) {
+            e = glu::copy_rows_launch(a.w[i], a.ldw[i], to, kp, a.N, a.K, s);
+            a.w[i] = to;
+            a.ldw[i] = kp;
+            to += (int64_t)N * kp;
+        }
+        if (e != hipSuccess) return launched(e);
+        a.K = kp;
+        K = kp;
+    }
     if (p.columns > 0) {
         glu_fp8_plan rest{};
         best_tile(mats, M, N - p.columns, K, out_dtype, &rest);
@@ -375,7 +413,7 @@ glu_status product_call(const glu_fp8_matrix* x, const glu_fp8_matrix* w0, const
         first.columns = 0;
         complete(mats, M, p.columns, K, out_dtype, &first);
         a.N = (int)p.columns;
-        const hipError_t e = run_product(mats, first, a, out_dtype, s);
+        const hipError_t e = run_product(mats, first, a, out_dtype, wide, s);
         if (e != hipSuccess) return launched(e);
         for (int i = 0; i < mats; ++i) {
             a.w[i] += p.columns * a.ldw[i];
@@ -384,9 +422,9 @@ glu_status product_call(const glu_fp8_matrix* x, const glu_fp8_matrix* w0, const
         a.out = static_cast<char*>(a.out) + p.columns * type_size(out_dtype);
         if (a.scale) a.scale += p.columns / kGroup * a.lds;
         a.N = (int)(N - p.columns);
-        return launched(run_product(mats, rest, a, out_dtype, s));
+        return launched(run_product(mats, rest, a, out_dtype, wide, s));
     }
-    return launched(run_product(mats, p, a, out_dtype, s));
+    return launched(run_product(mats, p, a, out_dtype, wide, s));
 }
 
 }  // namespace
@@ -523,6 +561,18 @@ glu_status glu_fp8_product_workspace(int mats, int64_t M, int64_t N, int64_t K, 
     glu_fp8_plan p;
     const glu_status st = product_plan(mats, M, N, K, out_dtype, true, plan, &p);
     if (st == GLU_OK) *bytes = p.workspace_bytes;
+    return st;
+}
+
+glu_status glu_fp8_copy_workspace(int mats, int64_t M, int64_t N, int64_t K, int out_dtype, int64_t* bytes)
+{
+    if (!bytes) return GLU_ERR_NULL_POINTER;
+    *bytes = 0;
+    const glu_status size = check_sizes(mats, M, N, K, out_dtype);
+    if (size != GLU_OK || M <= 16 || N == 0 || K == 0) return size;
+    glu_fp8_plan p;
+    const glu_status st = copy_plan(mats, M, N, K, out_dtype, &p, bytes);
+    if (st != GLU_OK) *bytes = 0;
     return st;
 }
 

@@ -146,6 +146,36 @@ quantize_blocks_kernel(const T* __restrict__ w, int64_t ldw, uint8_t* __restrict
     }
 }
 
+// A lane copies 16 bytes of each of 4 rows, all loaded before the first is stored.
+__global__ void __launch_bounds__(256)
+copy_rows_kernel(const uint8_t* __restrict__ x, int64_t ldx, uint8_t* __restrict__ out, int kp, int rows, int K,
+                 int col_blocks)
+{
+    const int rb = blockIdx.x / col_blocks, cb = blockIdx.x - rb * col_blocks;
+    const int off = 16 * (cb * 64 + (threadIdx.x & 63));
+    const int row0 = (rb * 4 + (threadIdx.x >> 6)) * kRowsPerWave;
+    if (off >= kp) return;
+    raw4_t v[kRowsPerWave];
+#pragma unroll
+    for (int i = 0; i < kRowsPerWave; ++i) {
+        const uint8_t* p = x + min(row0 + i, rows - 1) * ldx + off;
+        if (off + 16 <= K) {
+            v[i] = *reinterpret_cast<const u32x4_any*>(p);
+        } else {
+            uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+            for (int b = 0; b < 16; ++b) {
+                if (off + b < K) w[b >> 2] |= (uint32_t)p[b] << (8 * (b & 3));
+            }
+            v[i] = raw4_t{w[0], w[1], w[2], w[3]};
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kRowsPerWave; ++i) {
+        if (row0 + i < rows) *reinterpret_cast<raw4_t*>(out + (row0 + i) * (int64_t)kp + off) = v[i];
+    }
+}
+
 // rows per wave: one while the rows would not fill the card otherwise
 template <class Out, class Src>
 hipError_t convert_rows(const Src& src, void* out, int64_t ldo, float* scale, int64_t lds, int M, int K,
@@ -194,6 +224,15 @@ hipError_t quantize_blocks_launch(int dtype, const void* w, int64_t ldw, uint8_t
     case GLU_DTYPE_FP16: return blocks_t<Fp16>(w, ldw, q, ldq, scale, lds, N, K, stream);
     default: return blocks_t<Fp32>(w, ldw, q, ldq, scale, lds, N, K, stream);
     }
+}
+
+hipError_t copy_rows_launch(const uint8_t* x, int64_t ldx, uint8_t* out, int kp, int rows, int K, hipStream_t stream)
+{
+    const int col_blocks = (kp + 1023) / 1024;
+    const int64_t row_blocks = ((int64_t)rows + 4 * kRowsPerWave - 1) / (4 * kRowsPerWave);
+    hipLaunchKernelGGL(copy_rows_kernel, dim3((unsigned)(row_blocks * col_blocks)), dim3(256), 0, stream, x, ldx, out,
+                       kp, rows, K, col_blocks);
+    return hipGetLastError();
 }
 
 hipError_t finish_launch(int out_dtype, const FinishArgs& a, hipStream_t stream)

@@ -247,6 +247,14 @@ PyObject* product(PyObject*, PyObject* const* a, Py_ssize_t n)
             if (!s.ok) Py_RETURN_NONE;
             wm[i] = glu_fp8_matrix{(const uint8_t*)w.p, (const float*)s.p, w.ld, s.ld, 1};
         }
+        // a layout that the library copies first takes another workspace
+        uintptr_t bits = (uintptr_t)K | (uintptr_t)x.p | (uintptr_t)x.ld;
+        int64_t widest = x.ld;
+        for (int i = 0; i < mats; ++i) {
+            bits |= (uintptr_t)wm[i].data | (uintptr_t)wm[i].ld;
+            if (wm[i].ld > widest) widest = wm[i].ld;
+        }
+        if (M > 16 && ((bits & 15) || widest > 1 << 23)) Py_RETURN_NONE;
         int64_t bytes = 0;
         glu_status st = api.workspace(mats, M, N, K, (int)dt, &bytes);
         if (st != GLU_OK) return status_int(st);

@@ -314,6 +314,11 @@ def fp8_quantize_weight(w: torch.Tensor, out: Optional[torch.Tensor] = None,
 _product_workspace = functools.lru_cache(maxsize=256)(lambda *sizes: _bytes("glu_fp8_workspace", *sizes))
 
 
+def _fast_layout(K: int, *operands) -> bool:
+    """Whether the library reads (tensor, row stride) pairs of K columns 16 aligned bytes at a time."""
+    return K % 16 == 0 and all((t.data_ptr() | ld) % 16 == 0 and ld <= 1 << 23 for t, ld in operands)
+
+
 def _product(x, x_scale, weights, out_dtype, out, scale_out, plan, stream):
     if out is None and scale_out is None and plan is None and stream is None:
         r = (_fast or _load_fast()).product(DTYPES.get(out_dtype, -1), x, x_scale, *weights[0][1:],
@@ -342,6 +347,8 @@ def _product(x, x_scale, weights, out_dtype, out, scale_out, plan, stream):
     n = len(mats)
     if plan is None:
         need = _product_workspace(n, M, N, K, dt)
+        if M > 16 and not _fast_layout(K, (x, ldx), *((w, m.ld) for (_, w, _), m in zip(weights, mats))):
+            need = max(need, _bytes("glu_fp8_copy_workspace", n, M, N, K, dt))  # room for aligned copies
     else:
         need = _bytes("glu_fp8_product_workspace", n, M, N, K, dt, ctypes.byref(plan))
     ctx, handle = _on(dev, stream, x, x_scale, out, scale_out, *(t for _, w, s in weights for t in (w, s)))
@@ -371,7 +378,7 @@ def fp8_linear(x: torch.Tensor, x_scale: torch.Tensor, weight: torch.Tensor, wei
 
     Returns [M, N] in ``out_dtype`` (bf16, fp16, fp32), or for float8_e4m3fn the pair (q, scale).  fp32 accumulation
     over the K-blocks, one rounding.  K and the row strides should be multiples of 16 and the rows 16-byte
-    aligned; other layouts are read byte by byte, slower.
+    aligned; other layouts are copied first, or up to 16 rows of x read as they are, slower.
     """
     return _product(x, x_scale, (("weight", weight, weight_scale),), out_dtype, out, scale_out, plan, stream)
 
@@ -413,6 +420,7 @@ def _declare(lib):
         "glu_fp8_dual_glu": [mp, mp, mp] + tail + [vp, i64, vp],
         "glu_fp8_product_plan": [i32, i64, i64, i64, i32, i32, pp],
         "glu_fp8_workspace": [i32, i64, i64, i64, i32, bp],
+        "glu_fp8_copy_workspace": [i32, i64, i64, i64, i32, bp],
         "glu_fp8_product_tuned": [mp, mp, mp] + tail + [pp, vp, i64, vp],
         "glu_fp8_product_workspace": [i32, i64, i64, i64, i32, pp, bp],
     }.items():

@@ -186,6 +186,26 @@ def test_workspace_covers_either_layout(lib):
     assert lib.glu_fp8_product_plan(1, 1, 1, 1, BF16, 1, None) == NULLP
 
 
+def test_copy_workspace(lib):
+    def need(query, mats, M, N, K, dt=BF16):
+        b = ctypes.c_int64(-1)
+        return getattr(lib, query)(mats, M, N, K, dt, ctypes.byref(b)), b.value
+    for mats in (1, 2):
+        for M, N, K in ((17, 1, 1), (40, 300, 129), (300, 4096, 4100), (5000, 12288, 4096)):
+            plan = fp8.ProductPlan()
+            assert lib.glu_fp8_product_plan(mats, M, N, (K + 15) // 16 * 16, BF16, 1, ctypes.byref(plan)) == OK
+            copies = (M + mats * N) * ((K + 15) // 16 * 16)
+            assert need("glu_fp8_copy_workspace", mats, M, N, K) == (OK, (plan.workspace_bytes + 15) // 16 * 16 + copies)
+    assert need("glu_fp8_copy_workspace", 1, 16, 300, 129) == (OK, 0)
+    assert need("glu_fp8_copy_workspace", 1, 40, 300, 0) == (OK, 0)
+    assert need("glu_fp8_copy_workspace", 3, 40, 300, 128)[0] == ARG
+    assert need("glu_fp8_copy_workspace", 1, 40, 300, 128, 9)[0] == ARG
+    assert need("glu_fp8_copy_workspace", 1, 40, -1, 128)[0] == SHAPE
+    assert lib.glu_fp8_copy_workspace(1, 40, 300, 128, BF16, None) == NULLP
+    # sizes whose workspace would not fit 63 bits
+    assert need("glu_fp8_workspace", 2, 1 << 30, 1 << 30, 128)[0] == SHAPE
+
+
 def test_python_refuses_cpu_tensors():
     import torch
 

@@ -187,6 +187,22 @@ def test_any_contraction_length(M, N, K, mats):
         check(kind, got, want, err)
 
 
+@pytest.mark.parametrize("mats", [1, 2])
+@pytest.mark.parametrize("M,N,K,pad", [(17, 1, 33, 0), (300, 700, 1001, 0), (40, 130, 256, 1), (1100, 513, 272, 8)])
+def test_copied_layouts(M, N, K, pad, mats):
+    """More than 16 rows whose layout is not fast, by its length or by its strides, on the copies and in place."""
+    ops = [t if t.dtype is not E4M3 else torch.nn.functional.pad(t.view(torch.uint8), (0, pad), value=0x7f).view(E4M3)[:, :K]
+           for t in operands(M, N, K, K, mats)]
+    want, err = expected(ops)
+    for kind in ("bf16", "fp32", "e4m3"):
+        print(f"[copied] mats={mats} M={M} N={N} K={K} pad={pad} {kind}", flush=True)
+        got = run(ops, T[kind])
+        place = run(ops, T[kind], plan=fp8.ProductPlan(4, 16, 4, 1))
+        torch.cuda.synchronize()
+        check(kind, got, want, err)
+        check(kind + " in place", place, want, err)
+
+
 def plans():
     """Every kernel the library can launch, at sizes past and inside its tiles, with and without split sums."""
     out = []
