@@ -28,12 +28,10 @@ struct NormGradArgs {
     const float* rstd;    // [M]
     void* dx;             // [M][K]
     void* dw;             // [K]
-    float* part;          // [teams][K]: norm_grad_part_floats
+    float* part;          // [parts][K]: norm_grad_part_floats
     int64_t lddy, ldh, lddr, lddx;
     int M, K;
 };
-// Teams of waves, each walking its own rows and leaving one fp32 partial of dw; a single team writes dw itself.
-int norm_grad_teams(int dtype, int M, int K);
 int64_t norm_grad_part_floats(int dtype, int M, int K);
 hipError_t norm_grad_launch(int dtype, const NormGradArgs& a, hipStream_t stream);
 

@@ -159,9 +159,9 @@ norm_long_kernel(NormArgs a)
 //   xhat = h r,  a = dy w,  dx = r (a - xhat mean(a xhat)) + dres,  dw = sum over rows of dy xhat
 //
 // One pass: a team of waves walks a run of rows, keeps w and its columns' dw in registers and loads the next
-// row while the current one's mean is being reduced.  dw's partial sums, one per team, are joined in team order
-// by a second kernel, so the result does not change from run to run.  K past a team's registers walks column
-// slices in a first pass for the mean.
+// row while the current one's mean is being reduced.  dw's partial sums, one per workgroup, are joined in a fixed order
+// by a second kernel, so the result does not change from run to run; a single workgroup writes dw itself.  K past a
+// team's registers walks column slices in a first pass for the mean.
 
 namespace {
 
@@ -174,17 +174,18 @@ struct GradRow {
 
 template <class T, int C, int WAVES, bool ONCE>
 __global__ void __launch_bounds__(64 * WAVES)
-norm_grad_kernel(NormGradArgs a, int wpr, int teams_per_wg, int teams)
+norm_grad_kernel(NormGradArgs a, int wpr, int teams_per_wg)
 {
     __shared__ float red[2][kNormMaxWaves];
+    extern __shared__ float sum[];  // [teams_per_wg][K], with more than one
     const int lane = threadIdx.x & 63;
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wave = teams_per_wg > 1 ? 0 : wv;
-    const int team = blockIdx.x * teams_per_wg + (teams_per_wg > 1 ? wv : 0);
-    if (team >= teams) return;  // whole waves, and only where no barrier follows
+    const int own = wv / wpr, wave = wv - own * wpr;
+    const int team = blockIdx.x * teams_per_wg + own, teams = gridDim.x * teams_per_wg;
     const int per = a.M / teams, rem = a.M % teams;
     const int row0 = team * per + min(team, rem);
     const int row1 = row0 + per + (team < rem ? 1 : 0);
+    const int last = row0 + per + (rem > 0 ? 1 : 0);  // teams that share barriers take as many turns
 
     Chunk<T> w[C];
     float dw[C][8];
@@ -216,24 +217,27 @@ norm_grad_kernel(NormGradArgs a, int wpr, int teams_per_wg, int teams)
         fetch(row0, cur);
         r = a.rstd[row0];
     }
-    for (int row = row0; row < row1; ++row) {
+    for (int row = row0; row < last; ++row) {
         if (row + 1 < row1) {
             fetch(row + 1, nxt);
             rn = a.rstd[row + 1];
         }
         float s = 0.0f;
+        if (row < row1) {
 #pragma unroll
-        for (int i = 0; i < C; ++i) {
+            for (int i = 0; i < C; ++i) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float dy = widen(cur[i].dy.e[e]);
-                const float xh = widen(cur[i].h.e[e]) * r;
-                s = fmaf(dy * widen(w[i].e[e]), xh, s);
-                dw[i][e] = fmaf(dy, xh, dw[i][e]);
+                for (int e = 0; e < 8; ++e) {
+                    const float dy = widen(cur[i].dy.e[e]);
+                    const float xh = widen(cur[i].h.e[e]) * r;
+                    s = fmaf(dy * widen(w[i].e[e]), xh, s);
+                    dw[i][e] = fmaf(dy, xh, dw[i][e]);
+                }
             }
         }
         // the two LDS rows alternate: a wave writes one only after the barrier of the row between
-        const float mean = team_sum(s, red[row & 1], wave, lane, wpr) / (float)a.K;
+        const float mean = team_sum(s, &red[(row - row0) & 1][own * wpr], wave, lane, wpr) / (float)a.K;
+        if (row >= row1) break;
 #pragma unroll
         for (int i = 0; i < C; ++i) {
             const int c = lane + 64 * (wave + wpr * i);
@@ -256,11 +260,24 @@ norm_grad_kernel(NormGradArgs a, int wpr, int teams_per_wg, int teams)
         const int c = lane + 64 * (wave + wpr * i);
         const int n = a.K - 8 * c;
         if (n <= 0) continue;
-        if (teams == 1) {
+        if (teams_per_wg > 1) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                if (e < n) sum[own * a.K + 8 * c + e] = dw[i][e];
+            }
+        } else if (teams == 1) {
             store_chunk(static_cast<T*>(a.dw) + 8 * c, narrow8<T>(dw[i]), n);
         } else {
             store_chunk(reinterpret_cast<Fp32*>(a.part) + (int64_t)team * a.K + 8 * c, narrow8<Fp32>(dw[i]), n);
         }
+    }
+    if (teams_per_wg == 1) return;
+    __syncthreads();
+    for (int k = threadIdx.x; k < a.K; k += blockDim.x) {
+        float s = sum[k];
+        for (int t = 1; t < teams_per_wg; ++t) s += sum[t * a.K + k];
+        if (gridDim.x == 1) static_cast<T*>(a.dw)[k] = narrow<T>(s);
+        else a.part[(int64_t)blockIdx.x * a.K + k] = s;
     }
 }
 
@@ -382,16 +399,41 @@ RowShape norm_shape(int M, int K, int size)
 // 4096, 118.5 us for 16384 rows against 137 with two), two above, where registers allow: 16-bit types only.
 constexpr int kGradMaxK = 64 * kNormMaxWaves * 8;
 int64_t grad_max_k(int dtype) { return dtype == GLU_DTYPE_FP32 ? kGradMaxK : 2 * kGradMaxK; }
-RowShape grad_shape(int K)
+// A few rows go to the teams of one workgroup and need no second launch: up to 2 a team, each some 1.8 us (3 x 780
+// 3.9 us against 5.2, and 3 us less on the host).  Single waves, which share no barrier, are 16 to a workgroup and
+// leave one partial sum for all: 3090 x 192 6.8 us against 12.0, 8192 x 512 12.5 against 21.7.  Else 16 waves per
+// CU, all resident at once: at 16384 x 4096 118.5 us, against 132 at half and 119 at twice as many.
+struct GradShape {
+    int wpr, chunks, teams, grid;  // waves per row, chunks per lane, teams per workgroup
+};
+constexpr int kGradRows = 2;
+GradShape grad_shape(int M, int K)
 {
     const int need = (K + 511) / 512;
-    return need <= kNormMaxWaves ? RowShape{need, 1} : RowShape{(need + 1) / 2, 2};
+    if (need > kNormMaxWaves) {
+        const int wpr = (need + 1) / 2, most = 4096 / wpr;
+        return {wpr, 2, 1, M < most ? M : most};
+    }
+    const int fit = kNormMaxWaves / need;
+    if (M <= kGradRows * fit) return {need, 1, M < fit ? M : fit, 1};
+    if (need == 1) return {1, 1, fit, M < 256 * fit ? (M + fit - 1) / fit : 256};
+    const int most = 4096 / need;
+    return {need, 1, 1, M < most ? M : most};
+}
+
+// partial sums of dw that a second kernel joins; 0: none
+int grad_parts(int dtype, int M, int K)
+{
+    if (M < 1) return 0;
+    if (K > grad_max_k(dtype)) return M < 64 ? M : 64;
+    const GradShape p = grad_shape(M, K);
+    return p.grid > 1 ? p.grid : 0;
 }
 
 // What the backward reads is dropped from the caches where they could not hold it for the next reader anyway: 16384
-// x 4096 bf16 (403 MB) 117.7 -> 109.6 us; where they hold it that costs: 2048 x 4096 19.7 -> 22.3.
+// x 4096 bf16 (403 MB) 113.9 -> 106.3 us; where they hold it that costs: 2048 x 4096 19.7 -> 22.3.
 constexpr int64_t kLastLevelCache = 256 << 20;
-using GradFn = void (*)(NormGradArgs, int, int, int);
+using GradFn = void (*)(NormGradArgs, int, int);
 template <class T, int C, int WAVES>
 GradFn grad_kernel(bool once)
 {
@@ -422,7 +464,7 @@ hipError_t norm_launch_t(const NormArgs& a, hipStream_t s)
 template <class T>
 hipError_t norm_grad_launch_t(int dtype, const NormGradArgs& a, hipStream_t s)
 {
-    const int teams = norm_grad_teams(dtype, a.M, a.K);
+    const int parts = grad_parts(dtype, a.M, a.K);
     if (a.M > 0) {
         if (a.K > grad_max_k(dtype)) {
             for (int64_t row = 0; row < a.M; row += kNormRows) {
@@ -431,44 +473,33 @@ hipError_t norm_grad_launch_t(int dtype, const NormGradArgs& a, hipStream_t s)
                                    (int)row);
             }
             const int chunks = (a.K + 7) / 8;
-            hipLaunchKernelGGL((norm_grad_long_dw_kernel<T>), dim3((chunks + 255) / 256, teams), dim3(256), 0, s, a,
-                               teams);
+            hipLaunchKernelGGL((norm_grad_long_dw_kernel<T>), dim3((chunks + 255) / 256, parts), dim3(256), 0, s, a,
+                               parts);
         } else {
-            const RowShape p = grad_shape(a.K);
-            const int tpw = p.wpr == 1 ? 4 : 1;
-            const dim3 grid((teams + tpw - 1) / tpw), block(64 * p.wpr * tpw);
+            const GradShape p = grad_shape(a.M, a.K);
+            const int waves = p.wpr * p.teams;
             const bool once = sizeof(T) == 2 && (int64_t)a.M * a.K * 2 * (a.dres ? 3 : 2) > kLastLevelCache;
             const auto run = [&](auto kernel) {
-                hipLaunchKernelGGL(kernel, grid, block, 0, s, a, p.wpr, tpw, teams);
+                const size_t lds = p.teams > 1 ? (size_t)p.teams * a.K * 4 : 0;
+                hipLaunchKernelGGL(kernel, dim3(p.grid), dim3(64 * waves), lds, s, a, p.wpr, p.teams);
             };
             if (p.chunks == 2) {
                 if constexpr (sizeof(T) == 2) run(grad_kernel<T, 2, 16>(once));
-            } else if (p.wpr > 8) {
+            } else if (waves > 8) {
                 run(grad_kernel<T, 1, 16>(once));
             } else {
                 run(grad_kernel<T, 1, 8>(once));
             }
-            if (teams == 1) return hipGetLastError();
+            if (parts == 0) return hipGetLastError();
         }
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((norm_grad_dw_kernel<T>), dim3((a.K + 31) / 32), dim3(1024), 0, s, a.part, a.dw, a.K, teams);
+    hipLaunchKernelGGL((norm_grad_dw_kernel<T>), dim3((a.K + 31) / 32), dim3(1024), 0, s, a.part, a.dw, a.K, parts);
     return hipGetLastError();
 }
 
 }  // namespace
-
-int norm_grad_teams(int dtype, int M, int K)
-{
-    if (M < 1) return 0;
-    if (M == 1) return 1;
-    if (K > grad_max_k(dtype)) return M < 64 ? M : 64;
-    // 16 waves per CU, all resident at once: at 16384 x 4096 118.5 us, against 132 at half and 119 at twice as
-    // many
-    const int target = 4096 / grad_shape(K).wpr;
-    return M < target ? M : target;
-}
 
 hipError_t norm_launch(int dtype, bool e4m3, const NormArgs& all, hipStream_t s)
 {
@@ -497,8 +528,7 @@ hipError_t norm_launch(int dtype, bool e4m3, const NormArgs& all, hipStream_t s)
 
 int64_t norm_grad_part_floats(int dtype, int M, int K)
 {
-    const int teams = norm_grad_teams(dtype, M, K);
-    return teams > 1 || (teams == 1 && K > grad_max_k(dtype)) ? (int64_t)teams * K : 0;
+    return (int64_t)grad_parts(dtype, M, K) * K;
 }
 
 hipError_t norm_grad_launch(int dtype, const NormGradArgs& a, hipStream_t s)

@@ -70,6 +70,23 @@ def test_backward(M, K, residual, kind):
     assert torch.equal(gx, gx2) and torch.equal(gw, gw2), "a second call gives the same bits"
 
 
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+@pytest.mark.parametrize("M", [2, 5, 7, 16, 17, 33, 64, 65, 300, 3090])
+@pytest.mark.parametrize("K", [5, 192, 512, 520, 1030, 2560, 5100])
+def test_backward_workgroups(M, K, kind):
+    """Rows that one workgroup's teams share unevenly, and more."""
+    t = T[kind]
+    print(f"[norm grad] M={M} K={K} {kind}", flush=True)
+    h, dy, dr = tensors(M, K, t, M * K, 3.0, 0.1, 0.1)
+    w = weight(K, t, K)
+    rstd = torch.rsqrt(h.double().square().mean(1) + EPS).float()
+    dx, edx, dw, edw = ref.grad64(dy, h, w, rstd, dr)
+    gx, gw = glu.add_rms_norm_backward(dy, h, w, rstd, dresidual=dr)
+    torch.cuda.synchronize()
+    ref.check_store("dx", gx, dx, edx)
+    ref.check_store("dweight", gw, dw, edw)
+
+
 @pytest.mark.parametrize("M,K,residual", [(16390, 4099, False), (11000, 4099, True), (8300, 8200, False)])
 def test_backward_past_the_cache(M, K, residual):
     """More than the last-level cache holds, which is then read past it."""
