@@ -102,8 +102,12 @@ glu_status norm_call(const void* x, int64_t ldx, const void* residual, int64_t l
 
 // ---- products ----------------------------------------------------------------------
 
-// outputs that show more than the 8-bit matrix unit's sums hold (glu_fp8_mfma.h)
-bool needs_wide(int out_dtype) { return out_dtype == GLU_DTYPE_FP32 || out_dtype == GLU_DTYPE_E4M3; }
+// outputs that show more than the 8-bit matrix unit's sums hold (glu_fp8_mfma.h), and up to 16 rows, where the other
+// unit has the time, all of them
+bool needs_wide(int64_t M, int out_dtype)
+{
+    return M <= 16 || out_dtype == GLU_DTYPE_FP32 || out_dtype == GLU_DTYPE_E4M3;
+}
 
 // Microseconds that a tiled product is expected to take.  A workgroup takes a constant time per stage (one
 // K-block of its tile), each round of 256 workgroups (one per CU) has a start and an end, and sums that leave
@@ -127,13 +131,24 @@ double tile_cost(int mats, int64_t M, int64_t N, int64_t K, int out_dtype, int s
     const glu::TileShape& t = glu::kTileShapes[shape];
     const int64_t tiles = ceil_div(M, t.bm) * ceil_div(N, t.br / mats);
     const int stages = ((int)ceil_div(K, kGroup) + splits - 1) / splits;
-    const double round = stages * kStage[needs_wide(out_dtype)][shape] + kRound;
+    const double round = stages * kStage[needs_wide(M, out_dtype)][shape] + kRound;
     double us = kLaunch + (double)ceil_div(tiles * splits, kCUs) * round;
     if (has_planes(mats, out_dtype, shape, splits)) {
         us += kJoin + kJoinSplit * splits + (double)(splits * mats * 4) * (double)M * (double)N / kPlaneBytes;
     }
     const double read = kLaunch + ((double)M + (double)mats * (double)N) * (double)K / kReadBytes;
     return sqrt(sqrt(us * us * us * us + read * read * read * read));
+}
+
+// The same of the streaming kernel with 16 weight rows per workgroup: a CU with one workgroup more than the others is
+// waited for, which the tiled kernel avoids by splitting K (5 rows, K = 17408 N = 5120, 320 workgroups: 29.0 us
+// against 20.8; 16 rows 38.5 against 21.6).  A fit to 7 sizes at 5, 8 and 16 rows, all within 9 %.
+double stream_cost(int mats, int64_t M, int64_t N, int64_t K, int out_dtype)
+{
+    const double block = mats == 1 ? 0.0945 + 0.0027 * (double)M : 0.1575 + 0.0039 * (double)M;
+    double us = kLaunch + (double)(ceil_div(ceil_div(N, 16), kCUs) * ceil_div(K, kGroup)) * block;
+    if (out_dtype == GLU_DTYPE_E4M3) us += kJoin + kJoinSplit + (double)(mats * 4) * (double)M * (double)N / kPlaneBytes;
+    return us;
 }
 
 double best_tile(int mats, int64_t M, int64_t N, int64_t K, int out_dtype, glu_fp8_plan* p)
@@ -168,11 +183,18 @@ void choose(int mats, int64_t M, int64_t N, int64_t K, int out_dtype, bool fast,
         return;
     }
     if (M <= 16) {
+        // 4 weight rows a workgroup for one or two rows of x, and up to 4 for two matrices or where 16 would leave
+        // CUs idle; else 16 (4 rows, K = 12288 N = 4096: 13.1 us against 15.8; dual K = 2560 N = 9216: 13.2 against
+        // 12.5, K = 8192 N = 512: 8.0 against 4.6, K = 9216 N = 2560: 9.8 against 9.6)
+        const bool few = M <= 2 || (M <= 4 && (mats == 2 || N <= 2560));
+        if (!few && best_tile(mats, M, N, K, out_dtype, p) < stream_cost(mats, M, N, K, out_dtype)) return;
         p->kernel = GLU_FP8_KERNEL_STREAM;
-        p->tile = M <= 4 ? 4 : 16;
-        // 3 resp. 6 waves keep enough loads in flight; more only lengthen the join (8.1 us against 8.4 with 8
-        // waves at K = 9216 N = 2560, one row; 12.8 against 12.9 at K = 12288 N = 4096, 8 rows)
-        const int64_t steps = ceil_div(KB, 16 / p->tile), most = p->tile == 4 ? 3 : 6;
+        p->tile = few ? 4 : 16;
+        p->splits = 1;
+        // Waves that keep enough loads in flight; more only lengthen the join (one row, K = 9216 N = 2560: 8.1 us
+        // with 3, 8.4 with 8; 8 rows, K = 12288 N = 4096: 13.9 with 6, 14.1 with 8; dual K = 2560 N = 9216: 14.8 with 6,
+        // 14.0 with 8)
+        const int64_t steps = ceil_div(KB, 16 / p->tile), most = few ? 3 : mats == 1 ? 6 : 8;
         p->width = (int)(steps < most ? steps : most);
         return;
     }
@@ -387,7 +409,7 @@ glu_status product_call(const glu_fp8_matrix* x, const glu_fp8_matrix* w0, const
     a.M = (int)M;
     a.N = (int)N;
     a.K = (int)K;
-    const bool wide = copied || needs_wide(out_dtype);
+    const bool wide = copied || needs_wide(M, out_dtype);
     if (copied) {
         const int kp = (int)padded(K);
         uint8_t* to = static_cast<uint8_t*>(ws) + padded(p.workspace_bytes);
