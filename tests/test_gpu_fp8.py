@@ -174,6 +174,21 @@ def test_product(M, N, K, mats):
             check_rms(got, want, ops)
 
 
+@pytest.mark.parametrize("M", [3, 4, 5, 16])
+def test_few_rows_on_tiles(M):
+    """Up to 16 rows keep fp32 sums where tiles with K split serve them."""
+    N, K = 5120, 17408
+    ops = operands(M, N, K, M)
+    want, err = expected(ops)
+    for kind in ("bf16", "fp32", "e4m3"):
+        plan = fp8.product_plan(1, M, N, K, T[kind])
+        print(f"[few rows] M={M} {kind} {plan}", flush=True)
+        assert plan["kernel_name"] == "tile" or kind == "e4m3"
+        got = run(ops, T[kind])
+        torch.cuda.synchronize()
+        check(kind, got, want, err)
+
+
 @pytest.mark.parametrize("mats", [1, 2])
 @pytest.mark.parametrize("M,N,K", [(1, 100, 300), (6, 130, 257), (19, 64, 15), (70, 200, 1000 - 7), (2, 40, 1)])
 def test_any_contraction_length(M, N, K, mats):
