@@ -402,9 +402,10 @@ int64_t grad_max_k(int dtype) { return dtype == GLU_DTYPE_FP32 ? kGradMaxK : 2 *
 // A few rows go to the teams of one workgroup and need no second launch: up to 2 a team, each some 1.8 us (3 x 780
 // 3.9 us against 5.2, and 3 us less on the host).  Single waves, which share no barrier, are 16 to a workgroup and
 // leave one partial sum for all: 3090 x 192 6.8 us against 12.0, 8192 x 512 12.5 against 21.7.  So do longer rows' teams
-// where each has one row or two, though they wait for each other: 4096 x 1024 13.2 against 18.5, 1500 x 600 fp32 7.9
-// against 12.0; with more rows each that costs (1612 x 3392: 24.0 against 18.1), and with up to 256 teams, whose
-// sums are quickly joined (203 x 2560: 7.7 against 6.7).  Else 16 waves per CU, all resident at once: at 16384
+// where each has one row or two, pairs of waves up to four, though they wait for each other: 4096 x 1024 13.2 against
+// 18.5, 1500 x 600 fp32 7.9 against 12.0, 6000 x 800 14.3 against 17.4; with more rows each that costs (1612 x 3392
+// 24.0 against 18.1, 5000 x 1500 29.5 against 22.7), and with up to 256 teams, whose sums are quickly joined (203 x
+// 2560: 7.7 against 6.7).  Else 16 waves per CU, all resident at once: at 16384
 // x 4096 118.5 us, against 132 at half and 119 at twice as many.
 struct GradShape {
     int wpr, chunks, teams, grid;  // waves per row, chunks per lane, teams per workgroup
@@ -421,7 +422,7 @@ GradShape grad_shape(int M, int K)
     if (M <= kGradRows * fit) return {need, 1, M < fit ? M : fit, 1};
     const int most = 4096 / need;
     const int teams = M <= most ? M : M <= 2 * most ? (M + 1) / 2 : most;
-    const int share = need == 1 || (teams > 256 && M <= 2 * teams) ? fit : 1;
+    const int share = need == 1 || (teams > 256 && M <= (need == 2 ? 4 : 2) * teams) ? fit : 1;
     return {need, 1, share, (teams + share - 1) / share};
 }
 

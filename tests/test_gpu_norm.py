@@ -71,7 +71,7 @@ def test_backward(M, K, residual, kind):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "fp32"])
-@pytest.mark.parametrize("M", [2, 5, 7, 16, 17, 33, 64, 65, 300, 3090])
+@pytest.mark.parametrize("M", [2, 5, 7, 16, 17, 33, 64, 65, 300, 3090, 6001])
 @pytest.mark.parametrize("K", [5, 192, 512, 520, 1030, 2560, 5100])
 def test_backward_workgroups(M, K, kind):
     """Rows that one workgroup's teams share unevenly, and more."""
