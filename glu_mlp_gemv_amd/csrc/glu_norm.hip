@@ -396,7 +396,8 @@ RowShape norm_shape(int M, int K, int size)
 }
 
 // The backward holds three rows and their successors beside w and dw: one chunk per lane up to 8192 columns (at
-// 4096, 118.5 us for 16384 rows against 137 with two), two above, where registers allow: 16-bit types only.
+// 4096, 118.5 us for 16384 rows against 137 with two, and 106 since its reads go past the caches), two above, where
+// registers allow: 16-bit types only.
 constexpr int kGradMaxK = 64 * kNormMaxWaves * 8;
 int64_t grad_max_k(int dtype) { return dtype == GLU_DTYPE_FP32 ? kGradMaxK : 2 * kGradMaxK; }
 // A few rows go to the teams of one workgroup and need no second launch: up to 2 a team, each some 1.8 us (3 x 780
@@ -406,7 +407,7 @@ int64_t grad_max_k(int dtype) { return dtype == GLU_DTYPE_FP32 ? kGradMaxK : 2 *
 // 18.5, 1500 x 600 fp32 7.9 against 12.0, 6000 x 800 14.3 against 17.4; with more rows each that costs (1612 x 3392
 // 24.0 against 18.1, 5000 x 1500 29.5 against 22.7), and with up to 256 teams, whose sums are quickly joined (203 x
 // 2560: 7.7 against 6.7).  Else 16 waves per CU, all resident at once: at 16384
-// x 4096 118.5 us, against 132 at half and 119 at twice as many.
+// x 4096 118.5 us (reads through the caches), against 132 at half and 119 at twice as many.
 struct GradShape {
     int wpr, chunks, teams, grid;  // waves per row, chunks per lane, teams per workgroup
 };
