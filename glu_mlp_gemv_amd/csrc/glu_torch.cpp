@@ -27,6 +27,7 @@ struct Api {
     decltype(&glu_fp8_linear) linear;
     decltype(&glu_fp8_dual_glu) dual_glu;
     decltype(&glu_fp8_workspace) workspace;
+    decltype(&glu_fp8_product_workspace) fast_workspace;
 };
 Api api;
 
@@ -254,9 +255,11 @@ PyObject* product(PyObject*, PyObject* const* a, Py_ssize_t n)
             bits |= (uintptr_t)wm[i].data | (uintptr_t)wm[i].ld;
             if (wm[i].ld > widest) widest = wm[i].ld;
         }
-        if (M > 16 && ((bits & 15) || widest > 1 << 23)) Py_RETURN_NONE;
+        const bool fast = (bits & 15) == 0 && widest <= 1 << 23;
+        if (M > 16 && !fast) Py_RETURN_NONE;
         int64_t bytes = 0;
-        glu_status st = api.workspace(mats, M, N, K, (int)dt, &bytes);
+        glu_status st = fast ? api.fast_workspace(mats, M, N, K, (int)dt, nullptr, &bytes)
+                             : api.workspace(mats, M, N, K, (int)dt, &bytes);
         if (st != GLU_OK) return status_int(st);
         const bool e4m3 = dt == GLU_DTYPE_E4M3;
         at::Tensor t[2];

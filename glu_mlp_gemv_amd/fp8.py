@@ -51,7 +51,7 @@ class ProductPlan(ctypes.Structure):
 # in the order that _fast.bind takes them
 _BOUND = ("glu_add_rms_norm", "glu_add_rms_norm_fp8", "glu_add_rms_norm_backward",
           "glu_add_rms_norm_backward_workspace", "glu_fp8_quantize", "glu_fp8_quantize_weight", "glu_fp8_linear",
-          "glu_fp8_dual_glu", "glu_fp8_workspace")
+          "glu_fp8_dual_glu", "glu_fp8_workspace", "glu_fp8_product_workspace")
 _fast = None
 
 
@@ -311,7 +311,12 @@ def fp8_quantize_weight(w: torch.Tensor, out: Optional[torch.Tensor] = None,
     return out, scale
 
 
-_product_workspace = functools.lru_cache(maxsize=256)(lambda *sizes: _bytes("glu_fp8_workspace", *sizes))
+@functools.lru_cache(maxsize=256)
+def _product_workspace(mats: int, M: int, N: int, K: int, dt: int, fast: bool) -> int:
+    """Workspace bytes of a call on this layout: of the fast kernels, of aligned copies, or of reading in place."""
+    if fast:
+        return _bytes("glu_fp8_product_workspace", mats, M, N, K, dt, None)
+    return _bytes("glu_fp8_copy_workspace" if M > 16 else "glu_fp8_workspace", mats, M, N, K, dt)
 
 
 def _fast_layout(K: int, *operands) -> bool:
@@ -346,9 +351,8 @@ def _product(x, x_scale, weights, out_dtype, out, scale_out, plan, stream):
         raise ValueError("scale_out without an e4m3 output")
     n = len(mats)
     if plan is None:
-        need = _product_workspace(n, M, N, K, dt)
-        if M > 16 and not _fast_layout(K, (x, ldx), *((w, m.ld) for (_, w, _), m in zip(weights, mats))):
-            need = max(need, _bytes("glu_fp8_copy_workspace", n, M, N, K, dt))  # room for aligned copies
+        fast = _fast_layout(K, (x, ldx), *((w, m.ld) for (_, w, _), m in zip(weights, mats)))
+        need = _product_workspace(n, M, N, K, dt, fast)
     else:
         need = _bytes("glu_fp8_product_workspace", n, M, N, K, dt, ctypes.byref(plan))
     ctx, handle = _on(dev, stream, x, x_scale, out, scale_out, *(t for _, w, s in weights for t in (w, s)))

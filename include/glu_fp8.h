@@ -136,7 +136,8 @@ typedef struct glu_fp8_plan {
 glu_status glu_fp8_product_plan(int mats, int64_t M, int64_t N, int64_t K, int out_dtype, int fast,
                                 glu_fp8_plan* plan);
 
-/* Workspace bytes either product needs for these sizes, whatever its layout. */
+/* Workspace bytes either product needs for these sizes, whatever its layout; glu_fp8_product_workspace with
+ * plan NULL is what the fast layout needs, often less. */
 glu_status glu_fp8_workspace(int mats, int64_t M, int64_t N, int64_t K, int out_dtype, int64_t* bytes);
 
 /* Workspace bytes with which a call on a layout that is not fast copies its operands first (0: M <= 16). */
@@ -146,7 +147,7 @@ glu_status glu_fp8_copy_workspace(int mats, int64_t M, int64_t N, int64_t K, int
  * Either product with the launch shape of `plan` (kernel, tile, width, splits, columns;
  * launches and workspace_bytes are ignored), for sweeps and tests: up NULL is the linear one.  A shape that the library
  * was not built with or that cannot serve the operands returns GLU_ERR_UNSUPPORTED, before any HIP call.  The
- * workspace is that of glu_fp8_product_workspace for the same plan.
+ * workspace is that of glu_fp8_product_workspace for the same plan (NULL: the one that the library chooses).
  */
 glu_status glu_fp8_product_tuned(const glu_fp8_matrix* x, const glu_fp8_matrix* w, const glu_fp8_matrix* up,
                                  void* out, int64_t ldo, float* out_scale, int64_t ld_scale, int64_t M, int64_t N,

@@ -206,6 +206,17 @@ def test_copy_workspace(lib):
     assert need("glu_fp8_workspace", 2, 1 << 30, 1 << 30, 128)[0] == SHAPE
 
 
+def test_workspace_of_the_fast_layout(lib):
+    """A prefill that ends in e4m3 by itself needs none on the fast layout."""
+    need = ctypes.c_int64(-1)
+    for mats, M, N, K, t in ((2, 4096, 17408, 5120, E4M3), (1, 203, 4096, 12288, BF16), (2, 1, 9216, 2560, E4M3)):
+        plan = fp8.ProductPlan()
+        assert lib.glu_fp8_product_plan(mats, M, N, K, t, 1, ctypes.byref(plan)) == OK
+        assert lib.glu_fp8_product_workspace(mats, M, N, K, t, None, ctypes.byref(need)) == OK
+        assert need.value == plan.workspace_bytes
+        assert (need.value == 0) == (M == 4096)
+
+
 def test_python_refuses_cpu_tensors():
     import torch
 
