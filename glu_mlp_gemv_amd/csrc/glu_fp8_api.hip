@@ -315,8 +315,9 @@ hipError_t run_product(int mats, const glu_fp8_plan& p, glu::Fp8Args a, int out_
 // A layout that is not fast, above 16 rows: where the workspace has room for them the operands are copied to the
 // fast layout first, behind the product's own part of it: 2048 rows, K = 4100 N = 4096 in 95 us against 470 in
 // place, dual 4096 rows, K = 5125 N = 17408 in 1.29 ms against 21.  The copies run on the bf16 unit, as the kernel in
-// place does.
+// place does.  A row too long for the fast layout's strides stays in place, whose kernel counts in 64 bits.
 int64_t padded(int64_t K) { return (K + 15) / 16 * 16; }
+bool copies(int64_t M, int64_t K) { return M > 16 && padded(K) <= kMaxFastLd; }
 
 glu_status copy_plan(int mats, int64_t M, int64_t N, int64_t K, int out_dtype, glu_fp8_plan* p, int64_t* bytes)
 {
@@ -360,7 +361,7 @@ glu_status product_call(const glu_fp8_matrix* x, const glu_fp8_matrix* w0, const
     glu_fp8_plan p;
     bool copied = false;
     int64_t need = 0;
-    if (on && !fast && !asked && M > 16) {
+    if (on && !fast && !asked && copies(M, K)) {
         st = copy_plan(mats, M, N, K, out_dtype, &p, &need);
         copied = st == GLU_OK && ws && ((uintptr_t)ws & 15) == 0 && ws_bytes >= need;
     }
@@ -591,7 +592,7 @@ glu_status glu_fp8_copy_workspace(int mats, int64_t M, int64_t N, int64_t K, int
     if (!bytes) return GLU_ERR_NULL_POINTER;
     *bytes = 0;
     const glu_status size = check_sizes(mats, M, N, K, out_dtype);
-    if (size != GLU_OK || M <= 16 || N == 0 || K == 0) return size;
+    if (size != GLU_OK || !copies(M, K) || N == 0 || K == 0) return size;
     glu_fp8_plan p;
     const glu_status st = copy_plan(mats, M, N, K, out_dtype, &p, bytes);
     if (st != GLU_OK) *bytes = 0;

@@ -316,7 +316,8 @@ def _product_workspace(mats: int, M: int, N: int, K: int, dt: int, fast: bool) -
     """Workspace bytes of a call on this layout: of the fast kernels, of aligned copies, or of reading in place."""
     if fast:
         return _bytes("glu_fp8_product_workspace", mats, M, N, K, dt, None)
-    return _bytes("glu_fp8_copy_workspace" if M > 16 else "glu_fp8_workspace", mats, M, N, K, dt)
+    return (_bytes("glu_fp8_copy_workspace", mats, M, N, K, dt)  # 0: such a call is never copied
+            or _bytes("glu_fp8_workspace", mats, M, N, K, dt))
 
 
 def _fast_layout(K: int, *operands) -> bool:

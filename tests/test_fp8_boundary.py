@@ -206,6 +206,26 @@ def test_copy_workspace(lib):
     assert need("glu_fp8_workspace", 2, 1 << 30, 1 << 30, 128)[0] == SHAPE
 
 
+def test_no_copies_past_the_tile_kernels_strides(lib):
+    """The tile kernel's row offsets are 32 bits wide: a row longer than the fast layout's longest stride is never
+    copied for it, and a call from Python brings the workspace of the kernel that reads in place."""
+    def need(query, *size):
+        b = ctypes.c_int64(-1)
+        return getattr(lib, query)(*size, ctypes.byref(b)), b.value
+    longest = 1 << 23
+    for mats in (1, 2):
+        for t in (BF16, FP32, E4M3):
+            assert need("glu_fp8_copy_workspace", mats, 17, 5, longest - 1, t)[1] >= (17 + mats * 5) * longest
+            assert need("glu_fp8_copy_workspace", mats, 17, 5, longest, t)[1] >= (17 + mats * 5) * longest
+            for M, N, K in ((17, 5, longest + 1), (17, 5, longest + 16), (40, 200, 1 << 26), (17, 32, 1 << 28),
+                            (4096, 256, (1 << 24) + (1 << 18)), (17, 256, (1 << 25) + (1 << 20))):
+                assert need("glu_fp8_copy_workspace", mats, M, N, K, t) == (OK, 0)
+                plan = fp8.ProductPlan()
+                assert lib.glu_fp8_product_plan(mats, M, N, K, t, 0, ctypes.byref(plan)) == OK
+                assert fp8.KERNEL_NAMES[plan.kernel] == "any"
+                assert fp8._product_workspace(mats, M, N, K, t, False) >= plan.workspace_bytes
+
+
 def test_workspace_of_the_fast_layout(lib):
     """A prefill that ends in e4m3 by itself needs none on the fast layout."""
     need = ctypes.c_int64(-1)

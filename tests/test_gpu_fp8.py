@@ -218,6 +218,31 @@ def test_copied_layouts(M, N, K, pad, mats):
         check(kind + " in place", place, want, err)
 
 
+def test_long_contraction():
+    """Rows so far apart that 32-bit offsets within a tile would wrap: every row is read at its own place."""
+    M, N, K = 17, 128, (1 << 25) + (1 << 20) + 5
+    print(f"[long contraction] M={M} N={N} K={K}", flush=True)
+    g = gen(1)
+    # positive values of two neighbouring codes, in rows that differ by 2^(1/2) or more from the next 15
+    x = torch.randint(0x30, 0x32, (M, K), generator=g, device=DEV, dtype=torch.uint8)
+    w = torch.randint(0x20, 0x22, (N, K), generator=g, device=DEV, dtype=torch.uint8)
+    w += (4 * (torch.arange(N, device=DEV) % 16)).to(torch.uint8)[:, None]
+    x, w = x.view(E4M3), w.view(E4M3)
+    sx = torch.rand(M, ref.groups(K), generator=g, device=DEV) + 0.5
+    sw = torch.rand(1, ref.groups(K), generator=g, device=DEV) + 0.5
+    want = torch.zeros(M, N, dtype=torch.float64, device=DEV)
+    step = 1 << 20
+    for k in range(0, K, step):
+        part = slice(k, min(k + step, K))
+        n, blocks = part.stop - k, slice(k // 128, ref.groups(part.stop))
+        want += (x[:, part].double() * ref.per_element(sx[:, blocks].double(), M, n, False)) @ (
+            w[:, part].double() * ref.per_element(sw[:, blocks].double(), N, n, True)).t()
+    got = glu.fp8_linear(x, sx, w, sw, out_dtype=torch.float32)
+    torch.cuda.synchronize()
+    # all terms are positive: one addition per K-block and those of product64
+    ref.check_store("fp32", got, want, ref.U * (ref.groups(K) + 100) * want)
+
+
 def plans():
     """Every kernel the library can launch, at sizes past and inside its tiles, with and without split sums."""
     out = []
