@@ -65,17 +65,18 @@ struct PartSource {
     }
 };
 
-// 4 waves; a wave takes 512 columns (4 groups) of `R` rows
+// 4 waves; a wave takes 512 columns (4 groups) of `R` rows, the launch's first of which is row_base
 template <class Src, class Out, int R>
 __global__ void __launch_bounds__(256)
-convert_rows_kernel(Src src, void* out, int64_t ldo, float* scale, int64_t lds, int M, int K, int col_blocks)
+convert_rows_kernel(Src src, void* out, int64_t ldo, float* scale, int64_t lds, int M, int K, int col_blocks,
+                    int row_base)
 {
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int rb = blockIdx.x / col_blocks, cb = blockIdx.x - rb * col_blocks;
     const int c = cb * 64 + lane;
     const int n = K - 8 * c;
-    const int row0 = (rb * 4 + wave) * R;
+    const int row0 = row_base + (rb * 4 + wave) * R;
     float v[R][8];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
@@ -149,11 +150,11 @@ quantize_blocks_kernel(const T* __restrict__ w, int64_t ldw, uint8_t* __restrict
 // A lane copies 16 bytes of each of 4 rows, all loaded before the first is stored.
 __global__ void __launch_bounds__(256)
 copy_rows_kernel(const uint8_t* __restrict__ x, int64_t ldx, uint8_t* __restrict__ out, int kp, int rows, int K,
-                 int col_blocks)
+                 int col_blocks, int row_base)
 {
     const int rb = blockIdx.x / col_blocks, cb = blockIdx.x - rb * col_blocks;
     const int off = 16 * (cb * 64 + (threadIdx.x & 63));
-    const int row0 = (rb * 4 + (threadIdx.x >> 6)) * kRowsPerWave;
+    const int row0 = row_base + (rb * 4 + (threadIdx.x >> 6)) * kRowsPerWave;
     if (off >= kp) return;
     raw4_t v[kRowsPerWave];
 #pragma unroll
@@ -176,19 +177,33 @@ copy_rows_kernel(const uint8_t* __restrict__ x, int64_t ldx, uint8_t* __restrict
     }
 }
 
+// Launches over `rows` rows, `per_block` a workgroup of 256 threads and col_blocks workgroups wide, with the workgroups and
+// the first row of each: a grid holds fewer than 2^32 threads, which takes more than one launch from 2^28 rows on.
+template <class F>
+void by_rows(int rows, int per_block, int col_blocks, const F& launch)
+{
+    const int64_t blocks = ((int64_t)rows + per_block - 1) / per_block, fit = 0xffffffffLL / 256 / col_blocks;
+    for (int64_t b = 0; b < blocks; b += fit) {
+        launch(dim3((unsigned)((blocks - b < fit ? blocks - b : fit) * col_blocks)), (int)(b * per_block));
+    }
+}
+
 // rows per wave: one while the rows would not fill the card otherwise
 template <class Out, class Src>
 hipError_t convert_rows(const Src& src, void* out, int64_t ldo, float* scale, int64_t lds, int M, int K,
                         hipStream_t stream)
 {
     const int col_blocks = (K + 511) / 512;
-    const auto blocks = [&](int r) { return (int64_t)((M + 4 * r - 1) / (4 * r)) * col_blocks; };
-    if (blocks(kRowsPerWave) >= 1024) {
-        hipLaunchKernelGGL((convert_rows_kernel<Src, Out, kRowsPerWave>), dim3((unsigned)blocks(kRowsPerWave)),
-                           dim3(256), 0, stream, src, out, ldo, scale, lds, M, K, col_blocks);
+    if (((int64_t)M + 4 * kRowsPerWave - 1) / (4 * kRowsPerWave) * col_blocks >= 1024) {
+        by_rows(M, 4 * kRowsPerWave, col_blocks, [&](dim3 grid, int row) {
+            hipLaunchKernelGGL((convert_rows_kernel<Src, Out, kRowsPerWave>), grid, dim3(256), 0, stream, src, out, ldo,
+                               scale, lds, M, K, col_blocks, row);
+        });
     } else {
-        hipLaunchKernelGGL((convert_rows_kernel<Src, Out, 1>), dim3((unsigned)blocks(1)), dim3(256), 0, stream, src,
-                           out, ldo, scale, lds, M, K, col_blocks);
+        by_rows(M, 4, col_blocks, [&](dim3 grid, int row) {
+            hipLaunchKernelGGL((convert_rows_kernel<Src, Out, 1>), grid, dim3(256), 0, stream, src, out, ldo, scale,
+                               lds, M, K, col_blocks, row);
+        });
     }
     return hipGetLastError();
 }
@@ -229,9 +244,9 @@ hipError_t quantize_blocks_launch(int dtype, const void* w, int64_t ldw, uint8_t
 hipError_t copy_rows_launch(const uint8_t* x, int64_t ldx, uint8_t* out, int kp, int rows, int K, hipStream_t stream)
 {
     const int col_blocks = (kp + 1023) / 1024;
-    const int64_t row_blocks = ((int64_t)rows + 4 * kRowsPerWave - 1) / (4 * kRowsPerWave);
-    hipLaunchKernelGGL(copy_rows_kernel, dim3((unsigned)(row_blocks * col_blocks)), dim3(256), 0, stream, x, ldx, out,
-                       kp, rows, K, col_blocks);
+    by_rows(rows, 4 * kRowsPerWave, col_blocks, [&](dim3 grid, int row) {
+        hipLaunchKernelGGL(copy_rows_kernel, grid, dim3(256), 0, stream, x, ldx, out, kp, rows, K, col_blocks, row);
+    });
     return hipGetLastError();
 }
 

@@ -96,6 +96,19 @@ def test_quantize_strides():
         assert (store[:, :7] == 0x11).all() and (store[:, 340:] == 0x11).all()
 
 
+def test_quantize_many_rows():
+    """More rows than one grid of threads holds."""
+    M = (1 << 28) + 5
+    print(f"[many rows] quantize M={M}", flush=True)
+    x = torch.randint(0x3f00, 0x4100, (M, 1), generator=gen(6), device=DEV, dtype=torch.int16).view(torch.bfloat16)
+    q, s = glu.fp8_quantize(x)
+    torch.cuda.synchronize()
+    assert (q.view(torch.uint8) == 0x7e).all()  # a group of one: 448 of its scale
+    for at in (0, (1 << 28) - 500, M - 500):
+        assert torch.equal(s[at:at + 500].cpu(), ref.scale_of(x[at:at + 500].float().cpu()))
+    assert ((s * 448 - x.float()).abs() <= 4 * ref.U * x.float()).all()
+
+
 def test_quantize_empty():
     for shape in ((0, 256), (4, 0)):
         q, s = glu.fp8_quantize(torch.empty(shape, dtype=torch.bfloat16, device=DEV))
@@ -241,6 +254,29 @@ def test_long_contraction():
     torch.cuda.synchronize()
     # all terms are positive: one addition per K-block and those of product64
     ref.check_store("fp32", got, want, ref.U * (ref.groups(K) + 100) * want)
+
+
+def test_many_rows():
+    """More rows than one grid of threads holds: of the operands' copies, and of a product's end."""
+    M, N, K = 17, (1 << 28) + 5, 17
+    print(f"[many rows] M={M} N={N} K={K}", flush=True)
+    g = gen(2)
+    x = torch.randint(0x20, 0x50, (M, K), generator=g, device=DEV, dtype=torch.uint8).view(E4M3)
+    w = torch.randint(0x20, 0x50, (N, K), generator=g, device=DEV, dtype=torch.uint8).view(E4M3)
+    sx = torch.rand(M, 1, generator=g, device=DEV) + 0.5
+    sw = torch.rand(ref.groups(N), 1, generator=g, device=DEV) + 0.5
+    got = glu.fp8_linear(x, sx, w, sw)
+    torch.cuda.synchronize()
+    for at in (0, 128 * 100000, (1 << 28) - 512, N // 128 * 128 - 512):  # whole blocks of 128 from there on
+        part = slice(at, min(at + 700, N))
+        want, err = ref.product64(x, sx, w[part], sw[at // 128:ref.groups(part.stop)])
+        ref.check_store("bf16", got[:, part], want, err)
+    del got, w, sw
+    M, empty = (1 << 28) + 5, torch.empty(0, dtype=torch.uint8, device=DEV).view(E4M3)
+    y = glu.fp8_linear(empty.view(M, 0), torch.ones(M, 0, device=DEV), empty.view(1, 0), torch.ones(1, 0, device=DEV),
+                       out=torch.full((M, 1), 4.0, dtype=torch.bfloat16, device=DEV))
+    torch.cuda.synchronize()
+    assert (y == 0).all()
 
 
 def plans():
