@@ -344,14 +344,14 @@ norm_grad_long_dw_kernel(NormGradArgs a, int teams)
 }
 
 // dw[k] = T(sum of the teams' partials, lanes of a column striding the teams, then a tree over the lanes); no
-// teams: +0. 32 columns (a 128-byte line of a partial) x 32 lanes per column.
+// teams: +0. 32 columns (a 128-byte line of a partial) x 32 lanes per column, the launch's from k_base on.
 template <class T>
 __global__ void __launch_bounds__(1024)
-norm_grad_dw_kernel(const float* __restrict__ part, void* dw, int K, int teams)
+norm_grad_dw_kernel(const float* __restrict__ part, void* dw, int K, int teams, int k_base)
 {
     __shared__ float red[32][33];
     const int col = threadIdx.x & 31, ln = threadIdx.x >> 5;
-    const int k = blockIdx.x * 32 + col;
+    const int k = k_base + blockIdx.x * 32 + col;
     float s = 0.0f;
     if (k < K) {
         // 8 loads in flight, those past the last team of the last team's value, which is not added
@@ -378,6 +378,7 @@ norm_grad_dw_kernel(const float* __restrict__ part, void* dw, int K, int teams)
 namespace {
 
 constexpr int kNormRows = 1 << 21;  // rows per launch: a grid holds fewer than 2^32 threads
+constexpr int kGradColumns = 1 << 26;  // columns per launch of the join of dw, 32 threads each: likewise
 constexpr int kNormMaxK = 64 * kNormMaxWaves * kNormMaxChunks * 8;  // a row in one workgroup's registers
 
 // Waves per row and chunks per lane.  One chunk while the rows are too few to fill the card (a row then takes
@@ -501,7 +502,11 @@ hipError_t norm_grad_launch_t(int dtype, const NormGradArgs& a, hipStream_t s)
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((norm_grad_dw_kernel<T>), dim3((a.K + 31) / 32), dim3(1024), 0, s, a.part, a.dw, a.K, parts);
+    for (int64_t k = 0; k < a.K; k += kGradColumns) {
+        const int columns = (int)(a.K - k < kGradColumns ? a.K - k : kGradColumns);
+        hipLaunchKernelGGL((norm_grad_dw_kernel<T>), dim3((columns + 31) / 32), dim3(1024), 0, s, a.part, a.dw, a.K,
+                           parts, (int)k);
+    }
     return hipGetLastError();
 }
 

@@ -103,6 +103,33 @@ def test_backward_past_the_cache(M, K, residual):
     ref.check_store("dweight", gw, dw, edw)
 
 
+def test_backward_many_columns():
+    """More columns than one grid of threads joins."""
+    M, K = 2, (1 << 27) + 33
+    print(f"[norm grad] M={M} K={K}", flush=True)
+    h, dy = tensors(M, K, torch.bfloat16, 8, 3.0, 0.1)
+    w = weight(K, torch.bfloat16, 8)
+    rstd = torch.rsqrt(h.double().square().mean(1) + EPS).float()
+    gx, gw = glu.add_rms_norm_backward(dy, h, w, rstd)
+    torch.cuda.synchronize()
+    # grad64 with the length of this mean's sum: K / 1024 steps a lane, 6 + 16 across lanes and waves
+    r = rstd.double()[:, None]
+    sums = [(dy[m].double() * w.double() * h[m].double() * r[m]) for m in range(M)]
+    mean = torch.stack([s.mean() for s in sums])[:, None]
+    near = torch.stack([s.abs().mean() for s in sums])[:, None] * ref.U * (K / 1024 + 40)
+    del sums
+    for at in (0, (1 << 26) - 300, K - 600):
+        part = slice(at, at + 600)
+        xh, g = h[:, part].double() * r, dy[:, part].double()
+        a = g * w[part].double()
+        ref.check_store("dx", gx[:, part], r * (a - xh * mean), r * (4 * ref.U * a.abs() + xh.abs() * (near + 4 * ref.U * mean.abs())))
+        ref.check_store("dweight", gw[part], (g * xh).sum(0), 42 * ref.U * (g * xh).abs().sum(0))
+    terms = dy.float() * (h.float() * rstd[:, None])
+    # both sums in fp32
+    tol = 1.01 * ref.half(torch.bfloat16) * terms.sum(0).abs() + 2 * 42 * ref.U * terms.abs().sum(0)
+    assert ((gw.float() - terms.sum(0)).abs() <= tol).all()
+
+
 def test_gradient_against_differences():
     """The backward's formula against central differences of the 64-bit definition, and the kernels'
     gradient through autograd against the same differences."""
