@@ -398,6 +398,31 @@ def test_product_special_values(M):
     assert (q.view(torch.uint8) == 0).all() and (s == ref.TINY).all()
 
 
+@pytest.mark.parametrize("M", [1, 4, 9, 40])
+@pytest.mark.parametrize("blocks", [1, 2, 3, 5, 6, 7])
+def test_scales_past_fp32(M, blocks):
+    """Scales of the last K-block that are infinite, or whose product is: its sum goes to its own infinity, also where
+    a kernel's steps reach past it."""
+    N, K = 20, 128 * blocks - 16
+    x = torch.full((M, K), 0x38, dtype=torch.uint8, device=DEV)  # 1
+    w = x[:1].repeat(N, 1)
+    w[N // 2:] = 0xb8  # -1
+    sx = torch.ones(M, blocks, device=DEV)
+    sw = torch.ones(1, blocks, device=DEV)
+    want = torch.where(torch.arange(N, device=DEV) < N // 2, 1.0, -1.0).expand(M, N) * float("inf")
+    for a, b in ((float("inf"), 1.0), (1.0, float("inf")), (1e30, 1e30)):
+        sx[:, -1], sw[:, -1] = a, b
+        for plan in (None, fp8.ProductPlan(2, 16, 3, 1), fp8.ProductPlan(3, 4, 0, 1)):
+            y = glu.fp8_linear(x.view(E4M3), sx, w.view(E4M3), sw, out_dtype=torch.float32, plan=plan)
+            torch.cuda.synchronize()
+            assert torch.equal(y, want)
+        up = x[:1].repeat(N, 1).view(E4M3)
+        one = torch.ones_like(sw)
+        y = glu.fp8_dual_glu(x.view(E4M3), torch.ones_like(sx), up, one, w.view(E4M3), sw * sx[:1], out_dtype=torch.float32)
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
+
+
 def test_silu_range():
     """The activation over the whole range of gates: large either way, infinite, zero."""
     gates = torch.tensor([0.0, 1e-6, -1e-6, 1.0, -1.0, 20.0, -20.0, 87.0, -87.0, 88.5, -88.5, 300.0, -300.0, 1e30, -1e30,
