@@ -8,6 +8,7 @@
 #include <stdint.h>
 
 #include <ATen/hip/EmptyTensor.h>
+#include <c10/core/GradMode.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -138,6 +139,12 @@ PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t n)
         const double eps = PyFloat_Check(a[2]) ? PyFloat_AS_DOUBLE(a[2]) : -1.0;
         if (!w || eps < 0.0) Py_RETURN_NONE;
         const bool has = a[3] != Py_None, e4m3 = a[4] == Py_True;
+        // operands that autograd would record: fp8.py has them differentiated, or refuses
+        if (c10::GradMode::is_enabled()) {
+            for (PyObject* o : {a[0], a[1], a[3]}) {
+                if (THPVariable_Check(o) && THPVariable_Unpack(o).requires_grad()) Py_RETURN_NONE;
+            }
+        }
         void* res = nullptr;
         int64_t ldr = 0;
         if (has) {

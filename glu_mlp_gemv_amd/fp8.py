@@ -11,7 +11,7 @@ Block-scaled e4m3: a stored ``torch.float8_e4m3fn`` value q stands for ``q * sca
 group by group (``scale.t()`` is contiguous) and accept at any strides; weights [N, K] one per block of
 128 x 128, [ceil(N / 128), ceil(K / 128)].
 
-Row-strided views are taken at the stride they report.  With ``stream`` the work runs there and the
+The conversions and products carry no gradient.  Row-strided views are taken at the stride they report.  With ``stream`` the work runs there and the
 results belong to that stream's memory pool; the tensors given are recorded on it.
 """
 from __future__ import annotations
@@ -195,6 +195,12 @@ def _norm(x, weight, eps, residual, out, scale_out, residual_out, return_rstd, s
     return out, scale, h, rstd
 
 
+def _wants_gradient(x, weight, residual) -> bool:
+    """Whether autograd would record a call on these operands (none in a Function's own forward)."""
+    return torch.is_grad_enabled() and (getattr(x, "requires_grad", False) or getattr(weight, "requires_grad", False)
+                                        or getattr(residual, "requires_grad", False))
+
+
 def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: Optional[torch.Tensor] = None,
                  out: Optional[torch.Tensor] = None, residual_out: Optional[torch.Tensor] = None,
                  return_rstd: bool = False, stream: Optional[torch.cuda.Stream] = None):
@@ -202,12 +208,20 @@ def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: Op
 
     x and residual [M, K], weight [K], all bf16, fp16 or fp32; rms(h) = sqrt(mean(h^2) + eps) per
     row, in fp32, and y rounded once.  ``residual_out`` may be ``residual`` or ``x`` (in place).  With
-    ``return_rstd`` also 1 / rms [M] in fp32, which ``add_rms_norm_backward`` takes.
+    ``return_rstd`` also 1 / rms [M] in fp32, which ``add_rms_norm_backward`` takes.  Operands that require a gradient
+    have one, through ``autograd.rms_norm``; together with an output, stream or rstd they are refused.
     """
-    if out is None and residual_out is None and stream is None and not return_rstd:
+    plain = out is None and residual_out is None and stream is None and not return_rstd
+    if plain:
         r = (_fast or _load_fast()).norm(x, weight, eps, residual, False)
         if _taken(r):
             return r[0], x if residual is None else r[1]
+    if _wants_gradient(x, weight, residual):
+        if not plain:
+            raise RuntimeError("add_rms_norm with out, residual_out, return_rstd or stream has no gradient, and an operand "
+                               "requires one: call it without them, or under torch.no_grad()")
+        from .autograd import rms_norm
+        return rms_norm(x, weight, eps, residual=residual)
     out, _, h, rstd = _norm(x, weight, eps, residual, out, None, residual_out, return_rstd, stream, False)
     return (out, h, rstd) if return_rstd else (out, h)
 
@@ -216,11 +230,17 @@ def add_rms_norm_fp8(x: torch.Tensor, weight: torch.Tensor, eps: float, residual
                      out: Optional[torch.Tensor] = None, scale_out: Optional[torch.Tensor] = None,
                      residual_out: Optional[torch.Tensor] = None, return_rstd: bool = False,
                      stream: Optional[torch.cuda.Stream] = None):
-    """(q, scale, h): ``add_rms_norm`` with y converted to block-scaled e4m3 before any rounding to x's type."""
+    """(q, scale, h): ``add_rms_norm`` with y converted to block-scaled e4m3 before any rounding to x's type.
+
+    Has no gradient: operands that require one are refused where autograd records.
+    """
     if out is None and scale_out is None and residual_out is None and stream is None and not return_rstd:
         r = (_fast or _load_fast()).norm(x, weight, eps, residual, True)
         if _taken(r):
             return r[0], r[2], x if residual is None else r[1]
+    if _wants_gradient(x, weight, residual):
+        raise RuntimeError("add_rms_norm_fp8 has no gradient, and an operand requires one: call it under torch.no_grad(), or "
+                           "train with autograd.rms_norm")
     out, scale, h, rstd = _norm(x, weight, eps, residual, out, scale_out, residual_out, return_rstd, stream, True)
     return (out, scale, h, rstd) if return_rstd else (out, scale, h)
 

@@ -4,6 +4,8 @@
 token, norm -> gate and up -> down in three calls whose intermediate activations stay in block-scaled e4m3:
 
     h = x + residual;  y = down(silu(gate(norm(h))) * up(norm(h)))
+
+It infers: there is no gradient, and inputs that require one are refused where autograd records.
 """
 from __future__ import annotations
 

@@ -250,3 +250,33 @@ def test_python_refuses_cpu_tensors():
         glu.fp8_linear(x.to(fp8.E4M3), torch.ones(2, 1), x.to(fp8.E4M3), torch.ones(1, 1))
     with pytest.raises(TypeError):
         glu.add_rms_norm([1.0], x[0], 1e-6)
+
+
+def test_forms_without_a_gradient_refuse_operands_that_require_one():
+    import torch
+
+    import glu_mlp_gemv_amd as glu
+    for which in range(3):
+        x, w, r = torch.zeros(2, 128, dtype=torch.bfloat16), torch.ones(128, dtype=torch.bfloat16), torch.zeros(2, 128).bfloat16()
+        (x, w, r)[which].requires_grad_()
+        for call in (lambda: glu.add_rms_norm_fp8(x, w, 1e-6, residual=r),
+                     lambda: glu.add_rms_norm_fp8(x, w, 1e-6, residual=r, return_rstd=True),
+                     lambda: glu.add_rms_norm(x, w, 1e-6, residual=r, out=torch.zeros_like(x)),
+                     lambda: glu.add_rms_norm(x, w, 1e-6, residual=r, residual_out=torch.zeros_like(x)),
+                     lambda: glu.add_rms_norm(x, w, 1e-6, residual=r, return_rstd=True)):
+            with pytest.raises(RuntimeError, match="gradient"):
+                call()
+            with torch.no_grad(), pytest.raises(ValueError, match="GPU"):  # as far as a host goes
+                call()
+
+
+def test_mlp_refuses_inputs_that_require_a_gradient():
+    import torch
+
+    from glu_mlp_gemv_amd.mlp import Fp8GluMlp
+    mlp = Fp8GluMlp.__new__(Fp8GluMlp)  # what __call__ reads before its first kernel
+    mlp.eps, mlp.norm_weight = 1e-6, torch.ones(128, dtype=torch.bfloat16)
+    x = torch.zeros(2, 128, dtype=torch.bfloat16)
+    for a, b in ((x.clone().requires_grad_(), None), (x, x.clone().requires_grad_())):
+        with pytest.raises(RuntimeError, match="gradient"):
+            mlp(a, b)

@@ -185,6 +185,36 @@ def test_autograd_forms():
     assert torch.equal(x.grad, torch.ones_like(x)) and torch.equal(r.grad, torch.ones_like(x)) and w.grad is None
 
 
+@pytest.mark.parametrize("leaves", ["xwr", "x", "w", "r"])
+@pytest.mark.parametrize("residual", [True, False])
+def test_public_norm_keeps_gradients(residual, leaves):
+    """add_rms_norm on operands that require a gradient is autograd's rms_norm, bit for bit."""
+    from glu_mlp_gemv_amd.autograd import rms_norm
+    made = tensors(9, 300, torch.bfloat16, 7, 1.0, 1.0, 1.0)
+    w = weight(300, torch.bfloat16, 7)
+
+    def grads(f):
+        x, r, dy = (t.clone() for t in made)
+        v = {"x": x, "w": w.clone(), "r": r}
+        for name in leaves:
+            v[name].requires_grad_()
+        y, h = f(v["x"], v["w"], EPS, residual=v["r"] if residual else None)
+        out = [y.detach().clone(), h.detach().clone()]
+        if y.requires_grad:
+            (y * dy + h).sum().backward()
+        torch.cuda.synchronize()
+        return out, [v[name].grad for name in leaves]
+    (y, h), got = grads(glu.add_rms_norm)
+    (wy, wh), want = grads(rms_norm)
+    assert torch.equal(y, wy) and torch.equal(h, wh)
+    for name, a, b in zip(leaves, got, want):
+        assert (a is None) == (name == "r" and not residual)
+        assert a is None or torch.equal(a, b)
+    with torch.no_grad():
+        (y, h), got = grads(glu.add_rms_norm)
+    assert torch.equal(y, wy) and got == [None] * len(leaves)
+
+
 def test_gradient_of_the_gradient_is_refused():
     from glu_mlp_gemv_amd.autograd import rms_norm
     x, r = tensors(5, 256, torch.float32, 6, 1.0, 1.0)
