@@ -82,7 +82,6 @@ def groups(n: int) -> int:
 
 
 _INPUTS = (torch.bfloat16, torch.float16, torch.float32)
-_raw_stream = torch._C._cuda_getCurrentRawStream  # current_stream().cuda_stream without building a Stream object
 
 
 def _refuse(name: str, t, dtypes, shape, dev):
@@ -153,7 +152,8 @@ def _on(dev, stream, *tensors):
     if stream is None:
         index = dev.index
         ctx = _NO_CONTEXT if index == torch.cuda.current_device() else torch.cuda.device(dev)
-        return ctx, _raw_stream(index)
+        # current_stream().cuda_stream without building a Stream object; a torch without a GPU backend has no such name
+        return ctx, torch._C._cuda_getCurrentRawStream(index)
     if stream.device != dev:
         raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
     for t in tensors:

@@ -280,3 +280,13 @@ def test_mlp_refuses_inputs_that_require_a_gradient():
     for a, b in ((x.clone().requires_grad_(), None), (x, x.clone().requires_grad_())):
         with pytest.raises(RuntimeError, match="gradient"):
             mlp(a, b)
+
+
+def test_host_calls_load_on_a_torch_without_a_gpu_backend():
+    """The library and its planners are loaded where torch has no GPU backend's names."""
+    import subprocess
+    import sys
+    code = ("import torch\nfor n in [n for n in dir(torch._C) if n.startswith('_cuda_') or n.startswith('_hip_')]: delattr(torch._C, n)\n"
+            "from glu_mlp_gemv_amd import api, fp8\napi.library()\nprint(api.plan(1, 64, 64)['kernel'], fp8.product_plan(1, 1, 64, 64)['kernel'])")
+    res = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=api.__file__.rsplit("/", 2)[0])
+    assert res.returncode == 0, res.stderr
