@@ -82,19 +82,23 @@ def build_binding(verbose: bool = False) -> str:
 
 
 def build(verbose: bool = False, jobs: int = 8) -> str:
-    """Compile every HIP source, link libglu_gemv.so and compile the torch binding; returns the library's path."""
+    """Compile every HIP source, link libglu_gemv.so and compile the torch binding; returns the library's path.
+
+    The library is linked whatever becomes of the binding, whose failure is raised after it: callers of the C ABI need
+    no torch headers.
+    """
     os.makedirs(BUILD_DIR, exist_ok=True)
     srcs = sources()
     with ThreadPoolExecutor(max_workers=max(1, min(jobs, len(srcs)))) as ex:
         binding = ex.submit(build_binding, verbose)
         objs = list(ex.map(lambda s: _compile(s, verbose), srcs))
-        binding.result()
     tmp = LIBRARY + ".tmp"
     cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs]
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIBRARY)
+    binding.result()
     return LIBRARY
 
 

@@ -290,3 +290,23 @@ def test_host_calls_load_on_a_torch_without_a_gpu_backend():
             "from glu_mlp_gemv_amd import api, fp8\napi.library()\nprint(api.plan(1, 64, 64)['kernel'], fp8.product_plan(1, 1, 64, 64)['kernel'])")
     res = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=api.__file__.rsplit("/", 2)[0])
     assert res.returncode == 0, res.stderr
+
+
+def test_the_library_is_built_without_the_binding(monkeypatch, tmp_path):
+    """A torch binding that does not compile is an error, after the library has been linked."""
+    from glu_mlp_gemv_amd import build
+
+    def no_binding(verbose=False):
+        raise RuntimeError("no torch headers")
+
+    def link(cmd, check):
+        with open(cmd[cmd.index("-o") + 1], "w") as f:
+            f.write("library")
+    monkeypatch.setattr(build, "BUILD_DIR", str(tmp_path))
+    monkeypatch.setattr(build, "LIBRARY", str(tmp_path / "lib.so"))
+    monkeypatch.setattr(build, "_compile", lambda src, verbose: src + ".o")
+    monkeypatch.setattr(build, "build_binding", no_binding)
+    monkeypatch.setattr(build.subprocess, "run", link)
+    with pytest.raises(RuntimeError, match="torch headers"):
+        build.build()
+    assert (tmp_path / "lib.so").read_text() == "library"
