@@ -1,7 +1,7 @@
 """Host-side AddressSanitizer and UndefinedBehaviorSanitizer run of the C ABI and the oracle.
 
 Builds, beside the normal artefacts (under _build/san, not shipped):
-  * the C ABI's host code (glu_api.hip: argument validation and every launch planner, and
+  * the C ABI's host code (glu_api.hip and glu_fp8_api.hip: argument validation and every launch planner, and
     glu_noalloc.hip) compiled with -fsanitize=address,undefined for the host pass only (each
     -fsanitize= after -Xarch_host; the GPU code is built exactly as usual), linked with the
     other, unchanged objects of the library into libglu_gemv_san.so;
@@ -24,10 +24,10 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SAN_DIR = os.path.join(hip_build.BUILD_DIR, "san")
 LLVM = "/opt/rocm/llvm/bin"
-SAN_SOURCES = ("glu_api.hip", "glu_noalloc.hip")
+SAN_SOURCES = ("glu_api.hip", "glu_fp8_api.hip", "glu_noalloc.hip")
 HOST_SAN = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined",
             "-Xarch_host", "-fno-sanitize-recover=all", "-Xarch_host", "-fno-omit-frame-pointer"]
-TESTS = ["tests/test_boundary.py", "tests/test_plan_sweep.py", "tests/test_oracle_pins.py"]
+TESTS = ["tests/test_boundary.py", "tests/test_fp8_boundary.py", "tests/test_plan_sweep.py", "tests/test_oracle_pins.py"]
 
 
 def _run(cmd, **kw):

@@ -310,3 +310,14 @@ def test_the_library_is_built_without_the_binding(monkeypatch, tmp_path):
     with pytest.raises(RuntimeError, match="torch headers"):
         build.build()
     assert (tmp_path / "lib.so").read_text() == "library"
+
+
+def test_sanitizers_cover_every_c_entry():
+    import os
+
+    from glu_mlp_gemv_amd import build, sanitize
+    for src in build.sources():
+        with open(src) as f:
+            if 'extern "C"' in f.read():
+                assert os.path.basename(src) in sanitize.SAN_SOURCES
+    assert "tests/" + os.path.basename(__file__) in sanitize.TESTS
