@@ -183,10 +183,13 @@ void choose(int mats, int64_t M, int64_t N, int64_t K, int out_dtype, bool fast,
         return;
     }
     if (M <= 16) {
-        // 4 weight rows a workgroup for one or two rows of x, and up to 4 for two matrices or where 16 would leave
-        // CUs idle; else 16 (4 rows, K = 12288 N = 4096: 13.1 us against 15.8; dual K = 2560 N = 9216: 13.2 against
-        // 12.5, K = 8192 N = 512: 8.0 against 4.6, K = 9216 N = 2560: 9.8 against 9.6)
-        const bool few = M <= 2 || (M <= 4 && (mats == 2 || N <= 2560));
+        // 4 weight rows a workgroup for one or two rows of x, and up to 4 for two matrices or where 16 would leave a
+        // third of the CUs idle; else 16.  4 rows, in 4 and in 16: K = 9216 N = 2048 7.2 and 9.1 us, N = 2560 (160 of 256
+        // CUs) 9.9 and 10.0, N = 2816 (176) 10.9 and 10.1, N = 3328 13.1 and 10.2; K = 17408 N = 2560 17.1 and 17.2, N =
+        // 2816 17.2 and 16.8, N = 4096 21.6 and 16.8.  Dual, which goes up and down with N: K = 9216 N = 512 8.0 and 12.9,
+        // N = 2048 11.2 and 14.6, N = 4096 19.4 and 17.1, N = 6144 25.7 and 28.2, N = 9216 38.0 and 39.2, N = 12288 47.1
+        // and 42.9
+        const bool few = M <= 2 || (M <= 4 && (mats == 2 || 3 * ceil_div(N, 16) <= 2 * kCUs));
         if (!few && best_tile(mats, M, N, K, out_dtype, p) < stream_cost(mats, M, N, K, out_dtype)) return;
         p->kernel = GLU_FP8_KERNEL_STREAM;
         p->tile = few ? 4 : 16;

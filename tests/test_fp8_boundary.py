@@ -172,6 +172,17 @@ def test_plans_cover_every_size():
     assert fp8.product_plan(1, 5, 5, 0)["kernel_name"] == "zero"
 
 
+def test_few_rows_take_the_narrow_form_where_the_other_leaves_cus_idle():
+    """3 or 4 rows of one matrix: 4 weight rows a workgroup where 16 would have work for two thirds of 256 CUs or less."""
+    for K in (1024, 9216):
+        for M in (1, 2, 3, 4, 5):
+            for N in (16, 2560, 2561, 2720, 2721, 2816, 4096):
+                p = fp8.product_plan(1, M, N, K)
+                narrow = M <= 2 or M <= 4 and 3 * -(-N // 16) <= 512
+                assert p["kernel_name"] == "tile" or p["tile"] == (4 if narrow else 16)
+                assert p["kernel_name"] == "stream" or M > 2 and not narrow
+
+
 def test_workspace_covers_either_layout(lib):
     import torch
     need = ctypes.c_int64()
