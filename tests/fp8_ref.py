@@ -134,3 +134,23 @@ def check_e4m3(name, q, s, ref, err):
     tol = err + half(E4M3) * (ref.abs() + err) + (floor_of(E4M3) + 448 * 4 * U) * se
     bad = ~(d <= tol)
     assert not bad.any(), f"{name}: {int(bad.sum())} of {bad.numel()} outside"
+
+
+def rms(t):
+    return float(t.double().square().mean().sqrt())
+
+
+def check_unit_rms(name, got, ops):
+    """A 16-bit result of the 8-bit matrix path, of one product or of the pair's GLU, in the root mean square over
+    its outputs: the path cuts each product below 2^-13 of the largest of its 8 (half of what matrix_unit allows one
+    output), independently, which goes through silu(g) u to first order; then the fp32 steps' bound and the store's."""
+    y, e = product64(*ops[:4])
+    loss = matrix_unit(*ops[:4])[1] / 2
+    if len(ops) == 6:
+        u, eu = product64(*ops[:2], *ops[4:])
+        lu = matrix_unit(*ops[:2], *ops[4:])[1] / 2
+        s = torch.sigmoid(y)
+        loss = ((s * (1 + y * (1 - s)) * u * loss).square() + (y * s * lu).square()).sqrt()
+        y, e = glu64(y, e, u, eu)
+    off, most = rms(got.double() - y), rms(loss) + half(got.dtype) * rms(y) + rms(e) + floor_of(got.dtype)
+    assert off <= most, f"{name}: off by {off} in the root mean square, at most {most}"

@@ -310,6 +310,45 @@ def test_every_launch_shape(kernel, tile, width, splits, M, N, K, mats):
             assert same_bits(a, b), "a second call gives the same bits"
 
 
+def unit_cases():
+    """(M, N, K, plan) of 16-bit results on the 8-bit matrix path: as planned, every tile shape whole and split, weights read
+    past the caches, columns in two launches."""
+    out = [(M, N, K, None) for M, N, K in PRODUCTS if M > 16] + [(37, 12288, 4096, None), (203, 4096, 2048, None)]
+    for tile in range(5):
+        for splits in (1, 3):
+            out += [(M, N, K, (3, tile, 0, splits)) for M, N, K in ((17, 130, 784), (130, 640, 1024), (300, 515, 400))]
+    out += [(20, 4105, 16400, (3, tile, 0, 1)) for tile in (2, 3, 4)]
+    out += [(150, 515, 784, (3, tile, 0, splits, 0, 0, columns)) for tile, splits, columns in ((0, 1, 256), (1, 2, 128),
+                                                                                             (4, 1, 384))]
+    return out
+
+
+@pytest.mark.parametrize("mats", [1, 2])
+@pytest.mark.parametrize("M,N,K,plan", unit_cases())
+def test_root_mean_square(M, N, K, plan, mats):
+    """The worst case that one output is allowed is far from what all of them lose together."""
+    ops = operands(M, N, K, M + N + K, mats)
+    for kind in ("bf16", "fp16"):
+        print(f"[rms] mats={mats} M={M} N={N} K={K} {kind} {plan}", flush=True)
+        got = run(ops, T[kind], plan=None if plan is None else fp8.ProductPlan(*plan))
+        torch.cuda.synchronize()
+        ref.check_unit_rms(kind, got, ops)
+
+
+@pytest.mark.parametrize("mats", [1, 2])
+@pytest.mark.parametrize("M", [40, 150])
+def test_root_mean_square_of_strided_rows(M, mats):
+    N, K = 300, 656
+    ops = operands(M, N, K, M, mats)
+    wide = [torch.nn.functional.pad(t.view(torch.uint8), (16, 80), value=0x7f).view(E4M3)[:, 16:16 + K] if t.dtype is E4M3
+            else torch.nn.functional.pad(t, (1, 2), value=float("nan"))[:, 1:1 + t.shape[1]] for t in ops]
+    for kind in ("bf16", "fp16"):
+        store = torch.full((M, N + 11), 3.0, dtype=T[kind], device=DEV)
+        got = run(wide, T[kind], out=store[:, 5:5 + N])
+        torch.cuda.synchronize()
+        ref.check_unit_rms(kind, got, ops)
+
+
 @pytest.mark.parametrize("mats", [1, 2])
 @pytest.mark.parametrize("tile", [2, 3, 4])
 def test_weights_past_the_cache(tile, mats):
