@@ -315,12 +315,28 @@ hipError_t run_product(int mats, const glu_fp8_plan& p, glu::Fp8Args a, int out_
     return glu::finish_launch(out_dtype, fin, s);
 }
 
-// A layout that is not fast, above 16 rows: where the workspace has room for them the operands are copied to the
-// fast layout first, behind the product's own part of it: 2048 rows, K = 4100 N = 4096 in 95 us against 470 in
-// place, dual 4096 rows, K = 5125 N = 17408 in 1.29 ms against 21.  The copies run on the bf16 unit, as the kernel in
-// place does.  A row too long for the fast layout's strides stays in place, whose kernel counts in 64 bits.
+// A layout that is not fast, above 16 rows: where the workspace has room for them the operands may be copied to the
+// fast layout first, behind the product's own part of it.  The copies run on the bf16 unit, as the kernel in place
+// does.  A row too long for the fast layout's strides stays in place, whose kernel counts in 64 bits.
 int64_t padded(int64_t K) { return (K + 15) / 16 * 16; }
-bool copies(int64_t M, int64_t K) { return M > 16 && padded(K) <= kMaxFastLd; }
+bool may_copy(int64_t M, int64_t K) { return M > 16 && padded(K) <= kMaxFastLd; }
+
+// Whether copies are expected to pay.  In place 16 rows of x pass over the weights at a time, more than twice as slowly
+// where addresses are no multiples of 4 bytes; a copy costs its launch and its bytes there and back.  Over 107 sizes of
+// 17 to 512 rows the choice is 11 % slower than the better at most.  Copied and in place, us: K = 4100 N = 4096 17 rows
+// 29.3 and 12.9, 64 rows 30.6 and 19.8, 128 rows 39.3 and 37.6, 256 rows 39.7 and 65.6, 2048 rows 95 and 470; K = 12290
+// N = 4096 17 rows 40.6 and 61.2; K = 1030 N = 1024 256 rows 19.8 and 12.5, 512 rows 19.9 and 24.3; dual K = 2561 N =
+// 9216 17 rows 43 and 63; dual K = 5125 N = 17408 4096 rows 1290 and 21000.
+constexpr double kPlaceAligned = 1.3e-7, kPlace = 3.6e-7, kCopy = 6.0, kCopyBytes = 3e6;
+bool copies_pay(int mats, int64_t M, int64_t N, int64_t K, int out_dtype, bool aligned)
+{
+    glu_fp8_plan p{};
+    const double copied = best_tile(mats, M, N, padded(K), out_dtype, &p) + kCopy * (mats + 1) +
+                          ((double)M + (double)mats * (double)N) * (double)K / kCopyBytes;
+    const double k = (double)(K < 2 * kGroup ? 2 * kGroup : K);  // fewer K-blocks leave waves idle
+    const double place = kLaunch + (double)ceil_div(M, 16) * (double)N * k * (mats + 1) * (aligned ? kPlaceAligned : kPlace);
+    return copied < place;
+}
 
 glu_status copy_plan(int mats, int64_t M, int64_t N, int64_t K, int out_dtype, glu_fp8_plan* p, int64_t* bytes)
 {
@@ -364,7 +380,9 @@ glu_status product_call(const glu_fp8_matrix* x, const glu_fp8_matrix* w0, const
     glu_fp8_plan p;
     bool copied = false;
     int64_t need = 0;
-    if (on && !fast && !asked && copies(M, K)) {
+    if (on && !fast && !asked && may_copy(M, K) &&
+        (product_plan(mats, M, N, K, out_dtype, false, nullptr, &p) != GLU_OK ||
+         copies_pay(mats, M, N, K, out_dtype, (bits & 3) == 0))) {
         st = copy_plan(mats, M, N, K, out_dtype, &p, &need);
         copied = st == GLU_OK && ws && ((uintptr_t)ws & 15) == 0 && ws_bytes >= need;
     }
@@ -595,10 +613,14 @@ glu_status glu_fp8_copy_workspace(int mats, int64_t M, int64_t N, int64_t K, int
     if (!bytes) return GLU_ERR_NULL_POINTER;
     *bytes = 0;
     const glu_status size = check_sizes(mats, M, N, K, out_dtype);
-    if (size != GLU_OK || !copies(M, K) || N == 0 || K == 0) return size;
+    if (size != GLU_OK || !may_copy(M, K) || N == 0 || K == 0) return size;
     glu_fp8_plan p;
     const glu_status st = copy_plan(mats, M, N, K, out_dtype, &p, bytes);
-    if (st != GLU_OK) *bytes = 0;
+    if (st != GLU_OK) {
+        *bytes = 0;
+    } else if (product_plan(mats, M, N, K, out_dtype, false, nullptr, &p) == GLU_OK && p.workspace_bytes > *bytes) {
+        *bytes = p.workspace_bytes;  // a call that is not copied after all
+    }
     return st;
 }
 

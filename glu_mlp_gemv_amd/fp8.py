@@ -403,7 +403,7 @@ def fp8_linear(x: torch.Tensor, x_scale: torch.Tensor, weight: torch.Tensor, wei
 
     Returns [M, N] in ``out_dtype`` (bf16, fp16, fp32), or for float8_e4m3fn the pair (q, scale).  fp32 accumulation
     over the K-blocks, one rounding.  K and the row strides should be multiples of 16 and the rows 16-byte
-    aligned; other layouts are copied first, or up to 16 rows of x read as they are, slower.
+    aligned; other layouts are read as they are, slower, or above 16 rows of x copied first where that is faster.
     """
     return _product(x, x_scale, (("weight", weight, weight_scale),), out_dtype, out, scale_out, plan, stream)
 

@@ -103,7 +103,7 @@ typedef struct glu_fp8_matrix {
  * group g of row m at out_scale[g * ld_scale + m].  K == 0 writes the conversion of +0.  Fast layout: data
  * 16-byte aligned, K and the row strides multiples of 16, strides at most 2^23; any other layout takes a
  * slower kernel, or, with more than 16 rows of x, K at most 2^23 and glu_fp8_copy_workspace() bytes of workspace, is
- * copied to the fast one there first; either way the sums are fp32.  workspace: glu_fp8_workspace() bytes, 16-byte
+ * copied to the fast one there first where that is expected to be faster; either way the sums are fp32.  workspace: glu_fp8_workspace() bytes, 16-byte
  * aligned (NULL if 0).
  */
 glu_status glu_fp8_linear(const glu_fp8_matrix* x, const glu_fp8_matrix* w, void* out, int64_t ldo, float* out_scale,
@@ -140,8 +140,8 @@ glu_status glu_fp8_product_plan(int mats, int64_t M, int64_t N, int64_t K, int o
  * plan NULL is what the fast layout needs, often less. */
 glu_status glu_fp8_workspace(int mats, int64_t M, int64_t N, int64_t K, int out_dtype, int64_t* bytes);
 
-/* Workspace bytes with which a call on a layout that is not fast copies its operands first; 0 where none does
- * (M <= 16, K > 2^23 or an empty product). */
+/* Workspace bytes that serve a call on a layout that is not fast whether it copies its operands first or not; 0 where
+ * none does (M <= 16, K > 2^23 or an empty product). */
 glu_status glu_fp8_copy_workspace(int mats, int64_t M, int64_t N, int64_t K, int out_dtype, int64_t* bytes);
 
 /*

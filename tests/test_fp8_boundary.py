@@ -217,6 +217,17 @@ def test_copy_workspace(lib):
     assert need("glu_fp8_workspace", 2, 1 << 30, 1 << 30, 128)[0] == SHAPE
 
 
+def test_copy_workspace_serves_a_call_in_place(lib):
+    """Where copies do not pay a call of the same workspace is read in place."""
+    b, plan = ctypes.c_int64(), fp8.ProductPlan()
+    for mats in (1, 2):
+        for M, N, K in ((17, 1, 1), (300, 4096, 100), (40, 5000, 17), (5000, 12288, 40)):
+            for t in (BF16, E4M3):
+                assert lib.glu_fp8_copy_workspace(mats, M, N, K, t, ctypes.byref(b)) == OK
+                assert lib.glu_fp8_product_plan(mats, M, N, K, t, 0, ctypes.byref(plan)) == OK
+                assert b.value >= plan.workspace_bytes and (t == BF16 or plan.workspace_bytes == mats * M * N * 4)
+
+
 def test_no_copies_past_the_tile_kernels_strides(lib):
     """The tile kernel's row offsets are 32 bits wide: a row longer than the fast layout's longest stride is never
     copied for it, and a call from Python brings the workspace of the kernel that reads in place."""

@@ -231,6 +231,23 @@ def test_copied_layouts(M, N, K, pad, mats):
         check(kind + " in place", place, want, err)
 
 
+@pytest.mark.parametrize("mats", [1, 2])
+@pytest.mark.parametrize("M,N,K,pad", [(700, 1000, 1001, 0), (515, 2100, 528, 3), (17, 4100, 6001, 0), (2050, 520, 1030, 4)])
+def test_copies_that_pay(M, N, K, pad, mats):
+    """Layouts that are not fast at sizes whose operands are copied."""
+    ops = [t if t.dtype is not E4M3 else torch.nn.functional.pad(t.view(torch.uint8), (0, pad), value=0x7f).view(E4M3)[:, :K]
+           for t in operands(M, N, K, K, mats)]
+    want, err = expected(ops)
+    for kind in ("bf16", "fp32", "e4m3"):
+        print(f"[copies] mats={mats} M={M} N={N} K={K} pad={pad} {kind}", flush=True)
+        got = run(ops, T[kind])
+        torch.cuda.synchronize()
+        check(kind, got, want, err)
+        again = run(ops, T[kind])
+        for a, b in zip(got if isinstance(got, tuple) else (got,), again if isinstance(again, tuple) else (again,)):
+            assert same_bits(a, b)
+
+
 def test_long_contraction():
     """Rows so far apart that 32-bit offsets within a tile would wrap: every row is read at its own place."""
     M, N, K = 17, 128, (1 << 25) + (1 << 20) + 5
