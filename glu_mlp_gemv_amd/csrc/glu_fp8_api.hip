@@ -112,10 +112,10 @@ bool needs_wide(int64_t M, int out_dtype)
 // Microseconds that a tiled product is expected to take.  A workgroup takes a constant time per stage (one
 // K-block of its tile), each round of 256 workgroups (one per CU) has a start and an end, and sums that leave
 // the kernel cost their way to memory and back; that and the time to read the operands join as a fourth-power
-// mean.  The constants are a fit to 2200 timings of 100 sizes (M = 17 to 4096, K = 128 to 17408, N = 256 to
-// 17408), over which the shape of least expected time is 0.5 % slower than the best in the mean and 6 % at
-// most.  Leaving out one shape costs 1.5 to 6 % in the mean, 19 to 40 % at most; 128 x 128 and 256 x 128 tiles
-// were tried and are worth 0.2 %.
+// mean.  The constants are fitted to timings.  Over 98 other sizes (M = 17 to 4096, K = 128 to 17408, N = 256 to 17408;
+// 1978 timings, profiles/glu_fp8_tile_shapes.json) the plan of least expected time is 0.7 % slower than the best in the
+// mean, 23 % at most (270 rows, K = 11008 N = 2944), then 10 and 4.  By whole rounds of one shape alone it is 1.1 %, and
+// leaving out one shape makes that 2.7 to 9.3 % in the mean, 32 to 57 % at most.
 constexpr double kStage[2][glu::kTileShapeCount] = {{1.7, 0.98, 0.74, 0.44, 0.27}, {3.3, 1.8, 1.3, 0.8, 0.51}};
 constexpr double kRound = 2.4, kLaunch = 2.8, kJoinSplit = 0.41;
 constexpr double kJoin = 2.5;                              // 1.2 of it the kernel, the rest the host's launch

@@ -401,9 +401,13 @@ def fp8_linear(x: torch.Tensor, x_scale: torch.Tensor, weight: torch.Tensor, wei
                stream: Optional[torch.cuda.Stream] = None):
     """x @ weight.T on block-scaled e4m3: x [M, K] with x_scale [M, K / 128], weight [N, K] with its blocks' scales.
 
-    Returns [M, N] in ``out_dtype`` (bf16, fp16, fp32), or for float8_e4m3fn the pair (q, scale).  fp32 accumulation
-    over the K-blocks, one rounding.  K and the row strides should be multiples of 16 and the rows 16-byte
-    aligned; other layouts are read as they are, slower, or above 16 rows of x copied first where that is faster.
+    Returns [M, N] in ``out_dtype`` (bf16, fp16, fp32), or for float8_e4m3fn the pair (q, scale), rounded once.  The sums
+    are fp32, but for 16-bit outputs of more than 16 rows on aligned operands: those run on the matrix unit's 8-bit
+    path, which within 8 neighbouring products drops what lies 13 to 14 bits below the largest (some 2^-16 of a result,
+    without bias).  out_dtype=torch.float32 always has fp32 sums.
+
+    K and the row strides should be multiples of 16 and the rows 16-byte aligned; other layouts are read as they are,
+    slower, or above 16 rows of x copied first where that is faster.
     """
     return _product(x, x_scale, (("weight", weight, weight_scale),), out_dtype, out, scale_out, plan, stream)
 
@@ -414,7 +418,7 @@ def fp8_dual_glu(x: torch.Tensor, x_scale: torch.Tensor, gate: torch.Tensor, gat
                  plan: Optional[ProductPlan] = None, stream: Optional[torch.cuda.Stream] = None):
     """silu(x @ gate.T) * (x @ up.T) on block-scaled e4m3 operands, both weights read in place.
 
-    As ``fp8_linear``; the activation is evaluated in fp32 on the fp32 sums and the result rounded once, to
+    As ``fp8_linear``, its sums among it; the activation is evaluated in fp32 on them and the result rounded once, to
     ``out_dtype`` or to block-scaled e4m3 (a pair) for the projection that follows.
     """
     return _product(x, x_scale, (("gate", gate, gate_scale), ("up", up, up_scale)), out_dtype, out, scale_out, plan,

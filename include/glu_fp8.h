@@ -17,9 +17,10 @@
  *
  * Products: out[m, n] = sum_b sx[m, b] sw[n / 128, b] sum_{k in block b} x[m, k] w[n, k],
  * glu_fp8_dual_glu gives silu(gate) * up of two such sums, evaluated in fp32
- * and rounded once to the output's type.  The sums are fp32, except that with more than 16 rows of x and a 16-bit
- * output they run on the matrix unit's 8-bit path, which within 8 neighbouring products drops what lies 13
- * to 14 bits below the largest and adds the eighths in fp32.
+ * and rounded once to the output's type.  The sums are fp32, except that on the fast layout with more than 16 rows of x and
+ * a 16-bit output they run on the matrix unit's 8-bit path, which within 8 neighbouring products drops what lies 13
+ * to 14 bits below the largest and adds the eighths in fp32: a row's result can differ in that between a call of 16
+ * rows and one of 17, and between layouts.
  *
  * Ownership, execution, determinism and errors are those of glu_gemv.h: all
  * arrays are device memory of the caller, calls are asynchronous on `stream`,
@@ -53,6 +54,7 @@ enum {
  * NULL; sum may be exactly residual or x (same pointer and stride), any other overlap of an output is
  * refused.  rstd [M] (fp32, may be NULL) receives r, which the backward reads.
  * K >= 1 (GLU_ERR_BAD_SHAPE: the mean of an empty row is not defined); M == 0 is GLU_OK.
+ * The mean of squares is fp32: a row whose sum of squares passes its range (an element above some 1.8e19) has r = 0.
  * eps negative or not finite, or an unknown dtype: GLU_ERR_BAD_ARGUMENT.
  */
 glu_status glu_add_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t ldr, const void* weight,
