@@ -12,6 +12,9 @@ fallback path.
 on 8-bit (block-scaled e4m3) weights and activations (``include/glu_fp8.h``); ``mlp.Fp8GluMlp`` runs them
 together.
 
+``adapter_add``, ``adapter_glu`` and ``adapter_backward`` are low-rank adapters beside such projections, one per row of a
+batch of many requests (``include/glu_adapter.h``).
+
 ``inputs`` holds the seeded synthetic input generators.
 """
 from . import inputs  # noqa: F401
@@ -19,7 +22,9 @@ from . import inputs  # noqa: F401
 _FP8 = ("add_rms_norm", "add_rms_norm_fp8", "add_rms_norm_backward", "fp8_quantize", "fp8_quantize_weight",
         "fp8_linear", "fp8_dual_glu")
 
-__all__ = ["inputs", "dual_gemv", "library", *_FP8]
+_ADAPTERS = ("adapter_add", "adapter_glu", "adapter_backward")
+
+__all__ = ["inputs", "dual_gemv", "library", *_FP8, *_ADAPTERS]
 
 
 def __getattr__(name):
@@ -29,5 +34,9 @@ def __getattr__(name):
     if name in _FP8:
         from . import fp8
         value = globals()[name] = getattr(fp8, name)
+        return value
+    if name in _ADAPTERS:
+        from . import adapters
+        value = globals()[name] = getattr(adapters, name)
         return value
     raise AttributeError(name)

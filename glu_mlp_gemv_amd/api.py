@@ -72,6 +72,12 @@ EXPORTED_SYMBOLS = (
     "glu_fp8_copy_workspace",
     "glu_fp8_product_tuned",
     "glu_fp8_product_workspace",
+    # include/glu_adapter.h; declared and called in adapters.py
+    "glu_adapter_add",
+    "glu_adapter_glu",
+    "glu_adapter_workspace",
+    "glu_adapter_backward",
+    "glu_adapter_backward_workspace",
 )
 
 
@@ -174,8 +180,9 @@ def library() -> ctypes.CDLL:
     lib.glu_unit_ceiling_work.restype = ctypes.c_int
     lib.glu_copy_ceiling.argtypes = [vp, vp, vp, vp, i64, i64, ctypes.POINTER(Tuning), vp]
     lib.glu_copy_ceiling.restype = ctypes.c_int
-    from . import fp8
+    from . import adapters, fp8
     fp8._declare(lib)
+    adapters._declare(lib)
     _LIB = lib
     return lib
 

@@ -13,7 +13,7 @@ from typing import Optional
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import api, fp8
+from . import adapters, api, fp8
 
 
 class DualWeightGlu(torch.autograd.Function):
@@ -62,3 +62,34 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: Option
     """(y, h) of fp8.add_rms_norm, differentiable (once) in x, weight and residual."""
     out = AddRmsNorm.apply(x, weight, eps, residual)
     return (out, x) if residual is None else out
+
+
+class AdapterAdd(torch.autograd.Function):
+    """adapters.adapter_add; backward: adapters.adapter_backward."""
+
+    @staticmethod
+    def forward(ctx, y, x, a, b, index, scale):
+        if ctx.needs_input_grad[5]:
+            raise RuntimeError("adapter_add has no gradient for scale")
+        keep = any(ctx.needs_input_grad[1:4])
+        out, low = adapters._add(y, x, a, b, index, scale, None, keep, None)
+        if keep:
+            ctx.save_for_backward(x, a, b, index, scale, low)
+        return out
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dout):
+        wanted = ctx.needs_input_grad[1:4]
+        if not any(wanted):
+            return dout, None, None, None, None, None
+        x, a, b, index, scale, low = ctx.saved_tensors
+        # an expanded gradient (of a sum, say) has overlapping rows, which the library refuses
+        return (dout if ctx.needs_input_grad[0] else None,
+                *adapters.adapter_backward(dout.contiguous(), x, a, b, index, low, scale, wanted=wanted), None, None)
+
+
+def adapter_add(y: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, index: torch.Tensor,
+                scale: Optional[torch.Tensor] = None):
+    """adapters.adapter_add, differentiable (once) in y, x, a and b."""
+    return AdapterAdd.apply(y, x, a, b, index, scale)
