@@ -13,7 +13,9 @@ on 8-bit (block-scaled e4m3) weights and activations (``include/glu_fp8.h``); ``
 together.
 
 ``adapter_add``, ``adapter_glu`` and ``adapter_backward`` are low-rank adapters beside such projections, one per row of a
-batch of many requests (``include/glu_adapter.h``).
+batch of many requests (``include/glu_adapter.h``), and ``dropout`` is what they are trained behind
+(``include/glu_dropout.h``).  ``moe_glu`` is a mixture-of-experts GLU layer for a few tokens (``include/glu_moe.h``),
+``mlp.ExpertGluMlp`` a decoder layer's MLP with it.
 
 ``inputs`` holds the seeded synthetic input generators.
 """
@@ -24,7 +26,7 @@ _FP8 = ("add_rms_norm", "add_rms_norm_fp8", "add_rms_norm_backward", "fp8_quanti
 
 _ADAPTERS = ("adapter_add", "adapter_glu", "adapter_backward")
 
-__all__ = ["inputs", "dual_gemv", "library", *_FP8, *_ADAPTERS]
+__all__ = ["inputs", "dual_gemv", "library", "dropout", "moe_glu", *_FP8, *_ADAPTERS]
 
 
 def __getattr__(name):
@@ -38,5 +40,13 @@ def __getattr__(name):
     if name in _ADAPTERS:
         from . import adapters
         value = globals()[name] = getattr(adapters, name)
+        return value
+    if name == "moe_glu":
+        from . import moe
+        value = globals()[name] = moe.moe_glu
+        return value
+    if name == "dropout":
+        from . import counter_dropout
+        value = globals()[name] = counter_dropout.dropout
         return value
     raise AttributeError(name)

@@ -78,6 +78,11 @@ EXPORTED_SYMBOLS = (
     "glu_adapter_workspace",
     "glu_adapter_backward",
     "glu_adapter_backward_workspace",
+    # include/glu_dropout.h; declared and called in counter_dropout.py
+    "glu_dropout",
+    # include/glu_moe.h; declared and called in moe.py
+    "glu_moe_glu",
+    "glu_moe_workspace",
 )
 
 
@@ -180,9 +185,9 @@ def library() -> ctypes.CDLL:
     lib.glu_unit_ceiling_work.restype = ctypes.c_int
     lib.glu_copy_ceiling.argtypes = [vp, vp, vp, vp, i64, i64, ctypes.POINTER(Tuning), vp]
     lib.glu_copy_ceiling.restype = ctypes.c_int
-    from . import adapters, fp8
-    fp8._declare(lib)
-    adapters._declare(lib)
+    from . import adapters, counter_dropout, fp8, moe
+    for face in (fp8, adapters, counter_dropout, moe):
+        face._declare(lib)
     _LIB = lib
     return lib
 

@@ -1,4 +1,4 @@
-"""The dual-weight GLU and the RMS norm as autograd Functions over the library's entry points.
+"""The dual-weight GLU, the RMS norm, low-rank adapters and dropout as autograd Functions over the library's entry points.
 
 Mirrors the segKI "Plan B" design (DeepSpeed PR #8602, comment "Plan B:
 Dual-Weight GEMV", section "Plan B Design"): the Function keeps hidden, gate_w and up_w, reads the weight
@@ -6,14 +6,14 @@ Parameters in place in both directions, and returns gradients for all three,
 so training and generation share one forward and one set of weights.
 Forward: glu_dual_gemv; backward: glu_dual_gemv_backward (up to 65536 rows
 of hidden per call).  ``rms_norm`` does the same for the residual addition and
-norm.  Only argument marshalling happens here.
+norm, ``adapter_add`` for adapters' weights and ``dropout`` in front of them.  Only argument marshalling happens here.
 """
-from typing import Optional
+from typing import Optional, Union
 
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import adapters, api, fp8
+from . import adapters, api, counter_dropout, fp8
 
 
 class DualWeightGlu(torch.autograd.Function):
@@ -93,3 +93,31 @@ def adapter_add(y: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tens
                 scale: Optional[torch.Tensor] = None):
     """adapters.adapter_add, differentiable (once) in y, x, a and b."""
     return AdapterAdd.apply(y, x, a, b, index, scale)
+
+
+class Dropout(torch.autograd.Function):
+    """counter_dropout.dropout; backward: the same call on the gradient."""
+
+    @staticmethod
+    def forward(ctx, x, p, seed, offset, residual):
+        ctx.at = p, None if isinstance(seed, torch.Tensor) else seed, offset
+        if ctx.needs_input_grad[0] and isinstance(seed, torch.Tensor):
+            ctx.save_for_backward(seed)  # a seed changed in between is an error there, not another mask
+        return counter_dropout._dropout(x, p, seed, offset, residual, None, None)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dout):
+        dx = None
+        if ctx.needs_input_grad[0]:
+            p, seed, offset = ctx.at
+            if seed is None:
+                (seed,) = ctx.saved_tensors
+            dx = counter_dropout._dropout(dout.contiguous(), p, seed, offset, None, None, None)
+        return dx, None, None, None, dout if ctx.needs_input_grad[4] else None
+
+
+def dropout(x: torch.Tensor, p: float, seed: Union[int, torch.Tensor], offset: int = 0,
+            residual: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """counter_dropout.dropout, differentiable (once) in x and residual."""
+    return Dropout.apply(x, p, seed, offset, residual)

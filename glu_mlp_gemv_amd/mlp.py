@@ -13,7 +13,7 @@ from typing import Optional
 
 import torch
 
-from . import fp8
+from . import api, fp8, moe
 
 
 class Fp8GluMlp:
@@ -37,3 +37,24 @@ class Fp8GluMlp:
         q, scale, h = fp8.add_rms_norm_fp8(x, self.norm_weight, self.eps, residual=residual)
         a, a_scale = fp8.fp8_dual_glu(q, scale, *self.gate, *self.up, out_dtype=fp8.E4M3)
         return fp8.fp8_linear(a, a_scale, *self.down, out_dtype=x.dtype), h
+
+
+class ExpertGluMlp:
+    """The same with a mixture of experts: norm -> router -> the chosen experts' gate, up and down.
+
+    norm_weight [K] and router [E, K] in bf16 (as ``api.grouped_gemv`` takes them), gate and up [E, N, K], down [E, K, N] in
+    bf16, or e4m3 with ``scales`` of all three (``moe.moe_glu``).  ``top`` experts per row.
+    """
+
+    def __init__(self, norm_weight: torch.Tensor, router: torch.Tensor, gate: torch.Tensor, up: torch.Tensor,
+                 down: torch.Tensor, top: int, normalize: bool = True, eps: float = 1e-6, scales=(None, None, None)):
+        self.norm_weight, self.router = norm_weight.detach(), router.detach()
+        self.experts = tuple(w.detach() for w in (gate, up, down))
+        self.scales = dict(zip(("gate_scale", "up_scale", "down_scale"), scales))
+        self.top, self.normalize, self.eps = top, normalize, eps
+
+    def __call__(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None):
+        """(y, h) for x [M, K] and the residual stream, as ``Fp8GluMlp``."""
+        n, h = fp8.add_rms_norm(x, self.norm_weight, self.eps, residual=residual)
+        (logits,) = api.grouped_gemv(n, [self.router])
+        return moe.moe_glu(n, logits, *self.experts, self.top, normalize=self.normalize, **self.scales), h

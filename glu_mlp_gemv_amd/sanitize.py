@@ -24,11 +24,12 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SAN_DIR = os.path.join(hip_build.BUILD_DIR, "san")
 LLVM = "/opt/rocm/llvm/bin"
-SAN_SOURCES = ("glu_api.hip", "glu_fp8_api.hip", "glu_adapter_api.hip", "glu_noalloc.hip")
+SAN_SOURCES = ("glu_api.hip", "glu_fp8_api.hip", "glu_adapter_api.hip", "glu_dropout_api.hip", "glu_moe_api.hip",
+               "glu_noalloc.hip")
 HOST_SAN = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined",
             "-Xarch_host", "-fno-sanitize-recover=all", "-Xarch_host", "-fno-omit-frame-pointer"]
 TESTS = ["tests/test_boundary.py", "tests/test_fp8_boundary.py", "tests/test_adapter_boundary.py",
-         "tests/test_plan_sweep.py", "tests/test_oracle_pins.py"]
+         "tests/test_dropout_boundary.py", "tests/test_moe_boundary.py", "tests/test_plan_sweep.py", "tests/test_oracle_pins.py"]
 
 
 def _run(cmd, **kw):
