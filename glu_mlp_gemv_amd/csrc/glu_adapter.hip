@@ -21,6 +21,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
+constexpr int kTurnPitch = 68;  // of 64 results: a row's 16-byte pieces are one bank group on from the last row's
 constexpr int kStage = 64;  // contraction per wave and stage: one 128-byte line per row
 
 struct Whole { static constexpr bool value = true; };
@@ -55,23 +56,56 @@ __device__ __forceinline__ void take_out(int (&left)[TM], int cur)
     }
 }
 
-// First product.  Tile: 16 TM rows of v, 16 RT rows of w; the 4 waves take stages of 64 columns in turn and join in LDS.
-// COLUMNS: w is [C][R], and operand j of a lane is column RT (l % 16) + j.
-template <class T, int TM, int RT, bool COLUMNS>
-__global__ void __launch_bounds__(kThreads) adapter_low_kernel(LowArgs a, int slots, int rgroups, int tile0)
+// Loads of a tile are a uniform address plus 32 bits per lane: rows of a tile times a row's bytes stay below 2^31
+// (kMaxAdapterRow), and a lane keeps one register per row it reads instead of two and additions.
+__device__ __forceinline__ raw4_t read16(const char* base, uint32_t lane)
 {
-    __shared__ float red[kWaves][TM * RT][256];
+    return *reinterpret_cast<const u32x4_any*>(base + lane);
+}
+
+// 16 bytes per lane straight to LDS, lane l's at to + 16 l (to: uniform)
+__device__ __forceinline__ void direct16(const char* base, uint32_t lane, uint8_t* to)
+{
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(base + lane),
+                                     (__attribute__((address_space(3))) void*)to, 16, 0, 0);
+}
+
+// waits until all but this wave's last N loads are done; vmcnt in bits 3:0 and 15:14, nothing else waited for
+template <int N>
+__device__ __forceinline__ void wait_direct()
+{
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// waits until this wave's LDS reads are in registers
+__device__ __forceinline__ void reads_done()
+{
+    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// First product.  Tile: 16 TM rows of v, 16 RT rows of w and a part of the columns; the 4 waves take stages of 64 columns
+// in turn, keep U of them in flight, and join in LDS.  Tiles start at different columns, or rows of a power-of-two
+// stride would have all of them at the same few memory channels.  COLUMNS: w is [C][R], and operand j of a lane is
+// column RT (l % 16) + j.
+template <class T, int TM, int RT, int U, bool COLUMNS>
+__global__ void __launch_bounds__(kThreads, 3) adapter_low_kernel(LowArgs a, int slots, int rgroups, int tile0)
+{
+    constexpr int PIECES = TM * RT;
+    __shared__ float red[kWaves][PIECES][256];
     __shared__ int rows_of[16 * TM];
     const int lane = threadIdx.x & 63, i16 = lane & 15, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int m0 = (tile0 + blockIdx.x) * 16 * TM;
+    const int tile = tile0 + blockIdx.x, m0 = tile * 16 * TM;
     const int split = blockIdx.y % a.splits, rg = blockIdx.y / a.splits % rgroups, mat = blockIdx.y / a.splits / rgroups;
     const int slot = blockIdx.z;
     const int r0 = rg * 16 * RT;
-    const int stages = (a.C + kStage - 1) / kStage;
-    const int per = (stages + a.splits - 1) / a.splits;
-    const int s_end = min(stages, (split + 1) * per);
-    float* part = a.part + (int64_t)(split * a.mats + mat) * a.M * a.R;
+    // this part's stages: first .. first + count - 1 are whole, `tail` is one that ends past the columns, or -1
+    const int stages = (a.C + kStage - 1) / kStage, per = (stages + a.splits - 1) / a.splits;
+    const int first = min(split * per, a.C / kStage), count = min((split + 1) * per, a.C / kStage) - first;
+    const int tail = a.C % kStage && (stages - 1) / per == split ? stages - 1 : -1;
+    float* z = a.z + (int64_t)(split * a.mats + mat) * a.M * a.R;
 
     int idx[TM], left[TM];
 #pragma unroll
@@ -83,9 +117,11 @@ __global__ void __launch_bounds__(kThreads) adapter_low_kernel(LowArgs a, int sl
     if (slot == 0) {
         for (int j = threadIdx.x; j < 16 * TM * 16 * RT; j += kThreads) {
             const int m = m0 + j / (16 * RT), r = r0 + j % (16 * RT);
-            if (m < a.M && r < a.R && rows_of[j / (16 * RT)] < 0) part[(int64_t)m * a.R + r] = 0.0f;
+            if (m < a.M && r < a.R && rows_of[j / (16 * RT)] < 0) z[(int64_t)m * a.R + r] = 0.0f;
         }
     }
+    const char* vbase = reinterpret_cast<const char*>(static_cast<const T*>(a.v) + m0 * a.ldv);
+    const int rotate = count > 0 ? tile * 5 % count : 0;
     int seen = 0;
     for (;;) {
         const int cur = next_adapter<TM>(left);
@@ -94,53 +130,206 @@ __global__ void __launch_bounds__(kThreads) adapter_low_kernel(LowArgs a, int sl
         if (seen++ % slots != slot) continue;
 
         // rows of v: lanes whose row has another adapter read the first of this one's along
-        const T* v[TM];
+        uint32_t vo[TM];
         {
-            int first = 0;
+            int one = 0;
 #pragma unroll
             for (int t = TM - 1; t >= 0; --t) {
                 const uint64_t b = __ballot(idx[t] == cur);
-                if (b) first = m0 + 16 * t + __builtin_ctzll(b);
+                if (b) one = 16 * t + __builtin_ctzll(b);
             }
 #pragma unroll
             for (int t = 0; t < TM; ++t) {
-                const int m = idx[t] == cur ? m0 + 16 * t + i16 : first;
-                v[t] = static_cast<const T*>(a.v) + m * a.ldv;
+                vo[t] = ((uint32_t)(idx[t] == cur ? 16 * t + i16 : one) * (uint32_t)a.ldv + 8 * q) * 2;
             }
         }
         const T* w = static_cast<const T*>(a.w[mat].w) + cur * a.w[mat].stack;
         const int64_t wrow = a.w[mat].row;
+        const char* wbase = reinterpret_cast<const char*>(w + (COLUMNS ? r0 : r0 * wrow));
+        uint32_t wo[RT];  // COLUMNS: one of this lane's first column
+#pragma unroll
+        for (int j = 0; j < RT; ++j) wo[j] = ((uint32_t)min(16 * j + i16, a.R - 1 - r0) * (uint32_t)wrow + 8 * q) * 2;
+        if constexpr (COLUMNS) wo[0] = ((uint32_t)(8 * q) * (uint32_t)wrow + RT * i16) * 2;
         f32x4 acc[TM][RT];
 #pragma unroll
         for (int t = 0; t < TM; ++t) {
 #pragma unroll
             for (int j = 0; j < RT; ++j) acc[t][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         }
-        const int rl = r0 + RT * i16;  // COLUMNS: this lane's first column of w
-        auto stage = [&](int s, auto whole_tag) __attribute__((always_inline)) {
-            constexpr bool WHOLE = decltype(whole_tag)::value;
+        raw4_t vf[U][2][TM], wf[U][2][RT];
+        auto load = [&](int u, int s) __attribute__((always_inline)) {
+            s += rotate;
+            const int at = (first + (s < count ? s : s - count)) * kStage;
+            const char* vb = vbase + at * 2;
+            const char* wb = wbase + (COLUMNS ? at * wrow : (int64_t)at) * 2;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int c = s * kStage + 32 * h + 8 * q;
-                raw4_t vf[TM], wf[RT];
 #pragma unroll
-                for (int t = 0; t < TM; ++t) vf[t] = WHOLE ? *reinterpret_cast<const u32x4_any*>(v[t] + c) : load8(v[t] + c, a.C - c);
+                for (int t = 0; t < TM; ++t) vf[u][h][t] = read16(vb + 64 * h, vo[t]);
                 if constexpr (COLUMNS) {
-                    load_columns<T, RT>([&](int i) { return w + min(c + i, a.C - 1) * wrow + rl; }, a.R - rl, wf);
-                    if constexpr (!WHOLE) {
+                    load_columns<T, RT>([&](int i) { return wb + (32 * h + i) * wrow * 2 + wo[0]; }, a.R - r0 - RT * i16, wf[u][h]);
+                } else {
 #pragma unroll
-                        for (int j = 0; j < RT; ++j) {
+                    for (int j = 0; j < RT; ++j) wf[u][h][j] = read16(wb + 64 * h, wo[j]);
+                }
+            }
+        };
+        auto load_tail = [&](int u) __attribute__((always_inline)) {
+            const int at = tail * kStage;
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) wf[j][e] &= first_rows_mask(e, a.C - c);
-                        }
+            for (int h = 0; h < 2; ++h) {
+                const int c = at + 32 * h + 8 * q;  // this lane's first column
+#pragma unroll
+                for (int t = 0; t < TM; ++t) vf[u][h][t] = load8(reinterpret_cast<const T*>(vbase + vo[t]) + at + 32 * h, a.C - c);
+                if constexpr (COLUMNS) {
+                    load_columns<T, RT>([&](int i) { return w + min(c + i, a.C - 1) * wrow + r0 + RT * i16; },
+                                        a.R - r0 - RT * i16, wf[u][h]);
+#pragma unroll
+                    for (int j = 0; j < RT; ++j) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) wf[u][h][j][e] &= first_rows_mask(e, a.C - c);
                     }
                 } else {
 #pragma unroll
-                    for (int j = 0; j < RT; ++j) {
-                        const T* p = w + min(r0 + 16 * j + i16, a.R - 1) * wrow + c;
-                        wf[j] = WHOLE ? *reinterpret_cast<const u32x4_any*>(p) : load8(p, a.C - c);
-                    }
+                    for (int j = 0; j < RT; ++j) wf[u][h][j] = load8(reinterpret_cast<const T*>(wbase + wo[j]) + at + 32 * h, a.C - c);
                 }
+            }
+        };
+        auto use = [&](int u) __attribute__((always_inline)) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int t = 0; t < TM; ++t) {
+#pragma unroll
+                    for (int j = 0; j < RT; ++j) acc[t][j] = mfma16<T>(wf[u][h][j], vf[u][h][t], acc[t][j]);
+                }
+            }
+        };
+        // a ring of U stages: one is refilled as soon as it is used
+        int s = wave;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (s + u * kWaves < count) load(u, s + u * kWaves);
+        }
+        for (; s + (2 * U - 1) * kWaves < count; s += U * kWaves) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                use(u);
+                load(u, s + (u + U) * kWaves);
+            }
+        }
+        for (; s < count; s += U * kWaves) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (s + u * kWaves < count) use(u);
+                if (s + (u + U) * kWaves < count) load(u, s + (u + U) * kWaves);
+            }
+        }
+        if (tail >= 0 && wave == kWaves - 1) {
+            load_tail(0);
+            use(0);
+        }
+
+#pragma unroll
+        for (int p = 0; p < PIECES; ++p) *reinterpret_cast<f32x4*>(&red[wave][p][4 * lane]) = acc[p / RT][p % RT];
+        __syncthreads();
+        for (int i = threadIdx.x; i < PIECES * 256; i += kThreads) {
+            const int l = i >> 2 & 63, piece = i >> 8, t = piece / RT, j = piece % RT;
+            const int row = 16 * t + (l & 15), k = 4 * (l >> 4) + (i & 3);
+            const int r = r0 + (COLUMNS ? RT * k + j : 16 * j + k);
+            if (rows_of[row] != cur || r >= a.R) continue;
+            float sum = red[0][piece][i & 255];
+#pragma unroll
+            for (int o = 1; o < kWaves; ++o) sum += red[o][piece][i & 255];
+            z[(int64_t)(m0 + row) * a.R + r] = sum;
+        }
+        __syncthreads();
+    }
+}
+
+// The same for larger batches on whole 16-byte chunks.  In the kernel above neighbouring lanes load from different rows,
+// and the address unit takes 64 cycles for such a load of 1 KB: 16 bytes a cycle and CU, less than memory gives once
+// w's loads are counted too.  Here a load takes 8 rows' 128-byte lines, straight to LDS, where a wave has two
+// stages of its own, and the operands are read from there; no barrier is needed before the waves join.  Chunk c of row r
+// is in place c ^ (r / 2) of the row, so that 16 rows' chunks lie in different banks.
+template <class T, int TM, int RT>
+__global__ void __launch_bounds__(kThreads) adapter_low_tile_kernel(LowArgs a, int rgroups, int tile0)
+{
+    constexpr int PIECES = TM * RT, LOADS = 2 * (TM + RT), STAGE = LOADS * 1024, DEPTH = 2;
+    extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];  // [wave][DEPTH][rows of v, then of w][128 bytes]
+    __shared__ int rows_of[16 * TM];
+    const int lane = threadIdx.x & 63, i16 = lane & 15, q = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int tile = tile0 + blockIdx.x, m0 = tile * 16 * TM;
+    const int split = blockIdx.y % a.splits, rg = blockIdx.y / a.splits % rgroups, mat = blockIdx.y / a.splits / rgroups;
+    const int r0 = rg * 16 * RT;
+    const int stages = (a.C + kStage - 1) / kStage, per = (stages + a.splits - 1) / a.splits;
+    const int first = min(split * per, a.C / kStage), count = min((split + 1) * per, a.C / kStage) - first;
+    const int tail = a.C % kStage && (stages - 1) / per == split ? stages - 1 : -1;
+    float* z = a.z + (int64_t)(split * a.mats + mat) * a.M * a.R;
+    uint8_t* mine = smem + wave * DEPTH * STAGE;
+
+    int idx[TM], left[TM];
+#pragma unroll
+    for (int t = 0; t < TM; ++t) {
+        idx[t] = left[t] = adapter_of(a.index, m0 + 16 * t + i16, a.M, a.L);
+        if (wave == 0 && q == 0) rows_of[16 * t + i16] = idx[t];
+    }
+    __syncthreads();
+    for (int j = threadIdx.x; j < 16 * TM * 16 * RT; j += kThreads) {
+        const int m = m0 + j / (16 * RT), r = r0 + j % (16 * RT);
+        if (m < a.M && r < a.R && rows_of[j / (16 * RT)] < 0) z[(int64_t)m * a.R + r] = 0.0f;
+    }
+    const char* vbase = reinterpret_cast<const char*>(static_cast<const T*>(a.v) + m0 * a.ldv);
+    const int rotate = count > 0 ? tile * 5 % count : 0;
+    // what this lane loads: chunk lane % 8, turned by its row, of row lane / 8 of each 8; rows of two loads differ by 8
+    const int lr = lane >> 3, lc = lane & 7;
+    uint32_t vo[2 * TM], wo[2 * RT];
+#pragma unroll
+    for (int i = 0; i < 2 * TM; ++i) {
+        const int r = 8 * i + lr;
+        vo[i] = (uint32_t)min(r, a.M - 1 - m0) * (uint32_t)a.ldv * 2 + 16 * (lc ^ (r >> 1 & 7));
+    }
+#pragma unroll
+    for (int i = 0; i < 2 * RT; ++i) {
+        const int r = 8 * i + lr;
+        wo[i] = (uint32_t)min(r, a.R - 1 - r0) * (uint32_t)a.w[mat].row * 2 + 16 * (lc ^ (r >> 1 & 7));
+    }
+    const int rd[2] = {i16 * 128 + ((q ^ (i16 >> 1)) << 4), i16 * 128 + (((q + 4) ^ (i16 >> 1)) << 4)};
+    for (;;) {
+        const int cur = next_adapter<TM>(left);
+        if (cur < 0) break;
+        take_out<TM>(left, cur);
+        const int64_t wrow = a.w[mat].row;
+        const char* wbase = reinterpret_cast<const char*>(static_cast<const T*>(a.w[mat].w) + cur * a.w[mat].stack + r0 * wrow);
+        f32x4 acc[TM][RT];
+#pragma unroll
+        for (int t = 0; t < TM; ++t) {
+#pragma unroll
+            for (int j = 0; j < RT; ++j) acc[t][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+        // past the last stage the last one again, so that every stage waits for the same number of loads
+        const int turns = (count - wave + kWaves - 1) / kWaves;  // this wave's stages
+        auto load = [&](int k, int buf) __attribute__((always_inline)) {
+            int s = min(k, turns - 1) * kWaves + wave + rotate;
+            if (s >= count) s -= count;
+            const char* vb = vbase + (first + s) * 128;
+            const char* wb = wbase + (first + s) * 128;
+            uint8_t* to = mine + buf * STAGE;
+#pragma unroll
+            for (int i = 0; i < 2 * TM; ++i) direct16(vb, vo[i], to + i * 1024);
+#pragma unroll
+            for (int i = 0; i < 2 * RT; ++i) direct16(wb, wo[i], to + (2 * TM + i) * 1024);
+        };
+        auto use = [&](int buf) __attribute__((always_inline)) {
+            const uint8_t* from = mine + buf * STAGE;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                raw4_t vf[TM], wf[RT];
+#pragma unroll
+                for (int t = 0; t < TM; ++t) vf[t] = *reinterpret_cast<const raw4_t*>(from + t * 2048 + rd[h]);
+#pragma unroll
+                for (int j = 0; j < RT; ++j) wf[j] = *reinterpret_cast<const raw4_t*>(from + (TM + j) * 2048 + rd[h]);
 #pragma unroll
                 for (int t = 0; t < TM; ++t) {
 #pragma unroll
@@ -148,54 +337,82 @@ __global__ void __launch_bounds__(kThreads) adapter_low_kernel(LowArgs a, int sl
                 }
             }
         };
-        const int whole_end = min(s_end, a.C / kStage);
-        int s = split * per + wave;
-#pragma unroll 2
-        for (; s < whole_end; s += kWaves) stage(s, Whole{});
-        if (s < s_end) stage(s, Part{});
-
+        if (turns > 0) {
+            load(0, 0);
+            load(1, 1);
+            for (int k = 0; k < turns; ++k) {
+                wait_direct<LOADS>();  // all but the next stage's
+                use(k & 1);
+                reads_done();
+                load(k + 2, k & 1);
+            }
+            wait_direct<0>();  // the LDS they write is used again
+        }
+        if (tail >= 0 && wave == kWaves - 1) {
+            const int at = tail * kStage;
 #pragma unroll
-        for (int t = 0; t < TM; ++t) {
+            for (int h = 0; h < 2; ++h) {
+                const int c = at + 32 * h + 8 * q;
+                raw4_t vf[TM], wf[RT];
 #pragma unroll
-            for (int j = 0; j < RT; ++j) *reinterpret_cast<f32x4*>(&red[wave][t * RT + j][4 * lane]) = acc[t][j];
+                for (int t = 0; t < TM; ++t) {
+                    vf[t] = load8(reinterpret_cast<const T*>(vbase + (uint32_t)min(16 * t + i16, a.M - 1 - m0) * (uint32_t)a.ldv * 2) + c, a.C - c);
+                }
+#pragma unroll
+                for (int j = 0; j < RT; ++j) {
+                    wf[j] = load8(reinterpret_cast<const T*>(wbase + (uint32_t)min(16 * j + i16, a.R - 1 - r0) * (uint32_t)wrow * 2) + c, a.C - c);
+                }
+#pragma unroll
+                for (int t = 0; t < TM; ++t) {
+#pragma unroll
+                    for (int j = 0; j < RT; ++j) acc[t][j] = mfma16<T>(wf[j], vf[t], acc[t][j]);
+                }
+            }
         }
         __syncthreads();
-        for (int p = threadIdx.x; p < TM * RT * 64; p += kThreads) {
-            const int piece = p >> 6, l = p & 63, t = piece / RT, j = piece % RT;
-            const int row = 16 * t + (l & 15);
-            if (rows_of[row] != cur) continue;
+        float(*red)[PIECES][256] = reinterpret_cast<float(*)[PIECES][256]>(smem);  // fits: 1 KB a piece, 2 KB a tile of rows
+#pragma unroll
+        for (int p = 0; p < PIECES; ++p) *reinterpret_cast<f32x4*>(&red[wave][p][4 * lane]) = acc[p / RT][p % RT];
+        __syncthreads();
+        for (int i = threadIdx.x; i < PIECES * 64; i += kThreads) {
+            const int l = i & 63, piece = i >> 6, t = piece / RT, j = piece % RT;
+            const int row = 16 * t + (l & 15), r = r0 + 16 * j + 4 * (l >> 4);
+            if (rows_of[row] != cur || r >= a.R) continue;
             f32x4 sum = *reinterpret_cast<const f32x4*>(&red[0][piece][4 * l]);
 #pragma unroll
-            for (int k = 1; k < kWaves; ++k) sum += *reinterpret_cast<const f32x4*>(&red[k][piece][4 * l]);
-            float* to = part + (int64_t)(m0 + row) * a.R;
+            for (int o = 1; o < kWaves; ++o) sum += *reinterpret_cast<const f32x4*>(&red[o][piece][4 * l]);
+            float* to = z + (int64_t)(m0 + row) * a.R + r;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const int i = 4 * (l >> 4) + e;
-                const int r = r0 + (COLUMNS ? RT * i + j : 16 * j + i);
-                if (r < a.R) to[r] = sum[e];
+                if (r + e < a.R) to[e] = sum[e];
             }
         }
         __syncthreads();
     }
 }
 
-// Second product.  Tile: 16 TM rows of z, which the workgroup first puts into LDS as two numbers of T each, and runs
-// of 64 columns for each of its waves.  The contraction is 2 R8 chunks of 8 ranks: those of the first numbers
-// and then those of the second, so that ranks up to 16 take one instruction per 16 x 16 results.  The rows of w in an instruction
-// are chosen so that a lane's results are 8 neighbouring columns (COLUMNS: 16).
-template <class T, int TM, int NM, bool COLUMNS>
-__global__ void __launch_bounds__(kThreads) adapter_out_kernel(OutArgs a, int slots, int cblocks, int per, int tile0)
+// Second product.  Tile: 16 TM rows of z, which the workgroup puts into LDS as two numbers of T each, and runs of 64
+// columns for each of its waves, whose y and w are on their way meanwhile.  The contraction is RP = ranks rounded up places
+// of the first numbers and then RP of the second, so that up to 16 ranks (S = 1) they share one instruction's 32 places; S
+// instructions with H operands of w per 16 columns, or (S = 0) as many as there are ranks.  The results,
+// of which a lane holds 4 columns of its own row, go through LDS to lanes that hold 8 columns, 8 neighbouring lanes a line:
+// so y is read and out written.
+template <class T, int TM, int NM, int S, bool COLUMNS>
+__global__ void __launch_bounds__(kThreads, 2) adapter_out_kernel(OutArgs a, int slots, int cblocks, int per, int tile0)
 {
-    extern __shared__ uint16_t lds[];  // z: [NM][2][16 TM][pitch]; then the rows' powers of two and maxima
+    constexpr int ROWS = 16 * TM, H = S > 1 ? S / 2 : 1;
+    extern __shared__ __attribute__((aligned(16))) uint16_t lds[];  // z as T [NM][ROWS][pitch]; powers of two and maxima [NM][ROWS]; parts of z as fp32
+    __shared__ __attribute__((aligned(16))) float turned[kWaves][16 * kTurnPitch];
     const int lane = threadIdx.x & 63, i16 = lane & 15, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int tile = tile0 + blockIdx.x / cblocks, cb = blockIdx.x % cblocks;
-    const int m0 = tile * 16 * TM;
+    const int cb = blockIdx.x % cblocks, m0 = (tile0 + blockIdx.x / cblocks) * ROWS;
     const int slot = blockIdx.y;
-    const int R8 = (a.R + 7) >> 3, pitch = 8 * R8 + 8;
-    constexpr int ROWS = 16 * TM;
-    float* down = reinterpret_cast<float*>(lds + NM * 2 * ROWS * pitch);  // [NM][ROWS]
+    const int nb_first = cb * per * kWaves + wave, nb_end = min((a.N + 63) >> 6, (cb + 1) * per * kWaves);
+    const int RP = S ? 16 * (S == 1 ? 1 : S) : (a.R + 31) & ~31, R8 = RP >> 3, pitch = 2 * RP + 8;
+    const int steps = S ? S : RP >> 4;
+    float* down = reinterpret_cast<float*>(lds + NM * ROWS * pitch);
     uint32_t* most = reinterpret_cast<uint32_t*>(down + NM * ROWS);
+    float* parts = reinterpret_cast<float*>(most + NM * ROWS);
 
     int idx[TM], left[TM];
     bool bare = false;  // rows without an adapter
@@ -205,233 +422,383 @@ __global__ void __launch_bounds__(kThreads) adapter_out_kernel(OutArgs a, int sl
         idx[t] = left[t] = adapter_of(a.index, m, a.M, a.L);
         bare |= m < a.M && idx[t] < 0;
     }
+    // what this lane reads and writes: columns 8 (lane % 8) .. + 7 of a 64-column block, rows lane / 8 of each 8
+    const int lr = lane >> 3, lc = 8 * (lane & 7);
+    int own[2 * TM];  // their adapters; -2: no such row
+#pragma unroll
+    for (int i = 0; i < 2 * TM; ++i) {
+        const int m = m0 + 8 * i + lr;
+        own[i] = m < a.M ? adapter_of(a.index, m, a.M, a.L) : -2;
+    }
+    const char* ybase[NM];
+#pragma unroll
+    for (int mat = 0; mat < NM; ++mat) ybase[mat] = a.y[mat] ? reinterpret_cast<const char*>(static_cast<const T*>(a.y[mat]) + m0 * a.ldy[mat]) : nullptr;
+    char* obase = reinterpret_cast<char*>(static_cast<T*>(a.out) + m0 * a.ldo);
+    float* tp = turned[wave];
 
-    auto z8 = [&](int i, float (&v)[8]) __attribute__((always_inline)) {  // item i: mat, row, chunk
-        const int c = i % R8, row = i / R8 % ROWS, mat = i / R8 / ROWS;
-        const int n = m0 + row < a.M ? min(8, a.R - 8 * c) : 0;
+    // the operands of w for ranks 8 c .. + 7, c = c0 + q, and 64 columns from n0
+    auto load_w = [&](int mat, int cur, int n0, int c, raw4_t (&f)[4]) __attribute__((always_inline)) {
+        const int64_t wrow = a.w[mat].row;
+        const T* w = static_cast<const T*>(a.w[mat].w) + cur * a.w[mat].stack + (COLUMNS ? (int64_t)n0 : n0 * wrow);
+        const int r = 8 * c;
+        if constexpr (COLUMNS) {
+            load_columns<T, 4>(
+                [&](int i) { return reinterpret_cast<const char*>(w) + ((uint32_t)min(r + i, a.R - 1) * (uint32_t)wrow + 4 * i16) * 2; },
+                r < a.R ? a.N - n0 - 4 * i16 : 0, f);
+            if (r + 8 > a.R) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = 0.0f;
-        for (int s = 0; s < a.splits; ++s) {
-            const float* p = a.part + ((int64_t)(s * a.mats + mat) * a.M + m0 + row) * a.R + 8 * c;
-            if (n == 8) {
-                const Chunk<Fp32> k = load_chunk(reinterpret_cast<const Fp32*>(p), 8);
+                for (int j = 0; j < 4; ++j) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] += k.e[e].v;
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    if (e < n) v[e] += p[e];
+                    for (int e = 0; e < 4; ++e) f[j][e] &= first_rows_mask(e, a.R - r);
                 }
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const char* p = reinterpret_cast<const char*>(w) + ((uint32_t)min(16 * j + i16, a.N - 1 - n0) * (uint32_t)wrow + r) * 2;
+                f[j] = load8(reinterpret_cast<const T*>(p), a.R - r);
             }
         }
     };
-    const int items = NM * ROWS * R8;
-    if constexpr (!__is_same(T, Bf16)) {
-        for (int i = threadIdx.x; i < NM * ROWS; i += kThreads) most[i] = 0u;
-        __syncthreads();
-        for (int i = threadIdx.x; i < items; i += kThreads) {
-            float v[8];
-            z8(i, v);
-            atomicMax(&most[i / R8], abs_max8(v));  // a maximum: any order
-        }
-        __syncthreads();
-    }
-    for (int i = threadIdx.x; i < items; i += kThreads) {
-        float v[8];
-        z8(i, v);
-        const int c = i % R8, at = i / R8, row = at % ROWS, mat = at / ROWS;
-        if (a.low && cb == 0 && slot == 0 && m0 + row < a.M) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                if (8 * c + e < a.R) a.low[(int64_t)(m0 + row) * a.R + 8 * c + e] = v[e];
-            }
-        }
-        Pow2 f{1.0f, 1.0f};
-        if constexpr (!__is_same(T, Bf16)) {
-            f = pow2_for<T>(most[at]);
-            if (c == 0) down[at] = f.down;
-        }
-        raw4_t hi = {0u, 0u, 0u, 0u}, lo = {0u, 0u, 0u, 0u};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            uint16_t h, l;
-            split16<T>(v[e] * f.up, h, l);
-            hi[e >> 1] |= (uint32_t)h << (16 * (e & 1));
-            lo[e >> 1] |= (uint32_t)l << (16 * (e & 1));
-        }
-        *reinterpret_cast<raw4_t*>(lds + ((mat * 2 + 0) * ROWS + row) * pitch + 8 * c) = hi;
-        *reinterpret_cast<raw4_t*>(lds + ((mat * 2 + 1) * ROWS + row) * pitch + 8 * c) = lo;
-    }
-    __syncthreads();
 
-    const int nblocks = (a.N + 63) >> 6;
-    const int nb_first = (cb * per) * kWaves + wave, nb_end = min(nblocks, (cb + 1) * per * kWaves);
-    const int steps = (2 * R8 + 3) >> 2;
-    // this lane's 16 results of a 64-column block: group g of 8 at columns at[g] .. + 7
-    const int at[2] = {COLUMNS ? 16 * q : 8 * q, COLUMNS ? 16 * q + 8 : 32 + 8 * q};
-
-    auto pass = [&](int cur) __attribute__((always_inline)) {  // cur < 0: the rows without an adapter
-        const float scale = cur >= 0 && a.scale ? a.scale[cur] : 1.0f;
-        for (int nb = nb_first; nb < nb_end; nb += kWaves) {
-            const int n0 = 64 * nb;
-            f32x4 acc[NM][TM][4];
+    auto pass = [&](int cur, auto with) __attribute__((always_inline)) {
+        constexpr bool WITH = decltype(with)::value;  // false: the rows without an adapter
+        raw4_t y[2][NM][TM][2], wf[NM][H][4];
+        auto load_y = [&](int n0, int buf) __attribute__((always_inline)) {
+            const bool whole = n0 + 64 <= a.N;
 #pragma unroll
             for (int mat = 0; mat < NM; ++mat) {
+                if (!a.y[mat]) continue;
 #pragma unroll
-                for (int t = 0; t < TM; ++t) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) acc[mat][t][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                for (int i = 0; i < 2 * TM; ++i) {
+                    const char* p = ybase[mat] + 2 * n0 + ((uint32_t)(8 * i + lr) * (uint32_t)a.ldy[mat] + lc) * 2;
+                    if (own[i] == cur) y[buf][mat][i >> 1][i & 1] = load8(reinterpret_cast<const T*>(p), whole ? 8 : a.N - n0 - lc);
                 }
             }
-            if (cur >= 0) {
+        };
+        auto load_ws = [&](int n0) __attribute__((always_inline)) {
+            if constexpr (WITH && S > 0) {
 #pragma unroll
                 for (int mat = 0; mat < NM; ++mat) {
-                    const T* w = static_cast<const T*>(a.w[mat].w) + cur * a.w[mat].stack;
-                    const int64_t wrow = a.w[mat].row;
-                    for (int s = 0; s < steps; ++s) {
-                        const int c = 4 * s + q;
-                        const bool there = c < 2 * R8;
-                        const int second = c >= R8 ? 1 : 0, cc = there ? c - second * R8 : 0;
-                        raw4_t wf[4];
-                        if constexpr (COLUMNS) {
-                            const int n = n0 + 4 * i16;
-                            load_columns<T, 4>([&](int i) { return w + min(8 * cc + i, a.R - 1) * wrow + n; }, a.N - n, wf);
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
+                    for (int h = 0; h < H; ++h) load_w(mat, cur, n0, S == 1 ? q & 1 : 4 * h + q, wf[mat][h]);
+                }
+            }
+        };
+        if (nb_first < nb_end) {
+            load_y(64 * nb_first, 0);
+            load_ws(64 * nb_first);
+        }
+
+        float scale = 1.0f;
+        if constexpr (WITH) {
+            if (a.scale) scale = a.scale[cur];
+            // z: thread groups sum every groups-th part, then the groups' sums meet
+            const int items = NM * ROWS * R8, groups = max(1, min(a.splits, kThreads / items));
+            auto z8 = [&](int i, int from, int step, float (&v)[8]) __attribute__((always_inline)) {
+                const int c = i % R8, row = i / R8 % ROWS, mat = i / R8 / ROWS, m = m0 + row;
+                const bool wanted = m < a.M && 8 * c < a.R && a.index[m] == cur;
+                const float* p = a.z + ((int64_t)mat * a.M + m) * a.R + 8 * c;
+                const int64_t plane = (int64_t)a.mats * a.M * a.R;
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) wf[j][e] &= there ? first_rows_mask(e, a.R - 8 * cc) : 0u;
-                            }
-                        } else {
+                for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+                if (!wanted) return;
+#pragma unroll 4
+                for (int s = from; s < a.splits; s += step) {
+                    const Chunk<Fp32> k = load_chunk(reinterpret_cast<const Fp32*>(p + s * plane), a.R - 8 * c);
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const int n = n0 + (j >> 1) * 32 + (i16 >> 2) * 8 + (j & 1) * 4 + (i16 & 3);
-                                wf[j] = load8(w + min(n, a.N - 1) * wrow + 8 * cc, there ? a.R - 8 * cc : 0);
-                            }
-                        }
+                    for (int e = 0; e < 8; ++e) v[e] += k.e[e].v;
+                }
+            };
+            if (groups > 1) {
+                const int i = threadIdx.x % items, g = threadIdx.x / items;
+                if (g < groups) {
+                    float v[8];
+                    z8(i, g, groups, v);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) parts[(g * items + i) * 8 + e] = v[e];
+                }
+            }
+            if (!__is_same(T, Bf16)) {
+                for (int i = threadIdx.x; i < NM * ROWS; i += kThreads) most[i] = 0u;
+            }
+            if (groups > 1 || !__is_same(T, Bf16)) __syncthreads();
+            auto z_of = [&](int i, float (&v)[8]) __attribute__((always_inline)) {
+                if (groups > 1) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        v[e] = parts[i * 8 + e];
+                        for (int g = 1; g < groups; ++g) v[e] += parts[(g * items + i) * 8 + e];
+                    }
+                } else {
+                    z8(i, 0, 1, v);
+                }
+            };
+            if constexpr (!__is_same(T, Bf16)) {
+                for (int i = threadIdx.x; i < items; i += kThreads) {
+                    float v[8];
+                    z_of(i, v);
+                    atomicMax(&most[i / R8], abs_max8(v));  // a maximum: any order
+                }
+                __syncthreads();
+            }
+            for (int i = threadIdx.x; i < items; i += kThreads) {
+                float v[8];
+                z_of(i, v);
+                const int c = i % R8, row_at = i / R8, row = row_at % ROWS;
+                if (a.low && cb == 0 && m0 + row < a.M && a.index[m0 + row] == cur && 8 * c < a.R) {
+                    store_chunk(reinterpret_cast<Fp32*>(a.low) + (int64_t)(m0 + row) * a.R + 8 * c, narrow8<Fp32>(v), a.R - 8 * c);
+                }
+                Pow2 f{1.0f, 1.0f};
+                if constexpr (!__is_same(T, Bf16)) {
+                    f = pow2_for<T>(most[row_at]);
+                    if (c == 0) down[row_at] = f.down;
+                }
+                raw4_t hi = {0u, 0u, 0u, 0u}, lo = {0u, 0u, 0u, 0u};
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    uint16_t first, second;
+                    split16<T>(v[e] * f.up, first, second);
+                    hi[e >> 1] |= (uint32_t)first << (16 * (e & 1));
+                    lo[e >> 1] |= (uint32_t)second << (16 * (e & 1));
+                }
+                *reinterpret_cast<raw4_t*>(lds + row_at * pitch + 8 * c) = hi;
+                *reinterpret_cast<raw4_t*>(lds + row_at * pitch + RP + 8 * c) = lo;
+            }
+            __syncthreads();
+        } else if (a.low && cb == 0 && wave == 0) {
+#pragma unroll
+            for (int i = 0; i < 2 * TM; ++i) {
+                for (int r = lane & 7; own[i] == cur && r < a.R; r += 8) a.low[(int64_t)(m0 + 8 * i + lr) * a.R + r] = 0.0f;
+            }
+        }
+        auto block = [&](int nb, int buf) __attribute__((always_inline)) {
+            const int n0 = 64 * nb;
+            const bool whole = n0 + 64 <= a.N;
+            if (nb + kWaves < nb_end) load_y(64 * (nb + kWaves), buf ^ 1);
+            f32x4 acc[NM][S ? 1 : TM][4];
+            auto z_at = [&](int mat, int t, int s) __attribute__((always_inline)) {
+                return *reinterpret_cast<const raw4_t*>(lds + (mat * ROWS + 16 * t + i16) * pitch + 32 * s + 8 * q);
+            };
+            if constexpr (S == 0) {
+#pragma unroll
+                for (int mat = 0; mat < NM; ++mat) {
+#pragma unroll
+                    for (int t = 0; t < TM; ++t) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) acc[mat][t][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                    }
+                    for (int h = 0; WITH && h < steps / 2; ++h) {
+                        raw4_t f[4];
+                        load_w(mat, cur, n0, 4 * h + q, f);
 #pragma unroll
                         for (int t = 0; t < TM; ++t) {
-                            raw4_t z = *reinterpret_cast<const raw4_t*>(
-                                lds + ((mat * 2 + second) * ROWS + 16 * t + i16) * pitch + 8 * cc);
-                            if (!there) z = raw4_t{0u, 0u, 0u, 0u};
+                            const raw4_t first = z_at(mat, t, h), second = z_at(mat, t, steps / 2 + h);
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) acc[mat][t][j] = mfma16<T>(wf[j], z, acc[mat][t][j]);
+                            for (int j = 0; j < 4; ++j) {
+                                acc[mat][t][j] = mfma16<T>(f[j], first, acc[mat][t][j]);
+                                acc[mat][t][j] = mfma16<T>(f[j], second, acc[mat][t][j]);
+                            }
                         }
                     }
                 }
             }
 #pragma unroll
             for (int t = 0; t < TM; ++t) {
-                const int m = m0 + 16 * t + i16;
-                if (m >= a.M || idx[t] != cur) continue;
-                float f[NM];
-#pragma unroll
-                for (int mat = 0; mat < NM; ++mat) {
-                    f[mat] = cur < 0 ? 0.0f : scale * (__is_same(T, Bf16) ? 1.0f : down[mat * ROWS + 16 * t + i16]);
-                }
-#pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    const int n = n0 + at[g], cnt = a.N - n;
-                    if (cnt <= 0) continue;
-                    float o[NM][8];
+                if constexpr (S > 0) {
 #pragma unroll
                     for (int mat = 0; mat < NM; ++mat) {
-                        Chunk<T> y{};
-                        if (a.y[mat]) y = load_chunk(static_cast<const T*>(a.y[mat]) + m * a.ldy[mat] + n, cnt);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            // COLUMNS: column 16 q + 4 e' + j is element e' of operand j
-                            const float d = COLUMNS ? acc[mat][t][e & 3][2 * g + (e >> 2)] : acc[mat][t][2 * g + (e >> 2)][e & 3];
-                            o[mat][e] = fmaf(d, f[mat], widen(y.e[e]));
+                        for (int j = 0; j < 4; ++j) acc[mat][0][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                        for (int s = 0; WITH && s < S; ++s) {
+                            const raw4_t z = z_at(mat, t, s);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) acc[mat][0][j] = mfma16<T>(wf[mat][s % H][j], z, acc[mat][0][j]);
                         }
                     }
-                    if constexpr (NM == 2) {
+                }
+                float o[2][8];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) o[0][e] = silu_mul(o[0][e], o[1][e]);
+                for (int mat = 0; mat < NM; ++mat) {
+                    const f32x4(&d)[4] = acc[mat][S ? 0 : t];
+                    if constexpr (WITH) {
+                        // COLUMNS: column 4 (4 q + e) + j is element e of operand j, else column 16 j + 4 q + e
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const f32x4 v = COLUMNS ? f32x4{d[0][k], d[1][k], d[2][k], d[3][k]} : d[k];
+                            *reinterpret_cast<f32x4*>(tp + i16 * kTurnPitch + (COLUMNS ? 16 * q + 4 * k : 16 * k + 4 * q)) = v;
+                        }
+                        __builtin_amdgcn_wave_barrier();  // to other lanes of the wave, in LDS order
                     }
-                    store_chunk(static_cast<T*>(a.out) + m * a.ldo + n, narrow8<T>(o[0]), cnt);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const Chunk<T> base = __builtin_bit_cast(Chunk<T>, y[buf][mat][t][i]);
+                        float v[8];
+                        if constexpr (WITH) {
+                            const float* from = tp + (8 * i + lr) * kTurnPitch + lc;
+                            const f32x4 lo = *reinterpret_cast<const f32x4*>(from), hi = *reinterpret_cast<const f32x4*>(from + 4);
+                            const float f = __is_same(T, Bf16) ? scale : scale * down[mat * ROWS + 16 * t + 8 * i + lr];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) v[e] = fmaf(e < 4 ? lo[e] : hi[e - 4], f, a.y[mat] ? widen(base.e[e]) : 0.0f);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) v[e] = a.y[mat] ? widen(base.e[e]) : 0.0f;
+                        }
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) o[i][e] = mat == 0 ? v[e] : silu_mul(o[i][e], v[e]);
+                    }
+                    __builtin_amdgcn_wave_barrier();
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    char* to = obase + 2 * n0 + ((uint32_t)(16 * t + 8 * i + lr) * (uint32_t)a.ldo + lc) * 2;
+                    const int cnt = whole ? 8 : a.N - n0 - lc;
+                    if (own[2 * t + i] == cur && cnt > 0) store_chunk(reinterpret_cast<T*>(to), narrow8<T>(o[i]), cnt);
                 }
             }
+            if (nb + kWaves < nb_end) load_ws(64 * (nb + kWaves));
+        };
+        for (int nb = nb_first; nb < nb_end; nb += 2 * kWaves) {
+            block(nb, 0);
+            if (nb + kWaves < nb_end) block(nb + kWaves, 1);
         }
     };
-    if (slot == 0 && __ballot(bare)) pass(-1);
+    if (slot == 0 && __ballot(bare)) pass(-1, Part{});
     int seen = 0;
     for (;;) {
         const int cur = next_adapter<TM>(left);
         if (cur < 0) break;
         take_out<TM>(left, cur);
-        if (seen++ % slots == slot) pass(cur);
+        if (seen++ % slots != slot) continue;
+        if (seen > slots) __syncthreads();  // z of the adapter before is read
+        pass(cur, Whole{});
     }
 }
 
+constexpr int kTargetWaves = 2048;
 constexpr int64_t kMaxBlocks = 1 << 22;  // workgroups of 256 threads in a launch's first dimension
 
-// Rows per tile: 64 share an adapter's weights where there are enough rows for that to matter, 16 else.  A tile
-// of 16 rows has up to 16 adapters, whose workgroups are the launch's `slots`; larger batches are runs of rows.
-int tile_m(int M) { return M > 256 ? 4 : 1; }
-int slots_of(int M, int L) { return M > 256 ? 1 : (M < 16 ? (L < M ? L : M) : (L < 16 ? L : 16)); }
+// Up to kMixed rows a batch is taken to mix requests: tiles of 16 rows, whose up to 16 adapters have workgroups of their own
+// (the launch's `slots`), and waves side by side along the columns.  More rows are taken to be runs of one adapter.
+constexpr int kMixed = 256;
+int slots_of(int M, int L)
+{
+    const int most = M < 16 ? M : 16;
+    return M > kMixed ? 1 : L < most ? L : most;
+}
+
+// Tiles of the first product: 16 TM rows and 16 RT ranks.  Up to kMixed rows one instruction's, so that there are more of
+// them; else as many as registers hold with a stage in flight.  64 x 64 (from LDS) and 32 x 64, us: 16384 rows of 4096 34.7
+// and 40.2, 8192 of 5120 25.2 and 27.0, 5000 of 4096 23.6 and 23.4, 2050 of 4096 18.0 and 15.3.
+struct LowTile { int tm, rt; };
+LowTile low_tile(int M, int R, bool columns)
+{
+    if (M <= kMixed || columns) return {1, 1};
+    return R <= 16 ? LowTile{4, 1} : R <= 32 ? LowTile{4, 2} : M > 4096 ? LowTile{4, 4} : LowTile{2, 4};
+}
+
+template <class T, int TM, int RT, int U, bool COLUMNS>
+void low_tiles(const LowArgs& a, hipStream_t stream)
+{
+    const int slots = slots_of(a.M, a.L), rgroups = (a.R + 16 * RT - 1) / (16 * RT);
+    const int64_t tiles = ((int64_t)a.M + 16 * TM - 1) / (16 * TM);
+    for (int64_t t = 0; t < tiles; t += kMaxBlocks) {
+        const dim3 grid((unsigned)(tiles - t < kMaxBlocks ? tiles - t : kMaxBlocks), a.splits * rgroups * a.mats, slots);
+        hipLaunchKernelGGL((adapter_low_kernel<T, TM, RT, U, COLUMNS>), grid, dim3(kThreads), 0, stream, a, slots, rgroups,
+                           (int)t);
+    }
+}
+
+// whether rows are whole 16-byte chunks as far as whole stages go
+bool aligned(const LowArgs& a)
+{
+    uintptr_t bits = (uintptr_t)a.v | (uintptr_t)(a.ldv * 2);
+    for (int i = 0; i < a.mats; ++i) bits |= (uintptr_t)a.w[i].w | (uintptr_t)(a.w[i].stack * 2) | (uintptr_t)(a.w[i].row * 2);
+    return (bits & 15) == 0;
+}
+
+template <class T, int TM, int RT>
+hipError_t low_direct(const LowArgs& a, hipStream_t stream)
+{
+    constexpr int bytes = kWaves * 2 * 2 * (TM + RT) * 1024;
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(adapter_low_tile_kernel<T, TM, RT>),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != hipSuccess) return e;
+    const int rgroups = (a.R + 16 * RT - 1) / (16 * RT);
+    const int64_t tiles = ((int64_t)a.M + 16 * TM - 1) / (16 * TM);
+    for (int64_t t = 0; t < tiles; t += kMaxBlocks) {
+        const dim3 grid((unsigned)(tiles - t < kMaxBlocks ? tiles - t : kMaxBlocks), a.splits * rgroups * a.mats);
+        hipLaunchKernelGGL((adapter_low_tile_kernel<T, TM, RT>), grid, dim3(kThreads), bytes, stream, a, rgroups, (int)t);
+    }
+    return hipGetLastError();
+}
 
 template <class T, bool COLUMNS>
 hipError_t low_launch(const LowArgs& a, hipStream_t stream)
 {
-    const int tm = tile_m(a.M), slots = slots_of(a.M, a.L);
-    const int rt = a.R <= 16 ? 1 : a.R <= 32 ? 2 : 4;
-    const int rgroups = (a.R + 16 * rt - 1) / (16 * rt);
-    const int tiles = (a.M + 16 * tm - 1) / (16 * tm);
-    for (int64_t t = 0; t < tiles; t += kMaxBlocks) {
-        const dim3 grid((unsigned)(tiles - t < kMaxBlocks ? tiles - t : kMaxBlocks), a.splits * rgroups * a.mats, slots);
-#define GLU_LOW(TM, RT) \
-    hipLaunchKernelGGL((adapter_low_kernel<T, TM, RT, COLUMNS>), grid, dim3(kThreads), 0, stream, a, slots, rgroups, (int)t)
-        if (tm == 1) {
-            if (rt == 1) GLU_LOW(1, 1);
-            else if (rt == 2) GLU_LOW(1, 2);
-            else GLU_LOW(1, 4);
-        } else {
-            if (rt == 1) GLU_LOW(4, 1);
-            else if (rt == 2) GLU_LOW(4, 2);
-            else GLU_LOW(4, 4);
-        }
-#undef GLU_LOW
-    }
+    const LowTile t = low_tile(a.M, a.R, COLUMNS);
+    if (COLUMNS || t.tm == 1) low_tiles<T, 1, 1, 2, COLUMNS>(a, stream);
+    else if (aligned(a) && t.rt == 1) return low_direct<T, 4, 1>(a, stream);
+    else if (aligned(a) && t.rt == 2) return low_direct<T, 4, 2>(a, stream);
+    else if (aligned(a) && t.tm == 4) return low_direct<T, 4, 4>(a, stream);
+    else if (aligned(a)) return low_direct<T, 2, 4>(a, stream);
+    else if (t.rt == 1) low_tiles<T, 4, 1, 2, false>(a, stream);
+    else if (t.rt == 2) low_tiles<T, 4, 2, 2, false>(a, stream);
+    else low_tiles<T, 2, 4, 2, false>(a, stream);
     return hipGetLastError();
+}
+
+template <class T, int TM, int NM, int S, bool COLUMNS>
+void out_tiles(const OutArgs& a, hipStream_t stream)
+{
+    const int slots = slots_of(a.M, a.L);
+    const int64_t tiles = ((int64_t)a.M + 16 * TM - 1) / (16 * TM);
+    const int blocks = a.N > 0 ? (a.N + 63) / 64 : 1;  // N == 0: z alone, to low
+    // a wave keeps its z for several blocks where there are waves enough
+    const int64_t units = tiles * slots < a.M ? tiles * slots : a.M;  // tiles' adapters at most
+    int per = (int)((units * blocks + kTargetWaves - 1) / kTargetWaves);
+    per = per < 1 ? 1 : per > 32 ? 32 : per;
+    const int cblocks = (blocks + per * kWaves - 1) / (per * kWaves);
+    const int64_t fit = kMaxBlocks / cblocks < 1 ? 1 : kMaxBlocks / cblocks;
+    const int RP = S ? 16 * S : (a.R + 31) & ~31, rows = 16 * TM, items = NM * rows * RP / 8;
+    const int groups = kThreads / items < a.splits ? kThreads / items : a.splits;
+    const size_t bytes = (size_t)NM * rows * (2 * RP + 8) * 2 + (size_t)NM * rows * 8 + (groups > 1 ? (size_t)groups * items * 32 : 0);
+    for (int64_t t = 0; t < tiles; t += fit) {
+        const dim3 grid((unsigned)((tiles - t < fit ? tiles - t : fit) * cblocks), slots);
+        hipLaunchKernelGGL((adapter_out_kernel<T, TM, NM, S, COLUMNS>), grid, dim3(kThreads), bytes, stream, a, slots, cblocks,
+                           per, (int)t);
+    }
 }
 
 template <class T, int NM, bool COLUMNS>
 hipError_t out_launch(const OutArgs& a, hipStream_t stream)
 {
-    // ranks above 64 keep to 16 rows, whose z fits LDS at any rank
-    const int tm = a.R <= 64 ? tile_m(a.M) : 1, slots = tm == 1 ? slots_of(a.M, a.L) : 1;
-    const int rows = 16 * tm, tiles = (a.M + rows - 1) / rows;
-    const int columns = a.N > 0 ? a.N : 1;                              // N == 0: z alone goes to low
-    const int groups = (columns + 64 * kWaves - 1) / (64 * kWaves);  // one column block per wave
-    // a workgroup keeps its z for several of them where there are workgroups enough
-    int per = (int)((int64_t)tiles * groups / 2048);
-    per = per < 1 ? 1 : per > 4 ? 4 : per;
-    const int cblocks = (groups + per - 1) / per;
-    const int R8 = (a.R + 7) / 8;
-    const size_t bytes = (size_t)NM * 2 * rows * (8 * R8 + 8) * 2 + (size_t)NM * rows * 8;
-    const int64_t fit = kMaxBlocks / cblocks < 1 ? 1 : kMaxBlocks / cblocks;
-    for (int64_t t = 0; t < tiles; t += fit) {
-        const dim3 grid((unsigned)((tiles - t < fit ? tiles - t : fit) * cblocks), slots);
-        if (tm == 1) {
-            hipLaunchKernelGGL((adapter_out_kernel<T, 1, NM, COLUMNS>), grid, dim3(kThreads), bytes, stream, a, slots,
-                               cblocks, per, (int)t);
-        } else {
-            hipLaunchKernelGGL((adapter_out_kernel<T, 4, NM, COLUMNS>), grid, dim3(kThreads), bytes, stream, a, slots,
-                               cblocks, per, (int)t);
-        }
+    if (a.R > 64) {
+        out_tiles<T, 1, NM, 0, COLUMNS>(a, stream);
+    } else if (a.M <= kMixed) {
+        if (a.R <= 16) out_tiles<T, 1, NM, 1, COLUMNS>(a, stream);
+        else if (a.R <= 32) out_tiles<T, 1, NM, 2, COLUMNS>(a, stream);
+        else out_tiles<T, 1, NM, 4, COLUMNS>(a, stream);
+    } else {
+        if (a.R <= 16) out_tiles<T, NM == 1 ? 4 : 2, NM, 1, COLUMNS>(a, stream);
+        else if (a.R <= 32) out_tiles<T, NM == 1 ? 4 : 2, NM, 2, COLUMNS>(a, stream);
+        else out_tiles<T, NM == 1 ? 4 : 2, NM, 4, COLUMNS>(a, stream);
     }
     return hipGetLastError();
 }
 
 }  // namespace
 
-// Parts of the contraction: as many as give every CU four waves' workgroups, of at least 4 stages (one per wave).
-int adapter_low_splits(int M, int C, int R, int mats)
+// Parts of the columns.  A mixed batch: as many as make some 768 workgroups, of one stage per wave at least.  More rows: as
+// many as make a workgroup per CU, whose waves then go through more stages each (8192 rows of 5120, 16 ranks, in 256, 512
+// and 768 workgroups: 18.3, 21.7 and 25.4 us; 64 ranks 25.2, 32.6 and 41.4).
+int adapter_low_splits(int M, int C, int R, int L, int mats, bool columns)
 {
-    const int tm = tile_m(M);
-    const int64_t groups = ((int64_t)M + 16 * tm - 1) / (16 * tm) * mats * (R <= 64 ? 1 : (R + 63) / 64);
+    const LowTile t = low_tile(M, R, columns);
+    const int64_t groups = ((int64_t)M + 16 * t.tm - 1) / (16 * t.tm) * mats * ((R + 16 * t.rt - 1) / (16 * t.rt)) * slots_of(M, L);
     const int64_t most = ((int64_t)C + kStage * kWaves - 1) / (kStage * kWaves);
-    int64_t s = groups ? 512 / groups : 1;
+    int64_t s = groups ? (t.tm == 1 ? 768 : 256) / groups : 1;
     if (s > most) s = most;
     return (int)(s < 1 ? 1 : s > 16 ? 16 : s);
 }

@@ -15,7 +15,7 @@ using glu::Array;
 using glu::bad_dim;
 using glu::check_arrays;
 
-constexpr int64_t kMaxGradDim = 1 << 24, kMaxGradAdapters = 1 << 16;
+constexpr int64_t kMaxGradRows = 1 << 24, kMaxGradAdapters = 1 << 16;
 
 glu_status launched(hipError_t e) { return e == hipSuccess ? GLU_OK : glu::fail_launch(e); }
 
@@ -23,6 +23,7 @@ glu_status check_sizes(const glu_adapter_sizes* s)
 {
     if (!s) return GLU_ERR_NULL_POINTER;
     if (bad_dim(s->M) || bad_dim(s->N) || bad_dim(s->K) || bad_dim(s->L) || s->L == 0) return GLU_ERR_BAD_SHAPE;
+    if (s->N > glu::kMaxAdapterRow || s->K > glu::kMaxAdapterRow) return GLU_ERR_BAD_SHAPE;
     if (s->R < 1 || s->R > GLU_ADAPTER_MAX_RANK) return GLU_ERR_BAD_SHAPE;
     return GLU_OK;
 }
@@ -31,10 +32,11 @@ glu_status check_grad_sizes(const glu_adapter_sizes* s)
 {
     const glu_status st = check_sizes(s);
     if (st != GLU_OK) return st;
-    if (s->M > kMaxGradDim || s->N > kMaxGradDim || s->K > kMaxGradDim || s->L > kMaxGradAdapters) return GLU_ERR_BAD_SHAPE;
-    const int64_t rows = s->M + s->L, widest = s->N > s->K ? s->N : s->K, most = (int64_t)1 << 48;
-    return widest > 0 && rows > most / widest ? GLU_ERR_BAD_SHAPE : GLU_OK;
+    return s->M > kMaxGradRows || s->L > kMaxGradAdapters ? GLU_ERR_BAD_SHAPE : GLU_OK;
 }
+
+// whether a row stride that is used is past what a tile's offsets hold
+bool too_wide(int64_t rows, int64_t ld) { return rows > 1 && ld > glu::kMaxAdapterRow; }
 
 // L matrices of `rows` rows of `len` elements as one array: rows and matrices may lie apart, but not overlap
 glu_status stack_array(const void* p, int64_t L, int64_t rows, int64_t len, int64_t stack, int64_t row, Array* out)
@@ -42,7 +44,7 @@ glu_status stack_array(const void* p, int64_t L, int64_t rows, int64_t len, int6
     *out = Array{p, 0, 0, 0, 2, false};
     if (rows == 0 || len == 0) return GLU_OK;
     const Array one{p, rows, len, row, 2, false};
-    if (rows > 1 && row < len) return GLU_ERR_BAD_STRIDE;
+    if ((rows > 1 && row < len) || too_wide(rows, row)) return GLU_ERR_BAD_STRIDE;
     const int64_t bytes = glu::extent(one);
     if (bytes < 0) return GLU_ERR_BAD_STRIDE;
     *out = Array{p, L, bytes / 2, stack, 2, false};
@@ -57,10 +59,15 @@ glu_status stack_arrays(const glu_adapter* ab, const glu_adapter_sizes& s, Array
 
 int64_t align16(int64_t n) { return (n + 15) & ~(int64_t)15; }
 
-int64_t part_bytes(int mats, const glu_adapter_sizes& s)
+int low_splits(int mats, const glu_adapter_sizes& s, int64_t columns, bool down = false)
 {
-    if (s.M == 0) return 0;
-    return align16((int64_t)glu::adapter_low_splits((int)s.M, (int)s.K, (int)s.R, mats) * mats * s.M * s.R * 4);
+    return glu::adapter_low_splits((int)s.M, (int)columns, (int)s.R, (int)s.L, mats, down);
+}
+
+// t of every row, in its parts
+int64_t low_bytes(int mats, const glu_adapter_sizes& s, int64_t columns)
+{
+    return align16((int64_t)low_splits(mats, s, columns) * mats * s.M * s.R * 4);
 }
 
 bool bad_workspace(const void* p, int64_t given, int64_t need)
@@ -81,7 +88,10 @@ glu_status apply(int mats, const void* const* y, const int64_t* ldy, const void*
     for (int i = 0; i < mats; ++i) {
         if (!ab[i]) return GLU_ERR_NULL_POINTER;
     }
-    const int64_t need = part_bytes(mats, s);
+    if (too_wide(s.M, ldx) || too_wide(s.M, ldo) || too_wide(s.M, ldy[0]) || (mats == 2 && too_wide(s.M, ldy[1]))) {
+        return GLU_ERR_BAD_STRIDE;
+    }
+    const int64_t need = low_bytes(mats, s, s.K);
     Array arrays[12];
     int n = 0;
     arrays[n++] = {y[0], s.M, s.N, ldy[0], 2, false};
@@ -104,7 +114,6 @@ glu_status apply(int mats, const void* const* y, const int64_t* ldy, const void*
     st = check_arrays(arrays, n, shared_out, shared_in);
     if (st != GLU_OK) return st;
 
-    const int splits = glu::adapter_low_splits((int)s.M, (int)s.K, (int)s.R, mats);
     glu::LowArgs la{};
     glu::OutArgs oa{};
     for (int i = 0; i < mats; ++i) {
@@ -116,39 +125,45 @@ glu_status apply(int mats, const void* const* y, const int64_t* ldy, const void*
     la.v = x;
     la.ldv = ldx;
     la.index = oa.index = index;
-    la.part = (float*)workspace;
-    oa.part = la.part;
+    la.splits = oa.splits = low_splits(mats, s, s.K);
+    const bool straight = low && la.splits == 1;  // one part of t is t
+    la.z = straight ? low : (float*)workspace;
+    oa.z = la.z;
+    oa.low = straight ? nullptr : low;
     la.M = oa.M = (int)s.M;
     la.C = (int)s.K;
     la.R = oa.R = (int)s.R;
     la.L = oa.L = (int)s.L;
     la.mats = oa.mats = mats;
-    la.splits = oa.splits = splits;
     oa.scale = scale;
     oa.out = out;
     oa.ldo = ldo;
-    oa.low = low;
     oa.N = (int)s.N;
     const hipError_t e = glu::adapter_low_launch(dtype, false, la, (hipStream_t)stream);
-    return launched(e != hipSuccess ? e : glu::adapter_out_launch(dtype, false, oa, (hipStream_t)stream));
+    if (e != hipSuccess || (s.N == 0 && !oa.low)) return launched(e);
+    return launched(glu::adapter_out_launch(dtype, false, oa, (hipStream_t)stream));
 }
 
-// The backward's workspace: d, the rows' order, the items, the items' sums.
+// The backward's workspace: d in its parts, the rows' order, the items, b turned, the items' sums.
 struct GradPlan {
+    bool direct;
     int splits, rows;
-    int64_t items, d, order, table, part, bytes;  // offsets
+    int64_t items, order, table, turned, pitch, part, bytes;  // offsets; turned: rows of `pitch`
 };
 GradPlan grad_plan(const glu_adapter_sizes& s)
 {
     GradPlan p{};
-    p.splits = glu::adapter_low_splits((int)s.M, (int)s.N, (int)s.R, 1);
     p.rows = glu::adapter_grad_rows((int)s.M, s.K + s.N);
-    p.order = align16((int64_t)p.splits * s.M * s.R * 4);
+    p.direct = glu::adapter_grad_direct((int)s.M, p.rows);
+    p.splits = low_splits(1, s, s.N, p.direct);
+    p.order = align16(p.splits * s.M * s.R * 4);
     p.bytes = p.order;
-    if (!glu::adapter_grad_direct((int)s.M, p.rows)) {
+    if (!p.direct) {
         p.items = glu::adapter_grad_items((int)s.M, (int)s.L, p.rows);
         p.table = p.order + align16(s.M * 4);
-        p.part = p.table + align16(p.items * 16 + s.L * 8);
+        p.turned = p.table + align16(p.items * 16 + s.L * 8);
+        p.pitch = (s.N + 7) / 8 * 8;
+        p.part = p.turned + align16(s.L * s.R * p.pitch * 2);
         p.bytes = p.part + p.items * s.R * (s.K + s.N) * 4;
     }
     return p;
@@ -183,7 +198,7 @@ glu_status glu_adapter_workspace(int mats, const glu_adapter_sizes* sizes, int64
     *bytes = 0;
     if (mats != 1 && mats != 2) return GLU_ERR_BAD_ARGUMENT;
     const glu_status st = check_sizes(sizes);
-    if (st == GLU_OK) *bytes = part_bytes(mats, *sizes);
+    if (st == GLU_OK) *bytes = low_bytes(mats, *sizes, sizes->K);
     return st;
 }
 
@@ -207,6 +222,7 @@ glu_status glu_adapter_backward(const void* dout, int64_t ldd, const void* x, in
     const glu_adapter_sizes s = *sizes;
     if (!dx && !da && !db) return GLU_OK;
     if (!ab) return GLU_ERR_NULL_POINTER;
+    if (too_wide(s.M, ldd) || (da && too_wide(s.M, ldx)) || (dx && too_wide(s.M, lddx))) return GLU_ERR_BAD_STRIDE;
     const GradPlan p = grad_plan(s);
     Array arrays[12];
     int n = 0;
@@ -234,25 +250,43 @@ glu_status glu_adapter_backward(const void* dout, int64_t ldd, const void* x, in
     char* ws = (char*)workspace;
     float* d = (float*)ws;
     const hipStream_t hs = (hipStream_t)stream;
+    glu::GradArgs g{};
+    g.side[0] = {x, d, s.K > 0 ? da : nullptr, ldx, (int)s.K, p.splits, false};
+    g.side[1] = {dout, low, s.N > 0 ? db : nullptr, ldd, (int)s.N, 1, true};
+    g.index = index;
+    g.scale = scale;
+    g.order = (int32_t*)(ws + p.order);
+    g.items = (int32_t*)(ws + p.table);
+    g.part = (float*)(ws + p.part);
+    g.M = (int)s.M;
+    g.R = (int)s.R;
+    g.L = (int)s.L;
+    g.rows = p.rows;
+    const bool any_grad = g.side[0].grad || g.side[1].grad, through = s.M > 0 && (dx || da);
+    const glu::Stack b{ab->b, ab->b_stack, ab->b_row};
     hipError_t e = hipSuccess;
-    if (s.M > 0 && (dx || da)) {
+    if (!p.direct) {
+        const glu::Turn turn{b, (uint16_t*)(ws + p.turned), through ? (int)s.N : 0, p.pitch};
+        e = glu::adapter_prepare_launch(g, any_grad, turn, hs);
+    }
+    if (e == hipSuccess && through) {
         glu::LowArgs la{};
         la.v = dout;
         la.ldv = ldd;
-        la.w[0] = {ab->b, ab->b_stack, ab->b_row};
+        la.w[0] = p.direct ? b : glu::Stack{ws + p.turned, s.R * p.pitch, p.pitch};
         la.index = index;
-        la.part = d;
+        la.z = d;
         la.M = (int)s.M;
         la.C = (int)s.N;
         la.R = (int)s.R;
         la.L = (int)s.L;
         la.mats = 1;
         la.splits = p.splits;
-        e = glu::adapter_low_launch(dtype, true, la, hs);
+        e = glu::adapter_low_launch(dtype, p.direct, la, hs);
     }
     if (e == hipSuccess && dx && s.M > 0 && s.K > 0) {
         glu::OutArgs oa{};
-        oa.part = d;
+        oa.z = d;
         oa.w[0] = {ab->a, ab->a_stack, ab->a_row};
         oa.index = index;
         oa.scale = scale;
@@ -266,21 +300,7 @@ glu_status glu_adapter_backward(const void* dout, int64_t ldd, const void* x, in
         oa.splits = p.splits;
         e = glu::adapter_out_launch(dtype, true, oa, hs);
     }
-    if (e == hipSuccess && ((da && s.K > 0) || (db && s.N > 0))) {
-        glu::GradArgs g{};
-        g.side[0] = {x, d, s.K > 0 ? da : nullptr, ldx, (int)s.K, p.splits, false};
-        g.side[1] = {dout, low, s.N > 0 ? db : nullptr, ldd, (int)s.N, 1, true};
-        g.index = index;
-        g.scale = scale;
-        g.order = (int32_t*)(ws + p.order);
-        g.items = (int32_t*)(ws + p.table);
-        g.part = (float*)(ws + p.part);
-        g.M = (int)s.M;
-        g.R = (int)s.R;
-        g.L = (int)s.L;
-        g.rows = p.rows;
-        e = glu::adapter_grad_launch(dtype, g, hs);
-    }
+    if (e == hipSuccess && any_grad) e = glu::adapter_grad_launch(dtype, g, hs);
     return launched(e);
 }
 

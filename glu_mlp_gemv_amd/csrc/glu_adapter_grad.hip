@@ -19,8 +19,10 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kDirectRows = 512;
-constexpr int kChunkRows = 128;       // rows whose d or t are in LDS at a time
-constexpr int kPitch = kChunkRows + 8;
+template <int RT> constexpr int kChunkRows = RT == 4 ? 128 : 256;  // rows whose d or t are in LDS at a time
+constexpr int kItemStep = 256;        // items are multiples of it
+template <int RT> constexpr int kSteps = RT == 4 ? 2 : 4;         // steps of 32 rows in flight
+constexpr int kTurn = 256;            // columns that a workgroup turns to rows
 constexpr int kOrderThreads = 1024;
 
 int32_t* bounds_of(const GradArgs& a, int64_t items) { return a.items + 4 * items; }  // [L][2]: first, count
@@ -50,29 +52,60 @@ __device__ __forceinline__ int block_prefix(int v, int* scratch, int* total)
     return before + p - v;
 }
 
-// One workgroup per adapter: its rows in order, after those of the adapters before it, and its items.  Items are
-// numbered first / rows + adapter, which leaves room for all of every adapter's whatever the counts.
-__global__ void __launch_bounds__(kOrderThreads) adapter_order_kernel(GradArgs a, int items, int32_t* bounds)
+// An adapter's rows in order, after those of the adapters before it, and its items.  A thread takes 16
+// rows at a time, whose numbers it loads together.  Items are numbered first / rows + adapter, which leaves room for all
+// of every adapter's whatever the counts.
+__device__ __forceinline__ void list_rows(const GradArgs& a, int l, int items, int32_t* bounds, int* scratch)
 {
-    __shared__ int scratch[kOrderThreads / 64];
-    const int l = blockIdx.x, t = threadIdx.x;
-    int less = 0, mine = 0;
-    for (int m = t; m < a.M; m += kOrderThreads) {
-        const int i = a.index[m];
-        less += i >= 0 && i < l;
-        mine += i == l;
+    const int t = threadIdx.x;
+    constexpr int EACH = 16;
+    auto load = [&](int m0, int (&v)[EACH]) __attribute__((always_inline)) {
+        if (m0 + EACH <= a.M) {
+            typedef int int4_any __attribute__((ext_vector_type(4), aligned(4)));
+#pragma unroll
+            for (int i = 0; i < EACH / 4; ++i) {
+                const int4_any d = *reinterpret_cast<const int4_any*>(a.index + m0 + 4 * i);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[4 * i + j] = d[j];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < EACH; ++i) v[i] = m0 + i < a.M ? a.index[m0 + i] : -1;
+        }
+    };
+    int less = 0, mine = 0, v[EACH];
+    for (int m0 = EACH * t; m0 < a.M; m0 += EACH * kOrderThreads) {
+        load(m0, v);
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) {
+            less += v[i] >= 0 && v[i] < l;
+            mine += v[i] == l;
+        }
     }
     int first, count;
     block_prefix<kOrderThreads>(less, scratch, &first);
-    block_prefix<kOrderThreads>(mine, scratch, &count);
-    int at = first;
-    for (int m0 = 0; m0 < a.M; m0 += kOrderThreads) {
-        const int m = m0 + t;
-        const int hit = m < a.M && a.index[m] == l;
-        int n;
-        const int p = block_prefix<kOrderThreads>(hit, scratch, &n);
-        if (hit) a.order[at + p] = m;
-        at += n;
+    int at = block_prefix<kOrderThreads>(mine, scratch, &count);
+    const bool once = a.M <= EACH * kOrderThreads;  // the rows are still at hand, and so is their prefix
+    at = once ? first + at : first;
+    for (int base = 0; base < a.M; base += EACH * kOrderThreads) {
+        const int m0 = base + EACH * t;
+        int p = at;
+        if (!once) {
+            int hits = 0, n;
+            if (m0 < a.M) {
+                load(m0, v);
+#pragma unroll
+                for (int i = 0; i < EACH; ++i) hits += v[i] == l;
+            }
+            p += block_prefix<kOrderThreads>(hits, scratch, &n);
+            at += n;
+        }
+        if (m0 < a.M) {
+#pragma unroll
+            for (int i = 0; i < EACH; ++i) {
+                if (v[i] == l) a.order[p++] = m0 + i;
+            }
+        }
     }
     const int base = first / a.rows + l, end = l == a.L - 1 ? items : (first + count) / a.rows + l + 1;
     for (int k = base + t; k < end; k += kOrderThreads) {
@@ -88,13 +121,47 @@ __global__ void __launch_bounds__(kOrderThreads) adapter_order_kernel(GradArgs a
     }
 }
 
+// Columns c0 .. + 255 of one adapter's w [C][R] as rows: wt[r][c] = w[c][r]
+__device__ __forceinline__ void turn(const Turn& w, int R, int l, int c0, uint16_t (*tile)[kTurn + 2])
+{
+    const uint16_t* from = static_cast<const uint16_t*>(w.from.w) + l * w.from.stack;
+    uint16_t* to = w.to + (int64_t)l * R * w.pitch;
+    const int bits = R <= 16 ? 4 : 5, ranks = 1 << bits;
+    for (int r0 = 0; r0 < R; r0 += ranks) {
+        if (r0) __syncthreads();
+        for (int i = threadIdx.x; i < kTurn * ranks; i += kOrderThreads) {
+            const int c = i >> bits, r = i & (ranks - 1);
+            if (c0 + c < w.C && r0 + r < R) tile[r][c] = from[(c0 + c) * w.from.row + r0 + r];
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < kTurn * ranks; i += kOrderThreads) {
+            const int c = i % kTurn, r = i / kTurn;
+            if (c0 + c < w.C && r0 + r < R) to[(int64_t)(r0 + r) * w.pitch + c0 + c] = tile[r][c];
+        }
+    }
+}
+
+// What the other kernels need first: the rows by adapter, one workgroup each, and w turned, which the first product
+// would otherwise read 2 bytes at a time, once per tile of rows.
+__global__ void __launch_bounds__(kOrderThreads)
+adapter_prepare_kernel(GradArgs a, int listed, int items, int32_t* bounds, Turn w, int cblocks, int64_t block0)
+{
+    __shared__ int scratch[kOrderThreads / 64];
+    __shared__ uint16_t tile[32][kTurn + 2];
+    const int64_t b = block0 + blockIdx.x;
+    if (b < listed) list_rows(a, (int)b, items, bounds, scratch);
+    else turn(w, a.R, (int)((b - listed) / cblocks), (int)((b - listed) % cblocks) * kTurn, tile);
+}
+
 // One item, 64 columns per wave.  DIRECT: the item is the adapter, and its sums are the gradient.
 template <class T, int RT, bool DIRECT>
-__global__ void __launch_bounds__(kThreads) adapter_grad_kernel(GradArgs a, int cblocks0, int cblocks, int64_t columns,
-                                                                int item0)
+__global__ void __launch_bounds__(kThreads, 3) adapter_grad_kernel(GradArgs a, int cblocks0, int cblocks, int64_t columns,
+                                                                   int item0)
 {
-    __shared__ uint16_t zt[2][16 * RT * kPitch];  // [first, second number][rank][row]
-    __shared__ int list[DIRECT ? kDirectRows : kChunkRows];
+    constexpr int CHUNK = kChunkRows<RT>, PITCH = CHUNK + 8;
+    __shared__ uint16_t zt[2][16 * RT * PITCH];  // [first, second number][rank][row]
+    __shared__ int64_t offset[CHUNK];            // of a chunk's rows of v, in bytes
+    __shared__ int list[DIRECT ? kDirectRows : 1];
     __shared__ uint32_t most[16 * RT];
     __shared__ int scratch[kWaves];
     const int lane = threadIdx.x & 63, i16 = lane & 15, q = lane >> 4;
@@ -127,18 +194,39 @@ __global__ void __launch_bounds__(kThreads) adapter_grad_kernel(GradArgs a, int 
     }
     __syncthreads();
     auto row_at = [&](int i) __attribute__((always_inline)) { return DIRECT ? list[i] : order[i]; };
-    auto z_at = [&](int row, int r) __attribute__((always_inline)) {
+    // EACH ranks of one row of d or t: the sum of its parts
+    constexpr int EACH = 16 * RT * CHUNK / kThreads;
+    static_assert(EACH % 8 == 0 && 16 * RT % EACH == 0, "whole chunks of ranks");
+    auto z_of = [&](int row, int r, float (&z)[EACH]) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) z[i] = 0.0f;
         const float* p = s.z + (int64_t)row * a.R + r0 + r;
-        float v = *p;
-        for (int k = 1; k < s.splits; ++k) v += p[(int64_t)k * a.M * a.R];
-        return v;
+        for (int k = 0; k < s.splits; ++k, p += (int64_t)a.M * a.R) {
+#pragma unroll
+            for (int i = 0; i < EACH; i += 8) {
+                if (r + i < ranks) {
+                    const Chunk<Fp32> d = load_chunk(reinterpret_cast<const Fp32*>(p + i), ranks - r - i);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) z[i + e] += d.e[e].v;
+                }
+            }
+        }
     };
+    const int my_row = threadIdx.x % CHUNK, my_rank = threadIdx.x / CHUNK * EACH;
     if constexpr (!__is_same(T, Bf16)) {  // one power of two per rank for all of the item's rows
         if (threadIdx.x < 16 * RT) most[threadIdx.x] = 0u;
         __syncthreads();
-        for (int j = threadIdx.x; j < count * ranks; j += kThreads) {
-            atomicMax(&most[j % ranks], abs_bits(z_at(row_at(j / ranks), j % ranks)));
+        uint32_t top[EACH];
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) top[i] = 0u;
+        for (int i = my_row; i < count; i += CHUNK) {
+            float z[EACH];
+            z_of(row_at(i), my_rank, z);
+#pragma unroll
+            for (int e = 0; e < EACH; ++e) top[e] = max(top[e], abs_bits(z[e]));
         }
+#pragma unroll
+        for (int e = 0; e < EACH; ++e) atomicMax(&most[my_rank + e], top[e]);  // a maximum: any order
         __syncthreads();
     }
 
@@ -148,33 +236,67 @@ __global__ void __launch_bounds__(kThreads) adapter_grad_kernel(GradArgs a, int 
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[k][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    for (int base = 0; base < count; base += kChunkRows) {
-        const int n = min(kChunkRows, count - base);
+    const char* v = reinterpret_cast<const char*>(static_cast<const T*>(s.v) + c);
+    for (int base = 0; base < count; base += CHUNK) {
+        const int n = min(CHUNK, count - base), steps = (n + 31) >> 5;
         if (base) __syncthreads();
-        if constexpr (!DIRECT) {
-            if (threadIdx.x < kChunkRows) list[threadIdx.x] = order[base + min((int)threadIdx.x, n - 1)];
-            __syncthreads();
-        }
-        const int lbase = DIRECT ? base : 0;
-        const int padded = (n + 31) & ~31;
-        for (int j = threadIdx.x; j < padded * 16 * RT; j += kThreads) {
-            const int r = j % (16 * RT), i = j / (16 * RT);
-            uint16_t hi = 0, lo = 0;
-            if (i < n && r < ranks) {
-                const float f = __is_same(T, Bf16) ? 1.0f : pow2_for<T>(most[r]).up;
-                split16<T>(z_at(list[lbase + i], r) * f, hi, lo);
+        for (int i = threadIdx.x; i < 32 * steps; i += kThreads) offset[i] = row_at(base + min(i, n - 1)) * s.ldv * 2;
+        __syncthreads();
+        constexpr int U = kSteps<RT>;
+        uint32_t raw[U][8][2];
+        auto load = [&](int u, int k) __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const char* p = v + offset[32 * k + 8 * q + i];
+                if (c + 4 <= s.C) {
+                    const raw2_t d = *reinterpret_cast<const u32x2_any*>(p);
+                    raw[u][i][0] = d[0];
+                    raw[u][i][1] = d[1];
+                } else {
+                    const uint16_t* e = reinterpret_cast<const uint16_t*>(p);
+#pragma unroll
+                    for (int d = 0; d < 2; ++d) {
+                        raw[u][i][d] = (c + 2 * d < s.C ? (uint32_t)e[2 * d] : 0u) | (c + 2 * d + 1 < s.C ? (uint32_t)e[2 * d + 1] << 16 : 0u);
+                    }
+                }
             }
-            zt[0][r * kPitch + i] = hi;
-            zt[1][r * kPitch + i] = lo;
+        };
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (u < steps) load(u, u);
+        }
+        // the chunk's d or t while its rows are on their way
+        if (my_row < 32 * steps) {
+            float z[EACH];
+            if (my_row < n) {
+                z_of(row_at(base + my_row), my_rank, z);
+            } else {
+#pragma unroll
+                for (int e = 0; e < EACH; ++e) z[e] = 0.0f;
+            }
+#pragma unroll
+            for (int e = 0; e < EACH; ++e) {
+                const int r = my_rank + e;
+                const float f = __is_same(T, Bf16) ? 1.0f : pow2_for<T>(most[r]).up;
+                uint16_t hi, lo;
+                split16<T>(z[e] * f, hi, lo);
+                zt[0][r * PITCH + my_row] = hi;
+                zt[1][r * PITCH + my_row] = lo;
+            }
         }
         __syncthreads();
-        const T* v = static_cast<const T*>(s.v);
-#pragma unroll 2
-        for (int k = 0; k < n; k += 32) {
+        auto use = [&](int u, int k) __attribute__((always_inline)) {
             raw4_t vf[4];
-            const int i0 = k + 8 * q;
-            load_columns<T, 4>([&](int i) { return v + list[lbase + min(i0 + i, n - 1)] * s.ldv + c; }, s.C - c, vf);
-            if (k + 32 > n) {  // rows past the last are a row again: not even a NaN of theirs may count twice
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+#pragma unroll
+                for (int d = 0; d < 2; ++d) {
+                    vf[2 * d][h] = __builtin_amdgcn_perm(raw[u][2 * h + 1][d], raw[u][2 * h][d], 0x05040100u);
+                    vf[2 * d + 1][h] = __builtin_amdgcn_perm(raw[u][2 * h + 1][d], raw[u][2 * h][d], 0x07060302u);
+                }
+            }
+            const int i0 = 32 * k + 8 * q;
+            if (32 * k + 32 > n) {  // rows past the last are a row again: not even a NaN of theirs may count twice
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
 #pragma unroll
@@ -183,19 +305,26 @@ __global__ void __launch_bounds__(kThreads) adapter_grad_kernel(GradArgs a, int 
             }
 #pragma unroll
             for (int t = 0; t < RT; ++t) {
-                const raw4_t hi = *reinterpret_cast<const raw4_t*>(&zt[0][(16 * t + i16) * kPitch + i0]);
-                const raw4_t lo = *reinterpret_cast<const raw4_t*>(&zt[1][(16 * t + i16) * kPitch + i0]);
+                const raw4_t hi = *reinterpret_cast<const raw4_t*>(&zt[0][(16 * t + i16) * PITCH + i0]);
+                const raw4_t lo = *reinterpret_cast<const raw4_t*>(&zt[1][(16 * t + i16) * PITCH + i0]);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     acc[t][j] = mfma16<T>(hi, vf[j], acc[t][j]);
                     acc[t][j] = mfma16<T>(lo, vf[j], acc[t][j]);
                 }
             }
+        };
+        for (int k = 0; k < steps; k += U) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (k + u < steps) use(u, k + u);
+                if (k + u + U < steps) load(u, k + u + U);
+            }
         }
     }
 
     const float scale = DIRECT && a.scale ? a.scale[l] : 1.0f;
-    const int64_t offset = which ? a.side[0].grad ? a.side[0].C : 0 : 0;
+    const int64_t side = which && a.side[0].grad ? a.side[0].C : 0;
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
 #pragma unroll
@@ -212,61 +341,53 @@ __global__ void __launch_bounds__(kThreads) adapter_grad_kernel(GradArgs a, int 
                                                     : ((int64_t)l * a.R + r0 + r) * s.C + c + j;
                     static_cast<T*>(s.grad)[at] = narrow<T>(count ? scale * sum : 0.0f);
                 } else {
-                    a.part[((int64_t)item * a.R + r0 + r) * columns + offset + c + j] = sum;
+                    a.part[((int64_t)item * a.R + r0 + r) * columns + side + c + j] = sum;
                 }
             }
         }
     }
 }
 
-// The items' sums of 4 ranks and 4 columns of an adapter, in order, to the gradient
+// The items' sums, in order, to the gradient: a thread has 4 columns of a rank (da) or 4 ranks of a column (db), which
+// are neighbours where they are stored, and neighbouring threads neighbouring columns, which are where they are read.
+// The first `units0` units of workgroups of an adapter are the first side's.
 template <class T>
 __global__ void __launch_bounds__(kThreads) adapter_join_kernel(GradArgs a, const int32_t* bounds, int64_t columns,
-                                                                int quads, int64_t total, int64_t first_thread)
+                                                                int units0, int units, int l0)
 {
-    const int64_t id = first_thread + (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (id >= total) return;
-    const int rquads = (a.R + 3) >> 2;
-    const int cq = (int)(id % quads);
-    const int rq = (int)(id / quads % rquads), l = (int)(id / quads / rquads);
-    const int quads0 = a.side[0].grad ? (a.side[0].C + 3) >> 2 : 0;
-    const int which = cq >= quads0 ? 1 : 0;
+    const int l = l0 + blockIdx.x / units, unit = blockIdx.x % units;
+    const int which = unit >= units0 ? 1 : 0;
     const GradSide& s = a.side[which];
-    const int c = 4 * (cq - (which ? quads0 : 0)), r = 4 * rq;
-    const int64_t offset = which ? (a.side[0].grad ? a.side[0].C : 0) : 0;
+    const int inner = s.rank_inner ? s.C : (s.C + 3) >> 2, blocks = (inner + kThreads - 1) / kThreads;
+    const int u = unit - (which ? units0 : 0), i = u % blocks * kThreads + threadIdx.x;
+    if (i >= inner) return;
+    const int r = s.rank_inner ? u / blocks * 4 : u / blocks, c = s.rank_inner ? i : 4 * i;
+    const int n_here = s.rank_inner ? min(4, a.R - r) : min(4, s.C - c);
+    const int64_t step = s.rank_inner ? columns : 1;
     const int first = bounds[2 * l], count = bounds[2 * l + 1];
-    const int base = first / a.rows + l, n = (count + a.rows - 1) / a.rows;
-    float v[4][4] = {};
-    const bool whole = r + 4 <= a.R && c + 4 <= s.C;
-    for (int k = 0; k < n; ++k) {
-        const float* p = a.part + ((int64_t)(base + k) * a.R + r) * columns + offset + c;
-        if (whole) {
+    const int n = (count + a.rows - 1) / a.rows;
+    const int64_t item = (int64_t)a.R * columns;
+    const float* p = a.part + (first / a.rows + l) * item + r * columns + (which && a.side[0].grad ? a.side[0].C : 0) + c;
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (n_here == 4) {
+#pragma unroll 4
+        for (int k = 0; k < n; ++k) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const raw4_t d = *reinterpret_cast<const u32x4_any*>(p + i * columns);
+            for (int j = 0; j < 4; ++j) v[j] += p[k * item + j * step];
+        }
+    } else {
+        for (int k = 0; k < n; ++k) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) v[i][j] += __uint_as_float(d[j]);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (r + i < a.R && c + j < s.C) v[i][j] += p[i * columns + j];
-                }
+            for (int j = 0; j < 4; ++j) {
+                if (j < n_here) v[j] += p[k * item + j * step];
             }
         }
     }
     const float scale = a.scale ? a.scale[l] : 1.0f;
+    T* to = static_cast<T*>(s.grad) + (s.rank_inner ? ((int64_t)l * s.C + c) * a.R + r : ((int64_t)l * a.R + r) * s.C + c);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (r + i >= a.R || c + j >= s.C) continue;
-            const int64_t at = s.rank_inner ? ((int64_t)l * s.C + c + j) * a.R + r + i
-                                            : ((int64_t)l * a.R + r + i) * s.C + c + j;
-            static_cast<T*>(s.grad)[at] = narrow<T>(n ? scale * v[i][j] : 0.0f);
-        }
+    for (int j = 0; j < 4; ++j) {
+        if (j < n_here) to[j] = narrow<T>(n ? scale * v[j] : 0.0f);
     }
 }
 
@@ -297,21 +418,20 @@ hipError_t grad_launch(const GradArgs& a, hipStream_t stream)
     const int64_t items = direct ? a.L : adapter_grad_items(a.M, a.L, a.rows);
     const int64_t c0 = a.side[0].grad ? a.side[0].C : 0, c1 = a.side[1].grad ? a.side[1].C : 0, columns = c0 + c1;
     const int cblocks0 = (int)((c0 + 64 * kWaves - 1) / (64 * kWaves)), cblocks1 = (int)((c1 + 64 * kWaves - 1) / (64 * kWaves));
-    if (!direct) {
-        hipLaunchKernelGGL(adapter_order_kernel, dim3(a.L), dim3(kOrderThreads), 0, stream, a, (int)items,
-                           bounds_of(a, items));
-    }
     const int cblocks = cblocks0 + cblocks1;
     if (a.R <= 16) grad_items<T, 1>(a, direct, items, cblocks0, cblocks, columns, stream);
     else if (a.R <= 32) grad_items<T, 2>(a, direct, items, cblocks0, cblocks, columns, stream);
     else grad_items<T, 4>(a, direct, items, cblocks0, cblocks, columns, stream);
     if (!direct) {
-        const int quads = (int)((c0 + 3) / 4 + (c1 + 3) / 4);
-        const int64_t total = (int64_t)a.L * ((a.R + 3) / 4) * quads;
-        for (int64_t t = 0; t < total; t += kMaxBlocks * kThreads) {
-            const int64_t blocks = (total - t + kThreads - 1) / kThreads;
-            hipLaunchKernelGGL(adapter_join_kernel<T>, dim3((unsigned)(blocks < kMaxBlocks ? blocks : kMaxBlocks)),
-                               dim3(kThreads), 0, stream, a, bounds_of(a, items), columns, quads, total, t);
+        auto units = [&](const GradSide& s) {
+            const int inner = s.rank_inner ? s.C : (s.C + 3) / 4;
+            return s.grad ? (inner + kThreads - 1) / kThreads * (s.rank_inner ? (a.R + 3) / 4 : a.R) : 0;
+        };
+        const int units0 = units(a.side[0]), all = units0 + units(a.side[1]);
+        const int fit = kMaxBlocks / all < 1 ? 1 : (int)(kMaxBlocks / all);
+        for (int l = 0; l < a.L; l += fit) {
+            hipLaunchKernelGGL(adapter_join_kernel<T>, dim3((unsigned)((a.L - l < fit ? a.L - l : fit) * all)), dim3(kThreads), 0,
+                               stream, a, bounds_of(a, items), columns, units0, all, l);
         }
     }
     return hipGetLastError();
@@ -327,11 +447,23 @@ int adapter_grad_rows(int M, int64_t C)
 {
     if (M <= kDirectRows) return kDirectRows;
     const int64_t cblocks = (C + 64 * kWaves - 1) / (64 * kWaves);
-    int64_t rows = ((int64_t)M * cblocks / 1024 + kChunkRows - 1) / kChunkRows * kChunkRows;
-    return (int)(rows < 2 * kChunkRows ? 2 * kChunkRows : rows > 4096 ? 4096 : rows);
+    const int64_t rows = ((int64_t)M * cblocks / 1024 + kItemStep - 1) / kItemStep * kItemStep;
+    return (int)(rows < kItemStep ? kItemStep : rows > 4096 ? 4096 : rows);
 }
 
 int64_t adapter_grad_items(int M, int L, int rows) { return (int64_t)M / rows + L; }
+
+hipError_t adapter_prepare_launch(const GradArgs& a, bool list, const Turn& w, hipStream_t stream)
+{
+    const int64_t items = adapter_grad_items(a.M, a.L, a.rows);
+    const int cblocks = (w.C + kTurn - 1) / kTurn, listed = list ? a.L : 0;
+    const int64_t blocks = listed + (int64_t)a.L * cblocks, fit = 1 << 21;
+    for (int64_t b = 0; b < blocks; b += fit) {
+        hipLaunchKernelGGL(adapter_prepare_kernel, dim3((unsigned)(blocks - b < fit ? blocks - b : fit)), dim3(kOrderThreads), 0,
+                           stream, a, listed, (int)items, bounds_of(a, items), w, cblocks, b);
+    }
+    return hipGetLastError();
+}
 
 hipError_t adapter_grad_launch(int dtype, const GradArgs& a, hipStream_t stream)
 {

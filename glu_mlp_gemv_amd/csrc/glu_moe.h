@@ -36,8 +36,8 @@ struct MoeArgs {
 };
 
 // How the second product is cut: `splits` sets of workgroups take the active experts in turn, and within a workgroup
-// `parts` waves share one expert's columns.
-struct MoePlan { int splits, parts; };
+// `parts` waves share one expert's columns; rows: weight rows per workgroup, 4 or 16.
+struct MoePlan { int splits, parts, rows; };
 MoePlan moe_plan(int M, int K, int N, int E, int top, bool e4m3);
 hipError_t moe_launch(int dtype, int logits_dtype, bool e4m3, const MoeArgs& a, const MoePlan& p, hipStream_t stream);
 

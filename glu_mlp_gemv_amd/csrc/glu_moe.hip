@@ -2,8 +2,8 @@
 //
 //   out[m] = sum over the experts e of row m of p_e down_e (silu(gate_e x[m]) * (up_e x[m]))
 //
-// Bound by the bytes of the experts that some row chose: each of their matrices is read once.  Three launches.  The
-// first ranks the logits, one wave per row, and lists the active experts with their rows: a row's bit in a 64-bit
+// Bound by the bytes of the experts that some row chose: each of their matrices is read once.  Three launches, or two for up
+// to 4 rows, and a join where the third is cut.  The first ranks the logits, one wave per row, and lists the active experts with their rows: a row's bit in a 64-bit
 // mask per expert, so that the lists come out in order whatever order the waves ran in.  The second gives each active
 // expert's gate and up, 16 rows of weights at a time, to a workgroup whose waves share the contraction.  The third gives 16
 // rows of every active expert's down to a workgroup whose waves take experts in turn, and each wave adds what its experts
@@ -21,7 +21,8 @@ namespace {
 constexpr int kRouteThreads = 1024;
 constexpr int kRouteWaves = kRouteThreads / 64;
 constexpr int kMaxExperts = 1024;
-constexpr int kPerLane = kMaxExperts / 64;
+constexpr int kMaxTop = 32;
+constexpr int kRoutedRows = 4;
 constexpr int kUpThreads = 256;
 constexpr int kUpWaves = kUpThreads / 64;
 constexpr int kDownThreads = 512;
@@ -29,93 +30,103 @@ constexpr int kDownWaves = kDownThreads / 64;
 
 // ---- routing -----------------------------------------------------------------------
 
-// Order of logits as unsigned numbers: -inf (masked) is 0x007fffff, NaN is above all, and -0 equals +0.
+// Order of logits as unsigned numbers, above 0: NaN is above all, -0 equals +0, and -inf, which masks an expert, is 0.
 __device__ __forceinline__ uint32_t order_of(float f)
 {
     const uint32_t b = __float_as_uint(f + 0.0f);
     if ((b & 0x7fffffffu) > 0x7f800000u) return 0xffffffffu;
-    return b ^ (b >> 31 ? 0xffffffffu : 0x80000000u);
+    return b == 0xff800000u ? 0u : b ^ (b >> 31 ? 0xffffffffu : 0x80000000u);
 }
-constexpr uint32_t kMasked = 0x007fffffu;
-
-__device__ __forceinline__ uint64_t wave_max(uint64_t v)
+__device__ __forceinline__ float logit_of(uint32_t order)
 {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const uint64_t o = __shfl_xor(v, d);
-        v = o > v ? o : v;
-    }
-    return v;
+    return __uint_as_float(order ^ (order >> 31 ? 0x80000000u : 0xffffffffu));
 }
 
-template <class L>
-__global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(MoeArgs a)
+// the largest of the wave's numbers, in every lane
+__device__ __forceinline__ uint32_t wave_max(uint32_t x)
 {
-    __shared__ uint32_t mask[kMaxExperts][2];  // rows of an expert
-    __shared__ int first[kMaxExperts];
-    __shared__ int sums[kRouteWaves][2];
-    extern __shared__ int chosen[];            // [M][top] expert, or -1; then [M][top] its weight
-    float* p = reinterpret_cast<float*>(chosen + a.M * a.top);
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (int e = threadIdx.x; e < a.E; e += kRouteThreads) mask[e][0] = mask[e][1] = 0u;
+    x = max16(x);
+    x = max(x, (uint32_t)__builtin_amdgcn_ds_swizzle((int)x, 0x401F));  // lane ^ 16
+    auto pr = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+    return max(pr[0], pr[1]);
+}
+
+// What a workgroup of THREADS knows of the rows' experts, in LDS
+template <int THREADS>
+struct Routing {
+    uint32_t mask[kMaxExperts][2];  // rows of an expert
+    int first[kMaxExperts];         // its first slot
+    int sums[THREADS / 64][2];
+};
+
+// Ranks the logits, a wave per row, and lists the active experts with their rows.  chosen [M][top] and p [M][top]: LDS;
+// active, row and weight may be in LDS too.  PER: logits per lane.  Returns how many experts are active.
+template <int THREADS, int PER, class L>
+__device__ __forceinline__ int route(const MoeArgs& a, Routing<THREADS>& r, int* chosen, float* p, Active* active, int* row,
+                                     float* weight)
+{
+    constexpr int WAVES = THREADS / 64, EACH = kMaxExperts / THREADS;  // experts per thread
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    for (int e = threadIdx.x; e < a.E; e += THREADS) r.mask[e][0] = r.mask[e][1] = 0u;
     __syncthreads();
-    for (int m = wave; m < a.M; m += kRouteWaves) {
-        const L* row = static_cast<const L*>(a.logits) + m * a.ldl;
-        float f[kPerLane];
-        uint32_t left = 0;  // which of this lane's logits are not taken yet
+    L next[PER];  // the logits of the wave's next row
+    auto load = [&](int m) __attribute__((always_inline)) {
+        const L* logits = static_cast<const L*>(a.logits) + m * a.ldl;
 #pragma unroll
-        for (int i = 0; i < kPerLane; ++i) {
-            const int e = lane + 64 * i;
-            f[i] = e < a.E ? widen(row[e]) : 0.0f;
-            if (e < a.E && order_of(f[i]) != kMasked) left |= 1u << i;
-        }
-        float most = 0.0f, sum = 0.0f;
+        for (int i = 0; i < PER; ++i) next[i] = logits[min(lane + 64 * i, a.E - 1)];
+    };
+    if (wave < a.M) load(wave);
+    for (int m = wave; m < a.M; m += WAVES) {
+        uint32_t key[PER], all[PER];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) key[i] = all[i] = lane + 64 * i < a.E ? order_of(widen(next[i])) : 0u;
+        if (m + WAVES < a.M) load(m + WAVES);
+        uint32_t best = 0;  // lane j: the j-th of the row
+        int expert = -1;
         for (int j = 0; j < a.top; ++j) {
-            uint64_t best = 0;  // order, then the lowest expert
+            uint32_t most = key[0];
 #pragma unroll
-            for (int i = 0; i < kPerLane; ++i) {
-                const uint64_t key = (uint64_t)order_of(f[i]) << 32 | (uint32_t)(kMaxExperts - lane - 64 * i);
-                if ((left >> i & 1) && key > best) best = key;
-            }
-            best = wave_max(best);
-            if (best == 0) {
-                if (lane == 0) chosen[m * a.top + j] = -1;
-                continue;
-            }
-            const int e = kMaxExperts - (int)(uint32_t)best;
-            float l = 0.0f;
+            for (int i = 1; i < PER; ++i) most = max(most, key[i]);
+            most = wave_max(most);
+            if (most == 0) break;
+            int e = -1;  // of equal ones the lowest
 #pragma unroll
-            for (int i = 0; i < kPerLane; ++i) {
-                if (lane + 64 * i == e) {
-                    left &= ~(1u << i);
-                    l = f[i];
-                }
+            for (int i = 0; i < PER; ++i) {
+                const uint64_t b = __ballot(key[i] == most);
+                if (e < 0 && b) e = 64 * i + __builtin_ctzll(b);
             }
-            l = __shfl(l, e & 63);
-            if (j == 0) most = l;
-            const float w = expf(l - most);
-            sum += w;
-            if (lane == 0) {
-                chosen[m * a.top + j] = e;
-                p[m * a.top + j] = w;
-                atomicOr(&mask[e][m >> 5], 1u << (m & 31));
+#pragma unroll
+            for (int i = 0; i < PER; ++i) key[i] = e == lane + 64 * i ? 0u : key[i];
+            if (lane == j) {
+                best = most;
+                expert = e;
             }
         }
+        const float top = logit_of(__builtin_amdgcn_readfirstlane(best));
+        float w = expert >= 0 ? expf(logit_of(best) - top) : 0.0f, sum = w;
         if (!a.normalize) {
-            float s = 0.0f;
+            sum = 0.0f;
 #pragma unroll
-            for (int i = 0; i < kPerLane; ++i) {
-                if (lane + 64 * i < a.E) s += expf(f[i] - most);
-            }
-            sum = wave_sum(s);
+            for (int i = 0; i < PER; ++i) sum += all[i] ? expf(logit_of(all[i]) - top) : 0.0f;
         }
-        for (int j = lane; j < a.top; j += 64) p[m * a.top + j] /= sum;
+        sum = wave_sum(sum);
+        if (lane < a.top) {
+            chosen[m * a.top + lane] = expert;
+            p[m * a.top + lane] = w / sum;
+            if (expert >= 0) atomicOr(&r.mask[expert][m >> 5], 1u << (m & 31));
+        }
     }
     __syncthreads();
     // slots and the list of active experts, ascending
-    const int e = threadIdx.x;
-    const int count = e < a.E ? __popc(mask[e][0]) + __popc(mask[e][1]) : 0;
-    int slots = count, actives = count > 0;
+    const int e0 = threadIdx.x * EACH;
+    int count[EACH], slots = 0, actives = 0;
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+        count[i] = e0 + i < a.E ? __popc(r.mask[e0 + i][0]) + __popc(r.mask[e0 + i][1]) : 0;
+        slots += count[i];
+        actives += count[i] > 0;
+    }
+    const int my_slots = slots, my_actives = actives;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
         const int s = __shfl_up(slots, d), n = __shfl_up(actives, d);
@@ -125,28 +136,47 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(MoeArgs a)
         }
     }
     if (lane == 63) {
-        sums[wave][0] = slots;
-        sums[wave][1] = actives;
+        r.sums[wave][0] = slots;
+        r.sums[wave][1] = actives;
     }
     __syncthreads();
-    for (int w = 0; w < wave; ++w) {
-        slots += sums[w][0];
-        actives += sums[w][1];
+    slots -= my_slots;
+    actives -= my_actives;
+    int total = 0;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) {
+        if (w < wave) {
+            slots += r.sums[w][0];
+            actives += r.sums[w][1];
+        }
+        total += r.sums[w][1];
     }
-    if (e < a.E) {
-        first[e] = slots - count;
-        if (count > 0) a.active[actives - 1] = Active{e, slots - count, count};
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+        if (e0 + i < a.E) r.first[e0 + i] = slots;
+        if (count[i] > 0) active[actives++] = Active{e0 + i, slots, count[i]};
+        slots += count[i];
     }
-    if (e == kRouteThreads - 1) *a.actives = actives;
     __syncthreads();
-    for (int i = threadIdx.x; i < a.M * a.top; i += kRouteThreads) {
+    for (int i = threadIdx.x; i < a.M * a.top; i += THREADS) {
         const int x = chosen[i], m = i / a.top;
         if (x < 0) continue;
         const uint32_t low = m < 32 ? (1u << m) - 1u : 0xffffffffu, high = m < 32 ? 0u : (1u << (m - 32)) - 1u;
-        const int slot = first[x] + __popc(mask[x][0] & low) + __popc(mask[x][1] & high);
-        a.row[slot] = m;
-        a.weight[slot] = p[i];
+        const int slot = r.first[x] + __popc(r.mask[x][0] & low) + __popc(r.mask[x][1] & high);
+        row[slot] = m;
+        weight[slot] = p[i];
     }
+    return total;
+}
+
+template <class L, int PER>
+__global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(MoeArgs a)
+{
+    __shared__ Routing<kRouteThreads> r;
+    extern __shared__ int chosen[];  // [M][top] experts, then weights
+    const int n = route<kRouteThreads, PER, L>(a, r, chosen, reinterpret_cast<float*>(chosen + a.M * a.top), a.active, a.row,
+                                               a.weight);
+    if (threadIdx.x == 0) *a.actives = n;
 }
 
 // ---- products ----------------------------------------------------------------------
@@ -185,16 +215,17 @@ __device__ __forceinline__ raw4_t bytes16(const uint8_t* p, int n)
 template <bool E8> constexpr int kStageCols = E8 ? 128 : 64;
 
 // Stages s0, s0 + step, .. below s1 of NM products of 16 weight rows (this lane's at w[i]) with 16 TT rows of v (this lane's
-// at v[t]), C columns.  sc[i]: the scales of the weight rows' block, one per 128 columns.
-template <class T, bool E8, int NM, int TT>
+// at v[t]), C columns.  sc[i]: the scales of the weight rows' block, one per 128 columns.  With S places along the columns
+// a stage is S times as long, and this lane's rows are at `place` of it.
+template <class T, bool E8, int NM, int TT, int S>
 __device__ __forceinline__ void products(const uint8_t* const (&w)[NM], const float* const (&sc)[NM], const T* const (&v)[TT],
-                                         int C, int s0, int s1, int step, int q, f32x4 (&acc)[NM][TT])
+                                         int C, int s0, int s1, int step, int q, int place, f32x4 (&acc)[NM][TT])
 {
     constexpr int SC = kStageCols<E8>;
     auto stage = [&](int s, auto tag) __attribute__((always_inline)) {
         constexpr bool WHOLE = decltype(tag)::value;
         if constexpr (E8) {
-            const int c = s * SC + 16 * q;
+            const int c = (s * S + place) * SC + 16 * q;
             raw4_t wv[NM][2], xv[TT][4];
 #pragma unroll
             for (int i = 0; i < NM; ++i) {
@@ -214,7 +245,7 @@ __device__ __forceinline__ void products(const uint8_t* const (&w)[NM], const fl
                 raw4_t lo[2], hi[2];
                 widen16<T>(wv[i][0], lo);
                 widen16<T>(wv[i][1], hi);
-                const float scale = sc[i][s];
+                const float scale = sc[i][S == 1 ? s : min(s * S + place, (C - 1) / kGroup)];
 #pragma unroll
                 for (int t = 0; t < TT; ++t) {
                     f32x4 p = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -227,7 +258,7 @@ __device__ __forceinline__ void products(const uint8_t* const (&w)[NM], const fl
                 }
             }
         } else {
-            const int c = s * SC + 8 * q;
+            const int c = (s * S + place) * SC + 8 * q;
             raw4_t wv[NM][2], xv[TT][2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -250,7 +281,7 @@ __device__ __forceinline__ void products(const uint8_t* const (&w)[NM], const fl
             }
         }
     };
-    const int whole = min(s1, C / SC);
+    const int whole = min(s1, C / (SC * S));
     int s = s0;
 #pragma unroll 4
     for (; s < whole; s += step) stage(s, Whole{});
@@ -259,7 +290,8 @@ __device__ __forceinline__ void products(const uint8_t* const (&w)[NM], const fl
 
 // act[slot][n] = T(silu(gate x) * (up x)) of one active expert, 16 columns n
 template <class T, bool E8, int TT>
-__device__ __forceinline__ void gate_up(const MoeArgs& a, const Active& x, int n0, int t0, float (*red)[2][TT][256])
+__device__ __forceinline__ void gate_up(const MoeArgs& a, const int* row, const Active& x, int n0, int t0,
+                                        float (*red)[2][TT][256])
 {
     const int lane = threadIdx.x & 63, i16 = lane & 15, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -275,11 +307,11 @@ __device__ __forceinline__ void gate_up(const MoeArgs& a, const Active& x, int n
     f32x4 acc[2][TT];
 #pragma unroll
     for (int t = 0; t < TT; ++t) {
-        v[t] = static_cast<const T*>(a.x) + a.row[x.first + min(t0 + 16 * t + i16, x.count - 1)] * a.ldx;
+        v[t] = static_cast<const T*>(a.x) + row[x.first + min(t0 + 16 * t + i16, x.count - 1)] * a.ldx;
         acc[0][t] = acc[1][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
     const int stages = (a.K + kStageCols<E8> - 1) / kStageCols<E8>;
-    products<T, E8, 2, TT>(w, sc, v, a.K, wave, stages, kUpWaves, q, acc);
+    products<T, E8, 2, TT, 1>(w, sc, v, a.K, wave, stages, kUpWaves, q, 0, acc);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
 #pragma unroll
@@ -308,38 +340,68 @@ __global__ void __launch_bounds__(kUpThreads) moe_up_kernel(MoeArgs a, int block
     const int j = blockIdx.x / blocks, n0 = (blockIdx.x - j * blocks) * 16;
     if (j >= *a.actives) return;
     const Active x = a.active[j];
-    if (x.count <= 16) gate_up<T, E8, 1>(a, x, n0, 0, reinterpret_cast<float(*)[2][1][256]>(&red[0][0][0][0]));
-    else gate_up<T, E8, 4>(a, x, n0, 0, red);
+    if (x.count <= 16) gate_up<T, E8, 1>(a, a.row, x, n0, 0, reinterpret_cast<float(*)[2][1][256]>(&red[0][0][0][0]));
+    else gate_up<T, E8, 4>(a, a.row, x, n0, 0, red);
 }
 
-// out[m][c], 16 columns c, of the active experts that are this split's
-template <class T, bool E8>
+// The same for up to kRoutedRows rows, a wave for each: every workgroup ranks the logits itself, which takes less time
+// than a launch before it, and the first one leaves the lists for the next launch.
+template <class T, bool E8, class L, int PER>
+__global__ void __launch_bounds__(kUpThreads) moe_routed_up_kernel(MoeArgs a, int blocks)
+{
+    __shared__ union {
+        Routing<kUpThreads> r;
+        float red[kUpWaves][2][1][256];
+    } u;
+    __shared__ int chosen[kRoutedRows * kMaxTop], row[kRoutedRows * kMaxTop];
+    __shared__ float p[kRoutedRows * kMaxTop], weight[kRoutedRows * kMaxTop];
+    __shared__ Active active[kRoutedRows * kMaxTop];
+    const int j = blockIdx.x / blocks, n0 = (blockIdx.x - j * blocks) * 16;
+    const int n = route<kUpThreads, PER, L>(a, u.r, chosen, p, active, row, weight);
+    __syncthreads();
+    if (blockIdx.x == 0) {
+        if (threadIdx.x == 0) *a.actives = n;
+        for (int i = threadIdx.x; i < a.M * a.top; i += kUpThreads) {
+            if (i < n) a.active[i] = active[i];
+            a.row[i] = row[i];  // slots past the last hold nothing that is read
+            a.weight[i] = weight[i];
+        }
+    }
+    if (n0 < a.N && j < n) gate_up<T, E8, 1>(a, row, active[j], n0, 0, u.red);
+}
+
+// out[m][c], ROWS columns c, of the active experts that are this split's.  ROWS = 4, for up to 4 rows of x, takes the same 4
+// weight rows at 4 places along their columns as the 16 rows of an instruction, and x's rows likewise: of the results
+// the blocks on the diagonal are wanted, and there are 4 times the workgroups.
+template <class T, bool E8, int ROWS>
 __global__ void __launch_bounds__(kDownThreads) moe_down_kernel(MoeArgs a, MoePlan p)
 {
-    extern __shared__ float sums[];  // [wave][M][16]
+    constexpr int S = 16 / ROWS;     // places
+    extern __shared__ float sums[];  // [wave][place][M][ROWS]
     const int lane = threadIdx.x & 63, i16 = lane & 15, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int c0 = blockIdx.x * 16, split = blockIdx.y;
+    const int c0 = blockIdx.x * ROWS, split = blockIdx.y, place = i16 / ROWS;
     float* mine = sums + wave * a.M * 16;
     for (int i = lane; i < a.M * 16; i += 64) mine[i] = 0.0f;
     __builtin_amdgcn_wave_barrier();  // a row's sums pass between the wave's lanes, in LDS order
     const int actives = *a.actives;
-    const int stages = (a.N + kStageCols<E8> - 1) / kStageCols<E8>;
+    const int stages = (a.N + kStageCols<E8> * S - 1) / (kStageCols<E8> * S);
     const int per = (stages + p.parts - 1) / p.parts;
     constexpr int ES = E8 ? 1 : 2;
     for (int u = wave; ; u += kDownWaves) {
         const int j = u / p.parts * p.splits + split, part = u % p.parts;
         if (j >= actives) break;
         const Active x = a.active[j];
-        const uint8_t* const w[1] = {a.w[2].data + (x.expert * a.w[2].stack + min(c0 + i16, a.K - 1) * a.w[2].ld) * ES};
+        const uint8_t* const w[1] = {a.w[2].data + (x.expert * a.w[2].stack + min(c0 + i16 % ROWS, a.K - 1) * a.w[2].ld) * ES};
         const float* const sc[1] = {E8 ? a.w[2].scale + x.expert * a.w[2].scale_stack + (c0 / kGroup) * a.w[2].scale_ld : nullptr};
-        for (int t = 0; t < x.count; t += 16) {
-            const int s = x.first + min(t + i16, x.count - 1);
+        for (int t = 0; t < x.count; t += ROWS) {
+            const int s = x.first + min(t + i16 % ROWS, x.count - 1);
             const T* const v[1] = {reinterpret_cast<const T*>(a.act) + s * a.ld_act};
             f32x4 acc[1][1] = {{{0.0f, 0.0f, 0.0f, 0.0f}}};
-            products<T, E8, 1, 1>(w, sc, v, a.N, part * per, min(stages, (part + 1) * per), 1, q, acc);
-            if (t + i16 < x.count) {
-                float* to = mine + a.row[s] * 16 + 4 * q;
+            products<T, E8, 1, 1, S>(w, sc, v, a.N, part * per, min(stages, (part + 1) * per), 1, q, place, acc);
+            // rows 4 q .. + 3 of the instruction: with 4 places, place q
+            if (t + i16 % ROWS < x.count && (S == 1 || place == q)) {
+                float* to = mine + (S == 1 ? a.row[s] * 16 + 4 * q : (place * a.M + a.row[s]) * 4);
                 const float weight = a.weight[s];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) to[e] = fmaf(weight, acc[0][0][e], to[e]);
@@ -348,46 +410,62 @@ __global__ void __launch_bounds__(kDownThreads) moe_down_kernel(MoeArgs a, MoePl
         }
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < a.M * 16; i += kDownThreads) {
-        const int m = i >> 4, c = c0 + (i & 15);
+    for (int i = threadIdx.x; i < a.M * ROWS; i += kDownThreads) {
+        const int m = i / ROWS, c = c0 + i % ROWS;
         if (c >= a.K) continue;
-        float v = sums[i];
+        float v = 0.0f;
 #pragma unroll
-        for (int k = 1; k < kDownWaves; ++k) v += sums[k * a.M * 16 + i];
+        for (int k = 0; k < kDownWaves * S; ++k) v += sums[k * a.M * ROWS + i];
         if (p.splits == 1) static_cast<T*>(a.out)[m * a.ldo + c] = narrow<T>(v);
         else a.part[((int64_t)split * a.M + m) * a.K + c] = v;
     }
 }
 
+// The splits' sums of one row, in order
 template <class T>
 __global__ void __launch_bounds__(256) moe_join_kernel(MoeArgs a, int splits)
 {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, n = (int64_t)a.M * a.K;
-    if (i >= n) return;
-    float v = a.part[i];
-    for (int s = 1; s < splits; ++s) v += a.part[s * n + i];
-    static_cast<T*>(a.out)[i / a.K * a.ldo + i % a.K] = narrow<T>(v);
+    const int c = blockIdx.x * 256 + threadIdx.x, m = blockIdx.y;
+    if (c >= a.K) return;
+    const float* p = a.part + (int64_t)m * a.K + c;
+    float v = 0.0f;
+#pragma unroll 8
+    for (int s = 0; s < splits; ++s) v += p[(int64_t)s * a.M * a.K];
+    static_cast<T*>(a.out)[m * a.ldo + c] = narrow<T>(v);
+}
+
+template <class T, bool E8, class L, int PER>
+void first_launches(const MoeArgs& a, hipStream_t stream)
+{
+    const int most = a.M * a.top < a.E ? a.M * a.top : a.E, blocks = a.N > 0 ? (a.N + 15) / 16 : 1;
+    const dim3 grid((unsigned)(most * blocks));
+    if (a.M <= kRoutedRows) {
+        hipLaunchKernelGGL((moe_routed_up_kernel<T, E8, L, PER>), grid, dim3(kUpThreads), 0, stream, a, blocks);
+        return;
+    }
+    hipLaunchKernelGGL((moe_route_kernel<L, PER>), dim3(1), dim3(kRouteThreads), (size_t)a.M * a.top * 8, stream, a);
+    if (a.N > 0) hipLaunchKernelGGL((moe_up_kernel<T, E8>), grid, dim3(kUpThreads), 0, stream, a, blocks);
+}
+
+template <class T, bool E8, class L>
+void first_launches(const MoeArgs& a, hipStream_t stream)
+{
+    if (a.E <= 128) first_launches<T, E8, L, 2>(a, stream);
+    else if (a.E <= 256) first_launches<T, E8, L, 4>(a, stream);
+    else first_launches<T, E8, L, 16>(a, stream);
 }
 
 template <class T, bool E8>
 hipError_t launch(int logits_dtype, const MoeArgs& a, const MoePlan& p, hipStream_t stream)
 {
-    const size_t lds = (size_t)a.M * a.top * 8;
-    if (logits_dtype == GLU_DTYPE_FP32) {
-        hipLaunchKernelGGL(moe_route_kernel<Fp32>, dim3(1), dim3(kRouteThreads), lds, stream, a);
-    } else {
-        hipLaunchKernelGGL(moe_route_kernel<T>, dim3(1), dim3(kRouteThreads), lds, stream, a);
-    }
-    const int most = a.M * a.top < a.E ? a.M * a.top : a.E;
-    if (a.N > 0) {
-        const int blocks = (a.N + 15) / 16;
-        hipLaunchKernelGGL((moe_up_kernel<T, E8>), dim3((unsigned)(most * blocks)), dim3(kUpThreads), 0, stream, a, blocks);
-    }
-    hipLaunchKernelGGL((moe_down_kernel<T, E8>), dim3((a.K + 15) / 16, p.splits), dim3(kDownThreads),
-                       (size_t)kDownWaves * a.M * 64, stream, a, p);
+    if (logits_dtype == GLU_DTYPE_FP32) first_launches<T, E8, Fp32>(a, stream);
+    else first_launches<T, E8, T>(a, stream);
+    const dim3 grid((a.K + p.rows - 1) / p.rows, p.splits);
+    const size_t lds = (size_t)kDownWaves * a.M * 64;
+    if (p.rows == 4) hipLaunchKernelGGL((moe_down_kernel<T, E8, 4>), grid, dim3(kDownThreads), lds, stream, a, p);
+    else hipLaunchKernelGGL((moe_down_kernel<T, E8, 16>), grid, dim3(kDownThreads), lds, stream, a, p);
     if (p.splits > 1) {
-        const int64_t n = (int64_t)a.M * a.K;
-        hipLaunchKernelGGL(moe_join_kernel<T>, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, stream, a, p.splits);
+        hipLaunchKernelGGL(moe_join_kernel<T>, dim3((a.K + 255) / 256, a.M), dim3(256), 0, stream, a, p.splits);
     }
     return hipGetLastError();
 }
@@ -396,13 +474,14 @@ hipError_t launch(int logits_dtype, const MoeArgs& a, const MoePlan& p, hipStrea
 
 MoePlan moe_plan(int M, int K, int N, int E, int top, bool e4m3)
 {
-    const int most = M * top < E ? M * top : E, stages = (N + (e4m3 ? 127 : 63)) / (e4m3 ? 128 : 64);
-    MoePlan p{1, 1};
+    const int most = M * top < E ? M * top : E;
+    MoePlan p{1, 1, M <= 4 ? 4 : 16};
+    const int cols = (e4m3 ? 128 : 64) * 16 / p.rows, stages = (N + cols - 1) / cols;
     // every wave of a workgroup has something to do
-    while (most * p.parts < kDownWaves && p.parts < stages) p.parts *= 2;
-    // and workgroups fill the CUs twice
-    const int blocks = (K + 15) / 16;
-    while (blocks * p.splits < 512 && most * p.parts >= 2 * kDownWaves * p.splits && p.splits < 8) p.splits *= 2;
+    while (most * p.parts < kDownWaves && 2 * p.parts <= stages) p.parts *= 2;
+    // and the CUs have several workgroups; few rows are spared the join
+    const int blocks = (K + p.rows - 1) / p.rows;
+    while (M > kRoutedRows && blocks * p.splits < 1024 && most * p.parts >= 2 * kDownWaves * p.splits && p.splits < 8) p.splits *= 2;
     return p;
 }
 

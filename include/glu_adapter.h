@@ -19,8 +19,8 @@
  *
  * Ownership, execution, determinism and errors are those of glu_gemv.h: all arrays are device memory of the caller,
  * calls are asynchronous on `stream`, may be captured into a HIP graph, allocate nothing, and validate their
- * arguments before any HIP call.  Row strides are in elements and at least the row length; the elements of a row are
- * contiguous; pointers need the alignment of one element.  index is read on the device: nothing is known of it before.
+ * arguments before any HIP call.  Row strides are in elements, at least the row length and at most 2^23, and so are N and
+ * K; the elements of a row are contiguous; pointers need the alignment of one element.  index is read on the device: nothing is known of it before.
  */
 #ifndef GLU_ADAPTER_H
 #define GLU_ADAPTER_H
@@ -79,8 +79,7 @@ glu_status glu_adapter_workspace(int mats, const glu_adapter_sizes* sizes, int64
  *   db[l]  = T(scale[l] sum_{m: i = l} dout[m]^T t[m])     [L, N, R] dense
  * low is the forward's t.  Any of dx, da and db may be NULL: it is not computed.  The rows are summed in fp32 in an
  * order fixed by the sizes and index: deterministic.  An adapter without rows gets zeros.  The sum's operand d or t is two
- * numbers of T as above.  M, N, K <= 2^24, L <= 65536 and (M + L) N, (M + L) K <= 2^48:
- * GLU_ERR_BAD_SHAPE beyond.
+ * numbers of T as above.  M <= 2^24 and L <= 65536: GLU_ERR_BAD_SHAPE beyond.
  * workspace: glu_adapter_backward_workspace() bytes, 16-byte aligned (NULL if 0).
  */
 glu_status glu_adapter_backward(const void* dout, int64_t ldd, const void* x, int64_t ldx, const glu_adapter* ab,

@@ -33,6 +33,8 @@ def need_of(lib, query, *args):
 COMMON = [
     (dict(dtype=FP32), ARG), (dict(dtype=E4M3), ARG), (dict(dtype=-1), ARG),
     (dict(M=-1), SHAPE), (dict(N=-1), SHAPE), (dict(K=-1), SHAPE), (dict(L=0), SHAPE), (dict(R=0), SHAPE), (dict(R=257), SHAPE),
+    (dict(K=(1 << 23) + 1), SHAPE), (dict(N=(1 << 23) + 1), SHAPE), (dict(ldx=(1 << 23) + 1), STRIDE),
+    (dict(a_row=(1 << 23) + 1, a_stack=1 << 30), STRIDE),
     (dict(x=None), NULLP), (dict(a=None), NULLP), (dict(b=None), NULLP), (dict(index=None), NULLP), (dict(ab=None), NULLP),
     (dict(sizes=None), NULLP), (dict(ldx=127), STRIDE), (dict(a_row=127), STRIDE), (dict(a_stack=2047), STRIDE),
     (dict(b_row=15), STRIDE), (dict(b_stack=4095), STRIDE), (dict(a_stack=1 << 62), STRIDE), (dict(b_row=1 << 60), STRIDE),
@@ -97,8 +99,8 @@ def backward(lib, dout=P[0], ldd=256, dx=P[9], lddx=128, da=P[10], db=P[11], **k
 @pytest.mark.parametrize("kw,status", COMMON + [
     (dict(dout=None), NULLP), (dict(low=None), NULLP), (dict(ldd=255), STRIDE), (dict(lddx=127), STRIDE),
     (dict(dx=P[0]), ALIAS), (dict(da=P[2]), ALIAS), (dict(db=P[10]), ALIAS), (dict(dx=P[7]), ALIAS), (dict(da=P[8]), ALIAS),
-    (dict(dx=None, da=None, db=None), OK), (dict(M=(1 << 24) + 1), SHAPE), (dict(N=(1 << 24) + 1), SHAPE),
-    (dict(L=65537), SHAPE), (dict(M=1 << 24, K=1 << 24, L=65536), SHAPE),
+    (dict(dx=None, da=None, db=None), OK), (dict(M=(1 << 24) + 1), SHAPE), (dict(N=(1 << 23) + 1), SHAPE),
+    (dict(L=65537), SHAPE), (dict(ldd=(1 << 23) + 1), STRIDE), (dict(lddx=(1 << 23) + 1), STRIDE),
 ])
 def test_backward_refusals(lib, kw, status):
     assert backward(lib, **kw) == status
