@@ -14,8 +14,9 @@ from typing import Optional, Sequence
 
 import torch
 
+from . import fp8
 from .api import _raise_for, library
-from .fp8 import _bytes, _matrix, _on, _output, _ptr, _refuse, _rows, _vector
+from .fp8 import _bytes, _matrix, _on, _output, _ptr, _refuse, _rows, _taken, _vector
 
 MAX_RANK = 256
 _TYPES = (torch.bfloat16, torch.float16)
@@ -110,6 +111,10 @@ def adapter_add(y: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tens
     Operands that require a gradient have one, through ``autograd.adapter_add``; together with an output, stream or
     ``return_low`` they are refused.
     """
+    if out is None and stream is None and not return_low:
+        r = (fp8._fast or fp8._load_fast()).adapter(y, x, a, b, index, scale)
+        if _taken(r):
+            return r
     if _wants_gradient(y, x, a, b, scale):
         if out is not None or return_low or stream is not None:
             raise RuntimeError("adapter_add with out, return_low or stream has no gradient, and an operand requires one: "
@@ -128,6 +133,10 @@ def adapter_glu(gate: torch.Tensor, up: torch.Tensor, x: torch.Tensor, gate_a: t
     Both pairs of stacks have the same L and R, and share index and scale.  ``out`` may be ``gate`` or ``up``.  Has no
     gradient: operands that require one are refused where autograd records.
     """
+    if out is None and stream is None:
+        r = (fp8._fast or fp8._load_fast()).adapter(gate, up, x, gate_a, gate_b, up_a, up_b, index, scale)
+        if _taken(r):
+            return r
     if _wants_gradient(gate, up, x, gate_a, gate_b, up_a, up_b, scale):
         raise RuntimeError("adapter_glu has no gradient, and an operand requires one: call it under torch.no_grad(), or "
                            "train with adapter_add on gate and up")
@@ -163,6 +172,10 @@ def adapter_backward(dout: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: to
     rows.  ``wanted`` says which of the three are computed; the others are None.  Rows are summed in fp32, in an order
     fixed by the sizes and index.
     """
+    if stream is None and all(wanted):
+        r = (fp8._fast or fp8._load_fast()).adapter_grad(dout, x, a, b, index, low, scale)
+        if _taken(r):
+            return r
     M, N, dev = _matrix("dout", dout, _TYPES)
     dt = dout.dtype
     ldd = _rows("dout", dout, dt, M, N, dev)

@@ -6,8 +6,9 @@ from typing import Optional, Union
 
 import torch
 
+from . import fp8
 from .api import _raise_for, library
-from .fp8 import DTYPES, _INPUTS, _matrix, _on, _output, _ptr, _rows, _vector
+from .fp8 import DTYPES, _INPUTS, _matrix, _on, _output, _ptr, _rows, _taken, _vector
 
 _WORD = (1 << 64) - 1
 
@@ -50,6 +51,10 @@ def dropout(x: torch.Tensor, p: float, seed: Union[int, torch.Tensor], offset: i
     or ``residual``.  Operands that require a gradient have one, through ``autograd.dropout``; with an output or
     stream they are refused.
     """
+    if out is None and stream is None:
+        r = (fp8._fast or fp8._load_fast()).dropout(x, drop_of(p), seed, offset, residual)
+        if _taken(r):
+            return r
     if torch.is_grad_enabled() and (getattr(x, "requires_grad", False) or getattr(residual, "requires_grad", False)):
         if out is not None or stream is not None:
             raise RuntimeError("dropout with out or stream has no gradient, and an operand requires one: call it without "

@@ -25,8 +25,6 @@ constexpr int kMaxTop = 32;
 constexpr int kRoutedRows = 4;
 constexpr int kUpThreads = 256;
 constexpr int kUpWaves = kUpThreads / 64;
-constexpr int kDownThreads = 512;
-constexpr int kDownWaves = kDownThreads / 64;
 
 // ---- routing -----------------------------------------------------------------------
 
@@ -373,8 +371,8 @@ __global__ void __launch_bounds__(kUpThreads) moe_routed_up_kernel(MoeArgs a, in
 // out[m][c], ROWS columns c, of the active experts that are this split's.  ROWS = 4, for up to 4 rows of x, takes the same 4
 // weight rows at 4 places along their columns as the 16 rows of an instruction, and x's rows likewise: of the results
 // the blocks on the diagonal are wanted, and there are 4 times the workgroups.
-template <class T, bool E8, int ROWS>
-__global__ void __launch_bounds__(kDownThreads) moe_down_kernel(MoeArgs a, MoePlan p)
+template <class T, bool E8, int ROWS, int WAVES>
+__global__ void __launch_bounds__(64 * WAVES) moe_down_kernel(MoeArgs a, MoePlan p)
 {
     constexpr int S = 16 / ROWS;     // places
     extern __shared__ float sums[];  // [wave][place][M][ROWS]
@@ -388,7 +386,7 @@ __global__ void __launch_bounds__(kDownThreads) moe_down_kernel(MoeArgs a, MoePl
     const int stages = (a.N + kStageCols<E8> * S - 1) / (kStageCols<E8> * S);
     const int per = (stages + p.parts - 1) / p.parts;
     constexpr int ES = E8 ? 1 : 2;
-    for (int u = wave; ; u += kDownWaves) {
+    for (int u = wave; ; u += WAVES) {
         const int j = u / p.parts * p.splits + split, part = u % p.parts;
         if (j >= actives) break;
         const Active x = a.active[j];
@@ -410,12 +408,12 @@ __global__ void __launch_bounds__(kDownThreads) moe_down_kernel(MoeArgs a, MoePl
         }
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < a.M * ROWS; i += kDownThreads) {
+    for (int i = threadIdx.x; i < a.M * ROWS; i += 64 * WAVES) {
         const int m = i / ROWS, c = c0 + i % ROWS;
         if (c >= a.K) continue;
         float v = 0.0f;
 #pragma unroll
-        for (int k = 0; k < kDownWaves * S; ++k) v += sums[k * a.M * ROWS + i];
+        for (int k = 0; k < WAVES * S; ++k) v += sums[k * a.M * ROWS + i];
         if (p.splits == 1) static_cast<T*>(a.out)[m * a.ldo + c] = narrow<T>(v);
         else a.part[((int64_t)split * a.M + m) * a.K + c] = v;
     }
@@ -461,9 +459,9 @@ hipError_t launch(int logits_dtype, const MoeArgs& a, const MoePlan& p, hipStrea
     if (logits_dtype == GLU_DTYPE_FP32) first_launches<T, E8, Fp32>(a, stream);
     else first_launches<T, E8, T>(a, stream);
     const dim3 grid((a.K + p.rows - 1) / p.rows, p.splits);
-    const size_t lds = (size_t)kDownWaves * a.M * 64;
-    if (p.rows == 4) hipLaunchKernelGGL((moe_down_kernel<T, E8, 4>), grid, dim3(kDownThreads), lds, stream, a, p);
-    else hipLaunchKernelGGL((moe_down_kernel<T, E8, 16>), grid, dim3(kDownThreads), lds, stream, a, p);
+    const size_t lds = (size_t)a.M * 64;  // per wave
+    if (p.rows == 4) hipLaunchKernelGGL((moe_down_kernel<T, E8, 4, 8>), grid, dim3(512), 8 * lds, stream, a, p);
+    else hipLaunchKernelGGL((moe_down_kernel<T, E8, 16, 16>), grid, dim3(1024), 16 * lds, stream, a, p);
     if (p.splits > 1) {
         hipLaunchKernelGGL(moe_join_kernel<T>, dim3((a.K + 255) / 256, a.M), dim3(256), 0, stream, a, p.splits);
     }
@@ -472,16 +470,18 @@ hipError_t launch(int logits_dtype, const MoeArgs& a, const MoePlan& p, hipStrea
 
 }  // namespace
 
+// The second product's cut.  16 rows per workgroup of 16 waves, which share experts in halves or smaller parts so that no
+// wave has much more to do than another (37 rows, K = 4096 N = 768, 128 experts: 144 us with whole experts, 131 with halves;
+// 6 rows of e4m3, N = 1536: 62 and 55).  Workgroups for half of the CUs at least: their sums' join costs 5 us.
 MoePlan moe_plan(int M, int K, int N, int E, int top, bool e4m3)
 {
     const int most = M * top < E ? M * top : E;
     MoePlan p{1, 1, M <= 4 ? 4 : 16};
-    const int cols = (e4m3 ? 128 : 64) * 16 / p.rows, stages = (N + cols - 1) / cols;
-    // every wave of a workgroup has something to do
-    while (most * p.parts < kDownWaves && 2 * p.parts <= stages) p.parts *= 2;
-    // and the CUs have several workgroups; few rows are spared the join
+    const int waves = p.rows == 4 ? 8 : 16, cols = (e4m3 ? 128 : 64) * 16 / p.rows, stages = (N + cols - 1) / cols;
+    if (p.rows == 16 && stages >= 2) p.parts = 2;
+    while (most * p.parts < waves && 2 * p.parts <= stages) p.parts *= 2;
     const int blocks = (K + p.rows - 1) / p.rows;
-    while (M > kRoutedRows && blocks * p.splits < 1024 && most * p.parts >= 2 * kDownWaves * p.splits && p.splits < 8) p.splits *= 2;
+    while (p.rows == 16 && blocks * p.splits < 128 && most * p.parts >= 2 * waves * p.splits && p.splits < 8) p.splits *= 2;
     return p;
 }
 

@@ -1,7 +1,8 @@
-// The short way from torch tensors to the C ABI, for the calls of fp8.py in their usual form: every operand of
+// The short way from torch tensors to the C ABI, for the calls of fp8.py, adapters.py, moe.py and counter_dropout.py in
+// their usual form: every operand of
 // the expected type, shape and layout on the current device, outputs to be allocated, the current
 // stream.  Checking, allocating and calling take 1.5 to 2 us here against 8 in Python, which shows where a kernel
-// takes 3 us.  Whatever is not in that form returns None before anything is allocated, and fp8.py takes the call
+// takes 3 us.  Whatever is not in that form returns None before anything is allocated, and the Python takes the call
 // and says what is wrong. A status other than GLU_OK is returned as an int.
 #include <Python.h>
 
@@ -13,7 +14,10 @@
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include "../../include/glu_adapter.h"
+#include "../../include/glu_dropout.h"
 #include "../../include/glu_fp8.h"
+#include "../../include/glu_moe.h"
 
 namespace {
 
@@ -29,6 +33,14 @@ struct Api {
     decltype(&glu_fp8_dual_glu) dual_glu;
     decltype(&glu_fp8_workspace) workspace;
     decltype(&glu_fp8_product_workspace) fast_workspace;
+    decltype(&glu_adapter_add) adapter_add;
+    decltype(&glu_adapter_glu) adapter_glu;
+    decltype(&glu_adapter_workspace) adapter_workspace;
+    decltype(&glu_adapter_backward) adapter_backward;
+    decltype(&glu_adapter_backward_workspace) adapter_backward_workspace;
+    decltype(&glu_moe_glu) moe;
+    decltype(&glu_moe_workspace) moe_workspace;
+    decltype(&glu_dropout) dropout;
 };
 Api api;
 
@@ -64,6 +76,10 @@ struct Place {
     at::Tensor empty(int64_t rows, int64_t cols, int64_t row_stride, int64_t col_stride, c10::ScalarType t) const
     {
         return at::detail::empty_strided_cuda({rows, cols}, {row_stride, col_stride}, t, device);
+    }
+    at::Tensor empty(int64_t n, int64_t rows, int64_t cols, c10::ScalarType t) const
+    {
+        return at::detail::empty_strided_cuda({n, rows, cols}, {rows * cols, cols, 1}, t, device);
     }
     at::Tensor empty(int64_t n, c10::ScalarType t) const { return at::detail::empty_strided_cuda({n}, {1}, t, device); }
     at::Tensor workspace(int64_t bytes) const
@@ -282,6 +298,198 @@ PyObject* product(PyObject*, PyObject* const* a, Py_ssize_t n)
     });
 }
 
+// [n, rows, cols] of type t with contiguous rows; rows and matrices do not overlap
+struct Matrices {
+    bool ok = false;
+    int64_t n = 0, rows = 0, cols = 0, stack = 0, ld = 0;
+    void* p = nullptr;
+    c10::ScalarType type = c10::ScalarType::Undefined;
+    Matrices(PyObject* o, const Place& at, int64_t want_n, int64_t want_rows, int64_t want_cols)
+    {
+        if (!THPVariable_Check(o)) return;
+        const at::Tensor& t = THPVariable_Unpack(o);
+        if (t.layout() != c10::kStrided || t.dim() != 3 || t.device() != at.device) return;
+        type = t.scalar_type();
+        n = t.size(0);
+        rows = t.size(1);
+        cols = t.size(2);
+        if (n < 1 || rows < 1 || cols < 1) return;
+        if ((want_n >= 0 && n != want_n) || (want_rows >= 0 && rows != want_rows) || (want_cols >= 0 && cols != want_cols)) return;
+        if (cols > 1 && t.stride(2) != 1) return;
+        ld = rows > 1 ? t.stride(1) : cols;
+        stack = n > 1 ? t.stride(0) : rows * ld;
+        p = t.data_ptr();
+        ok = ld >= cols && stack >= (rows - 1) * ld + cols;
+    }
+};
+
+bool half_type(c10::ScalarType t) { return t == c10::ScalarType::BFloat16 || t == c10::ScalarType::Half; }
+
+bool recorded(PyObject* const* a, Py_ssize_t n)
+{
+    if (!c10::GradMode::is_enabled()) return false;
+    for (Py_ssize_t i = 0; i < n; ++i) {
+        if (THPVariable_Check(a[i]) && THPVariable_Unpack(a[i]).requires_grad()) return true;
+    }
+    return false;
+}
+
+// an optional vector: false where it is there and not as wanted
+bool optional_vector(PyObject* o, const Place& at, int64_t n, c10::ScalarType want, void** p)
+{
+    *p = nullptr;
+    return o == Py_None || (*p = vector(o, at, n, want)) != nullptr;
+}
+
+// (y, x, a, b, index, scale or None) or (gate, up, x, gate_a, gate_b, up_a, up_b, index, scale or None) -> out
+PyObject* adapter(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    return guarded([&]() -> PyObject* {
+        if (n != 6 && n != 9) Py_RETURN_NONE;
+        const int mats = n == 9 ? 2 : 1;
+        const Place at(a[0]);
+        if (!at.ok || recorded(a, n)) Py_RETURN_NONE;
+        const Rows y(a[0], at, -1, -1, c10::ScalarType::Undefined);
+        if (!y.ok || !half_type(y.type)) Py_RETURN_NONE;
+        const Rows y2(a[mats - 1], at, y.rows, y.cols, y.type), x(a[mats], at, y.rows, -1, y.type);
+        if (!y2.ok || !x.ok) Py_RETURN_NONE;
+        glu_adapter ab[2];
+        int64_t L = -1, R = -1;
+        for (int i = 0; i < mats; ++i) {
+            const Matrices wa(a[mats + 1 + 2 * i], at, L, R, x.cols);
+            if (!wa.ok || wa.type != y.type) Py_RETURN_NONE;
+            L = wa.n;
+            R = wa.rows;
+            const Matrices wb(a[mats + 2 + 2 * i], at, L, y.cols, R);
+            if (!wb.ok || wb.type != y.type || R > GLU_ADAPTER_MAX_RANK) Py_RETURN_NONE;
+            ab[i] = glu_adapter{wa.p, wb.p, wa.stack, wa.ld, wb.stack, wb.ld};
+        }
+        void *index = vector(a[n - 2], at, y.rows, c10::ScalarType::Int), *scale;
+        if (!index || !optional_vector(a[n - 1], at, L, c10::ScalarType::Float, &scale)) Py_RETURN_NONE;
+        const glu_adapter_sizes sizes{y.rows, y.cols, x.cols, R, L};
+        int64_t bytes = 0;
+        glu_status st = api.adapter_workspace(mats, &sizes, &bytes);
+        if (st != GLU_OK) return status_int(st);
+        const at::Tensor out = at.empty(y.rows, y.cols, y.cols, 1, y.type), ws = at.workspace(bytes);
+        void* wsp = bytes ? ws.data_ptr() : nullptr;
+        const int dt = dtype_code(y.type);
+        st = mats == 2 ? api.adapter_glu(y.p, y.ld, y2.p, y2.ld, x.p, x.ld, &ab[0], &ab[1], (const int32_t*)index,
+                                         (const float*)scale, out.data_ptr(), y.cols, &sizes, dt, wsp, bytes, at.stream)
+                       : api.adapter_add(y.p, y.ld, x.p, x.ld, &ab[0], (const int32_t*)index, (const float*)scale,
+                                         out.data_ptr(), y.cols, nullptr, &sizes, dt, wsp, bytes, at.stream);
+        return st == GLU_OK ? THPVariable_Wrap(out) : status_int(st);
+    });
+}
+
+// (dout, x, a, b, index, low, scale or None) -> (dx, da, db)
+PyObject* adapter_grad(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    return guarded([&]() -> PyObject* {
+        if (n != 7) Py_RETURN_NONE;
+        const Place at(a[0]);
+        if (!at.ok) Py_RETURN_NONE;
+        const Rows d(a[0], at, -1, -1, c10::ScalarType::Undefined);
+        if (!d.ok || !half_type(d.type)) Py_RETURN_NONE;
+        const Rows x(a[1], at, d.rows, -1, d.type);
+        if (!x.ok) Py_RETURN_NONE;
+        const Matrices wa(a[2], at, -1, -1, x.cols);
+        if (!wa.ok || wa.type != d.type) Py_RETURN_NONE;
+        const int64_t L = wa.n, R = wa.rows;
+        const Matrices wb(a[3], at, L, d.cols, R);
+        if (!wb.ok || wb.type != d.type || R > GLU_ADAPTER_MAX_RANK) Py_RETURN_NONE;
+        const Rows low(a[5], at, d.rows, R, c10::ScalarType::Float);
+        void *index = vector(a[4], at, d.rows, c10::ScalarType::Int), *scale;
+        if (!index || !low.ok || low.ld != R || !optional_vector(a[6], at, L, c10::ScalarType::Float, &scale)) Py_RETURN_NONE;
+        const glu_adapter_sizes sizes{d.rows, d.cols, x.cols, R, L};
+        int64_t bytes = 0;
+        glu_status st = api.adapter_backward_workspace(&sizes, &bytes);
+        if (st != GLU_OK) return status_int(st);
+        const at::Tensor t[3] = {at.empty(d.rows, x.cols, x.cols, 1, d.type), at.empty(L, R, x.cols, d.type),
+                                 at.empty(L, d.cols, R, d.type)};
+        const at::Tensor ws = at.workspace(bytes);
+        const glu_adapter ab{wa.p, wb.p, wa.stack, wa.ld, wb.stack, wb.ld};
+        st = api.adapter_backward(d.p, d.ld, x.p, x.ld, &ab, (const int32_t*)index, (const float*)scale, (const float*)low.p,
+                                  t[0].data_ptr(), x.cols, t[1].data_ptr(), t[2].data_ptr(), &sizes, dtype_code(d.type),
+                                  bytes ? ws.data_ptr() : nullptr, bytes, at.stream);
+        return st == GLU_OK ? pack(3, t) : status_int(st);
+    });
+}
+
+// (x, logits, gate, up, down, top, normalize, gate_scale, up_scale, down_scale: three or None) -> out
+PyObject* moe(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    return guarded([&]() -> PyObject* {
+        if (n != 10) Py_RETURN_NONE;
+        const Place at(a[0]);
+        if (!at.ok || recorded(a, 5)) Py_RETURN_NONE;
+        const Rows x(a[0], at, -1, -1, c10::ScalarType::Undefined);
+        if (!x.ok || !half_type(x.type) || !PyLong_Check(a[5])) Py_RETURN_NONE;
+        const Rows logits(a[1], at, x.rows, -1, c10::ScalarType::Undefined);
+        if (!logits.ok || (logits.type != x.type && logits.type != c10::ScalarType::Float)) Py_RETURN_NONE;
+        const int64_t E = logits.cols, K = x.cols;
+        const long top = PyLong_AsLong(a[5]);
+        if (top < 1 || top > E || top > GLU_MOE_MAX_TOP || E > GLU_MOE_MAX_EXPERTS) {
+            PyErr_Clear();
+            Py_RETURN_NONE;
+        }
+        glu_expert_matrix w[3];
+        c10::ScalarType wt = c10::ScalarType::Undefined;
+        int64_t N = -1;
+        for (int i = 0; i < 3; ++i) {
+            const Matrices m(a[2 + i], at, E, i < 2 ? N : K, i < 2 ? K : N);
+            if (!m.ok || (i && m.type != wt) || (m.type != x.type && m.type != kE4m3)) Py_RETURN_NONE;
+            wt = m.type;
+            if (i == 0) N = m.rows;
+            w[i] = glu_expert_matrix{m.p, nullptr, m.stack, m.ld, 0, 0};
+            if (wt != kE4m3) {
+                if (a[7 + i] != Py_None) Py_RETURN_NONE;
+                continue;
+            }
+            const Matrices s(a[7 + i], at, E, groups(m.rows), groups(m.cols));
+            if (!s.ok || s.type != c10::ScalarType::Float) Py_RETURN_NONE;
+            w[i].scale = (const float*)s.p;
+            w[i].scale_stack = s.stack;
+            w[i].scale_ld = s.ld;
+        }
+        const glu_moe_sizes sizes{x.rows, K, N, E, top};
+        int64_t bytes = 0;
+        glu_status st = api.moe_workspace(&sizes, &bytes);
+        if (st != GLU_OK) return status_int(st);
+        const at::Tensor out = at.empty(x.rows, K, K, 1, x.type), ws = at.workspace(bytes);
+        st = api.moe(x.p, x.ld, logits.p, logits.ld, dtype_code(logits.type), &w[0], &w[1], &w[2], out.data_ptr(), K, &sizes,
+                     a[6] == Py_True, dtype_code(x.type), dtype_code(wt), bytes ? ws.data_ptr() : nullptr, bytes, at.stream);
+        return st == GLU_OK ? THPVariable_Wrap(out) : status_int(st);
+    });
+}
+
+// (x, drop of 65536, seed below 2^64 or tensor, offset below 2^64, residual or None) -> out
+PyObject* dropout(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    return guarded([&]() -> PyObject* {
+        if (n != 5 || !PyLong_Check(a[1]) || !PyLong_Check(a[3])) Py_RETURN_NONE;
+        const Place at(a[0]);
+        if (!at.ok || recorded(a, 1) || recorded(a + 4, 1)) Py_RETURN_NONE;
+        const Rows x(a[0], at, -1, -1, c10::ScalarType::Undefined);
+        const int dt = x.ok ? dtype_code(x.type) : -1;
+        if (dt < 0 || dt == GLU_DTYPE_E4M3) Py_RETURN_NONE;
+        void *seed_at = nullptr, *res = nullptr;
+        uint64_t seed = 0;
+        if (PyLong_Check(a[2])) seed = PyLong_AsUnsignedLongLongMask(a[2]);
+        else if (!(seed_at = vector(a[2], at, 1, c10::ScalarType::Long))) Py_RETURN_NONE;
+        int64_t ldr = 0;
+        if (a[4] != Py_None) {
+            const Rows r(a[4], at, x.rows, x.cols, x.type);
+            if (!r.ok) Py_RETURN_NONE;
+            res = r.p;
+            ldr = r.ld;
+        }
+        const at::Tensor out = at.empty(x.rows, x.cols, x.cols, 1, x.type);
+        const glu_status st = api.dropout(x.p, x.ld, res, ldr, out.data_ptr(), x.cols, x.rows, x.cols, PyLong_AsLong(a[1]), seed,
+                                          (const uint64_t*)seed_at, PyLong_AsUnsignedLongLongMask(a[3]), dt, at.stream);
+        return st == GLU_OK ? THPVariable_Wrap(out) : status_int(st);
+    });
+}
+
 // the addresses of the C functions, in the order of Api
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
@@ -305,7 +513,8 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n)
 
 #define GLU_METHOD(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {GLU_METHOD(norm),    GLU_METHOD(norm_grad), GLU_METHOD(quantize),
-                         GLU_METHOD(product), GLU_METHOD(bind),      {nullptr, nullptr, 0, nullptr}};
+                         GLU_METHOD(product), GLU_METHOD(adapter), GLU_METHOD(adapter_grad), GLU_METHOD(moe),
+                         GLU_METHOD(dropout), GLU_METHOD(bind),      {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fast", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

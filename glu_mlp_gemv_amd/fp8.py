@@ -51,7 +51,9 @@ class ProductPlan(ctypes.Structure):
 # in the order that _fast.bind takes them
 _BOUND = ("glu_add_rms_norm", "glu_add_rms_norm_fp8", "glu_add_rms_norm_backward",
           "glu_add_rms_norm_backward_workspace", "glu_fp8_quantize", "glu_fp8_quantize_weight", "glu_fp8_linear",
-          "glu_fp8_dual_glu", "glu_fp8_workspace", "glu_fp8_product_workspace")
+          "glu_fp8_dual_glu", "glu_fp8_workspace", "glu_fp8_product_workspace", "glu_adapter_add", "glu_adapter_glu",
+          "glu_adapter_workspace", "glu_adapter_backward", "glu_adapter_backward_workspace", "glu_moe_glu",
+          "glu_moe_workspace", "glu_dropout")
 _fast = None
 
 

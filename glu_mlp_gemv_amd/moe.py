@@ -11,9 +11,10 @@ from typing import Optional
 
 import torch
 
+from . import fp8
 from .adapters import _CODES, _TYPES, _scratch, _stack, _wants_gradient
 from .api import _raise_for, library
-from .fp8 import DTYPES, E4M3, _bytes, _matrix, _on, _output, _ptr, _refuse, _rows, groups
+from .fp8 import DTYPES, E4M3, _bytes, _matrix, _on, _output, _ptr, _refuse, _rows, _taken, groups
 
 MAX_EXPERTS = 1024
 MAX_TOP = 32
@@ -59,6 +60,11 @@ def moe_glu(x: torch.Tensor, logits: torch.Tensor, gate: torch.Tensor, up: torch
     Each chosen expert's weights are read once per 64 rows: meant for the tokens of a decode step, right for any number.  At
     most 1024 experts, 32 per row.  Has no gradient: operands that require one are refused where autograd records.
     """
+    if out is None and stream is None:
+        r = (fp8._fast or fp8._load_fast()).moe(x, logits, gate, up, down, top, normalize is True or bool(normalize), gate_scale,
+                                                up_scale, down_scale)
+        if _taken(r):
+            return r
     if _wants_gradient(x, logits, gate, up, down):
         raise RuntimeError("moe_glu has no gradient, and an operand requires one: call it under torch.no_grad()")
     M, K, dev = _matrix("x", x, _TYPES)
