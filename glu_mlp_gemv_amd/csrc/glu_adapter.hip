@@ -27,33 +27,30 @@ constexpr int kStage = 64;  // contraction per wave and stage: one 128-byte line
 struct Whole { static constexpr bool value = true; };
 struct Part { static constexpr bool value = false; };
 
-// adapter of a row; -1: none
+// adapter of a row; -1: none; -2: no such row
 __device__ __forceinline__ int adapter_of(const int32_t* index, int m, int M, int L)
 {
-    if (m >= M) return -1;
+    if (m >= M) return -2;
     const int i = index[m];
     return (unsigned)i < (unsigned)L ? i : -1;
 }
 
-// the first adapter left in a tile (the same in every lane); -1: none
-template <int TM>
-__device__ __forceinline__ int next_adapter(const int (&left)[TM])
+// the first adapter left in a tile, whose rows' adapters the lanes hold (the same in every lane); -1: none
+__device__ __forceinline__ int next_adapter(int left)
 {
-#pragma unroll
-    for (int t = 0; t < TM; ++t) {
-        const uint64_t b = __ballot(left[t] >= 0);
-        if (b) return __builtin_amdgcn_readlane(left[t], __builtin_ctzll(b));
-    }
-    return -1;
+    const uint64_t b = __ballot(left >= 0);
+    return b ? __builtin_amdgcn_readlane(left, __builtin_ctzll(b)) : -1;
 }
 
-template <int TM>
-__device__ __forceinline__ void take_out(int (&left)[TM], int cur)
+// The rows of a tile that have this adapter, in order, to a list of the wave's own in LDS; how many there are
+__device__ __forceinline__ int list_rows(int idx, int cur, uint8_t* list)
 {
-#pragma unroll
-    for (int t = 0; t < TM; ++t) {
-        if (left[t] == cur) left[t] = -1;
-    }
+    const int lane = threadIdx.x & 63;
+    const uint64_t b = __ballot(idx == cur);
+    __builtin_amdgcn_wave_barrier();  // the last list is read; other lanes read this one, in LDS order
+    if (idx == cur) list[__popcll(b & ((1ull << lane) - 1ull))] = (uint8_t)lane;
+    __builtin_amdgcn_wave_barrier();
+    return __popcll(b);
 }
 
 // Loads of a tile are a uniform address plus 32 bits per lane: rows of a tile times a row's bytes stay below 2^31
@@ -85,19 +82,19 @@ __device__ __forceinline__ void reads_done()
     __builtin_amdgcn_sched_barrier(0);
 }
 
-// First product.  Tile: 16 TM rows of v, 16 RT rows of w and a part of the columns; the 4 waves take stages of 64 columns
-// in turn, keep U of them in flight, and join in LDS.  Tiles start at different columns, or rows of a power-of-two
-// stride would have all of them at the same few memory channels.  COLUMNS: w is [C][R], and operand j of a lane is
-// column RT (l % 16) + j.
+// First product.  Tile: up to 64 rows of v, of which those of one adapter are taken 16 TM at a time, 16 RT rows of w and a
+// part of the columns; the 4 waves take stages of 64 columns in turn, keep U of them in flight, and join in LDS.
+// COLUMNS: w is [C][R], and operand j of a lane is column RT (l % 16) + j.
 template <class T, int TM, int RT, int U, bool COLUMNS>
-__global__ void __launch_bounds__(kThreads, 3) adapter_low_kernel(LowArgs a, int slots, int rgroups, int tile0)
+__global__ void __launch_bounds__(kThreads, 3) adapter_low_kernel(LowArgs a, int tile_rows, int slots, int rgroups,
+                                                                  int tile0)
 {
     constexpr int PIECES = TM * RT;
     __shared__ float red[kWaves][PIECES][256];
-    __shared__ int rows_of[16 * TM];
+    __shared__ uint8_t lists[kWaves][64];
     const int lane = threadIdx.x & 63, i16 = lane & 15, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int tile = tile0 + blockIdx.x, m0 = tile * 16 * TM;
+    const int m0 = (tile0 + blockIdx.x) * tile_rows;
     const int split = blockIdx.y % a.splits, rg = blockIdx.y / a.splits % rgroups, mat = blockIdx.y / a.splits / rgroups;
     const int slot = blockIdx.z;
     const int r0 = rg * 16 * RT;
@@ -107,42 +104,25 @@ __global__ void __launch_bounds__(kThreads, 3) adapter_low_kernel(LowArgs a, int
     const int tail = a.C % kStage && (stages - 1) / per == split ? stages - 1 : -1;
     float* z = a.z + (int64_t)(split * a.mats + mat) * a.M * a.R;
 
-    int idx[TM], left[TM];
-#pragma unroll
-    for (int t = 0; t < TM; ++t) {
-        idx[t] = left[t] = adapter_of(a.index, m0 + 16 * t + i16, a.M, a.L);
-        if (wave == 0 && q == 0) rows_of[16 * t + i16] = idx[t];
-    }
-    __syncthreads();
+    const int idx = lane < tile_rows ? adapter_of(a.index, m0 + lane, a.M, a.L) : -2;
+    int left = idx;
+    uint8_t* list = lists[wave];
     if (slot == 0) {
-        for (int j = threadIdx.x; j < 16 * TM * 16 * RT; j += kThreads) {
-            const int m = m0 + j / (16 * RT), r = r0 + j % (16 * RT);
-            if (m < a.M && r < a.R && rows_of[j / (16 * RT)] < 0) z[(int64_t)m * a.R + r] = 0.0f;
+        const uint64_t bare = __ballot(idx == -1);
+        for (int j = threadIdx.x; j < tile_rows * 16 * RT; j += kThreads) {
+            const int row = j / (16 * RT), r = r0 + j % (16 * RT);
+            if ((bare >> row & 1) && r < a.R) z[(int64_t)(m0 + row) * a.R + r] = 0.0f;
         }
     }
     const char* vbase = reinterpret_cast<const char*>(static_cast<const T*>(a.v) + m0 * a.ldv);
-    const int rotate = count > 0 ? tile * 5 % count : 0;
     int seen = 0;
     for (;;) {
-        const int cur = next_adapter<TM>(left);
+        const int cur = next_adapter(left);
         if (cur < 0) break;
-        take_out<TM>(left, cur);
+        if (left == cur) left = -1;
         if (seen++ % slots != slot) continue;
 
-        // rows of v: lanes whose row has another adapter read the first of this one's along
-        uint32_t vo[TM];
-        {
-            int one = 0;
-#pragma unroll
-            for (int t = TM - 1; t >= 0; --t) {
-                const uint64_t b = __ballot(idx[t] == cur);
-                if (b) one = 16 * t + __builtin_ctzll(b);
-            }
-#pragma unroll
-            for (int t = 0; t < TM; ++t) {
-                vo[t] = ((uint32_t)(idx[t] == cur ? 16 * t + i16 : one) * (uint32_t)a.ldv + 8 * q) * 2;
-            }
-        }
+        const int n = list_rows(idx, cur, list);
         const T* w = static_cast<const T*>(a.w[mat].w) + cur * a.w[mat].stack;
         const int64_t wrow = a.w[mat].row;
         const char* wbase = reinterpret_cast<const char*>(w + (COLUMNS ? r0 : r0 * wrow));
@@ -150,6 +130,10 @@ __global__ void __launch_bounds__(kThreads, 3) adapter_low_kernel(LowArgs a, int
 #pragma unroll
         for (int j = 0; j < RT; ++j) wo[j] = ((uint32_t)min(16 * j + i16, a.R - 1 - r0) * (uint32_t)wrow + 8 * q) * 2;
         if constexpr (COLUMNS) wo[0] = ((uint32_t)(8 * q) * (uint32_t)wrow + RT * i16) * 2;
+        for (int g = 0; g < n; g += 16 * TM) {
+        uint32_t vo[TM];  // places past the last row take the last row along
+#pragma unroll
+        for (int t = 0; t < TM; ++t) vo[t] = ((uint32_t)list[min(g + 16 * t + i16, n - 1)] * (uint32_t)a.ldv + 8 * q) * 2;
         f32x4 acc[TM][RT];
 #pragma unroll
         for (int t = 0; t < TM; ++t) {
@@ -158,8 +142,7 @@ __global__ void __launch_bounds__(kThreads, 3) adapter_low_kernel(LowArgs a, int
         }
         raw4_t vf[U][2][TM], wf[U][2][RT];
         auto load = [&](int u, int s) __attribute__((always_inline)) {
-            s += rotate;
-            const int at = (first + (s < count ? s : s - count)) * kStage;
+            const int at = (first + s) * kStage;
             const char* vb = vbase + at * 2;
             const char* wb = wbase + (COLUMNS ? at * wrow : (int64_t)at) * 2;
 #pragma unroll
@@ -235,15 +218,16 @@ __global__ void __launch_bounds__(kThreads, 3) adapter_low_kernel(LowArgs a, int
         __syncthreads();
         for (int i = threadIdx.x; i < PIECES * 256; i += kThreads) {
             const int l = i >> 2 & 63, piece = i >> 8, t = piece / RT, j = piece % RT;
-            const int row = 16 * t + (l & 15), k = 4 * (l >> 4) + (i & 3);
+            const int at = g + 16 * t + (l & 15), k = 4 * (l >> 4) + (i & 3);
             const int r = r0 + (COLUMNS ? RT * k + j : 16 * j + k);
-            if (rows_of[row] != cur || r >= a.R) continue;
+            if (at >= n || r >= a.R) continue;
             float sum = red[0][piece][i & 255];
 #pragma unroll
             for (int o = 1; o < kWaves; ++o) sum += red[o][piece][i & 255];
-            z[(int64_t)(m0 + row) * a.R + r] = sum;
+            z[(int64_t)(m0 + list[at]) * a.R + r] = sum;
         }
         __syncthreads();
+        }
     }
 }
 
@@ -257,10 +241,9 @@ __global__ void __launch_bounds__(kThreads) adapter_low_tile_kernel(LowArgs a, i
 {
     constexpr int PIECES = TM * RT, LOADS = 2 * (TM + RT), STAGE = LOADS * 1024, DEPTH = 2;
     extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];  // [wave][DEPTH][rows of v, then of w][128 bytes]
-    __shared__ int rows_of[16 * TM];
     const int lane = threadIdx.x & 63, i16 = lane & 15, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int tile = tile0 + blockIdx.x, m0 = tile * 16 * TM;
+    const int m0 = (tile0 + blockIdx.x) * 16 * TM;
     const int split = blockIdx.y % a.splits, rg = blockIdx.y / a.splits % rgroups, mat = blockIdx.y / a.splits / rgroups;
     const int r0 = rg * 16 * RT;
     const int stages = (a.C + kStage - 1) / kStage, per = (stages + a.splits - 1) / a.splits;
@@ -269,19 +252,14 @@ __global__ void __launch_bounds__(kThreads) adapter_low_tile_kernel(LowArgs a, i
     float* z = a.z + (int64_t)(split * a.mats + mat) * a.M * a.R;
     uint8_t* mine = smem + wave * DEPTH * STAGE;
 
-    int idx[TM], left[TM];
-#pragma unroll
-    for (int t = 0; t < TM; ++t) {
-        idx[t] = left[t] = adapter_of(a.index, m0 + 16 * t + i16, a.M, a.L);
-        if (wave == 0 && q == 0) rows_of[16 * t + i16] = idx[t];
-    }
-    __syncthreads();
+    const int idx = lane < 16 * TM ? adapter_of(a.index, m0 + lane, a.M, a.L) : -2;
+    int left = idx;
+    const uint64_t bare = __ballot(idx == -1);
     for (int j = threadIdx.x; j < 16 * TM * 16 * RT; j += kThreads) {
-        const int m = m0 + j / (16 * RT), r = r0 + j % (16 * RT);
-        if (m < a.M && r < a.R && rows_of[j / (16 * RT)] < 0) z[(int64_t)m * a.R + r] = 0.0f;
+        const int row = j / (16 * RT), r = r0 + j % (16 * RT);
+        if ((bare >> row & 1) && r < a.R) z[(int64_t)(m0 + row) * a.R + r] = 0.0f;
     }
     const char* vbase = reinterpret_cast<const char*>(static_cast<const T*>(a.v) + m0 * a.ldv);
-    const int rotate = count > 0 ? tile * 5 % count : 0;
     // what this lane loads: chunk lane % 8, turned by its row, of row lane / 8 of each 8; rows of two loads differ by 8
     const int lr = lane >> 3, lc = lane & 7;
     uint32_t vo[2 * TM], wo[2 * RT];
@@ -297,9 +275,10 @@ __global__ void __launch_bounds__(kThreads) adapter_low_tile_kernel(LowArgs a, i
     }
     const int rd[2] = {i16 * 128 + ((q ^ (i16 >> 1)) << 4), i16 * 128 + (((q + 4) ^ (i16 >> 1)) << 4)};
     for (;;) {
-        const int cur = next_adapter<TM>(left);
+        const int cur = next_adapter(left);
         if (cur < 0) break;
-        take_out<TM>(left, cur);
+        if (left == cur) left = -1;
+        const uint64_t rows = __ballot(idx == cur);
         const int64_t wrow = a.w[mat].row;
         const char* wbase = reinterpret_cast<const char*>(static_cast<const T*>(a.w[mat].w) + cur * a.w[mat].stack + r0 * wrow);
         f32x4 acc[TM][RT];
@@ -311,8 +290,7 @@ __global__ void __launch_bounds__(kThreads) adapter_low_tile_kernel(LowArgs a, i
         // past the last stage the last one again, so that every stage waits for the same number of loads
         const int turns = (count - wave + kWaves - 1) / kWaves;  // this wave's stages
         auto load = [&](int k, int buf) __attribute__((always_inline)) {
-            int s = min(k, turns - 1) * kWaves + wave + rotate;
-            if (s >= count) s -= count;
+            const int s = min(k, turns - 1) * kWaves + wave;
             const char* vb = vbase + (first + s) * 128;
             const char* wb = wbase + (first + s) * 128;
             uint8_t* to = mine + buf * STAGE;
@@ -377,7 +355,7 @@ __global__ void __launch_bounds__(kThreads) adapter_low_tile_kernel(LowArgs a, i
         for (int i = threadIdx.x; i < PIECES * 64; i += kThreads) {
             const int l = i & 63, piece = i >> 6, t = piece / RT, j = piece % RT;
             const int row = 16 * t + (l & 15), r = r0 + 16 * j + 4 * (l >> 4);
-            if (rows_of[row] != cur || r >= a.R) continue;
+            if (!(rows >> row & 1) || r >= a.R) continue;
             f32x4 sum = *reinterpret_cast<const f32x4*>(&red[0][piece][4 * l]);
 #pragma unroll
             for (int o = 1; o < kWaves; ++o) sum += *reinterpret_cast<const f32x4*>(&red[o][piece][4 * l]);
@@ -391,45 +369,35 @@ __global__ void __launch_bounds__(kThreads) adapter_low_tile_kernel(LowArgs a, i
     }
 }
 
-// Second product.  Tile: 16 TM rows of z, which the workgroup puts into LDS as two numbers of T each, and runs of 64
-// columns for each of its waves, whose y and w are on their way meanwhile.  The contraction is RP = ranks rounded up places
+// Second product.  Tile: up to 64 rows, of which those of one adapter are taken 16 TM at a time: their z, which the workgroup
+// puts into LDS as two numbers of T each, and runs of 64 columns for each of its waves, whose y and w are on their way meanwhile.  The contraction is RP = ranks rounded up places
 // of the first numbers and then RP of the second, so that up to 16 ranks (S = 1) they share one instruction's 32 places; S
 // instructions with H operands of w per 16 columns, or (S = 0) as many as there are ranks.  The results,
 // of which a lane holds 4 columns of its own row, go through LDS to lanes that hold 8 columns, 8 neighbouring lanes a line:
 // so y is read and out written.
 template <class T, int TM, int NM, int S, bool COLUMNS>
-__global__ void __launch_bounds__(kThreads, 2) adapter_out_kernel(OutArgs a, int slots, int cblocks, int per, int tile0)
+__global__ void __launch_bounds__(kThreads, 2) adapter_out_kernel(OutArgs a, int tile_rows, int slots, int cblocks,
+                                                                  int per, int tile0)
 {
     constexpr int ROWS = 16 * TM, H = S > 1 ? S / 2 : 1;
-    extern __shared__ __attribute__((aligned(16))) uint16_t lds[];  // z as T [NM][ROWS][pitch]; powers of two and maxima [NM][ROWS]; parts of z as fp32
+    extern __shared__ __attribute__((aligned(16))) uint16_t lds[];  // z as T [NM][ROWS][pitch]; powers of two and maxima [NM][ROWS]
+    __shared__ uint8_t lists[kWaves][64];
     __shared__ __attribute__((aligned(16))) float turned[kWaves][16 * kTurnPitch];
     const int lane = threadIdx.x & 63, i16 = lane & 15, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int cb = blockIdx.x % cblocks, m0 = (tile0 + blockIdx.x / cblocks) * ROWS;
+    const int cb = blockIdx.x % cblocks, m0 = (tile0 + blockIdx.x / cblocks) * tile_rows;
     const int slot = blockIdx.y;
     const int nb_first = cb * per * kWaves + wave, nb_end = min((a.N + 63) >> 6, (cb + 1) * per * kWaves);
     const int RP = S ? 16 * (S == 1 ? 1 : S) : (a.R + 31) & ~31, R8 = RP >> 3, pitch = 2 * RP + 8;
     const int steps = S ? S : RP >> 4;
     float* down = reinterpret_cast<float*>(lds + NM * ROWS * pitch);
     uint32_t* most = reinterpret_cast<uint32_t*>(down + NM * ROWS);
-    float* parts = reinterpret_cast<float*>(most + NM * ROWS);
 
-    int idx[TM], left[TM];
-    bool bare = false;  // rows without an adapter
-#pragma unroll
-    for (int t = 0; t < TM; ++t) {
-        const int m = m0 + 16 * t + i16;
-        idx[t] = left[t] = adapter_of(a.index, m, a.M, a.L);
-        bare |= m < a.M && idx[t] < 0;
-    }
-    // what this lane reads and writes: columns 8 (lane % 8) .. + 7 of a 64-column block, rows lane / 8 of each 8
+    const int idx = lane < tile_rows ? adapter_of(a.index, m0 + lane, a.M, a.L) : -2;
+    int left = idx;
+    uint8_t* list = lists[wave];
+    // what this lane reads and writes: columns 8 (lane % 8) .. + 7 of a 64-column block of each 8th row
     const int lr = lane >> 3, lc = 8 * (lane & 7);
-    int own[2 * TM];  // their adapters; -2: no such row
-#pragma unroll
-    for (int i = 0; i < 2 * TM; ++i) {
-        const int m = m0 + 8 * i + lr;
-        own[i] = m < a.M ? adapter_of(a.index, m, a.M, a.L) : -2;
-    }
     const char* ybase[NM];
 #pragma unroll
     for (int mat = 0; mat < NM; ++mat) ybase[mat] = a.y[mat] ? reinterpret_cast<const char*>(static_cast<const T*>(a.y[mat]) + m0 * a.ldy[mat]) : nullptr;
@@ -461,8 +429,12 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_out_kernel(OutArgs a, int
         }
     };
 
-    auto pass = [&](int cur, auto with) __attribute__((always_inline)) {
+    // rows g .. g + ROWS - 1 of the n that the list holds
+    auto pass = [&](int cur, int g, int n, auto with) __attribute__((always_inline)) {
         constexpr bool WITH = decltype(with)::value;  // false: the rows without an adapter
+        int own[2 * TM];  // this lane's rows; -1: none
+#pragma unroll
+        for (int i = 0; i < 2 * TM; ++i) own[i] = g + 8 * i + lr < n ? list[g + 8 * i + lr] : -1;
         raw4_t y[2][NM][TM][2], wf[NM][H][4];
         auto load_y = [&](int n0, int buf) __attribute__((always_inline)) {
             const bool whole = n0 + 64 <= a.N;
@@ -471,8 +443,8 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_out_kernel(OutArgs a, int
                 if (!a.y[mat]) continue;
 #pragma unroll
                 for (int i = 0; i < 2 * TM; ++i) {
-                    const char* p = ybase[mat] + 2 * n0 + ((uint32_t)(8 * i + lr) * (uint32_t)a.ldy[mat] + lc) * 2;
-                    if (own[i] == cur) y[buf][mat][i >> 1][i & 1] = load8(reinterpret_cast<const T*>(p), whole ? 8 : a.N - n0 - lc);
+                    const char* p = ybase[mat] + 2 * n0 + ((uint32_t)max(own[i], 0) * (uint32_t)a.ldy[mat] + lc) * 2;
+                    if (own[i] >= 0) y[buf][mat][i >> 1][i & 1] = load8(reinterpret_cast<const T*>(p), whole ? 8 : a.N - n0 - lc);
                 }
             }
         };
@@ -493,61 +465,42 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_out_kernel(OutArgs a, int
         float scale = 1.0f;
         if constexpr (WITH) {
             if (a.scale) scale = a.scale[cur];
-            // z: thread groups sum every groups-th part, then the groups' sums meet
-            const int items = NM * ROWS * R8, groups = max(1, min(a.splits, kThreads / items));
-            auto z8 = [&](int i, int from, int step, float (&v)[8]) __attribute__((always_inline)) {
-                const int c = i % R8, row = i / R8 % ROWS, mat = i / R8 / ROWS, m = m0 + row;
-                const bool wanted = m < a.M && 8 * c < a.R && a.index[m] == cur;
+            // z: the parts' sums
+            const int items = NM * ROWS * R8;
+            auto z8 = [&](int i, float (&v)[8]) __attribute__((always_inline)) {
+                const int c = i % R8, at = g + i / R8 % ROWS, mat = i / R8 / ROWS;
+                const bool wanted = at < n && 8 * c < a.R;
+                const int m = m0 + (wanted ? list[at] : 0);
                 const float* p = a.z + ((int64_t)mat * a.M + m) * a.R + 8 * c;
                 const int64_t plane = (int64_t)a.mats * a.M * a.R;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) v[e] = 0.0f;
                 if (!wanted) return;
 #pragma unroll 4
-                for (int s = from; s < a.splits; s += step) {
+                for (int s = 0; s < a.splits; ++s) {
                     const Chunk<Fp32> k = load_chunk(reinterpret_cast<const Fp32*>(p + s * plane), a.R - 8 * c);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) v[e] += k.e[e].v;
                 }
             };
-            if (groups > 1) {
-                const int i = threadIdx.x % items, g = threadIdx.x / items;
-                if (g < groups) {
-                    float v[8];
-                    z8(i, g, groups, v);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) parts[(g * items + i) * 8 + e] = v[e];
-                }
-            }
-            if (!__is_same(T, Bf16)) {
+            if constexpr (!__is_same(T, Bf16)) {
                 for (int i = threadIdx.x; i < NM * ROWS; i += kThreads) most[i] = 0u;
+                __syncthreads();
             }
-            if (groups > 1 || !__is_same(T, Bf16)) __syncthreads();
-            auto z_of = [&](int i, float (&v)[8]) __attribute__((always_inline)) {
-                if (groups > 1) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        v[e] = parts[i * 8 + e];
-                        for (int g = 1; g < groups; ++g) v[e] += parts[(g * items + i) * 8 + e];
-                    }
-                } else {
-                    z8(i, 0, 1, v);
-                }
-            };
             if constexpr (!__is_same(T, Bf16)) {
                 for (int i = threadIdx.x; i < items; i += kThreads) {
                     float v[8];
-                    z_of(i, v);
+                    z8(i, v);
                     atomicMax(&most[i / R8], abs_max8(v));  // a maximum: any order
                 }
                 __syncthreads();
             }
             for (int i = threadIdx.x; i < items; i += kThreads) {
                 float v[8];
-                z_of(i, v);
-                const int c = i % R8, row_at = i / R8, row = row_at % ROWS;
-                if (a.low && cb == 0 && m0 + row < a.M && a.index[m0 + row] == cur && 8 * c < a.R) {
-                    store_chunk(reinterpret_cast<Fp32*>(a.low) + (int64_t)(m0 + row) * a.R + 8 * c, narrow8<Fp32>(v), a.R - 8 * c);
+                z8(i, v);
+                const int c = i % R8, row_at = i / R8, at = g + row_at % ROWS;
+                if (a.low && cb == 0 && at < n && 8 * c < a.R) {
+                    store_chunk(reinterpret_cast<Fp32*>(a.low) + (int64_t)(m0 + list[at]) * a.R + 8 * c, narrow8<Fp32>(v), a.R - 8 * c);
                 }
                 Pow2 f{1.0f, 1.0f};
                 if constexpr (!__is_same(T, Bf16)) {
@@ -569,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_out_kernel(OutArgs a, int
         } else if (a.low && cb == 0 && wave == 0) {
 #pragma unroll
             for (int i = 0; i < 2 * TM; ++i) {
-                for (int r = lane & 7; own[i] == cur && r < a.R; r += 8) a.low[(int64_t)(m0 + 8 * i + lr) * a.R + r] = 0.0f;
+                for (int r = lane & 7; own[i] >= 0 && r < a.R; r += 8) a.low[(int64_t)(m0 + own[i]) * a.R + r] = 0.0f;
             }
         }
         auto block = [&](int nb, int buf) __attribute__((always_inline)) {
@@ -652,9 +605,9 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_out_kernel(OutArgs a, int
                 }
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    char* to = obase + 2 * n0 + ((uint32_t)(16 * t + 8 * i + lr) * (uint32_t)a.ldo + lc) * 2;
+                    char* to = obase + 2 * n0 + ((uint32_t)max(own[2 * t + i], 0) * (uint32_t)a.ldo + lc) * 2;
                     const int cnt = whole ? 8 : a.N - n0 - lc;
-                    if (own[2 * t + i] == cur && cnt > 0) store_chunk(reinterpret_cast<T*>(to), narrow8<T>(o[i]), cnt);
+                    if (own[2 * t + i] >= 0 && cnt > 0) store_chunk(reinterpret_cast<T*>(to), narrow8<T>(o[i]), cnt);
                 }
             }
             if (nb + kWaves < nb_end) load_ws(64 * (nb + kWaves));
@@ -664,49 +617,71 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_out_kernel(OutArgs a, int
             if (nb + kWaves < nb_end) block(nb + kWaves, 1);
         }
     };
-    if (slot == 0 && __ballot(bare)) pass(-1, Part{});
+    if (slot == 0) {
+        const int n = list_rows(idx, -1, list);
+        for (int g = 0; g < n; g += ROWS) pass(-1, g, n, Part{});
+    }
     int seen = 0;
+    bool again = false;
     for (;;) {
-        const int cur = next_adapter<TM>(left);
+        const int cur = next_adapter(left);
         if (cur < 0) break;
-        take_out<TM>(left, cur);
+        if (left == cur) left = -1;
         if (seen++ % slots != slot) continue;
-        if (seen > slots) __syncthreads();  // z of the adapter before is read
-        pass(cur, Whole{});
+        const int n = list_rows(idx, cur, list);
+        for (int g = 0; g < n; g += ROWS) {
+            if (again) __syncthreads();  // z of the rows before is read
+            again = true;
+            pass(cur, g, n, Whole{});
+        }
     }
 }
 
 constexpr int kTargetWaves = 2048;
 constexpr int64_t kMaxBlocks = 1 << 22;  // workgroups of 256 threads in a launch's first dimension
 
-// Up to kMixed rows a batch is taken to mix requests: tiles of 16 rows, whose up to 16 adapters have workgroups of their own
-// (the launch's `slots`), and waves side by side along the columns.  More rows are taken to be runs of one adapter.
-constexpr int kMixed = 256;
-int slots_of(int M, int L)
+// How a batch's rows are cut.  A batch of up to kFew rows, fewer than 16 per adapter there is, is taken to mix requests: a
+// tile of 64 rows, and workgroups of their own (the launch's `slots`) for its up to 64 adapters, each of which takes its rows
+// 16 at a time and reads its weights once for them.  Otherwise the rows are taken to be runs of one adapter, and a tile
+// is what a workgroup takes at a time: 16 rows of up to kFew, so that there are workgroups enough, else 64 or 32.  64 rows
+// of 16 adapters (GLU, K = 2560 N = 9216, rank 32): second product 18.2 us with tiles of 16, 11.9 with 64; 203 rows of 2
+// (backward, 2560 x 2560): 4.2 and 16.5 us.
+constexpr int kFew = 256;
+struct Cut {
+    int rows, slots;  // of a tile
+    int64_t tiles, units;  // units: expected adapters of all tiles
+};
+Cut cut(int M, int L, int tm)
 {
-    const int most = M < 16 ? M : 16;
-    return M > kMixed ? 1 : L < most ? L : most;
+    const bool mixed = M <= kFew && M < 16 * L;
+    Cut c;
+    c.rows = tm > 1 ? 16 * tm : mixed ? 64 : 16;
+    c.tiles = ((int64_t)M + c.rows - 1) / c.rows;
+    const int most = M < c.rows ? M : c.rows;
+    c.slots = M > kFew ? 1 : L < most ? L : most;
+    c.units = !mixed ? c.tiles : c.tiles * c.slots < M ? c.tiles * c.slots : M;
+    return c;
 }
 
-// Tiles of the first product: 16 TM rows and 16 RT ranks.  Up to kMixed rows one instruction's, so that there are more of
+// Tiles of the first product: 16 TM rows and 16 RT ranks.  Up to kFew rows one instruction's, so that there are more of
 // them; else as many as registers hold with a stage in flight.  64 x 64 (from LDS) and 32 x 64, us: 16384 rows of 4096 34.7
 // and 40.2, 8192 of 5120 25.2 and 27.0, 5000 of 4096 23.6 and 23.4, 2050 of 4096 18.0 and 15.3.
 struct LowTile { int tm, rt; };
 LowTile low_tile(int M, int R, bool columns)
 {
-    if (M <= kMixed || columns) return {1, 1};
+    if (M <= kFew || columns) return {1, 1};
     return R <= 16 ? LowTile{4, 1} : R <= 32 ? LowTile{4, 2} : M > 4096 ? LowTile{4, 4} : LowTile{2, 4};
 }
 
 template <class T, int TM, int RT, int U, bool COLUMNS>
 void low_tiles(const LowArgs& a, hipStream_t stream)
 {
-    const int slots = slots_of(a.M, a.L), rgroups = (a.R + 16 * RT - 1) / (16 * RT);
-    const int64_t tiles = ((int64_t)a.M + 16 * TM - 1) / (16 * TM);
-    for (int64_t t = 0; t < tiles; t += kMaxBlocks) {
-        const dim3 grid((unsigned)(tiles - t < kMaxBlocks ? tiles - t : kMaxBlocks), a.splits * rgroups * a.mats, slots);
-        hipLaunchKernelGGL((adapter_low_kernel<T, TM, RT, U, COLUMNS>), grid, dim3(kThreads), 0, stream, a, slots, rgroups,
-                           (int)t);
+    const Cut c = cut(a.M, a.L, TM);
+    const int rgroups = (a.R + 16 * RT - 1) / (16 * RT);
+    for (int64_t t = 0; t < c.tiles; t += kMaxBlocks) {
+        const dim3 grid((unsigned)(c.tiles - t < kMaxBlocks ? c.tiles - t : kMaxBlocks), a.splits * rgroups * a.mats, c.slots);
+        hipLaunchKernelGGL((adapter_low_kernel<T, TM, RT, U, COLUMNS>), grid, dim3(kThreads), 0, stream, a, c.rows,
+                           c.slots, rgroups, (int)t);
     }
 }
 
@@ -752,22 +727,19 @@ hipError_t low_launch(const LowArgs& a, hipStream_t stream)
 template <class T, int TM, int NM, int S, bool COLUMNS>
 void out_tiles(const OutArgs& a, hipStream_t stream)
 {
-    const int slots = slots_of(a.M, a.L);
-    const int64_t tiles = ((int64_t)a.M + 16 * TM - 1) / (16 * TM);
+    const Cut c = cut(a.M, a.L, TM);
     const int blocks = a.N > 0 ? (a.N + 63) / 64 : 1;  // N == 0: z alone, to low
     // a wave keeps its z for several blocks where there are waves enough
-    const int64_t units = tiles * slots < a.M ? tiles * slots : a.M;  // tiles' adapters at most
-    int per = (int)((units * blocks + kTargetWaves - 1) / kTargetWaves);
+    int per = (int)((c.units * blocks + kTargetWaves - 1) / kTargetWaves);
     per = per < 1 ? 1 : per > 32 ? 32 : per;
     const int cblocks = (blocks + per * kWaves - 1) / (per * kWaves);
     const int64_t fit = kMaxBlocks / cblocks < 1 ? 1 : kMaxBlocks / cblocks;
-    const int RP = S ? 16 * S : (a.R + 31) & ~31, rows = 16 * TM, items = NM * rows * RP / 8;
-    const int groups = kThreads / items < a.splits ? kThreads / items : a.splits;
-    const size_t bytes = (size_t)NM * rows * (2 * RP + 8) * 2 + (size_t)NM * rows * 8 + (groups > 1 ? (size_t)groups * items * 32 : 0);
-    for (int64_t t = 0; t < tiles; t += fit) {
-        const dim3 grid((unsigned)((tiles - t < fit ? tiles - t : fit) * cblocks), slots);
-        hipLaunchKernelGGL((adapter_out_kernel<T, TM, NM, S, COLUMNS>), grid, dim3(kThreads), bytes, stream, a, slots, cblocks,
-                           per, (int)t);
+    const int RP = S ? 16 * S : (a.R + 31) & ~31, rows = 16 * TM;
+    const size_t bytes = (size_t)NM * rows * (2 * RP + 8) * 2 + (size_t)NM * rows * 8;
+    for (int64_t t = 0; t < c.tiles; t += fit) {
+        const dim3 grid((unsigned)((c.tiles - t < fit ? c.tiles - t : fit) * cblocks), c.slots);
+        hipLaunchKernelGGL((adapter_out_kernel<T, TM, NM, S, COLUMNS>), grid, dim3(kThreads), bytes, stream, a, c.rows, c.slots,
+                           cblocks, per, (int)t);
     }
 }
 
@@ -776,7 +748,7 @@ hipError_t out_launch(const OutArgs& a, hipStream_t stream)
 {
     if (a.R > 64) {
         out_tiles<T, 1, NM, 0, COLUMNS>(a, stream);
-    } else if (a.M <= kMixed) {
+    } else if (a.M <= kFew) {
         if (a.R <= 16) out_tiles<T, 1, NM, 1, COLUMNS>(a, stream);
         else if (a.R <= 32) out_tiles<T, 1, NM, 2, COLUMNS>(a, stream);
         else out_tiles<T, 1, NM, 4, COLUMNS>(a, stream);
@@ -790,17 +762,19 @@ hipError_t out_launch(const OutArgs& a, hipStream_t stream)
 
 }  // namespace
 
-// Parts of the columns.  A mixed batch: as many as make some 768 workgroups, of one stage per wave at least.  More rows: as
-// many as make a workgroup per CU, whose waves then go through more stages each (8192 rows of 5120, 16 ranks, in 256, 512
-// and 768 workgroups: 18.3, 21.7 and 25.4 us; 64 ranks 25.2, 32.6 and 41.4).
+// Parts of the columns.  A mixed batch: as many as make some 768 workgroups, of one stage per wave at least, but 4 at
+// most, which the second product has to add up (one row of 2560, 9216 columns: both products 10.7 us with 10 parts, 8.8
+// with 4, 8.9 with 2; 37 rows of 4096, 12288 columns: 19.6, 17.2 and 17.0).  More rows: as many as make a workgroup per CU,
+// whose waves then go through more stages each (8192 rows of 5120, 16 ranks, in 256, 512 and 768 workgroups: 18.3, 21.7
+// and 25.4 us; 64 ranks 25.2, 32.6 and 41.4).
 int adapter_low_splits(int M, int C, int R, int L, int mats, bool columns)
 {
     const LowTile t = low_tile(M, R, columns);
-    const int64_t groups = ((int64_t)M + 16 * t.tm - 1) / (16 * t.tm) * mats * ((R + 16 * t.rt - 1) / (16 * t.rt)) * slots_of(M, L);
-    const int64_t most = ((int64_t)C + kStage * kWaves - 1) / (kStage * kWaves);
+    const int64_t groups = cut(M, L, t.tm).units * mats * ((R + 16 * t.rt - 1) / (16 * t.rt));
+    const int64_t most = ((int64_t)C + kStage * kWaves - 1) / (kStage * kWaves), cap = t.tm == 1 ? 4 : 16;
     int64_t s = groups ? (t.tm == 1 ? 768 : 256) / groups : 1;
     if (s > most) s = most;
-    return (int)(s < 1 ? 1 : s > 16 ? 16 : s);
+    return (int)(s < 1 ? 1 : s > cap ? cap : s);
 }
 
 hipError_t adapter_low_launch(int dtype, bool columns, const LowArgs& a, hipStream_t stream)
