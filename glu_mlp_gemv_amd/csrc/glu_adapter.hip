@@ -435,7 +435,9 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_out_kernel(OutArgs a, int
         int own[2 * TM];  // this lane's rows; -1: none
 #pragma unroll
         for (int i = 0; i < 2 * TM; ++i) own[i] = g + 8 * i + lr < n ? list[g + 8 * i + lr] : -1;
-        raw4_t y[2][NM][TM][2], wf[NM][H][4];
+        // two blocks' y and, where registers hold them, w: the next block's are on their way during this one
+        constexpr int WB = H == 1 && NM * TM < 4 ? 2 : 1;
+        raw4_t y[2][NM][TM][2], wf[WB][NM][H][4];
         auto load_y = [&](int n0, int buf) __attribute__((always_inline)) {
             const bool whole = n0 + 64 <= a.N;
 #pragma unroll
@@ -448,18 +450,18 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_out_kernel(OutArgs a, int
                 }
             }
         };
-        auto load_ws = [&](int n0) __attribute__((always_inline)) {
+        auto load_ws = [&](int n0, int buf) __attribute__((always_inline)) {
             if constexpr (WITH && S > 0) {
 #pragma unroll
                 for (int mat = 0; mat < NM; ++mat) {
 #pragma unroll
-                    for (int h = 0; h < H; ++h) load_w(mat, cur, n0, S == 1 ? q & 1 : 4 * h + q, wf[mat][h]);
+                    for (int h = 0; h < H; ++h) load_w(mat, cur, n0, S == 1 ? q & 1 : 4 * h + q, wf[buf % WB][mat][h]);
                 }
             }
         };
         if (nb_first < nb_end) {
             load_y(64 * nb_first, 0);
-            load_ws(64 * nb_first);
+            load_ws(64 * nb_first, 0);
         }
 
         float scale = 1.0f;
@@ -528,7 +530,10 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_out_kernel(OutArgs a, int
         auto block = [&](int nb, int buf) __attribute__((always_inline)) {
             const int n0 = 64 * nb;
             const bool whole = n0 + 64 <= a.N;
-            if (nb + kWaves < nb_end) load_y(64 * (nb + kWaves), buf ^ 1);
+            if (nb + kWaves < nb_end) {
+                load_y(64 * (nb + kWaves), buf ^ 1);
+                if constexpr (WB == 2) load_ws(64 * (nb + kWaves), buf ^ 1);
+            }
             f32x4 acc[NM][S ? 1 : TM][4];
             auto z_at = [&](int mat, int t, int s) __attribute__((always_inline)) {
                 return *reinterpret_cast<const raw4_t*>(lds + (mat * ROWS + 16 * t + i16) * pitch + 32 * s + 8 * q);
@@ -567,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_out_kernel(OutArgs a, int
                         for (int s = 0; WITH && s < S; ++s) {
                             const raw4_t z = z_at(mat, t, s);
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) acc[mat][0][j] = mfma16<T>(wf[mat][s % H][j], z, acc[mat][0][j]);
+                            for (int j = 0; j < 4; ++j) acc[mat][0][j] = mfma16<T>(wf[buf % WB][mat][s % H][j], z, acc[mat][0][j]);
                         }
                     }
                 }
@@ -610,16 +615,19 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_out_kernel(OutArgs a, int
                     if (own[2 * t + i] >= 0 && cnt > 0) store_chunk(reinterpret_cast<T*>(to), narrow8<T>(o[i]), cnt);
                 }
             }
-            if (nb + kWaves < nb_end) load_ws(64 * (nb + kWaves));
+            if constexpr (WB == 1) {
+                if (nb + kWaves < nb_end) load_ws(64 * (nb + kWaves), 0);
+            }
         };
         for (int nb = nb_first; nb < nb_end; nb += 2 * kWaves) {
             block(nb, 0);
             if (nb + kWaves < nb_end) block(nb + kWaves, 1);
         }
     };
-    if (slot == 0) {
+    if (slot == (slots > 1 ? slots : 0)) {  // a mixed batch's rows without an adapter have a slot of their own, the last
         const int n = list_rows(idx, -1, list);
         for (int g = 0; g < n; g += ROWS) pass(-1, g, n, Part{});
+        if (slots > 1) return;
     }
     int seen = 0;
     bool again = false;
@@ -737,7 +745,7 @@ void out_tiles(const OutArgs& a, hipStream_t stream)
     const int RP = S ? 16 * S : (a.R + 31) & ~31, rows = 16 * TM;
     const size_t bytes = (size_t)NM * rows * (2 * RP + 8) * 2 + (size_t)NM * rows * 8;
     for (int64_t t = 0; t < c.tiles; t += fit) {
-        const dim3 grid((unsigned)((c.tiles - t < fit ? c.tiles - t : fit) * cblocks), c.slots);
+        const dim3 grid((unsigned)((c.tiles - t < fit ? c.tiles - t : fit) * cblocks), c.slots > 1 ? c.slots + 1 : 1);
         hipLaunchKernelGGL((adapter_out_kernel<T, TM, NM, S, COLUMNS>), grid, dim3(kThreads), bytes, stream, a, c.rows, c.slots,
                            cblocks, per, (int)t);
     }
