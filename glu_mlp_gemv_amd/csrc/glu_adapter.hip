@@ -42,6 +42,14 @@ __device__ __forceinline__ int next_adapter(int left)
     return b ? __builtin_amdgcn_readlane(left, __builtin_ctzll(b)) : -1;
 }
 
+// Whether this row is the tile's first with its adapter (or without one); cur: which.  The workgroup of a row that is not
+// leaves its work to that of the first.
+__device__ __forceinline__ bool leads(int idx, int row, int& cur)
+{
+    cur = __builtin_amdgcn_readlane(idx, row);
+    return cur != -2 && __builtin_ctzll(__ballot(idx == cur)) == row;
+}
+
 // The rows of a tile that have this adapter, in order, to a list of the wave's own in LDS; how many there are
 __device__ __forceinline__ int list_rows(int idx, int cur, uint8_t* list)
 {
@@ -58,6 +66,13 @@ __device__ __forceinline__ int list_rows(int idx, int cur, uint8_t* list)
 __device__ __forceinline__ raw4_t read16(const char* base, uint32_t lane)
 {
     return *reinterpret_cast<const u32x4_any*>(base + lane);
+}
+
+// silu(g) u for results of 16 bits: without the correction of silu_mul the rounding of the exponent stays, 2 |g| units of
+// 2^-24 of the result at most, which does not show there; a prefill's GLU (2050 x 12288) takes 56 us instead of 63
+__device__ __forceinline__ float silu_mul16(float g, float u)
+{
+    return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504088896340736f)) * u;
 }
 
 // 16 bytes per lane straight to LDS, lane l's at to + 16 l (to: uniform)
@@ -86,7 +101,7 @@ __device__ __forceinline__ void reads_done()
 // part of the columns; the 4 waves take stages of 64 columns in turn, keep U of them in flight, and join in LDS.
 // COLUMNS: w is [C][R], and operand j of a lane is column RT (l % 16) + j.
 template <class T, int TM, int RT, int U, bool COLUMNS>
-__global__ void __launch_bounds__(kThreads, 3) adapter_low_kernel(LowArgs a, int tile_rows, int slots, int rgroups,
+__global__ void __launch_bounds__(kThreads, 3) adapter_low_kernel(LowArgs a, int tile_rows, bool by_row, int rgroups,
                                                                   int tile0)
 {
     constexpr int PIECES = TM * RT;
@@ -96,7 +111,6 @@ __global__ void __launch_bounds__(kThreads, 3) adapter_low_kernel(LowArgs a, int
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int m0 = (tile0 + blockIdx.x) * tile_rows;
     const int split = blockIdx.y % a.splits, rg = blockIdx.y / a.splits % rgroups, mat = blockIdx.y / a.splits / rgroups;
-    const int slot = blockIdx.z;
     const int r0 = rg * 16 * RT;
     // this part's stages: first .. first + count - 1 are whole, `tail` is one that ends past the columns, or -1
     const int stages = (a.C + kStage - 1) / kStage, per = (stages + a.splits - 1) / a.splits;
@@ -107,20 +121,21 @@ __global__ void __launch_bounds__(kThreads, 3) adapter_low_kernel(LowArgs a, int
     const int idx = lane < tile_rows ? adapter_of(a.index, m0 + lane, a.M, a.L) : -2;
     int left = idx;
     uint8_t* list = lists[wave];
-    if (slot == 0) {
-        const uint64_t bare = __ballot(idx == -1);
+    int alone;  // the workgroup's one adapter, where rows have workgroups of their own
+    if (by_row && !leads(idx, blockIdx.z, alone)) return;
+    const uint64_t bare = __ballot(idx == -1);
+    if (bare && (!by_row || alone == -1)) {
         for (int j = threadIdx.x; j < tile_rows * 16 * RT; j += kThreads) {
             const int row = j / (16 * RT), r = r0 + j % (16 * RT);
             if ((bare >> row & 1) && r < a.R) z[(int64_t)(m0 + row) * a.R + r] = 0.0f;
         }
+        if (by_row) return;
     }
     const char* vbase = reinterpret_cast<const char*>(static_cast<const T*>(a.v) + m0 * a.ldv);
-    int seen = 0;
     for (;;) {
-        const int cur = next_adapter(left);
+        const int cur = by_row ? alone : next_adapter(left);
         if (cur < 0) break;
         if (left == cur) left = -1;
-        if (seen++ % slots != slot) continue;
 
         const int n = list_rows(idx, cur, list);
         const T* w = static_cast<const T*>(a.w[mat].w) + cur * a.w[mat].stack;
@@ -228,6 +243,7 @@ __global__ void __launch_bounds__(kThreads, 3) adapter_low_kernel(LowArgs a, int
         }
         __syncthreads();
         }
+        if (by_row) break;
     }
 }
 
@@ -376,7 +392,7 @@ __global__ void __launch_bounds__(kThreads) adapter_low_tile_kernel(LowArgs a, i
 // of which a lane holds 4 columns of its own row, go through LDS to lanes that hold 8 columns, 8 neighbouring lanes a line:
 // so y is read and out written.
 template <class T, int TM, int NM, int S, bool COLUMNS>
-__global__ void __launch_bounds__(kThreads, 2) adapter_out_kernel(OutArgs a, int tile_rows, int slots, int cblocks,
+__global__ void __launch_bounds__(kThreads, 2) adapter_out_kernel(OutArgs a, int tile_rows, bool by_row, int cblocks,
                                                                   int per, int tile0)
 {
     constexpr int ROWS = 16 * TM, H = S > 1 ? S / 2 : 1;
@@ -386,7 +402,6 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_out_kernel(OutArgs a, int
     const int lane = threadIdx.x & 63, i16 = lane & 15, q = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int cb = blockIdx.x % cblocks, m0 = (tile0 + blockIdx.x / cblocks) * tile_rows;
-    const int slot = blockIdx.y;
     const int nb_first = cb * per * kWaves + wave, nb_end = min((a.N + 63) >> 6, (cb + 1) * per * kWaves);
     const int RP = S ? 16 * (S == 1 ? 1 : S) : (a.R + 31) & ~31, R8 = RP >> 3, pitch = 2 * RP + 8;
     const int steps = S ? S : RP >> 4;
@@ -604,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_out_kernel(OutArgs a, int
                             for (int e = 0; e < 8; ++e) v[e] = a.y[mat] ? widen(base.e[e]) : 0.0f;
                         }
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) o[i][e] = mat == 0 ? v[e] : silu_mul(o[i][e], v[e]);
+                        for (int e = 0; e < 8; ++e) o[i][e] = mat == 0 ? v[e] : silu_mul16(o[i][e], v[e]);
                     }
                     __builtin_amdgcn_wave_barrier();
                 }
@@ -624,50 +639,61 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_out_kernel(OutArgs a, int
             if (nb + kWaves < nb_end) block(nb + kWaves, 1);
         }
     };
-    if (slot == (slots > 1 ? slots : 0)) {  // a mixed batch's rows without an adapter have a slot of their own, the last
+    auto bare = [&]() __attribute__((always_inline)) {
         const int n = list_rows(idx, -1, list);
         for (int g = 0; g < n; g += ROWS) pass(-1, g, n, Part{});
-        if (slots > 1) return;
-    }
-    int seen = 0;
+    };
     bool again = false;
-    for (;;) {
-        const int cur = next_adapter(left);
-        if (cur < 0) break;
-        if (left == cur) left = -1;
-        if (seen++ % slots != slot) continue;
+    auto rows_of = [&](int cur) __attribute__((always_inline)) {
         const int n = list_rows(idx, cur, list);
         for (int g = 0; g < n; g += ROWS) {
             if (again) __syncthreads();  // z of the rows before is read
             again = true;
             pass(cur, g, n, Whole{});
         }
+    };
+    if constexpr (TM == 1) {
+        if (by_row) {
+            int cur;
+            if (!leads(idx, blockIdx.y, cur)) return;
+            if (cur < 0) bare();
+            else rows_of(cur);
+            return;
+        }
+    }
+    bare();
+    for (;;) {
+        const int cur = next_adapter(left);
+        if (cur < 0) break;
+        if (left == cur) left = -1;
+        rows_of(cur);
     }
 }
 
 constexpr int kTargetWaves = 2048;
 constexpr int64_t kMaxBlocks = 1 << 22;  // workgroups of 256 threads in a launch's first dimension
 
-// How a batch's rows are cut.  A batch of up to kFew rows, fewer than 16 per adapter there is, is taken to mix requests: a
-// tile of 64 rows, and workgroups of their own (the launch's `slots`) for its up to 64 adapters, each of which takes its rows
-// 16 at a time and reads its weights once for them.  Otherwise the rows are taken to be runs of one adapter, and a tile
-// is what a workgroup takes at a time: 16 rows of up to kFew, so that there are workgroups enough, else 64 or 32.  64 rows
-// of 16 adapters (GLU, K = 2560 N = 9216, rank 32): second product 18.2 us with tiles of 16, 11.9 with 64; 203 rows of 2
+// How a batch's rows are cut.  A batch of up to kFew rows, fewer than 16 per adapter there is, is taken to mix requests: in
+// tiles of 64 rows each row has workgroups of its own (the launch's `slots`), of which those of an adapter's first row take
+// all of its rows, 16 at a time, and read its weights once for them.  (Going through a tile's adapters to find the
+// workgroup's own took 3 us at 32 of them.)  Otherwise the rows are taken to be runs of one adapter, and a tile is what a
+// workgroup takes at a time: 16 rows of up to kFew, so that there are workgroups enough, with slots too, so that none has
+// two runs' rows, else 64 or 32.  64 rows of 16
+// adapters (GLU, K = 2560 N = 9216, rank 32): second product 18.2 us with tiles of 16, 11.9 with 64; 203 rows of 2
 // (backward, 2560 x 2560): 4.2 and 16.5 us.
 constexpr int kFew = 256;
 struct Cut {
-    int rows, slots;  // of a tile
+    int rows, slots;       // of a tile
     int64_t tiles, units;  // units: expected adapters of all tiles
 };
 Cut cut(int M, int L, int tm)
 {
-    const bool mixed = M <= kFew && M < 16 * L;
+    const bool mixed = M <= kFew && M < 16 * (int64_t)L;
     Cut c;
     c.rows = tm > 1 ? 16 * tm : mixed ? 64 : 16;
     c.tiles = ((int64_t)M + c.rows - 1) / c.rows;
-    const int most = M < c.rows ? M : c.rows;
-    c.slots = M > kFew ? 1 : L < most ? L : most;
-    c.units = !mixed ? c.tiles : c.tiles * c.slots < M ? c.tiles * c.slots : M;
+    c.slots = M > kFew ? 1 : M < c.rows ? M : c.rows;
+    c.units = !mixed ? c.tiles : c.tiles * L < M ? c.tiles * L : M;
     return c;
 }
 
@@ -689,7 +715,7 @@ void low_tiles(const LowArgs& a, hipStream_t stream)
     for (int64_t t = 0; t < c.tiles; t += kMaxBlocks) {
         const dim3 grid((unsigned)(c.tiles - t < kMaxBlocks ? c.tiles - t : kMaxBlocks), a.splits * rgroups * a.mats, c.slots);
         hipLaunchKernelGGL((adapter_low_kernel<T, TM, RT, U, COLUMNS>), grid, dim3(kThreads), 0, stream, a, c.rows,
-                           c.slots, rgroups, (int)t);
+                           c.slots > 1, rgroups, (int)t);
     }
 }
 
@@ -737,16 +763,19 @@ void out_tiles(const OutArgs& a, hipStream_t stream)
 {
     const Cut c = cut(a.M, a.L, TM);
     const int blocks = a.N > 0 ? (a.N + 63) / 64 : 1;  // N == 0: z alone, to low
-    // a wave keeps its z for several blocks where there are waves enough
-    int per = (int)((c.units * blocks + kTargetWaves - 1) / kTargetWaves);
+    // A wave takes several blocks where there are waves enough: those of a round of workgroups, two per CU, or three such
+    // rounds of the pair, whose workgroups take longer (8192 x 5120, rank 64: 48 us, 60 in two rounds; pair, 2050 x 12288, rank
+    // 16: 63 us in one, 54 in three).
+    const int64_t target = NM == 2 && TM > 1 ? 3 * kTargetWaves : kTargetWaves;
+    int per = (int)((c.units * blocks + target - 1) / target);
     per = per < 1 ? 1 : per > 32 ? 32 : per;
     const int cblocks = (blocks + per * kWaves - 1) / (per * kWaves);
     const int64_t fit = kMaxBlocks / cblocks < 1 ? 1 : kMaxBlocks / cblocks;
     const int RP = S ? 16 * S : (a.R + 31) & ~31, rows = 16 * TM;
     const size_t bytes = (size_t)NM * rows * (2 * RP + 8) * 2 + (size_t)NM * rows * 8;
     for (int64_t t = 0; t < c.tiles; t += fit) {
-        const dim3 grid((unsigned)((c.tiles - t < fit ? c.tiles - t : fit) * cblocks), c.slots > 1 ? c.slots + 1 : 1);
-        hipLaunchKernelGGL((adapter_out_kernel<T, TM, NM, S, COLUMNS>), grid, dim3(kThreads), bytes, stream, a, c.rows, c.slots,
+        const dim3 grid((unsigned)((c.tiles - t < fit ? c.tiles - t : fit) * cblocks), c.slots);
+        hipLaunchKernelGGL((adapter_out_kernel<T, TM, NM, S, COLUMNS>), grid, dim3(kThreads), bytes, stream, a, c.rows, c.slots > 1,
                            cblocks, per, (int)t);
     }
 }

@@ -21,7 +21,7 @@ constexpr int kWaves = kThreads / 64;
 constexpr int kDirectRows = 512;
 template <int RT> constexpr int kChunkRows = RT == 4 ? 128 : 256;  // rows whose d or t are in LDS at a time
 constexpr int kItemStep = 256;        // items are multiples of it
-template <int RT> constexpr int kSteps = RT == 4 ? 2 : 4;         // steps of 32 rows in flight
+constexpr int kSteps = 2;             // steps of 32 rows in flight
 constexpr int kTurn = 256;            // columns that a workgroup turns to rows
 constexpr int kOrderThreads = 1024;
 
@@ -155,7 +155,7 @@ adapter_prepare_kernel(GradArgs a, int listed, int items, int32_t* bounds, Turn 
 
 // One item, 64 columns per wave.  DIRECT: the item is the adapter, and its sums are the gradient.
 template <class T, int RT, bool DIRECT>
-__global__ void __launch_bounds__(kThreads, 3) adapter_grad_kernel(GradArgs a, int cblocks0, int cblocks, int64_t columns,
+__global__ void __launch_bounds__(kThreads, RT == 4 ? 2 : 3) adapter_grad_kernel(GradArgs a, int cblocks0, int cblocks, int64_t columns,
                                                                    int item0)
 {
     constexpr int CHUNK = kChunkRows<RT>, PITCH = CHUNK + 8;
@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 3) adapter_grad_kernel(GradArgs a, i
         if (base) __syncthreads();
         for (int i = threadIdx.x; i < 32 * steps; i += kThreads) offset[i] = row_at(base + min(i, n - 1)) * s.ldv * 2;
         __syncthreads();
-        constexpr int U = kSteps<RT>;
+        constexpr int U = kSteps;
         uint32_t raw[U][8][2];
         auto load = [&](int u, int k) __attribute__((always_inline)) {
 #pragma unroll
@@ -327,21 +327,48 @@ __global__ void __launch_bounds__(kThreads, 3) adapter_grad_kernel(GradArgs a, i
     const int64_t side = which && a.side[0].grad ? a.side[0].C : 0;
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
+        const int r = 16 * t + 4 * q;  // this lane's 4 ranks and columns
+        float v[4][4];                 // [rank][column]
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const int r = 16 * t + 4 * q + e;  // of this group of ranks
-            if (r >= ranks) continue;
-            const float f = __is_same(T, Bf16) ? 1.0f : pow2_for<T>(most[r]).down;
+            const float f = __is_same(T, Bf16) ? 1.0f : pow2_for<T>(most[r + e]).down;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (c + j >= s.C) continue;
-                const float sum = acc[t][j][e] * f;
-                if constexpr (DIRECT) {
-                    const int64_t at = s.rank_inner ? ((int64_t)l * s.C + c + j) * a.R + r0 + r
-                                                    : ((int64_t)l * a.R + r0 + r) * s.C + c + j;
-                    static_cast<T*>(s.grad)[at] = narrow<T>(count ? scale * sum : 0.0f);
+            for (int j = 0; j < 4; ++j) v[e][j] = acc[t][j][e] * f;
+        }
+        const bool whole = r + 4 <= ranks && c + 4 <= s.C;
+        if constexpr (DIRECT) {
+            T* grad = static_cast<T*>(s.grad);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {  // 4 neighbours at a time: columns of a rank, or ranks of a column
+                uint16_t o[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) o[k] = count ? bits16<T>(scale * (s.rank_inner ? v[k][i] : v[i][k])) : (uint16_t)0;
+                const int64_t at = s.rank_inner ? ((int64_t)l * s.C + c + i) * a.R + r0 + r
+                                                : ((int64_t)l * a.R + r0 + r + i) * s.C + c;
+                if (whole) {
+                    *reinterpret_cast<u32x2_any*>(grad + at) = raw2_t{o[0] | (uint32_t)o[1] << 16, o[2] | (uint32_t)o[3] << 16};
                 } else {
-                    a.part[((int64_t)item * a.R + r0 + r) * columns + side + c + j] = sum;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const bool in = s.rank_inner ? r + k < ranks && c + i < s.C : r + i < ranks && c + k < s.C;
+                        if (in) reinterpret_cast<uint16_t*>(grad)[at + k] = o[k];
+                    }
+                }
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float* to = a.part + ((int64_t)item * a.R + r0 + r + e) * columns + side + c;
+                if (whole) {
+                    raw4_t o;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) o[j] = __float_as_uint(v[e][j]);
+                    *reinterpret_cast<u32x4_any*>(to) = o;
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if (r + e < ranks && c + j < s.C) to[j] = v[e][j];
+                    }
                 }
             }
         }

@@ -53,10 +53,11 @@ def add64(y, x, a, b, index, scale):
 
 
 def glu64(gate, up, eg, eu):
-    """silu(g) u and its bound from those of g and u: |silu'| <= 1.1, 8 fp32 roundings in the activation."""
+    """silu(g) u and its bound from those of g and u: |silu'| <= 1.1, 8 fp32 roundings in the activation, and exp(-g) taken as
+    2^t, where t = -g log2(e) is off by 1.6 units of its own: 1.6 |g| units of the exponential."""
     s = gate * torch.sigmoid(gate)
     out = s * up
-    return out, 1.1 * eg * up.abs() + s.abs() * eu + 1.1 * eg * eu + 8 * U * out.abs()
+    return out, 1.1 * eg * up.abs() + s.abs() * eu + 1.1 * eg * eu + (8 + 2 * gate.abs()) * U * out.abs()
 
 
 def backward64(dout, x, a, b, index, low, scale):
