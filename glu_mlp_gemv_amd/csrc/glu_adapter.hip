@@ -42,12 +42,13 @@ __device__ __forceinline__ int next_adapter(int left)
     return b ? __builtin_amdgcn_readlane(left, __builtin_ctzll(b)) : -1;
 }
 
-// Whether this row is the tile's first with its adapter (or without one); cur: which.  The workgroup of a row that is not
-// leaves its work to that of the first.
-__device__ __forceinline__ bool leads(int idx, int row, int& cur)
+// Whether this row is the first of 16 that a workgroup takes of the tile's rows with its adapter (or without one); cur: which
+// adapter, from: its place among them.  The workgroups of the other rows have nothing to do.
+__device__ __forceinline__ bool leads(int idx, int row, int& cur, int& from)
 {
     cur = __builtin_amdgcn_readlane(idx, row);
-    return cur != -2 && __builtin_ctzll(__ballot(idx == cur)) == row;
+    from = __popcll(__ballot(idx == cur) & ((1ull << row) - 1ull));
+    return cur != -2 && from % 16 == 0;
 }
 
 // The rows of a tile that have this adapter, in order, to a list of the wave's own in LDS; how many there are
@@ -121,15 +122,14 @@ __global__ void __launch_bounds__(kThreads, 3) adapter_low_kernel(LowArgs a, int
     const int idx = lane < tile_rows ? adapter_of(a.index, m0 + lane, a.M, a.L) : -2;
     int left = idx;
     uint8_t* list = lists[wave];
-    int alone;  // the workgroup's one adapter, where rows have workgroups of their own
-    if (by_row && !leads(idx, blockIdx.z, alone)) return;
+    int alone, from = 0;  // the workgroup's one adapter, where rows have workgroups of their own
+    if (by_row && !leads(idx, blockIdx.z, alone, from)) return;
     const uint64_t bare = __ballot(idx == -1);
-    if (bare && (!by_row || alone == -1)) {
+    if (bare && (!by_row || (alone == -1 && from == 0))) {
         for (int j = threadIdx.x; j < tile_rows * 16 * RT; j += kThreads) {
             const int row = j / (16 * RT), r = r0 + j % (16 * RT);
             if ((bare >> row & 1) && r < a.R) z[(int64_t)(m0 + row) * a.R + r] = 0.0f;
         }
-        if (by_row) return;
     }
     const char* vbase = reinterpret_cast<const char*>(static_cast<const T*>(a.v) + m0 * a.ldv);
     for (;;) {
@@ -137,7 +137,8 @@ __global__ void __launch_bounds__(kThreads, 3) adapter_low_kernel(LowArgs a, int
         if (cur < 0) break;
         if (left == cur) left = -1;
 
-        const int n = list_rows(idx, cur, list);
+        int n = list_rows(idx, cur, list);
+        if (by_row) n = min(n, from + 16);
         const T* w = static_cast<const T*>(a.w[mat].w) + cur * a.w[mat].stack;
         const int64_t wrow = a.w[mat].row;
         const char* wbase = reinterpret_cast<const char*>(w + (COLUMNS ? r0 : r0 * wrow));
@@ -145,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, 3) adapter_low_kernel(LowArgs a, int
 #pragma unroll
         for (int j = 0; j < RT; ++j) wo[j] = ((uint32_t)min(16 * j + i16, a.R - 1 - r0) * (uint32_t)wrow + 8 * q) * 2;
         if constexpr (COLUMNS) wo[0] = ((uint32_t)(8 * q) * (uint32_t)wrow + RT * i16) * 2;
-        for (int g = 0; g < n; g += 16 * TM) {
+        for (int g = from; g < n; g += 16 * TM) {
         uint32_t vo[TM];  // places past the last row take the last row along
 #pragma unroll
         for (int t = 0; t < TM; ++t) vo[t] = ((uint32_t)list[min(g + 16 * t + i16, n - 1)] * (uint32_t)a.ldv + 8 * q) * 2;
@@ -639,71 +640,71 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_out_kernel(OutArgs a, int
             if (nb + kWaves < nb_end) block(nb + kWaves, 1);
         }
     };
-    auto bare = [&]() __attribute__((always_inline)) {
-        const int n = list_rows(idx, -1, list);
-        for (int g = 0; g < n; g += ROWS) pass(-1, g, n, Part{});
-    };
     bool again = false;
-    auto rows_of = [&](int cur) __attribute__((always_inline)) {
-        const int n = list_rows(idx, cur, list);
-        for (int g = 0; g < n; g += ROWS) {
-            if (again) __syncthreads();  // z of the rows before is read
-            again = true;
-            pass(cur, g, n, Whole{});
+    // rows from .. to - 1 of those with this adapter, or without one
+    auto rows_of = [&](int cur, int from, int to) __attribute__((always_inline)) {
+        const int n = min(list_rows(idx, cur, list), to);
+        for (int g = from; g < n; g += ROWS) {
+            if (cur < 0) {
+                pass(-1, g, n, Part{});
+            } else {
+                if (again) __syncthreads();  // z of the rows before is read
+                again = true;
+                pass(cur, g, n, Whole{});
+            }
         }
     };
     if constexpr (TM == 1) {
         if (by_row) {
-            int cur;
-            if (!leads(idx, blockIdx.y, cur)) return;
-            if (cur < 0) bare();
-            else rows_of(cur);
+            int cur, from;
+            if (leads(idx, blockIdx.y, cur, from)) rows_of(cur, from, from + 16);
             return;
         }
     }
-    bare();
+    rows_of(-1, 0, 64);
     for (;;) {
         const int cur = next_adapter(left);
         if (cur < 0) break;
         if (left == cur) left = -1;
-        rows_of(cur);
+        rows_of(cur, 0, 64);
     }
 }
 
 constexpr int kTargetWaves = 2048;
 constexpr int64_t kMaxBlocks = 1 << 22;  // workgroups of 256 threads in a launch's first dimension
 
-// How a batch's rows are cut.  A batch of up to kFew rows, fewer than 16 per adapter there is, is taken to mix requests: in
-// tiles of 64 rows each row has workgroups of its own (the launch's `slots`), of which those of an adapter's first row take
-// all of its rows, 16 at a time, and read its weights once for them.  (Going through a tile's adapters to find the
-// workgroup's own took 3 us at 32 of them.)  Otherwise the rows are taken to be runs of one adapter, and a tile is what a
-// workgroup takes at a time: 16 rows of up to kFew, so that there are workgroups enough, with slots too, so that none has
-// two runs' rows, else 64 or 32.  64 rows of 16
-// adapters (GLU, K = 2560 N = 9216, rank 32): second product 18.2 us with tiles of 16, 11.9 with 64; 203 rows of 2
-// (backward, 2560 x 2560): 4.2 and 16.5 us.
-constexpr int kFew = 256;
+// How a batch's rows are cut.  A batch of up to kMost rows, fewer than 16 per adapter there is, is taken to mix requests: in
+// tiles of 64 rows each row has workgroups of its own (the launch's `slots`), of which every 16th of an adapter's rows takes
+// 16 of them, so that its weights are read once for these.  (Going through a tile's adapters to find the workgroup's own took
+// 3 us at 32 of them.)  Otherwise the rows are taken to be runs of one adapter, and a tile is what a workgroup takes at a
+// time: 16 rows of up to kFew, so that there are workgroups enough, with slots too, so that none has two runs' rows, else 64
+// or 32, whose adapters it goes through.  64 rows of 16 adapters (GLU, K = 2560 N = 9216, rank 32): second product 18.2
+// us with tiles of 16, 11.9 with 64; 512 rows of 512 adapters, 4096 x 4096: both products 372 us as runs, 38 as a mixture.
+constexpr int kFew = 256, kMost = 1024;
 struct Cut {
     int rows, slots;       // of a tile
     int64_t tiles, units;  // units: expected adapters of all tiles
 };
+bool is_mixed(int M, int L) { return M <= kMost && M < 16 * (int64_t)L; }
+bool few(int M, int L) { return M <= kFew || is_mixed(M, L); }
 Cut cut(int M, int L, int tm)
 {
-    const bool mixed = M <= kFew && M < 16 * (int64_t)L;
+    const bool mixed = is_mixed(M, L);
     Cut c;
     c.rows = tm > 1 ? 16 * tm : mixed ? 64 : 16;
     c.tiles = ((int64_t)M + c.rows - 1) / c.rows;
-    c.slots = M > kFew ? 1 : M < c.rows ? M : c.rows;
+    c.slots = tm > 1 || !few(M, L) ? 1 : M < c.rows ? M : c.rows;
     c.units = !mixed ? c.tiles : c.tiles * L < M ? c.tiles * L : M;
     return c;
 }
 
-// Tiles of the first product: 16 TM rows and 16 RT ranks.  Up to kFew rows one instruction's, so that there are more of
+// Tiles of the first product: 16 TM rows and 16 RT ranks.  Few rows, or a mixture: one instruction's, so that there are more of
 // them; else as many as registers hold with a stage in flight.  64 x 64 (from LDS) and 32 x 64, us: 16384 rows of 4096 34.7
 // and 40.2, 8192 of 5120 25.2 and 27.0, 5000 of 4096 23.6 and 23.4, 2050 of 4096 18.0 and 15.3.
 struct LowTile { int tm, rt; };
-LowTile low_tile(int M, int R, bool columns)
+LowTile low_tile(int M, int R, int L, bool columns)
 {
-    if (M <= kFew || columns) return {1, 1};
+    if (few(M, L) || columns) return {1, 1};
     return R <= 16 ? LowTile{4, 1} : R <= 32 ? LowTile{4, 2} : M > 4096 ? LowTile{4, 4} : LowTile{2, 4};
 }
 
@@ -746,7 +747,7 @@ hipError_t low_direct(const LowArgs& a, hipStream_t stream)
 template <class T, bool COLUMNS>
 hipError_t low_launch(const LowArgs& a, hipStream_t stream)
 {
-    const LowTile t = low_tile(a.M, a.R, COLUMNS);
+    const LowTile t = low_tile(a.M, a.R, a.L, COLUMNS);
     if (COLUMNS || t.tm == 1) low_tiles<T, 1, 1, 2, COLUMNS>(a, stream);
     else if (aligned(a) && t.rt == 1) return low_direct<T, 4, 1>(a, stream);
     else if (aligned(a) && t.rt == 2) return low_direct<T, 4, 2>(a, stream);
@@ -785,7 +786,7 @@ hipError_t out_launch(const OutArgs& a, hipStream_t stream)
 {
     if (a.R > 64) {
         out_tiles<T, 1, NM, 0, COLUMNS>(a, stream);
-    } else if (a.M <= kFew) {
+    } else if (few(a.M, a.L)) {
         if (a.R <= 16) out_tiles<T, 1, NM, 1, COLUMNS>(a, stream);
         else if (a.R <= 32) out_tiles<T, 1, NM, 2, COLUMNS>(a, stream);
         else out_tiles<T, 1, NM, 4, COLUMNS>(a, stream);
@@ -806,7 +807,7 @@ hipError_t out_launch(const OutArgs& a, hipStream_t stream)
 // and 25.4 us; 64 ranks 25.2, 32.6 and 41.4).
 int adapter_low_splits(int M, int C, int R, int L, int mats, bool columns)
 {
-    const LowTile t = low_tile(M, R, columns);
+    const LowTile t = low_tile(M, R, L, columns);
     const int64_t groups = cut(M, L, t.tm).units * mats * ((R + 16 * t.rt - 1) / (16 * t.rt));
     const int64_t most = ((int64_t)C + kStage * kWaves - 1) / (kStage * kWaves), cap = t.tm == 1 ? 4 : 16;
     int64_t s = groups ? (t.tm == 1 ? 768 : 256) / groups : 1;

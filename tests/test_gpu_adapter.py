@@ -17,7 +17,9 @@ T = {"bf16": torch.bfloat16, "fp16": torch.float16}
 SHAPES = [(1, 64, 64, 8, 1), (1, 2560, 9216, 16, 8), (2, 4100, 300, 4, 3), (3, 7, 9, 1, 2), (16, 128, 256, 16, 16),
           (17, 100, 75, 5, 3), (33, 130, 257, 17, 40), (64, 512, 520, 32, 16), (100, 1030, 1027, 24, 9),
           (256, 256, 192, 64, 31), (257, 64, 64, 64, 2), (300, 520, 333, 33, 5), (1000, 1030, 900, 48, 7),
-          (40, 96, 100, 100, 6), (270, 200, 130, 256, 3), (5, 300, 70, 256, 2), (2050, 256, 260, 16, 3)]
+          (40, 96, 100, 100, 6), (270, 200, 130, 256, 3), (5, 300, 70, 256, 2), (2050, 256, 260, 16, 3),
+          # mixtures of more rows, ranks past a tile's among them, and rows past the largest mixture, an adapter for each
+          (520, 192, 130, 20, 40), (1024, 72, 200, 8, 300), (600, 64, 68, 72, 50), (1100, 64, 70, 16, 1100)]
 
 
 def rand(g, *shape):
@@ -125,6 +127,19 @@ def test_views(M):
     assert torch.equal(g, glu.adapter_glu(spaced(y), y, vx, va, vb, a, b, index, scale))
     u = y.clone()
     assert torch.equal(g, glu.adapter_glu(y, u, x, a, b, a, b, index, scale, out=u))
+
+
+@pytest.mark.parametrize("M", [64, 65, 300, 1024])
+def test_one_adapter_of_many_held(M):
+    """A run of rows that the sizes alone do not tell from a mixture, and rows without an adapter in between."""
+    (y,), x, ((a, b),), index, scale = operands(M, 128, 200, 16, 100, torch.bfloat16, "mixed", 6)
+    index.fill_(71)
+    index[5:40] = -1
+    want, bound = ref.add64(y, x, a, b, index, scale)
+    out, low = glu.adapter_add(y, x, a, b, index, scale, return_low=True)
+    torch.cuda.synchronize()
+    check_store("out", out, want, bound)
+    check_store("low", low, *ref.low64(x, a, index))
 
 
 def test_no_scale_is_one():
