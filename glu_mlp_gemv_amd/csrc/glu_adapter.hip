@@ -4,13 +4,15 @@
 //
 // and the same two products of the backward, d = dout b and dx = scale d a, whose weights lie the other way round.
 //
-// Bound by memory: x, y and out are touched once and the products are 2 R operations per number of them.  Rows of
-// one adapter need not lie together: a tile of 16 or 64 neighbouring rows finds the distinct adapters among its
-// own rows and goes through them one after another (a prefill: one or two), or, where a batch mixes requests, in
+// Bound by memory, and for a few rows by two launches: x, y and out are touched once, and the products are 2 R operations per
+// number of them.  Rows of one adapter need not lie together: a tile of neighbouring rows finds the distinct adapters
+// among its own rows and goes through them one after another (a prefill: one or two), or, where a batch mixes requests, in
 // workgroups of their own.  So no call sorts anything, and an adapter's weights are read once per tile that has it.
-// In every product the rows of w are the matrix instruction's rows and the batch's rows its columns: a lane then
-// holds neighbouring numbers of one row of the result, and a row's own adapter is a lane's own condition.  Rows
-// of other adapters are left out of the loads and stores, not multiplied by zero.
+// In every product the rows of w are the matrix instruction's rows and the batch's rows its columns, gathered from the
+// tile: rows of other adapters are left out, not multiplied by zero.  Kernel times: one row, K = 2560 N = 9216 rank 16,
+// 3.6 + 4.9 us (an empty launch: 2.3); 37 rows of 32 adapters, K = 4096 N = 12288 rank 16, 5.0 + 7.6; 8192 rows, K = N =
+// 5120 rank 64, 25 + 48 (84 MB read, 168 MB read and written: 3.3 and 3.5 TB/s); pair, 2050 rows, K = 4096 N = 12288
+// rank 16, 13 + 50.
 #include "../../include/glu_fp8.h"
 #include "glu_adapter.h"
 #include "glu_mat16.h"
@@ -248,11 +250,11 @@ __global__ void __launch_bounds__(kThreads, 3) adapter_low_kernel(LowArgs a, int
     }
 }
 
-// The same for larger batches on whole 16-byte chunks.  In the kernel above neighbouring lanes load from different rows,
-// and the address unit takes 64 cycles for such a load of 1 KB: 16 bytes a cycle and CU, less than memory gives once
-// w's loads are counted too.  Here a load takes 8 rows' 128-byte lines, straight to LDS, where a wave has two
-// stages of its own, and the operands are read from there; no barrier is needed before the waves join.  Chunk c of row r
-// is in place c ^ (r / 2) of the row, so that 16 rows' chunks lie in different banks.
+// The same for larger batches on whole 16-byte chunks.  In the kernel above neighbouring lanes load from different rows;
+// here a load takes 8 rows' 128-byte lines, straight to LDS, where a wave has two stages of its own, and the operands are
+// read from there; no barrier is needed before the waves join.  With a workgroup per CU (8192 rows of 5120): 16 ranks
+// 18.3 us against 21.0, 64 ranks 25.2 against 36.8.  Chunk c of row r is in place c ^ (r / 2) of the row, so that 16 rows'
+// chunks lie in different banks.
 template <class T, int TM, int RT>
 __global__ void __launch_bounds__(kThreads) adapter_low_tile_kernel(LowArgs a, int rgroups, int tile0)
 {
@@ -386,12 +388,13 @@ __global__ void __launch_bounds__(kThreads) adapter_low_tile_kernel(LowArgs a, i
     }
 }
 
-// Second product.  Tile: up to 64 rows, of which those of one adapter are taken 16 TM at a time: their z, which the workgroup
-// puts into LDS as two numbers of T each, and runs of 64 columns for each of its waves, whose y and w are on their way meanwhile.  The contraction is RP = ranks rounded up places
-// of the first numbers and then RP of the second, so that up to 16 ranks (S = 1) they share one instruction's 32 places; S
-// instructions with H operands of w per 16 columns, or (S = 0) as many as there are ranks.  The results,
-// of which a lane holds 4 columns of its own row, go through LDS to lanes that hold 8 columns, 8 neighbouring lanes a line:
-// so y is read and out written.
+// Second product.  Tile: up to 64 rows, of which those of one adapter are taken 16 TM at a time: their z, which the
+// workgroup puts into LDS as two numbers of T each, and runs of 64 columns for each of its waves, whose y and w are on their
+// way meanwhile.  The contraction is RP = ranks rounded up places of the first numbers and then RP of the second, so that up
+// to 16 ranks (S = 1) they share one instruction's 32 places; S instructions with H operands of w per 16 columns, or
+// (S = 0) as many as there are ranks.  The results, of which a lane holds 4 columns of its own row, go through LDS to lanes
+// that hold 8 columns, 8 neighbouring lanes a line: so y is read and out written (8192 x 5120, rank 64: 58 us with each
+// lane's own row, 51 so; rank 16 42 and 37).
 template <class T, int TM, int NM, int S, bool COLUMNS>
 __global__ void __launch_bounds__(kThreads, 2) adapter_out_kernel(OutArgs a, int tile_rows, bool by_row, int cblocks,
                                                                   int per, int tile0)
@@ -679,7 +682,7 @@ constexpr int64_t kMaxBlocks = 1 << 22;  // workgroups of 256 threads in a launc
 // 3 us at 32 of them.)  Otherwise the rows are taken to be runs of one adapter, and a tile is what a workgroup takes at a
 // time: 16 rows of up to kFew, so that there are workgroups enough, with slots too, so that none has two runs' rows, else 64
 // or 32, whose adapters it goes through.  64 rows of 16 adapters (GLU, K = 2560 N = 9216, rank 32): second product 18.2
-// us with tiles of 16, 11.9 with 64; 512 rows of 512 adapters, 4096 x 4096: both products 372 us as runs, 38 as a mixture.
+// us with tiles of 16, 11.9 with 64; 512 rows of 512 adapters, 4096 x 4096: both products 372 us as runs, 42 as a mixture.
 constexpr int kFew = 256, kMost = 1024;
 struct Cut {
     int rows, slots;       // of a tile

@@ -144,11 +144,12 @@ glu_status apply(int mats, const void* const* y, const int64_t* ldy, const void*
     return launched(glu::adapter_out_launch(dtype, false, oa, (hipStream_t)stream));
 }
 
-// The backward's workspace: d in its parts, the rows' order, the items, b turned, the items' sums.
+// The backward's workspace: d in its parts and, where there are several, their sum, the rows' order, the items, b turned, the
+// items' sums.
 struct GradPlan {
     bool direct;
     int splits, rows;
-    int64_t items, order, table, turned, pitch, part, bytes;  // offsets; turned: rows of `pitch`
+    int64_t items, sum, order, table, turned, pitch, part, bytes;  // offsets; turned: rows of `pitch`
 };
 GradPlan grad_plan(const glu_adapter_sizes& s)
 {
@@ -156,7 +157,8 @@ GradPlan grad_plan(const glu_adapter_sizes& s)
     p.rows = glu::adapter_grad_rows((int)s.M, s.K + s.N);
     p.direct = glu::adapter_grad_direct((int)s.M, p.rows);
     p.splits = low_splits(1, s, s.N, p.direct);
-    p.order = align16(p.splits * s.M * s.R * 4);
+    p.sum = align16(p.splits * s.M * s.R * 4);
+    p.order = p.sum + (p.splits > 1 ? align16(s.M * s.R * 4) : 0);
     p.bytes = p.order;
     if (!p.direct) {
         p.items = glu::adapter_grad_items((int)s.M, (int)s.L, p.rows);
@@ -251,7 +253,9 @@ glu_status glu_adapter_backward(const void* dout, int64_t ldd, const void* x, in
     float* d = (float*)ws;
     const hipStream_t hs = (hipStream_t)stream;
     glu::GradArgs g{};
-    g.side[0] = {x, d, s.K > 0 ? da : nullptr, ldx, (int)s.K, p.splits, false};
+    // the second product adds d's parts up and leaves the sum for the gradient
+    float* const sum = p.splits > 1 && dx && s.K > 0 ? (float*)(ws + p.sum) : nullptr;
+    g.side[0] = {x, sum ? sum : d, s.K > 0 ? da : nullptr, ldx, (int)s.K, sum ? 1 : p.splits, false};
     g.side[1] = {dout, low, s.N > 0 ? db : nullptr, ldd, (int)s.N, 1, true};
     g.index = index;
     g.scale = scale;
@@ -292,6 +296,7 @@ glu_status glu_adapter_backward(const void* dout, int64_t ldd, const void* x, in
         oa.scale = scale;
         oa.out = dx;
         oa.ldo = lddx;
+        oa.low = da ? sum : nullptr;
         oa.M = (int)s.M;
         oa.N = (int)s.K;
         oa.R = (int)s.R;

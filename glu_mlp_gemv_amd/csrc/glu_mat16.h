@@ -43,6 +43,15 @@ __device__ __forceinline__ raw4_t load8(const T* p, int n)
     return v;
 }
 
+// the largest of the wave's numbers, in every lane
+__device__ __forceinline__ uint32_t wave_max(uint32_t x)
+{
+    x = max16(x);
+    x = max(x, (uint32_t)__builtin_amdgcn_ds_swizzle((int)x, 0x401F));  // lane ^ 16
+    auto pr = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+    return max(pr[0], pr[1]);
+}
+
 // A number of 32 bits as two of 16: its rounding and the rounding of what that left (nothing where it is not finite,
 // which would be inf - inf).
 template <class T>

@@ -9,7 +9,9 @@
 // rows of every active expert's down to a workgroup whose waves take experts in turn, and each wave adds what its experts
 // give to rows of its own in LDS, which are summed in wave order at the end.
 // The weights go from memory straight into matrix instructions as their 16 rows; the columns are rows of x, of
-// which an expert of a small batch has one or two: the matrix unit has more than ten times the rate needed.
+// which an expert of a small batch has one or two: the matrix unit has more than ten times the rate needed.  37 rows, K =
+// 4096 N = 768, 8 of 128 experts, bf16: 9 + 244 + 131 us, 6.0 and 5.6 TB/s; 6 rows, N = 1536, e4m3: 6 + 102 + 55 us, 5.1 and
+// 4.7 TB/s; one row, K = 2560 N = 1024, 8 of 64: 20 + 11 us, 4.2 and 3.8 TB/s with a launch's ramp.
 #include "../../include/glu_fp8.h"
 #include "glu_mat16.h"
 #include "glu_moe.h"
@@ -38,15 +40,6 @@ __device__ __forceinline__ uint32_t order_of(float f)
 __device__ __forceinline__ float logit_of(uint32_t order)
 {
     return __uint_as_float(order ^ (order >> 31 ? 0x80000000u : 0xffffffffu));
-}
-
-// the largest of the wave's numbers, in every lane
-__device__ __forceinline__ uint32_t wave_max(uint32_t x)
-{
-    x = max16(x);
-    x = max(x, (uint32_t)__builtin_amdgcn_ds_swizzle((int)x, 0x401F));  // lane ^ 16
-    auto pr = __builtin_amdgcn_permlane32_swap(x, x, false, false);
-    return max(pr[0], pr[1]);
 }
 
 // What a workgroup of THREADS knows of the rows' experts, in LDS
