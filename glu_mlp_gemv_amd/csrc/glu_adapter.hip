@@ -751,14 +751,14 @@ template <class T, bool COLUMNS>
 hipError_t low_launch(const LowArgs& a, hipStream_t stream)
 {
     const LowTile t = low_tile(a.M, a.R, a.L, COLUMNS);
-    if (COLUMNS || t.tm == 1) low_tiles<T, 1, 1, 2, COLUMNS>(a, stream);
+    if (COLUMNS || t.tm == 1) low_tiles<T, 1, 1, COLUMNS ? 1 : 2, COLUMNS>(a, stream);
     else if (aligned(a) && t.rt == 1) return low_direct<T, 4, 1>(a, stream);
     else if (aligned(a) && t.rt == 2) return low_direct<T, 4, 2>(a, stream);
     else if (aligned(a) && t.tm == 4) return low_direct<T, 4, 4>(a, stream);
     else if (aligned(a)) return low_direct<T, 2, 4>(a, stream);
     else if (t.rt == 1) low_tiles<T, 4, 1, 2, false>(a, stream);
     else if (t.rt == 2) low_tiles<T, 4, 2, 2, false>(a, stream);
-    else low_tiles<T, 2, 4, 2, false>(a, stream);
+    else low_tiles<T, 2, 4, 1, false>(a, stream);
     return hipGetLastError();
 }
 
