@@ -199,6 +199,36 @@ def test_empty(M, N):
     assert dx.shape == (M, 64) and not dx.any() and not da.any() and not db.any() and db.shape == (3, N, 8)
 
 
+@pytest.mark.parametrize("K,N", [(0, 96), (96, 0)])
+def test_backward_of_empty_products(K, N):
+    """One width empty, with more rows than one item."""
+    M, R, L = 600, 8, 3
+    g = torch.Generator(device=DEV).manual_seed(1)
+    t = torch.bfloat16
+    dout, x = rand(g, M, N).to(t), rand(g, M, K).to(t)
+    a, b, low = rand(g, L, R, K).to(t), rand(g, L, N, R).to(t), rand(g, M, R)
+    index = index_of(g, M, L, "mixed")
+    dx, da, db = glu.adapter_backward(dout, x, a, b, index, low)
+    torch.cuda.synchronize()
+    for name, v, (w, bound) in zip(("dx", "da", "db"), (dx, da, db), ref.backward64(dout, x, a, b, index, low, None)):
+        check_store(name, v, w, bound)
+
+
+@pytest.mark.parametrize("M,L", [(600, 3), (300, 100)])
+def test_far_rows(M, L):
+    """Rows 2^23 elements apart: offsets past 32 bits in x, y and out, with the largest row stride."""
+    K, N, R, t = 128, 96, 16, torch.bfloat16
+    (y,), x, ((a, b),), index, scale = operands(M, K, N, R, L, t, "mixed", 8)
+    far = torch.empty(M, 1 << 23, dtype=t, device=DEV)
+    vx, vy, out = far[:, :K], far[:, 1000:1000 + N], torch.empty_like(far)[:, :N]  # an output's span may hold no input
+    vx.copy_(x)
+    vy.copy_(y)
+    want, low = glu.adapter_add(y, x, a, b, index, scale, return_low=True)
+    assert torch.equal(glu.adapter_add(vy, vx, a, b, index, scale, out=out), want)
+    for p, q in zip(glu.adapter_backward(vy, vx, a, b, index, low, scale), glu.adapter_backward(y, x, a, b, index, low, scale)):
+        assert torch.equal(p, q)
+
+
 def test_no_columns_of_x():
     y = torch.randn(5, 64, device=DEV).bfloat16()
     x, a, b = y[:, :0], torch.empty(2, 4, 0, dtype=y.dtype, device=DEV), torch.ones(2, 64, 4, dtype=y.dtype, device=DEV)

@@ -69,6 +69,17 @@ def test_dropped_specials_do_not_show():
     assert out.isfinite().all() and torch.equal(out[gone], r[gone])
 
 
+def test_far_rows():
+    x, r = tensors(3, 100, torch.bfloat16, 4)
+    far = torch.empty((1 << 32) + 1000, dtype=torch.bfloat16, device=DEV)
+    vx, vr, out = (f.as_strided((3, 100), (1 << 31, 1)) for f in (far, far[200:], torch.empty_like(far)))
+    vx.copy_(x)
+    vr.copy_(r)
+    glu.dropout(vx, 0.3, 5, residual=vr, out=out)
+    torch.cuda.synchronize()
+    assert torch.equal(out, ref.dropout32(x, 0.3, 5, 0, r))
+
+
 def test_empty():
     for shape in ((0, 8), (8, 0)):
         x = torch.empty(shape, device=DEV)

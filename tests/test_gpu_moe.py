@@ -128,6 +128,21 @@ def test_views():
     assert torch.equal(out, want) and (into[:, :3] == 3).all() and (into[:, K + 3:] == 3).all()
 
 
+def test_far_experts():
+    """Experts 2^31 elements apart and more."""
+    M, K, N, E, top = 5, 64, 48, 3, 2
+    x, logits, gate, up, down = layer(M, K, N, E, top, torch.bfloat16, 2)
+    far = torch.empty((1 << 32) + (1 << 20), dtype=torch.bfloat16, device=DEV)
+    views = []
+    for i, w in enumerate((gate, up, down)):
+        v = far[i * 100000:].as_strided(w.shape, ((1 << 31) + 8, w.shape[2], 1))
+        v.copy_(w)
+        views.append(v)
+    out = glu.moe_glu(x, logits, *views, top)
+    torch.cuda.synchronize()
+    assert torch.equal(out, glu.moe_glu(x, logits, gate, up, down, top))
+
+
 @pytest.mark.parametrize("M,K,N", [(0, 64, 64), (3, 64, 0), (3, 0, 64)])
 def test_empty(M, K, N):
     x, logits, gate, up, down = layer(M, K or 1, N or 1, 4, 2, torch.bfloat16, 1)
