@@ -149,102 +149,102 @@ __global__ void __launch_bounds__(kThreads, 3) adapter_low_kernel(LowArgs a, int
         for (int j = 0; j < RT; ++j) wo[j] = ((uint32_t)min(16 * j + i16, a.R - 1 - r0) * (uint32_t)wrow + 8 * q) * 2;
         if constexpr (COLUMNS) wo[0] = ((uint32_t)(8 * q) * (uint32_t)wrow + RT * i16) * 2;
         for (int g = from; g < n; g += 16 * TM) {
-        uint32_t vo[TM];  // places past the last row take the last row along
+            uint32_t vo[TM];  // places past the last row take the last row along
 #pragma unroll
-        for (int t = 0; t < TM; ++t) vo[t] = ((uint32_t)list[min(g + 16 * t + i16, n - 1)] * (uint32_t)a.ldv + 8 * q) * 2;
-        f32x4 acc[TM][RT];
+            for (int t = 0; t < TM; ++t) vo[t] = ((uint32_t)list[min(g + 16 * t + i16, n - 1)] * (uint32_t)a.ldv + 8 * q) * 2;
+            f32x4 acc[TM][RT];
 #pragma unroll
-        for (int t = 0; t < TM; ++t) {
+            for (int t = 0; t < TM; ++t) {
 #pragma unroll
-            for (int j = 0; j < RT; ++j) acc[t][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        }
-        raw4_t vf[U][2][TM], wf[U][2][RT];
-        auto load = [&](int u, int s) __attribute__((always_inline)) {
-            const int at = (first + s) * kStage;
-            const char* vb = vbase + at * 2;
-            const char* wb = wbase + (COLUMNS ? at * wrow : (int64_t)at) * 2;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                for (int t = 0; t < TM; ++t) vf[u][h][t] = read16(vb + 64 * h, vo[t]);
-                if constexpr (COLUMNS) {
-                    load_columns<T, RT>([&](int i) { return wb + (32 * h + i) * wrow * 2 + wo[0]; }, a.R - r0 - RT * i16, wf[u][h]);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < RT; ++j) wf[u][h][j] = read16(wb + 64 * h, wo[j]);
-                }
+                for (int j = 0; j < RT; ++j) acc[t][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
             }
-        };
-        auto load_tail = [&](int u) __attribute__((always_inline)) {
-            const int at = tail * kStage;
+            raw4_t vf[U][2][TM], wf[U][2][RT];
+            auto load = [&](int u, int s) __attribute__((always_inline)) {
+                const int at = (first + s) * kStage;
+                const char* vb = vbase + at * 2;
+                const char* wb = wbase + (COLUMNS ? at * wrow : (int64_t)at) * 2;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int c = at + 32 * h + 8 * q;  // this lane's first column
+                for (int h = 0; h < 2; ++h) {
 #pragma unroll
-                for (int t = 0; t < TM; ++t) vf[u][h][t] = load8(reinterpret_cast<const T*>(vbase + vo[t]) + at + 32 * h, a.C - c);
-                if constexpr (COLUMNS) {
-                    load_columns<T, RT>([&](int i) { return w + min(c + i, a.C - 1) * wrow + r0 + RT * i16; },
-                                        a.R - r0 - RT * i16, wf[u][h]);
+                    for (int t = 0; t < TM; ++t) vf[u][h][t] = read16(vb + 64 * h, vo[t]);
+                    if constexpr (COLUMNS) {
+                        load_columns<T, RT>([&](int i) { return wb + (32 * h + i) * wrow * 2 + wo[0]; }, a.R - r0 - RT * i16, wf[u][h]);
+                    } else {
 #pragma unroll
-                    for (int j = 0; j < RT; ++j) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) wf[u][h][j][e] &= first_rows_mask(e, a.C - c);
+                        for (int j = 0; j < RT; ++j) wf[u][h][j] = read16(wb + 64 * h, wo[j]);
                     }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < RT; ++j) wf[u][h][j] = load8(reinterpret_cast<const T*>(wbase + wo[j]) + at + 32 * h, a.C - c);
                 }
-            }
-        };
-        auto use = [&](int u) __attribute__((always_inline)) {
+            };
+            auto load_tail = [&](int u) __attribute__((always_inline)) {
+                const int at = tail * kStage;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+                for (int h = 0; h < 2; ++h) {
+                    const int c = at + 32 * h + 8 * q;  // this lane's first column
 #pragma unroll
-                for (int t = 0; t < TM; ++t) {
+                    for (int t = 0; t < TM; ++t) vf[u][h][t] = load8(reinterpret_cast<const T*>(vbase + vo[t]) + at + 32 * h, a.C - c);
+                    if constexpr (COLUMNS) {
+                        load_columns<T, RT>([&](int i) { return w + min(c + i, a.C - 1) * wrow + r0 + RT * i16; },
+                                            a.R - r0 - RT * i16, wf[u][h]);
 #pragma unroll
-                    for (int j = 0; j < RT; ++j) acc[t][j] = mfma16<T>(wf[u][h][j], vf[u][h][t], acc[t][j]);
+                        for (int j = 0; j < RT; ++j) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) wf[u][h][j][e] &= first_rows_mask(e, a.C - c);
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < RT; ++j) wf[u][h][j] = load8(reinterpret_cast<const T*>(wbase + wo[j]) + at + 32 * h, a.C - c);
+                    }
                 }
-            }
-        };
-        // a ring of U stages: one is refilled as soon as it is used
-        int s = wave;
+            };
+            auto use = [&](int u) __attribute__((always_inline)) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (s + u * kWaves < count) load(u, s + u * kWaves);
-        }
-        for (; s + (2 * U - 1) * kWaves < count; s += U * kWaves) {
+                for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                    for (int t = 0; t < TM; ++t) {
+#pragma unroll
+                        for (int j = 0; j < RT; ++j) acc[t][j] = mfma16<T>(wf[u][h][j], vf[u][h][t], acc[t][j]);
+                    }
+                }
+            };
+            // a ring of U stages: one is refilled as soon as it is used
+            int s = wave;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                use(u);
-                load(u, s + (u + U) * kWaves);
+                if (s + u * kWaves < count) load(u, s + u * kWaves);
             }
-        }
-        for (; s < count; s += U * kWaves) {
+            for (; s + (2 * U - 1) * kWaves < count; s += U * kWaves) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (s + u * kWaves < count) use(u);
-                if (s + (u + U) * kWaves < count) load(u, s + (u + U) * kWaves);
+                for (int u = 0; u < U; ++u) {
+                    use(u);
+                    load(u, s + (u + U) * kWaves);
+                }
             }
-        }
-        if (tail >= 0 && wave == kWaves - 1) {
-            load_tail(0);
-            use(0);
-        }
+            for (; s < count; s += U * kWaves) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (s + u * kWaves < count) use(u);
+                    if (s + (u + U) * kWaves < count) load(u, s + (u + U) * kWaves);
+                }
+            }
+            if (tail >= 0 && wave == kWaves - 1) {
+                load_tail(0);
+                use(0);
+            }
 
 #pragma unroll
-        for (int p = 0; p < PIECES; ++p) *reinterpret_cast<f32x4*>(&red[wave][p][4 * lane]) = acc[p / RT][p % RT];
-        __syncthreads();
-        for (int i = threadIdx.x; i < PIECES * 256; i += kThreads) {
-            const int l = i >> 2 & 63, piece = i >> 8, t = piece / RT, j = piece % RT;
-            const int at = g + 16 * t + (l & 15), k = 4 * (l >> 4) + (i & 3);
-            const int r = r0 + (COLUMNS ? RT * k + j : 16 * j + k);
-            if (at >= n || r >= a.R) continue;
-            float sum = red[0][piece][i & 255];
+            for (int p = 0; p < PIECES; ++p) *reinterpret_cast<f32x4*>(&red[wave][p][4 * lane]) = acc[p / RT][p % RT];
+            __syncthreads();
+            for (int i = threadIdx.x; i < PIECES * 256; i += kThreads) {
+                const int l = i >> 2 & 63, piece = i >> 8, t = piece / RT, j = piece % RT;
+                const int at = g + 16 * t + (l & 15), k = 4 * (l >> 4) + (i & 3);
+                const int r = r0 + (COLUMNS ? RT * k + j : 16 * j + k);
+                if (at >= n || r >= a.R) continue;
+                float sum = red[0][piece][i & 255];
 #pragma unroll
-            for (int o = 1; o < kWaves; ++o) sum += red[o][piece][i & 255];
-            z[(int64_t)(m0 + list[at]) * a.R + r] = sum;
-        }
-        __syncthreads();
+                for (int o = 1; o < kWaves; ++o) sum += red[o][piece][i & 255];
+                z[(int64_t)(m0 + list[at]) * a.R + r] = sum;
+            }
+            __syncthreads();
         }
         if (by_row) break;
     }
@@ -400,7 +400,8 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_out_kernel(OutArgs a, int
                                                                   int per, int tile0)
 {
     constexpr int ROWS = 16 * TM, H = S > 1 ? S / 2 : 1;
-    extern __shared__ __attribute__((aligned(16))) uint16_t lds[];  // z as T [NM][ROWS][pitch]; powers of two and maxima [NM][ROWS]
+    // z as T [NM][ROWS][pitch]; the rows' powers of two and maxima [NM][ROWS]
+    extern __shared__ __attribute__((aligned(16))) uint16_t lds[];
     __shared__ uint8_t lists[kWaves][64];
     __shared__ __attribute__((aligned(16))) float turned[kWaves][16 * kTurnPitch];
     const int lane = threadIdx.x & 63, i16 = lane & 15, q = lane >> 4;
@@ -419,7 +420,9 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_out_kernel(OutArgs a, int
     const int lr = lane >> 3, lc = 8 * (lane & 7);
     const char* ybase[NM];
 #pragma unroll
-    for (int mat = 0; mat < NM; ++mat) ybase[mat] = a.y[mat] ? reinterpret_cast<const char*>(static_cast<const T*>(a.y[mat]) + m0 * a.ldy[mat]) : nullptr;
+    for (int mat = 0; mat < NM; ++mat) {
+        ybase[mat] = a.y[mat] ? reinterpret_cast<const char*>(static_cast<const T*>(a.y[mat]) + m0 * a.ldy[mat]) : nullptr;
+    }
     char* obase = reinterpret_cast<char*>(static_cast<T*>(a.out) + m0 * a.ldo);
     float* tp = turned[wave];
 
