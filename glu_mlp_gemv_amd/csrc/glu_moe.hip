@@ -240,7 +240,9 @@ __device__ __forceinline__ void products(const uint8_t* const (&w)[NM], const fl
                 raw4_t lo[2], hi[2];
                 widen16<T>(wv[i][0], lo);
                 widen16<T>(wv[i][1], hi);
-                const float scale = sc[i][S == 1 ? s : min(s * S + place, (C - 1) / kGroup)];
+                float scale = sc[i][S == 1 || WHOLE ? s * S + place : min(s * S + place, (C - 1) / kGroup)];
+                // places past the last block hold zeros, and so does the scale: the last one, which was read, may be infinite
+                if (S > 1 && !WHOLE && c - 16 * q >= C) scale = 0.0f;
 #pragma unroll
                 for (int t = 0; t < TT; ++t) {
                     f32x4 p = {0.0f, 0.0f, 0.0f, 0.0f};
