@@ -30,7 +30,7 @@ struct MoeArgs {
     Active* active;        // [E], ascending
     int* row;              // [M top] row of each slot
     float* weight;         // [M top] its weight
-    uint16_t* act;         // [M top][ld_act] activations of T
+    uint16_t* act;         // [M top][2][ld_act] activations, two numbers of T each
     float* part;           // [splits][M][K] sums of the second product's parts, where splits > 1
     int64_t ld_act;
 };

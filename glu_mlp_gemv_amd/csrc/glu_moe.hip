@@ -209,7 +209,7 @@ template <bool E8> constexpr int kStageCols = E8 ? 128 : 64;
 // Stages s0, s0 + step, .. below s1 of NM products of 16 weight rows (this lane's at w[i]) with 16 TT rows of v (this lane's
 // at v[t]), C columns.  sc[i]: the scales of the weight rows' block, one per 128 columns.  With S places along the columns
 // a stage is S times as long, and this lane's rows are at `place` of it.
-template <class T, bool E8, int NM, int TT, int S>
+template <class T, bool E8, int NM, int TT, int S, int UNROLL = 4>
 __device__ __forceinline__ void products(const uint8_t* const (&w)[NM], const float* const (&sc)[NM], const T* const (&v)[TT],
                                          int C, int s0, int s1, int step, int q, int place, f32x4 (&acc)[NM][TT])
 {
@@ -280,14 +280,13 @@ __device__ __forceinline__ void products(const uint8_t* const (&w)[NM], const fl
     };
     const int whole = min(s1, C / (SC * S));
     int s = s0;
-#pragma unroll 4
+#pragma unroll UNROLL
     for (; s < whole; s += step) stage(s, Whole{});
     if (s < s1) stage(s, Part{});
 }
 
-// act[slot][n] = T(silu(gate x) * (up x)) of one active expert, 16 columns n.  Rounded once to T, as the next product's
-// operand: a result is then 1.4 times as far off as by its own rounding alone.  Two numbers of T would end that, but the second
-// product took 168 us instead of 134 (37 rows, K = 4096 N = 768, 128 experts) and 79 instead of 60 (6 rows of e4m3).
+// act[slot][..][n] = silu(gate x) * (up x) of one active expert, 16 columns n, as two numbers of T: rounded once to T a
+// result would be 1.4 times as far off as by its own rounding alone.
 template <class T, bool E8, int TT>
 __device__ __forceinline__ void gate_up(const MoeArgs& a, const int* row, const Active& x, int n0, int t0,
                                         float (*red)[2][TT][256])
@@ -327,7 +326,10 @@ __device__ __forceinline__ void gate_up(const MoeArgs& a, const int* row, const 
             g += red[k][0][t][at];
             u += red[k][1][t][at];
         }
-        a.act[(x.first + s) * a.ld_act + n] = bits16<T>(silu_mul(g, u));
+        uint16_t hi, lo, *to = a.act + (x.first + s) * 2 * a.ld_act + n;
+        split16<T>(silu_mul(g, u), hi, lo);
+        to[0] = hi;
+        to[a.ld_act] = lo;
     }
     __syncthreads();
 }
@@ -369,6 +371,47 @@ __global__ void __launch_bounds__(kUpThreads) moe_routed_up_kernel(MoeArgs a, in
     if (n0 < a.N && j < n) gate_up<T, E8, 1>(a, row, active[j], n0, 0, u.red);
 }
 
+// Adds one active expert's part of the results' ROWS columns from c0 on to the wave's sums, for TT tiles of its slots from t0
+// on.  The two numbers of an activation are two columns of the matrix instruction, whose sums are added: a tile is ROWS / 2
+// slots, which is as many as an expert of a small batch has, and the second numbers cost no instruction and no load.
+// ROWS = 4: see the kernel.
+template <class T, bool E8, int ROWS, int TT>
+__device__ __forceinline__ void down(const MoeArgs& a, const Active& x, int c0, int t0, int s0, int s1, float* mine)
+{
+    constexpr int S = 16 / ROWS, EACH = ROWS / 2, ES = E8 ? 1 : 2;
+    const int lane = threadIdx.x & 63, i16 = lane & 15, q = lane >> 4;
+    const int place = i16 / ROWS, at = i16 % EACH, second = i16 / EACH % 2;
+    const uint8_t* const w[1] = {a.w[2].data + (x.expert * a.w[2].stack + min(c0 + i16 % ROWS, a.K - 1) * a.w[2].ld) * ES};
+    const float* const sc[1] = {E8 ? a.w[2].scale + x.expert * a.w[2].scale_stack + (c0 / kGroup) * a.w[2].scale_ld : nullptr};
+    const T* v[TT];
+    f32x4 acc[1][TT];
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+        const int s = x.first + min(t0 + EACH * t + at, x.count - 1);
+        v[t] = reinterpret_cast<const T*>(a.act) + (s * 2 + second) * a.ld_act;
+        acc[0][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    products<T, E8, 1, TT, S, 4 / TT>(w, sc, v, a.N, s0, s1, 1, q, place, acc);
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {  // lane ^ EACH: a turn of 16 lanes by 8, or of 4 lanes by 2
+            const int other = __builtin_amdgcn_update_dpp(0, __float_as_int(acc[0][t][e]), EACH == 8 ? 0x128 : 0x4E, 0xF, 0xF, false);
+            acc[0][t][e] += __int_as_float(other);
+        }
+        const int slot = t0 + EACH * t + at;
+        // rows 4 q .. + 3 of the instruction: with 4 places, place q
+        if (slot < x.count && !second && (S == 1 || place == q)) {
+            const int m = a.row[x.first + slot];
+            float* to = mine + (S == 1 ? m * 16 + 4 * q : (place * a.M + m) * 4);
+            const float weight = a.weight[x.first + slot];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) to[e] = fmaf(weight, acc[0][t][e], to[e]);
+        }
+    }
+    __builtin_amdgcn_wave_barrier();  // a row's sums pass between the wave's lanes, in LDS order
+}
+
 // out[m][c], ROWS columns c, of the active experts that are this split's.  ROWS = 4, for up to 4 rows of x, takes the same 4
 // weight rows at 4 places along their columns as the 16 rows of an instruction, and x's rows likewise: of the results
 // the blocks on the diagonal are wanted, and there are 4 times the workgroups.
@@ -376,36 +419,36 @@ template <class T, bool E8, int ROWS, int WAVES>
 __global__ void __launch_bounds__(64 * WAVES) moe_down_kernel(MoeArgs a, MoePlan p)
 {
     constexpr int S = 16 / ROWS;     // places
+    constexpr int EACH = ROWS / 2;   // slots per tile
     extern __shared__ float sums[];  // [wave][place][M][ROWS]
-    const int lane = threadIdx.x & 63, i16 = lane & 15, q = lane >> 4;
+    const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int c0 = blockIdx.x * ROWS, split = blockIdx.y, place = i16 / ROWS;
+    const int c0 = blockIdx.x * ROWS, split = blockIdx.y;
     float* mine = sums + wave * a.M * 16;
     for (int i = lane; i < a.M * 16; i += 64) mine[i] = 0.0f;
-    __builtin_amdgcn_wave_barrier();  // a row's sums pass between the wave's lanes, in LDS order
+    __builtin_amdgcn_wave_barrier();
     const int actives = *a.actives;
     const int stages = (a.N + kStageCols<E8> * S - 1) / (kStageCols<E8> * S);
     const int per = (stages + p.parts - 1) / p.parts;
-    constexpr int ES = E8 ? 1 : 2;
     for (int u = wave; ; u += WAVES) {
         const int j = u / p.parts * p.splits + split, part = u % p.parts;
         if (j >= actives) break;
         const Active x = a.active[j];
-        const uint8_t* const w[1] = {a.w[2].data + (x.expert * a.w[2].stack + min(c0 + i16 % ROWS, a.K - 1) * a.w[2].ld) * ES};
-        const float* const sc[1] = {E8 ? a.w[2].scale + x.expert * a.w[2].scale_stack + (c0 / kGroup) * a.w[2].scale_ld : nullptr};
-        for (int t = 0; t < x.count; t += ROWS) {
-            const int s = x.first + min(t + i16 % ROWS, x.count - 1);
-            const T* const v[1] = {reinterpret_cast<const T*>(a.act) + s * a.ld_act};
-            f32x4 acc[1][1] = {{{0.0f, 0.0f, 0.0f, 0.0f}}};
-            products<T, E8, 1, 1, S>(w, sc, v, a.N, part * per, min(stages, (part + 1) * per), 1, q, place, acc);
-            // rows 4 q .. + 3 of the instruction: with 4 places, place q
-            if (t + i16 % ROWS < x.count && (S == 1 || place == q)) {
-                float* to = mine + (S == 1 ? a.row[s] * 16 + 4 * q : (place * a.M + a.row[s]) * 4);
-                const float weight = a.weight[s];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) to[e] = fmaf(weight, acc[0][0][e], to[e]);
+        const int s0 = part * per, s1 = min(stages, (part + 1) * per);
+        // the registers of two tiles cost a workgroup per CU with 4 places (one row, K = 2560 N = 1024 of e4m3: 23.8 us, 21.0
+        // with one), and those of four with e4m3
+        for (int t = 0; t < x.count;) {
+            const int left = x.count - t;
+            if (left <= EACH || ROWS == 4) {
+                down<T, E8, ROWS, 1>(a, x, c0, t, s0, s1, mine);
+                t += EACH;
+            } else if (left <= 2 * EACH || E8) {
+                if constexpr (ROWS == 16) down<T, E8, ROWS, 2>(a, x, c0, t, s0, s1, mine);
+                t += 2 * EACH;
+            } else {
+                if constexpr (ROWS == 16 && !E8) down<T, E8, ROWS, 4>(a, x, c0, t, s0, s1, mine);
+                t += 4 * EACH;
             }
-            __builtin_amdgcn_wave_barrier();
         }
     }
     __syncthreads();

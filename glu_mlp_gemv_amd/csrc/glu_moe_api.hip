@@ -44,7 +44,7 @@ Layout layout(const glu_moe_sizes& s, int rows, bool e4m3)
     l.row = l.active + align16(s.E * (int64_t)sizeof(glu::Active));
     l.weight = l.row + align16(rows * s.top * 4);
     l.act = l.weight + align16(rows * s.top * 4);
-    l.part = l.act + align16(rows * s.top * l.ld_act * 2);
+    l.part = l.act + align16(rows * s.top * l.ld_act * 4);
     l.bytes = l.part + (l.plan.splits > 1 ? align16((int64_t)l.plan.splits * rows * s.K * 4) : 0);
     return l;
 }

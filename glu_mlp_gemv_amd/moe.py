@@ -55,7 +55,8 @@ def moe_glu(x: torch.Tensor, logits: torch.Tensor, gate: torch.Tensor, up: torch
     with one fp32 scale per 128 x 128 block ([E, N / 128, K / 128], [E, K / 128, N / 128], rounded up), as
     ``fp8_quantize_weight`` gives them per expert.  A row's experts are those of its largest logits, of equal ones
     the lowest; p is the softmax over them, or with ``normalize=False`` over all experts.  -inf masks an expert: a row whose
-    logits are all -inf is 0.  Sums are fp32, the activation is rounded once to x's type, the result once.
+    logits are all -inf is 0.  Sums and the activation are fp32 (the second product takes it as two numbers of x's type), the
+    result is rounded once.
 
     Each chosen expert's weights are read once per 64 rows: meant for the tokens of a decode step, right for any number.  At
     most 1024 experts, 32 per row.  Has no gradient: operands that require one are refused where autograd records.

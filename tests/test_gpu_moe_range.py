@@ -1,10 +1,13 @@
-"""moe_glu at the ends of its number formats: infinite scales of e4m3 blocks."""
+"""moe_glu at the ends of its number formats: infinite scales of e4m3 blocks, and what is kept of the activation."""
 import math
 
 import pytest
 import torch
 
 import glu_mlp_gemv_amd as glu
+import moe_ref
+from adapter_ref import LEFT
+from fp8_ref import U, check_store
 
 pytestmark = pytest.mark.gpu
 
@@ -33,3 +36,66 @@ def test_infinite_scale_of_the_last_block(M, blocks, kind):
     torch.cuda.synchronize()
     want = torch.where(torch.arange(K, device=DEV) < K // 2, math.inf, -math.inf).expand(M, K)
     assert torch.equal(out.float(), want)
+
+
+# rows of an expert: one to some past what the second product takes at a time, in either of its forms; odd widths
+ROWS = [(1, 200, 130), (2, 64, 300), (3, 70, 257), (4, 128, 1030), (5, 96, 64), (8, 130, 520), (9, 64, 75), (16, 40, 260),
+        (17, 72, 136), (32, 33, 513), (33, 64, 130), (50, 48, 96), (64, 64, 200), (65, 40, 72)]
+
+
+def wide64(x, logits, gate, up, down, top, scales=(None, None, None)):
+    """out before its rounding, and its bound where the activation goes into the second product as two numbers."""
+    t, K, N = x.dtype, x.shape[1], gate.shape[1]
+    take = moe_ref.chosen(logits, top)
+    p = moe_ref.weights(logits, take, True)
+    x = x.double()
+    out = torch.zeros_like(x)
+    err = out.clone()
+    nk, nn = K / 16 + 40, N / 16 + 40  # chains of fp32 sums, as in moe_ref
+    for e in take.any(0).nonzero()[:, 0].tolist():
+        rows = take[:, e].nonzero()[:, 0]
+        wg, wu, wd = (moe_ref.expert(w, s, e) for w, s in zip((gate, up, down), scales))
+        g, u = x[rows] @ wg.t(), x[rows] @ wu.t()
+        eg, eu = (2 * U * nk * (x[rows].abs() @ w.abs().t()) for w in (wg, wu))
+        a = g * torch.sigmoid(g) * u
+        ea = 1.1 * eg * (u.abs() + eu) + (g * torch.sigmoid(g)).abs() * eu + 8 * U * a.abs()
+        # two roundings of at most half a step each, of bf16 numbers behind e4m3 weights, and of an fp16 number below 2^-14
+        # half of 2^-24
+        ea = ea + LEFT[t if scales[0] is None else torch.bfloat16] * (a.abs() + ea) + (2.0 ** -25 if t is torch.float16 else 0.0)
+        pe = p[rows, e, None]
+        out[rows] += pe * (a @ wd.t())
+        err[rows] += pe * (ea @ wd.abs().t() + 2 * U * nn * (a.abs() @ wd.abs().t()) + 100 * U * (a @ wd.t()).abs())
+    return out, err + 40 * U * out.abs() + (top + 8) * U * err
+
+
+def e4m3_of(w):
+    q, s = zip(*(glu.fp8_quantize_weight(m) for m in w))
+    return torch.stack([m.view(torch.uint8) for m in q]).view(E4M3), torch.stack(s)
+
+
+def layer(M, K, N, E, t, e4m3, seed):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    rand = lambda *s: torch.randn(*s, generator=g, device=DEV)  # noqa: E731
+    x, logits = rand(M, K).to(t), rand(M, E)
+    w = [(rand(E, a, b) * b ** -0.5).to(t) for a, b in ((N, K), (N, K), (K, N))]
+    if not e4m3:
+        return x, logits, w, (None, None, None)
+    w, s = zip(*(e4m3_of(m) for m in w))
+    return x, logits, w, s
+
+
+def run(x, logits, w, s, top):
+    out = glu.moe_glu(x, logits, *w, top, gate_scale=s[0], up_scale=s[1], down_scale=s[2])
+    torch.cuda.synchronize()
+    return out
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("E,top", [(1, 1), (3, 2)])
+@pytest.mark.parametrize("M,K,N", ROWS)
+def test_activation_keeps_its_bits(M, K, N, E, top, e4m3, kind):
+    """The activation is not rounded to x's type between the products."""
+    print(f"[moe bits] {M=} {K=} {N=} {E=} {e4m3=} {kind}", flush=True)
+    x, logits, w, s = layer(M, K, N, E, T[kind], e4m3, M + N)
+    check_store("out", run(x, logits, w, s, top), *wide64(x, logits, *w, top, s))
