@@ -11,6 +11,7 @@ namespace glu {
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x4_t __attribute__((ext_vector_type(4)));
 
 template <class T>
 __device__ __forceinline__ f32x4 mfma16(raw4_t a, raw4_t b, f32x4 c)

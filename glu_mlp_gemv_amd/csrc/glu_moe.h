@@ -30,9 +30,10 @@ struct MoeArgs {
     Active* active;        // [E], ascending
     int* row;              // [M top] row of each slot
     float* weight;         // [M top] its weight
-    uint16_t* act;         // [M top][2][ld_act] activations, two numbers of T each
+    uint16_t* act;         // [M top][2][ld_act] activations, two numbers each
+    float* factor;         // [M top][ld_factor] what 16 columns of them are multiplied with, where they are fp16
     float* part;           // [splits][M][K] sums of the second product's parts, where splits > 1
-    int64_t ld_act;
+    int64_t ld_act, ld_factor;
 };
 
 // How the second product is cut: `splits` sets of workgroups take the active experts in turn, and within a workgroup

@@ -176,6 +176,19 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(MoeArgs a)
 struct Whole { static constexpr bool value = true; };
 struct Part { static constexpr bool value = false; };
 
+// The type of an activation's two numbers.  fp16's range is too small for any fp32 number: behind e4m3 weights, which
+// are numbers of bf16 too, they are bf16; behind fp16 weights they are fp16 times a power of two (kScaled) of 16 columns,
+// whose products are summed apart and multiplied by its reciprocal.
+template <class T, bool E8> struct Act { using type = T; };
+template <> struct Act<Fp16, true> { using type = Bf16; };
+template <class T, bool E8> constexpr bool kScaled = __is_same(T, Fp16) && !E8;
+
+// Those 16 columns are an instruction of 16 places of lanes that read 8 neighbours each: number i of group g (n0 = 16 g)
+__device__ __forceinline__ int scaled_column(int n0, int i) { return (n0 & ~31) + 8 * (i >> 2) + (n0 >> 2 & 4) + (i & 3); }
+// Whether a workgroup has anything to do (a group's factor is written even if its columns are all past N)
+template <class T, bool E8>
+__device__ __forceinline__ bool has_columns(int n0, int N) { return (kScaled<T, E8> ? n0 & ~31 : n0) < N; }
+
 // 16 e4m3 numbers as two operands of T; every one of them is a number of T
 template <class T>
 __device__ __forceinline__ void widen16(raw4_t c, raw4_t (&v)[2])
@@ -206,86 +219,132 @@ __device__ __forceinline__ raw4_t bytes16(const uint8_t* p, int n)
 // contraction per stage: a whole 128-byte line of each weight row
 template <bool E8> constexpr int kStageCols = E8 ? 128 : 64;
 
+// numbers 4 h .. + 3 of eight
+template <int H>
+__device__ __forceinline__ f16x4_t four_of(raw4_t v)
+{
+    return __builtin_bit_cast(f16x4_t, raw2_t{v[2 * H], v[2 * H + 1]});
+}
+
 // Stages s0, s0 + step, .. below s1 of NM products of 16 weight rows (this lane's at w[i]) with 16 TT rows of v (this lane's
 // at v[t]), C columns.  sc[i]: the scales of the weight rows' block, one per 128 columns.  With S places along the columns
-// a stage is S times as long, and this lane's rows are at `place` of it.
-template <class T, bool E8, int NM, int TT, int S, int UNROLL = 4>
+// a stage is S times as long, and this lane's rows are at `place` of it.  SCALED: f[t] are the factors of v[t]'s groups of 16
+// columns, four per stage.  U > 1: so many stages are read ahead.
+template <class T, bool E8, int NM, int TT, int S, int U = 1, bool SCALED = false>
 __device__ __forceinline__ void products(const uint8_t* const (&w)[NM], const float* const (&sc)[NM], const T* const (&v)[TT],
-                                         int C, int s0, int s1, int step, int q, int place, f32x4 (&acc)[NM][TT])
+                                         int C, int s0, int s1, int step, int q, int place, f32x4 (&acc)[NM][TT],
+                                         const float* const (&f)[TT])
 {
-    constexpr int SC = kStageCols<E8>;
-    auto stage = [&](int s, auto tag) __attribute__((always_inline)) {
+    constexpr int SC = kStageCols<E8>, XH = E8 ? 4 : 2;
+    raw4_t wv[U][NM][2], xv[U][TT][XH];
+    f32x4 by[U][TT];
+    auto load = [&](int u, int s, auto tag) __attribute__((always_inline)) {
         constexpr bool WHOLE = decltype(tag)::value;
-        if constexpr (E8) {
-            const int c = (s * S + place) * SC + 16 * q;
-            raw4_t wv[NM][2], xv[TT][4];
+        const int c = (s * S + place) * SC + (E8 ? 16 : 8) * q;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int k = c + (E8 ? 64 : 32) * h;
 #pragma unroll
             for (int i = 0; i < NM; ++i) {
+                const uint8_t* p = w[i] + (E8 ? k : 2 * k);
+                if constexpr (WHOLE) wv[u][i][h] = *reinterpret_cast<const u32x4_any*>(p);
+                else if constexpr (E8) wv[u][i][h] = bytes16(p, C - k);
+                else wv[u][i][h] = load8(reinterpret_cast<const T*>(p), C - k);
+            }
+        }
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint8_t* p = w[i] + c + 64 * h;
-                    wv[i][h] = WHOLE ? *reinterpret_cast<const u32x4_any*>(p) : bytes16(p, C - c - 64 * h);
+        for (int t = 0; t < TT; ++t) {
+#pragma unroll
+            for (int h = 0; h < XH; ++h) {
+                const int k = c + (E8 ? 64 * (h >> 1) + 8 * (h & 1) : 32 * h);
+                xv[u][t][h] = WHOLE ? *reinterpret_cast<const u32x4_any*>(v[t] + k) : load8(v[t] + k, C - k);
+            }
+            if constexpr (SCALED) {
+                by[u][t] = *reinterpret_cast<const f32x4*>(f[t] + 4 * (WHOLE ? s * S + place : min(s * S + place, (C - 1) / SC)));
+                if constexpr (!WHOLE) {  // past the last group operands are zeros and factors are whatever memory holds
+                    const int left = C - (s * S + place) * SC;
+                    const f32x4 b = by[u][t];
+                    by[u][t] = f32x4{left > 0 ? b[0] : 0.0f, left > 0 ? b[1] : 0.0f, left > 32 ? b[2] : 0.0f, left > 32 ? b[3] : 0.0f};
                 }
             }
+        }
+    };
+    auto use = [&](int u, int s, auto tag) __attribute__((always_inline)) {
+        constexpr bool WHOLE = decltype(tag)::value;
 #pragma unroll
-            for (int t = 0; t < TT; ++t) {
-#pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    const int k = c + 64 * (h >> 1) + 8 * (h & 1);
-                    xv[t][h] = WHOLE ? *reinterpret_cast<const u32x4_any*>(v[t] + k) : load8(v[t] + k, C - k);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < NM; ++i) {
+        for (int i = 0; i < NM; ++i) {
+            if constexpr (E8) {
                 raw4_t lo[2], hi[2];
-                widen16<T>(wv[i][0], lo);
-                widen16<T>(wv[i][1], hi);
+                widen16<T>(wv[u][i][0], lo);
+                widen16<T>(wv[u][i][1], hi);
                 float scale = sc[i][S == 1 || WHOLE ? s * S + place : min(s * S + place, (C - 1) / kGroup)];
                 // places past the last block hold zeros, and so does the scale: the last one, which was read, may be infinite
-                if (S > 1 && !WHOLE && c - 16 * q >= C) scale = 0.0f;
+                if (S > 1 && !WHOLE && (s * S + place) * SC >= C) scale = 0.0f;
 #pragma unroll
                 for (int t = 0; t < TT; ++t) {
                     f32x4 p = {0.0f, 0.0f, 0.0f, 0.0f};
-                    p = mfma16<T>(lo[0], xv[t][0], p);
-                    p = mfma16<T>(lo[1], xv[t][1], p);
-                    p = mfma16<T>(hi[0], xv[t][2], p);
-                    p = mfma16<T>(hi[1], xv[t][3], p);
+                    p = mfma16<T>(lo[0], xv[u][t][0], p);
+                    p = mfma16<T>(lo[1], xv[u][t][1], p);
+                    p = mfma16<T>(hi[0], xv[u][t][2], p);
+                    p = mfma16<T>(hi[1], xv[u][t][3], p);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) acc[i][t][e] = fmaf(p[e], scale, acc[i][t][e]);
                 }
-            }
-        } else {
-            const int c = (s * S + place) * SC + 8 * q;
-            raw4_t wv[NM][2], xv[TT][2];
+            } else if constexpr (SCALED) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int k = c + 32 * h;
+                for (int t = 0; t < TT; ++t) {
+                    const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+                    f32x4 p[4];
 #pragma unroll
-                for (int i = 0; i < NM; ++i) {
-                    const T* p = reinterpret_cast<const T*>(w[i]) + k;
-                    wv[i][h] = WHOLE ? *reinterpret_cast<const u32x4_any*>(p) : load8(p, C - k);
+                    for (int h = 0; h < 2; ++h) {
+                        p[2 * h] = __builtin_amdgcn_mfma_f32_16x16x16f16(four_of<0>(wv[u][i][h]), four_of<0>(xv[u][t][h]), zero, 0, 0, 0);
+                        p[2 * h + 1] = __builtin_amdgcn_mfma_f32_16x16x16f16(four_of<1>(wv[u][i][h]), four_of<1>(xv[u][t][h]), zero, 0, 0, 0);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) acc[i][t][e] = fmaf(p[g][e], by[u][t][g], acc[i][t][e]);
+                    }
                 }
+            } else {
 #pragma unroll
-                for (int t = 0; t < TT; ++t) xv[t][h] = WHOLE ? *reinterpret_cast<const u32x4_any*>(v[t] + k) : load8(v[t] + k, C - k);
-            }
+                for (int h = 0; h < 2; ++h) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                for (int i = 0; i < NM; ++i) {
-#pragma unroll
-                    for (int t = 0; t < TT; ++t) acc[i][t] = mfma16<T>(wv[i][h], xv[t][h], acc[i][t]);
+                    for (int t = 0; t < TT; ++t) acc[i][t] = mfma16<T>(wv[u][i][h], xv[u][t][h], acc[i][t]);
                 }
             }
         }
     };
     const int whole = min(s1, C / (SC * S));
     int s = s0;
-#pragma unroll UNROLL
-    for (; s < whole; s += step) stage(s, Whole{});
-    if (s < s1) stage(s, Part{});
+    if constexpr (U == 1) {
+#pragma unroll 4
+        for (; s < whole; s += step) {
+            load(0, s, Whole{});
+            use(0, s, Whole{});
+        }
+    } else {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (s + u * step < whole) load(u, s + u * step, Whole{});
+        }
+        while (s < whole) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (s >= whole) break;
+                use(u, s, Whole{});
+                if (s + U * step < whole) load(u, s + U * step, Whole{});
+                s += step;
+            }
+        }
+    }
+    if (s < s1) {
+        load(0, s, Part{});
+        use(0, s, Part{});
+    }
 }
 
-// act[slot][..][n] = silu(gate x) * (up x) of one active expert, 16 columns n, as two numbers of T: rounded once to T a
+// act[slot][..][n] = silu(gate x) * (up x) of one active expert, 16 columns n, as two 16-bit numbers: rounded once to T a
 // result would be 1.4 times as far off as by its own rounding alone.
 template <class T, bool E8, int TT>
 __device__ __forceinline__ void gate_up(const MoeArgs& a, const int* row, const Active& x, int n0, int t0,
@@ -298,7 +357,8 @@ __device__ __forceinline__ void gate_up(const MoeArgs& a, const int* row, const 
     const float* sc[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        w[i] = a.w[i].data + (x.expert * a.w[i].stack + min(n0 + i16, a.N - 1) * a.w[i].ld) * ES;
+        const int n = kScaled<T, E8> ? scaled_column(n0, i16) : n0 + i16;
+        w[i] = a.w[i].data + (x.expert * a.w[i].stack + min(n, a.N - 1) * a.w[i].ld) * ES;
         sc[i] = E8 ? a.w[i].scale + x.expert * a.w[i].scale_stack + (n0 / kGroup) * a.w[i].scale_ld : nullptr;
     }
     const T* v[TT];
@@ -309,7 +369,8 @@ __device__ __forceinline__ void gate_up(const MoeArgs& a, const int* row, const 
         acc[0][t] = acc[1][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
     const int stages = (a.K + kStageCols<E8> - 1) / kStageCols<E8>;
-    products<T, E8, 2, TT, 1>(w, sc, v, a.K, wave, stages, kUpWaves, q, 0, acc);
+    const float* const none[TT] = {};
+    products<T, E8, 2, TT, 1>(w, sc, v, a.K, wave, stages, kUpWaves, q, 0, acc, none);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
 #pragma unroll
@@ -317,8 +378,8 @@ __device__ __forceinline__ void gate_up(const MoeArgs& a, const int* row, const 
     }
     __syncthreads();
     for (int j = threadIdx.x; j < TT * 256; j += kUpThreads) {
-        const int i = j & 15, c = j >> 4 & 15, t = j >> 8, s = t0 + 16 * t + c, n = n0 + i;
-        if (s >= x.count || n >= a.N) continue;
+        const int i = j & 15, c = j >> 4 & 15, t = j >> 8, s = t0 + 16 * t + c;
+        const int n = kScaled<T, E8> ? scaled_column(n0, i) : n0 + i;
         const int at = 4 * ((i >> 2) * 16 + c) + (i & 3);
         float g = red[0][0][t][at], u = red[0][1][t][at];
 #pragma unroll
@@ -326,8 +387,16 @@ __device__ __forceinline__ void gate_up(const MoeArgs& a, const int* row, const 
             g += red[k][0][t][at];
             u += red[k][1][t][at];
         }
+        float act = silu_mul(g, u);
+        if constexpr (kScaled<T, E8>) {  // of the finite ones: infinities stay what they are
+            const uint32_t size = abs_bits(act);
+            const Pow2 f = pow2_for<T>(max16(n < a.N && size < 0x7f800000u ? size : 0u));
+            act *= f.up;
+            if (i == 0 && s < x.count) a.factor[(x.first + s) * a.ld_factor + (n0 >> 4)] = f.down;
+        }
+        if (s >= x.count || n >= a.N) continue;
         uint16_t hi, lo, *to = a.act + (x.first + s) * 2 * a.ld_act + n;
-        split16<T>(silu_mul(g, u), hi, lo);
+        split16<typename Act<T, E8>::type>(act, hi, lo);
         to[0] = hi;
         to[a.ld_act] = lo;
     }
@@ -339,7 +408,7 @@ __global__ void __launch_bounds__(kUpThreads) moe_up_kernel(MoeArgs a, int block
 {
     __shared__ float red[kUpWaves][2][4][256];
     const int j = blockIdx.x / blocks, n0 = (blockIdx.x - j * blocks) * 16;
-    if (j >= *a.actives) return;
+    if (j >= *a.actives || !has_columns<T, E8>(n0, a.N)) return;
     const Active x = a.active[j];
     if (x.count <= 16) gate_up<T, E8, 1>(a, a.row, x, n0, 0, reinterpret_cast<float(*)[2][1][256]>(&red[0][0][0][0]));
     else gate_up<T, E8, 4>(a, a.row, x, n0, 0, red);
@@ -368,7 +437,7 @@ __global__ void __launch_bounds__(kUpThreads) moe_routed_up_kernel(MoeArgs a, in
             a.weight[i] = weight[i];
         }
     }
-    if (n0 < a.N && j < n) gate_up<T, E8, 1>(a, row, active[j], n0, 0, u.red);
+    if (has_columns<T, E8>(n0, a.N) && j < n) gate_up<T, E8, 1>(a, row, active[j], n0, 0, u.red);
 }
 
 // Adds one active expert's part of the results' ROWS columns from c0 on to the wave's sums, for TT tiles of its slots from t0
@@ -378,20 +447,26 @@ __global__ void __launch_bounds__(kUpThreads) moe_routed_up_kernel(MoeArgs a, in
 template <class T, bool E8, int ROWS, int TT>
 __device__ __forceinline__ void down(const MoeArgs& a, const Active& x, int c0, int t0, int s0, int s1, float* mine)
 {
+    using A = typename Act<T, E8>::type;
     constexpr int S = 16 / ROWS, EACH = ROWS / 2, ES = E8 ? 1 : 2;
     const int lane = threadIdx.x & 63, i16 = lane & 15, q = lane >> 4;
     const int place = i16 / ROWS, at = i16 % EACH, second = i16 / EACH % 2;
     const uint8_t* const w[1] = {a.w[2].data + (x.expert * a.w[2].stack + min(c0 + i16 % ROWS, a.K - 1) * a.w[2].ld) * ES};
     const float* const sc[1] = {E8 ? a.w[2].scale + x.expert * a.w[2].scale_stack + (c0 / kGroup) * a.w[2].scale_ld : nullptr};
-    const T* v[TT];
+    const A* v[TT];
+    const float* f[TT];
     f32x4 acc[1][TT];
 #pragma unroll
     for (int t = 0; t < TT; ++t) {
         const int s = x.first + min(t0 + EACH * t + at, x.count - 1);
-        v[t] = reinterpret_cast<const T*>(a.act) + (s * 2 + second) * a.ld_act;
+        v[t] = reinterpret_cast<const A*>(a.act) + (s * 2 + second) * a.ld_act;
+        f[t] = a.factor + s * a.ld_factor;
         acc[0][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    products<T, E8, 1, TT, S, 4 / TT>(w, sc, v, a.N, s0, s1, 1, q, place, acc);
+    // stages read ahead where a workgroup has its CU to itself and registers to spare (37 rows, K = 4096 N = 768, 128 experts,
+    // the layer: fp16 408 us with three, 429 with one; bf16 395 and 403)
+    constexpr int U = ROWS == 16 && !E8 && TT == 1 ? 3 : 1;
+    products<A, E8, 1, TT, S, U, kScaled<T, E8>>(w, sc, v, a.N, s0, s1, 1, q, place, acc, f);
 #pragma unroll
     for (int t = 0; t < TT; ++t) {
 #pragma unroll
@@ -436,17 +511,18 @@ __global__ void __launch_bounds__(64 * WAVES) moe_down_kernel(MoeArgs a, MoePlan
         const Active x = a.active[j];
         const int s0 = part * per, s1 = min(stages, (part + 1) * per);
         // the registers of two tiles cost a workgroup per CU with 4 places (one row, K = 2560 N = 1024 of e4m3: 23.8 us, 21.0
-        // with one), and those of four with e4m3
+        // with one), and those of four are too many with e4m3 or factors
+        constexpr int MOST = ROWS == 4 ? 1 : E8 || kScaled<T, E8> ? 2 : 4;
         for (int t = 0; t < x.count;) {
             const int left = x.count - t;
-            if (left <= EACH || ROWS == 4) {
+            if (MOST == 1 || left <= EACH) {
                 down<T, E8, ROWS, 1>(a, x, c0, t, s0, s1, mine);
                 t += EACH;
-            } else if (left <= 2 * EACH || E8) {
-                if constexpr (ROWS == 16) down<T, E8, ROWS, 2>(a, x, c0, t, s0, s1, mine);
+            } else if (MOST == 2 || left <= 2 * EACH) {
+                if constexpr (MOST >= 2) down<T, E8, ROWS, 2>(a, x, c0, t, s0, s1, mine);
                 t += 2 * EACH;
             } else {
-                if constexpr (ROWS == 16 && !E8) down<T, E8, ROWS, 4>(a, x, c0, t, s0, s1, mine);
+                if constexpr (MOST == 4) down<T, E8, ROWS, 4>(a, x, c0, t, s0, s1, mine);
                 t += 4 * EACH;
             }
         }
@@ -479,7 +555,8 @@ __global__ void __launch_bounds__(256) moe_join_kernel(MoeArgs a, int splits)
 template <class T, bool E8, class L, int PER>
 void first_launches(const MoeArgs& a, hipStream_t stream)
 {
-    const int most = a.M * a.top < a.E ? a.M * a.top : a.E, blocks = a.N > 0 ? (a.N + 15) / 16 : 1;
+    // whole pairs of 16 columns, which share an activation's lines
+    const int most = a.M * a.top < a.E ? a.M * a.top : a.E, blocks = a.N > 0 ? (a.N + 31) / 32 * 2 : 1;
     const dim3 grid((unsigned)(most * blocks));
     if (a.M <= kRoutedRows) {
         hipLaunchKernelGGL((moe_routed_up_kernel<T, E8, L, PER>), grid, dim3(kUpThreads), 0, stream, a, blocks);

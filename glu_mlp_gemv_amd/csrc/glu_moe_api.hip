@@ -28,23 +28,25 @@ glu_status check_sizes(const glu_moe_sizes* s)
     // workgroups of the first product below 2^32 threads
     const int64_t rows = s->M < glu::kMoeRows ? s->M : glu::kMoeRows;
     const int64_t most = rows * s->top < s->E ? rows * s->top : s->E;
-    return most * ceil_div(s->N, 16) >= (int64_t)1 << 24 ? GLU_ERR_BAD_SHAPE : GLU_OK;
+    return most * ceil_div(s->N, 32) >= (int64_t)1 << 23 ? GLU_ERR_BAD_SHAPE : GLU_OK;
 }
 
 struct Layout {
     glu::MoePlan plan;
-    int64_t active, row, weight, act, part, bytes, ld_act;  // offsets; how many experts are active is at 0
+    int64_t active, row, weight, act, factor, part, bytes, ld_act, ld_factor;  // offsets; how many experts are active is at 0
 };
 Layout layout(const glu_moe_sizes& s, int rows, bool e4m3)
 {
     Layout l{};
     l.plan = glu::moe_plan(rows, (int)s.K, (int)s.N, (int)s.E, (int)s.top, e4m3);
     l.ld_act = (s.N + 7) / 8 * 8;
+    l.ld_factor = ceil_div(s.N, 64) * 4;  // the second product reads four at a time
     l.active = 16;
     l.row = l.active + align16(s.E * (int64_t)sizeof(glu::Active));
     l.weight = l.row + align16(rows * s.top * 4);
     l.act = l.weight + align16(rows * s.top * 4);
-    l.part = l.act + align16(rows * s.top * l.ld_act * 4);
+    l.factor = l.act + align16(rows * s.top * l.ld_act * 4);
+    l.part = l.factor + rows * s.top * l.ld_factor * 4;
     l.bytes = l.part + (l.plan.splits > 1 ? align16((int64_t)l.plan.splits * rows * s.K * 4) : 0);
     return l;
 }
@@ -149,8 +151,10 @@ glu_status glu_moe_glu(const void* x, int64_t ldx, const void* logits, int64_t l
         a.row = (int*)(ws + l.row);
         a.weight = (float*)(ws + l.weight);
         a.act = (uint16_t*)(ws + l.act);
+        a.factor = (float*)(ws + l.factor);
         a.part = (float*)(ws + l.part);
         a.ld_act = l.ld_act;
+        a.ld_factor = l.ld_factor;
         const hipError_t e = glu::moe_launch(dtype, logits_dtype, e4m3, a, l.plan, (hipStream_t)stream);
         if (e != hipSuccess) return glu::fail_launch(e);
     }

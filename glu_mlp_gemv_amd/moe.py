@@ -55,7 +55,7 @@ def moe_glu(x: torch.Tensor, logits: torch.Tensor, gate: torch.Tensor, up: torch
     with one fp32 scale per 128 x 128 block ([E, N / 128, K / 128], [E, K / 128, N / 128], rounded up), as
     ``fp8_quantize_weight`` gives them per expert.  A row's experts are those of its largest logits, of equal ones
     the lowest; p is the softmax over them, or with ``normalize=False`` over all experts.  -inf masks an expert: a row whose
-    logits are all -inf is 0.  Sums and the activation are fp32 (the second product takes it as two numbers of x's type), the
+    logits are all -inf is 0.  Sums and the activation are fp32 (the second product takes it as two 16-bit numbers, in fp32's range), the
     result is rounded once.
 
     Each chosen expert's weights are read once per 64 rows: meant for the tokens of a decode step, right for any number.  At

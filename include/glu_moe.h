@@ -7,8 +7,9 @@
  *
  * Every matrix of an expert that some row needs is read once per 64 rows, which is what bounds the layer: it is meant for
  * the tokens of a decode step, and correct for any number of rows.  The products' sums, the activation, the softmax and the
- * sum over experts are fp32; as the operand of the second product the activation is two numbers of T, its rounding and the
- * rounding of what that left, so that 2^-17 of it is lost at most (fp16: 2^-23).
+ * sum over experts are fp32; as the operand of the second product the activation is two 16-bit numbers, its rounding and the
+ * rounding of what that left, so that 2^-17 of it is lost at most (fp16 weights: 2^-23, and 2^-39 of the largest of 16
+ * columns).  It has fp32's range for every T.
  *
  * A logit of -inf is an expert masked away: it is never chosen, and a row without any other has fewer experts, or none
  * and out = 0.  A NaN logit ranks above all others and makes its row NaN.  Experts that a row did not choose do not

@@ -43,8 +43,9 @@ ROWS = [(1, 200, 130), (2, 64, 300), (3, 70, 257), (4, 128, 1030), (5, 96, 64), 
         (17, 72, 136), (32, 33, 513), (33, 64, 130), (50, 48, 96), (64, 64, 200), (65, 40, 72)]
 
 
-def wide64(x, logits, gate, up, down, top, scales=(None, None, None)):
-    """out before its rounding, and its bound where the activation goes into the second product as two numbers."""
+def wide64(x, logits, gate, up, down, top, scales=(None, None, None), floor=None):
+    """out before its rounding, and its bound where the activation goes into the second product as two numbers.  floor: what
+    fp16 numbers may lose of the largest of 32 columns, whose 16 they share a factor with; else half of 2^-24."""
     t, K, N = x.dtype, x.shape[1], gate.shape[1]
     take = moe_ref.chosen(logits, top)
     p = moe_ref.weights(logits, take, True)
@@ -61,7 +62,12 @@ def wide64(x, logits, gate, up, down, top, scales=(None, None, None)):
         ea = 1.1 * eg * (u.abs() + eu) + (g * torch.sigmoid(g)).abs() * eu + 8 * U * a.abs()
         # two roundings of at most half a step each, of bf16 numbers behind e4m3 weights, and of an fp16 number below 2^-14
         # half of 2^-24
-        ea = ea + LEFT[t if scales[0] is None else torch.bfloat16] * (a.abs() + ea) + (2.0 ** -25 if t is torch.float16 else 0.0)
+        ea = ea + LEFT[t if scales[0] is None else torch.bfloat16] * (a.abs() + ea)
+        if floor is not None:
+            most = torch.nn.functional.pad(a.abs(), (0, -N % 32)).unflatten(1, (-1, 32)).amax(2).repeat_interleave(32, 1)[:, :N]
+            ea = ea + floor * most
+        elif t is torch.float16:
+            ea = ea + 2.0 ** -25
         pe = p[rows, e, None]
         out[rows] += pe * (a @ wd.t())
         err[rows] += pe * (ea @ wd.abs().t() + 2 * U * nn * (a.abs() @ wd.abs().t()) + 100 * U * (a @ wd.t()).abs())
@@ -99,3 +105,44 @@ def test_activation_keeps_its_bits(M, K, N, E, top, e4m3, kind):
     print(f"[moe bits] {M=} {K=} {N=} {E=} {e4m3=} {kind}", flush=True)
     x, logits, w, s = layer(M, K, N, E, T[kind], e4m3, M + N)
     check_store("out", run(x, logits, w, s, top), *wide64(x, logits, *w, top, s))
+
+
+# activations past fp16's range on either side, of very different sizes in one row, and results that fp16 holds
+SIZES = {"large": (2.0 ** 10, 2.0 ** -13), "huge": (2.0 ** 14, 2.0 ** -21), "small": (2.0 ** -11, 2.0 ** 11)}
+
+
+@pytest.mark.parametrize("size", [*SIZES, "mixed"])
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("M", [1, 2, 3, 5, 9, 17, 33, 64])
+def test_activations_past_the_range_of_fp16(M, e4m3, size):
+    print(f"[moe range] {M=} {e4m3=} {size}", flush=True)
+    K, N, E, top, t = 72, 213, 3, 2, torch.float16
+    x, logits, w, s = layer(M, K, N, E, t, False, M)
+    x.clamp_(-3, 3)
+    up = down = None
+    if size == "mixed":  # by runs of 32 columns, whose groups of 16 share a factor at most with each other
+        up = 2.0 ** (9.0 - 5 * (torch.arange(N, device=DEV) // 32 % 4))  # down's stay below 2^15, fp16 numbers
+        down = up ** -2 * 8
+    else:
+        up, down = (torch.full((N,), v, device=DEV) for v in SIZES[size])
+    w = [(m.float() * f).to(t) for m, f in zip(w, (up[:, None], up[:, None], down))]
+    if e4m3:
+        w, s = zip(*(e4m3_of(m) for m in w))
+    out = run(x, logits, w, s, top)
+    want, err = wide64(x, logits, *w, top, s, floor=2.0 ** -39)
+    assert want.abs().max() < 6e4
+    check_store("out", out, want, err)
+
+
+@pytest.mark.parametrize("M", [2, 7, 40])
+def test_infinite_activations_in_fp16(M):
+    """One infinite number of an activation, large finite ones beside it: results are that one's infinity."""
+    K, N, E = 64, 70, 2
+    x, logits, w, s = layer(M, K, N, E, torch.float16, False, M)
+    x.abs_().clamp_(0.5, 3)
+    w[0].abs_()
+    w[1].mul_(2 ** 12)
+    w[1][:, 37] = math.inf
+    w[2][:, :, 37] = torch.where(torch.arange(K, device=DEV) % 2 == 0, 1.0, -1.0)
+    want = (math.inf * w[2][0, :, 37].float()).expand(M, K)
+    assert torch.equal(run(x, logits, w, s, 2).float(), want)
