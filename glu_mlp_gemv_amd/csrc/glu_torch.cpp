@@ -421,7 +421,7 @@ PyObject* moe(PyObject*, PyObject* const* a, Py_ssize_t n)
     return guarded([&]() -> PyObject* {
         if (n != 10) Py_RETURN_NONE;
         const Place at(a[0]);
-        if (!at.ok || recorded(a, 5)) Py_RETURN_NONE;
+        if (!at.ok || recorded(a, n)) Py_RETURN_NONE;
         const Rows x(a[0], at, -1, -1, c10::ScalarType::Undefined);
         if (!x.ok || !half_type(x.type) || !PyLong_Check(a[5])) Py_RETURN_NONE;
         const Rows logits(a[1], at, x.rows, -1, c10::ScalarType::Undefined);

@@ -66,7 +66,7 @@ def moe_glu(x: torch.Tensor, logits: torch.Tensor, gate: torch.Tensor, up: torch
                                                 up_scale, down_scale)
         if _taken(r):
             return r
-    if _wants_gradient(x, logits, gate, up, down):
+    if _wants_gradient(x, logits, gate, up, down, gate_scale, up_scale, down_scale):
         raise RuntimeError("moe_glu has no gradient, and an operand requires one: call it under torch.no_grad()")
     M, K, dev = _matrix("x", x, _TYPES)
     dt = x.dtype
