@@ -16,7 +16,8 @@ import torch
 
 from . import fp8
 from .api import _raise_for, library
-from .fp8 import _bytes, _matrix, _on, _output, _ptr, _refuse, _rows, _taken, _vector
+from .fp8 import (_bytes, _matrix, _on, _output, _ptr, _refuse, _refuse_tangents, _rows, _taken, _vector,
+                  _wants_gradient)
 
 MAX_RANK = 256
 _TYPES = (torch.bfloat16, torch.float16)
@@ -56,10 +57,6 @@ def _adapter(prefix: str, a, b, dtype, K: int, N: int, dev, L=None, R=None):
     sa = _stack(prefix + "a", a, dtype, (L, R, K), dev)
     sb = _stack(prefix + "b", b, dtype, (L, N, R), dev)
     return Adapter(a.data_ptr(), b.data_ptr(), *sa, *sb), L, R
-
-
-def _wants_gradient(*tensors) -> bool:
-    return torch.is_grad_enabled() and any(getattr(t, "requires_grad", False) for t in tensors)
 
 
 @functools.lru_cache(maxsize=256)
@@ -115,6 +112,7 @@ def adapter_add(y: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tens
         r = (fp8._fast or fp8._load_fast()).adapter(y, x, a, b, index, scale)
         if _taken(r):
             return r
+    _refuse_tangents("adapter_add", y, x, a, b, scale)
     if _wants_gradient(y, x, a, b, scale):
         if out is not None or return_low or stream is not None:
             raise RuntimeError("adapter_add with out, return_low or stream has no gradient, and an operand requires one: "
@@ -137,6 +135,7 @@ def adapter_glu(gate: torch.Tensor, up: torch.Tensor, x: torch.Tensor, gate_a: t
         r = (fp8._fast or fp8._load_fast()).adapter(gate, up, x, gate_a, gate_b, up_a, up_b, index, scale)
         if _taken(r):
             return r
+    _refuse_tangents("adapter_glu", gate, up, x, gate_a, gate_b, up_a, up_b, scale)
     if _wants_gradient(gate, up, x, gate_a, gate_b, up_a, up_b, scale):
         raise RuntimeError("adapter_glu has no gradient, and an operand requires one: call it under torch.no_grad(), or "
                            "train with adapter_add on gate and up")

@@ -8,7 +8,8 @@ import torch
 
 from . import fp8
 from .api import _raise_for, library
-from .fp8 import DTYPES, _INPUTS, _matrix, _on, _output, _ptr, _rows, _taken, _vector
+from .fp8 import (DTYPES, _INPUTS, _matrix, _on, _output, _ptr, _refuse_tangents, _rows, _taken, _vector,
+                  _wants_gradient)
 
 _WORD = (1 << 64) - 1
 
@@ -55,7 +56,8 @@ def dropout(x: torch.Tensor, p: float, seed: Union[int, torch.Tensor], offset: i
         r = (fp8._fast or fp8._load_fast()).dropout(x, drop_of(p), seed, offset, residual)
         if _taken(r):
             return r
-    if torch.is_grad_enabled() and (getattr(x, "requires_grad", False) or getattr(residual, "requires_grad", False)):
+    _refuse_tangents("dropout", x, residual)
+    if _wants_gradient(x, residual):
         if out is not None or stream is not None:
             raise RuntimeError("dropout with out or stream has no gradient, and an operand requires one: call it without "
                                "them, or under torch.no_grad()")

@@ -141,6 +141,18 @@ PyObject* guarded(F&& f)
     END_HANDLE_TH_ERRORS
 }
 
+// Whether autograd follows any of these: they require a gradient where it records, or carry a tangent of forward mode,
+// which no_grad does not switch off
+bool recorded(PyObject* const* a, Py_ssize_t n)
+{
+    for (Py_ssize_t i = 0; i < n; ++i) {
+        if (!THPVariable_Check(a[i])) continue;
+        const at::Tensor& t = THPVariable_Unpack(a[i]);
+        if ((t.requires_grad() && c10::GradMode::is_enabled()) || t._fw_grad(0).defined()) return true;
+    }
+    return false;
+}
+
 // (x, weight, eps, residual or None, e4m3) -> (out, h or None[, scale])
 PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
@@ -155,12 +167,7 @@ PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t n)
         const double eps = PyFloat_Check(a[2]) ? PyFloat_AS_DOUBLE(a[2]) : -1.0;
         if (!w || eps < 0.0) Py_RETURN_NONE;
         const bool has = a[3] != Py_None, e4m3 = a[4] == Py_True;
-        // operands that autograd would record: fp8.py has them differentiated, or refuses
-        if (c10::GradMode::is_enabled()) {
-            for (PyObject* o : {a[0], a[1], a[3]}) {
-                if (THPVariable_Check(o) && THPVariable_Unpack(o).requires_grad()) Py_RETURN_NONE;
-            }
-        }
+        if (recorded(a, 4)) Py_RETURN_NONE;  // fp8.py has them differentiated, or refuses
         void* res = nullptr;
         int64_t ldr = 0;
         if (has) {
@@ -324,15 +331,6 @@ struct Matrices {
 };
 
 bool half_type(c10::ScalarType t) { return t == c10::ScalarType::BFloat16 || t == c10::ScalarType::Half; }
-
-bool recorded(PyObject* const* a, Py_ssize_t n)
-{
-    if (!c10::GradMode::is_enabled()) return false;
-    for (Py_ssize_t i = 0; i < n; ++i) {
-        if (THPVariable_Check(a[i]) && THPVariable_Unpack(a[i]).requires_grad()) return true;
-    }
-    return false;
-}
 
 // an optional vector: false where it is there and not as wanted
 bool optional_vector(PyObject* o, const Place& at, int64_t n, c10::ScalarType want, void** p)

@@ -23,6 +23,7 @@ import importlib
 from typing import Optional
 
 import torch
+from torch.autograd import forward_ad
 
 from .api import _raise_for, _row_stride, library
 
@@ -197,10 +198,17 @@ def _norm(x, weight, eps, residual, out, scale_out, residual_out, return_rstd, s
     return out, scale, h, rstd
 
 
-def _wants_gradient(x, weight, residual) -> bool:
+def _wants_gradient(*tensors) -> bool:
     """Whether autograd would record a call on these operands (none in a Function's own forward)."""
-    return torch.is_grad_enabled() and (getattr(x, "requires_grad", False) or getattr(weight, "requires_grad", False)
-                                        or getattr(residual, "requires_grad", False))
+    return torch.is_grad_enabled() and any(getattr(t, "requires_grad", False) for t in tensors)
+
+
+def _refuse_tangents(call: str, *tensors) -> None:
+    """Forward mode's tangents would be lost in silence: no call here has a derivative of that kind, and none of torch's
+    switches but its own leaves them out."""
+    if forward_ad._current_level >= 0 and any(isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None
+                                              for t in tensors):
+        raise RuntimeError(f"{call} has no derivative in forward mode, and an operand has a tangent")
 
 
 def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: Optional[torch.Tensor] = None,
@@ -218,6 +226,7 @@ def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: Op
         r = (_fast or _load_fast()).norm(x, weight, eps, residual, False)
         if _taken(r):
             return r[0], x if residual is None else r[1]
+    _refuse_tangents("add_rms_norm", x, weight, residual)
     if _wants_gradient(x, weight, residual):
         if not plain:
             raise RuntimeError("add_rms_norm with out, residual_out, return_rstd or stream has no gradient, and an operand "
@@ -240,6 +249,7 @@ def add_rms_norm_fp8(x: torch.Tensor, weight: torch.Tensor, eps: float, residual
         r = (_fast or _load_fast()).norm(x, weight, eps, residual, True)
         if _taken(r):
             return r[0], r[2], x if residual is None else r[1]
+    _refuse_tangents("add_rms_norm_fp8", x, weight, residual)
     if _wants_gradient(x, weight, residual):
         raise RuntimeError("add_rms_norm_fp8 has no gradient, and an operand requires one: call it under torch.no_grad(), or "
                            "train with autograd.rms_norm")

@@ -12,9 +12,10 @@ from typing import Optional
 import torch
 
 from . import fp8
-from .adapters import _CODES, _TYPES, _scratch, _stack, _wants_gradient
+from .adapters import _CODES, _TYPES, _scratch, _stack
 from .api import _raise_for, library
-from .fp8 import DTYPES, E4M3, _bytes, _matrix, _on, _output, _ptr, _refuse, _rows, _taken, groups
+from .fp8 import (DTYPES, E4M3, _bytes, _matrix, _on, _output, _ptr, _refuse, _refuse_tangents, _rows, _taken,
+                  _wants_gradient, groups)
 
 MAX_EXPERTS = 1024
 MAX_TOP = 32
@@ -66,6 +67,7 @@ def moe_glu(x: torch.Tensor, logits: torch.Tensor, gate: torch.Tensor, up: torch
                                                 up_scale, down_scale)
         if _taken(r):
             return r
+    _refuse_tangents("moe_glu", x, logits, gate, up, down, gate_scale, up_scale, down_scale)
     if _wants_gradient(x, logits, gate, up, down, gate_scale, up_scale, down_scale):
         raise RuntimeError("moe_glu has no gradient, and an operand requires one: call it under torch.no_grad()")
     M, K, dev = _matrix("x", x, _TYPES)
