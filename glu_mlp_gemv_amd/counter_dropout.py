@@ -2,6 +2,7 @@
 from __future__ import annotations
 
 import ctypes
+import operator
 from typing import Optional, Union
 
 import torch
@@ -34,7 +35,8 @@ def _dropout(x, p, seed, offset, residual, out, stream):
     with ctx:
         out, ldo = _output("out", out, dt, M, K, dev)
         st = library().glu_dropout(x.data_ptr(), ldx, _ptr(residual), ldr, out.data_ptr(), ldo, M, K, drop,
-                                   0 if at is not None else seed & _WORD, _ptr(at), offset & _WORD, DTYPES[dt], handle)
+                                   0 if at is not None else operator.index(seed) & _WORD, _ptr(at),
+                                   operator.index(offset) & _WORD, DTYPES[dt], handle)
     if st:
         _raise_for(st)
     return out
