@@ -83,6 +83,7 @@ EXPORTED_SYMBOLS = (
     # include/glu_moe.h; declared and called in moe.py
     "glu_moe_glu",
     "glu_moe_workspace",
+    "glu_moe_logits",
 )
 
 

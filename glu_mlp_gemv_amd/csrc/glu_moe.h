@@ -42,4 +42,13 @@ struct MoePlan { int splits, parts, rows; };
 MoePlan moe_plan(int M, int K, int N, int E, int top, bool e4m3);
 hipError_t moe_launch(int dtype, int logits_dtype, bool e4m3, const MoeArgs& a, const MoePlan& p, hipStream_t stream);
 
+struct LogitsArgs {
+    const void* x;       // [M][K]
+    const void* router;  // [E][K]
+    float* logits;       // [M][E]
+    int64_t ldx, ldr;
+    int M, K, E;
+};
+hipError_t moe_logits_launch(int dtype, const LogitsArgs& a, hipStream_t stream);
+
 }  // namespace glu

@@ -161,4 +161,21 @@ glu_status glu_moe_glu(const void* x, int64_t ldx, const void* logits, int64_t l
     return GLU_OK;
 }
 
+glu_status glu_moe_logits(const void* x, int64_t ldx, const void* router, int64_t ldr, float* logits, int64_t M, int64_t K,
+                          int64_t E, int dtype, void* stream)
+{
+    if (dtype != GLU_DTYPE_BF16 && dtype != GLU_DTYPE_FP16) return GLU_ERR_BAD_ARGUMENT;
+    if (bad_dim(M) || K < 0 || K > kMaxInner || E < 1 || E > GLU_MOE_MAX_EXPERTS) return GLU_ERR_BAD_SHAPE;
+    if (M == 0) return GLU_OK;
+    const Array arrays[] = {
+        {x, M, K, ldx, 2, false},
+        {router, E, K, ldr, 2, false},
+        {logits, M, E, E, 4, true},
+    };
+    const glu_status st = glu::check_arrays(arrays, 3);
+    if (st != GLU_OK) return st;
+    const hipError_t e = glu::moe_logits_launch(dtype, {x, router, logits, ldx, ldr, (int)M, (int)K, (int)E}, (hipStream_t)stream);
+    return e == hipSuccess ? GLU_OK : glu::fail_launch(e);
+}
+
 }  // extern "C"

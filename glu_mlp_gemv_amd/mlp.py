@@ -14,7 +14,7 @@ from typing import NamedTuple, Optional, Tuple
 
 import torch
 
-from . import adapters as low_rank, api, fp8, moe
+from . import adapters as low_rank, fp8, moe
 
 
 class MlpAdapters(NamedTuple):
@@ -67,8 +67,8 @@ class Fp8GluMlp:
 class ExpertGluMlp:
     """The same with a mixture of experts: norm -> router -> the chosen experts' gate, up and down.
 
-    norm_weight [K] and router [E, K] in bf16 (as ``api.grouped_gemv`` takes them), gate and up [E, N, K], down [E, K, N] in
-    bf16, or e4m3 with ``scales`` of all three (``moe.moe_glu``).  ``top`` experts per row.
+    norm_weight [K] and router [E, K] in bf16 or fp16, gate and up [E, N, K], down [E, K, N] in the same type, or e4m3 with
+    ``scales`` of all three (``moe.moe_glu``).  ``top`` experts per row, ranked by fp32 logits.
     """
 
     def __init__(self, norm_weight: torch.Tensor, router: torch.Tensor, gate: torch.Tensor, up: torch.Tensor,
@@ -81,5 +81,4 @@ class ExpertGluMlp:
     def __call__(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None):
         """(y, h) for x [M, K] and the residual stream, as ``Fp8GluMlp``."""
         n, h = fp8.add_rms_norm(x, self.norm_weight, self.eps, residual=residual)
-        (logits,) = api.grouped_gemv(n, [self.router])
-        return moe.moe_glu(n, logits, *self.experts, self.top, normalize=self.normalize, **self.scales), h
+        return moe.moe_glu(n, moe.moe_logits(n, self.router), *self.experts, self.top, normalize=self.normalize, **self.scales), h

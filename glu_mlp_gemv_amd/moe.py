@@ -98,6 +98,32 @@ def moe_glu(x: torch.Tensor, logits: torch.Tensor, gate: torch.Tensor, up: torch
     return out
 
 
+def moe_logits(x: torch.Tensor, router: torch.Tensor, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """x @ router.T in fp32, [M, E]: the logits of ``moe_glu``, not rounded to x's type, which would change their order.
+
+    x [M, K] and router [E, K], both bf16 or fp16.  Has no gradient: operands that require one are refused where autograd
+    records.
+    """
+    _refuse_tangents("moe_logits", x, router)
+    if _wants_gradient(x, router):
+        raise RuntimeError("moe_logits has no gradient, and an operand requires one: call it under torch.no_grad()")
+    M, K, dev = _matrix("x", x, _TYPES)
+    dt = x.dtype
+    ldx = _rows("x", x, dt, M, K, dev)
+    _refuse("router", router, (dt,), (None, K), dev)
+    E = router.shape[0]
+    ldr = _rows("router", router, dt, E, K, dev)
+    if not 1 <= E <= MAX_EXPERTS:
+        raise ValueError(f"1 to {MAX_EXPERTS} experts, got {E}")
+    ctx, handle = _on(dev, stream, x, router)
+    with ctx:
+        out = torch.empty(M, E, dtype=torch.float32, device=dev)
+        st = library().glu_moe_logits(x.data_ptr(), ldx, router.data_ptr(), ldr, out.data_ptr(), M, K, E, _CODES[dt], handle)
+    if st:
+        _raise_for(st)
+    return out
+
+
 def _declare(lib):
     """Argument types of include/glu_moe.h (called once by ``api.library``)."""
     vp, i64, i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
@@ -105,6 +131,7 @@ def _declare(lib):
     for name, args in {
         "glu_moe_glu": [vp, i64, vp, i64, i32, mp, mp, mp, vp, i64, sp, i32, i32, i32, vp, i64, vp],
         "glu_moe_workspace": [sp, ctypes.POINTER(i64)],
+        "glu_moe_logits": [vp, i64, vp, i64, vp, i64, i64, i64, i32, vp],
     }.items():
         f = getattr(lib, name)
         f.argtypes = args

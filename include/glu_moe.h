@@ -65,6 +65,14 @@ glu_status glu_moe_glu(const void* x, int64_t ldx, const void* logits, int64_t l
                        void* workspace, int64_t workspace_bytes, void* stream);
 glu_status glu_moe_workspace(const glu_moe_sizes* sizes, int64_t* bytes);
 
+/*
+ * logits[m] = x[m] router^T, fp32 sums that are not rounded: what glu_moe_glu ranks.  Rounded to 16 bits, logits of neighbouring
+ * experts become equal or change places, and the lowest of equal ones is taken.
+ * x [M, K] and router [E, K] of dtype (BF16 or FP16), logits [M, E] dense.  M == 0: GLU_OK, nothing launched; K == 0: zeros.
+ */
+glu_status glu_moe_logits(const void* x, int64_t ldx, const void* router, int64_t ldr, float* logits, int64_t M, int64_t K,
+                          int64_t E, int dtype, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
