@@ -9,10 +9,11 @@
 // among its own rows and goes through them one after another (a prefill: one or two), or, where a batch mixes requests, in
 // workgroups of their own.  So no call sorts anything, and an adapter's weights are read once per tile that has it.
 // In every product the rows of w are the matrix instruction's rows and the batch's rows its columns, gathered from the
-// tile: rows of other adapters are left out, not multiplied by zero.  Kernel times: one row, K = 2560 N = 9216 rank 16,
-// 3.6 + 4.9 us (an empty launch: 2.3); 37 rows of 32 adapters, K = 4096 N = 12288 rank 16, 5.0 + 7.6; 8192 rows, K = N =
-// 5120 rank 64, 25 + 48 (84 MB read, 168 MB read and written: 3.3 and 3.5 TB/s); pair, 2050 rows, K = 4096 N = 12288
-// rank 16, 13 + 50.
+// tile: rows of other adapters are left out, not multiplied by zero.  The first product through LDS alone does not gather: it
+// goes through the whole tile once per adapter in it and keeps the columns of that adapter's rows.  Kernel times: one row,
+// K = 2560 N = 9216 rank 16, 3.4 + 4.9 us (an empty launch: 2.3); 37 rows of 32 adapters, K = 4096 N = 12288 rank 16, 4.8 +
+// 7.6; 8192 rows, K = N = 5120 rank 64, 26 + 49 (84 MB read, 168 MB read and written: 3.3 and 3.4 TB/s); pair, 2050 rows,
+// K = 4096 N = 12288 rank 16, 13 + 51.
 #include "../../include/glu_fp8.h"
 #include "glu_adapter.h"
 #include "glu_mat16.h"
@@ -71,8 +72,10 @@ __device__ __forceinline__ raw4_t read16(const char* base, uint32_t lane)
     return *reinterpret_cast<const u32x4_any*>(base + lane);
 }
 
-// silu(g) u for results of 16 bits: without the correction of silu_mul the rounding of the exponent stays, 2 |g| units of
-// 2^-24 of the result at most, which does not show there; a prefill's GLU (2050 x 12288) takes 56 us instead of 63
+// silu(g) u for results of 16 bits: without the correction of silu_mul the rounding of the exponent stays, for g > -87 at most
+// 2 |g| units of 2^-24 of the result, of which at most one result in some hundred lands on the number next to it.  Below,
+// where silu is less than 2^-119 in magnitude, the result may be -0 u, as with silu_mul (and as exp(-g) overflows in fp32).  A
+// prefill's second product (2050 x 12288) takes 51 us instead of 54.
 __device__ __forceinline__ float silu_mul16(float g, float u)
 {
     return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504088896340736f)) * u;
@@ -770,9 +773,10 @@ void out_tiles(const OutArgs& a, hipStream_t stream)
 {
     const Cut c = cut(a.M, a.L, TM);
     const int blocks = a.N > 0 ? (a.N + 63) / 64 : 1;  // N == 0: z alone, to low
-    // A wave takes several blocks where there are waves enough: those of a round of workgroups, two per CU, or three such
-    // rounds of the pair, whose workgroups take longer (8192 x 5120, rank 64: 48 us, 60 in two rounds; pair, 2050 x 12288, rank
-    // 16: 63 us in one, 54 in three).
+    // A wave takes several blocks where there are waves enough: as many, rounded up, as make a round of workgroups, two per
+    // CU (8192 x 5120, rank 64: 49 us; 63 with half as many), or three such rounds of the pair, whose workgroups take longer.
+    // Rounding up leaves fewer: of the pair, 2050 x 12288, rank 16, 1040 workgroups, 51 us (55 with the 780 of a target of two
+    // rounds, 56 with the 455 of one).
     const int64_t target = NM == 2 && TM > 1 ? 3 * kTargetWaves : kTargetWaves;
     int per = (int)((c.units * blocks + target - 1) / target);
     per = per < 1 ? 1 : per > 32 ? 32 : per;

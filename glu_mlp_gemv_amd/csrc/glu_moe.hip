@@ -2,17 +2,17 @@
 //
 //   out[m] = sum over the experts e of row m of p_e down_e (silu(gate_e x[m]) * (up_e x[m]))
 //
-// Bound by the bytes of the experts that some row chose: each of their matrices is read once.  Three launches, or two for up
-// to 4 rows, and a join where the third is cut.  The first ranks the logits, one wave per row, and lists the active
-// experts with their rows: a row's bit in a 64-bit mask per expert, so that the lists come out in order whatever order the
-// waves ran in.  The second gives each active
+// Bound by the bytes of the experts that some row chose: each of their matrices is read once, down of more than 8 rows of an
+// expert again from the caches.  Three launches, or two for up to 4 rows, and a join where the third is cut.  The first ranks
+// the logits, one wave per row, and lists the active experts with their rows: a row's bit in a 64-bit mask per expert, so
+// that the lists come out in order whatever order the waves ran in.  The second gives each active
 // expert's gate and up, 16 rows of weights at a time, to a workgroup whose waves share the contraction.  The third gives 16
 // rows of every active expert's down to a workgroup whose waves take experts in turn, and each wave adds what its experts
 // give to rows of its own in LDS, which are summed in wave order at the end.
 // The weights go from memory straight into matrix instructions as their 16 rows; the columns are rows of x, of
 // which an expert of a small batch has one or two: the matrix unit has more than ten times the rate needed.  37 rows, K =
-// 4096 N = 768, 8 of 128 experts, bf16: 9 + 244 + 131 us, 6.0 and 5.6 TB/s; 6 rows, N = 1536, e4m3: 6 + 102 + 55 us, 5.1 and
-// 4.7 TB/s; one row, K = 2560 N = 1024, 8 of 64: 20 + 11 us, 4.2 and 3.8 TB/s with a launch's ramp.
+// 4096 N = 768, 8 of 128 experts, bf16: 9 + 249 + 143 us, 5.9 and 5.1 TB/s; 6 rows, N = 1536, e4m3: 6 + 103 + 61 us, 5.0 and
+// 4.3 TB/s; one row, K = 2560 N = 1024, 8 of 64: 19 + 12 us, 4.4 and 3.4 TB/s with a launch's ramp.
 #include "../../include/glu_fp8.h"
 #include "glu_mat16.h"
 #include "glu_moe.h"
@@ -644,8 +644,8 @@ hipError_t launch(int logits_dtype, const MoeArgs& a, const MoePlan& p, hipStrea
 }  // namespace
 
 // The second product's cut.  16 rows per workgroup of 16 waves, which share experts in halves or smaller parts so that no
-// wave has much more to do than another (37 rows, K = 4096 N = 768, 128 experts: 144 us with whole experts, 131 with halves;
-// 6 rows of e4m3, N = 1536: 62 and 55).  Workgroups for half of the CUs at least: their sums' join costs 5 us.
+// wave has much more to do than another (6 rows of e4m3, K = 4096 N = 1536, 128 experts: 64 us with whole experts, 62 with
+// halves; 37 rows of bf16, N = 768: 143 either way).  Workgroups for half of the CUs at least: their sums' join costs 5 us.
 MoePlan moe_plan(int M, int K, int N, int E, int top, bool e4m3)
 {
     const int most = M * top < E ? M * top : E;

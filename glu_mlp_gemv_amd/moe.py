@@ -59,8 +59,8 @@ def moe_glu(x: torch.Tensor, logits: torch.Tensor, gate: torch.Tensor, up: torch
     logits are all -inf is 0.  Sums and the activation are fp32 (the second product takes it as two 16-bit numbers, in fp32's range), the
     result is rounded once.
 
-    Each chosen expert's weights are read once per 64 rows: meant for the tokens of a decode step, right for any number.  At
-    most 1024 experts, 32 per row.  Has no gradient: operands that require one are refused where autograd records.
+    Each chosen expert's gate and up are read once per 64 rows, down once per 32 rows of its own or fewer: meant for the tokens of
+    a decode step, right for any number.  At most 1024 experts, 32 per row.  Has no gradient: operands that require one are refused where autograd records.
     """
     if out is None and stream is None:
         r = (fp8._fast or fp8._load_fast()).moe(x, logits, gate, up, down, top, normalize is True or bool(normalize), gate_scale,

@@ -29,7 +29,7 @@ SAN_SOURCES = ("glu_api.hip", "glu_fp8_api.hip", "glu_adapter_api.hip", "glu_dro
 HOST_SAN = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined",
             "-Xarch_host", "-fno-sanitize-recover=all", "-Xarch_host", "-fno-omit-frame-pointer"]
 TESTS = ["tests/test_boundary.py", "tests/test_fp8_boundary.py", "tests/test_adapter_boundary.py",
-         "tests/test_dropout_boundary.py", "tests/test_moe_boundary.py", "tests/test_plan_sweep.py",
+         "tests/test_dropout_boundary.py", "tests/test_moe_boundary.py", "tests/test_moe_logits.py", "tests/test_plan_sweep.py",
          "tests/test_oracle_pins.py"]
 
 

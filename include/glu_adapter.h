@@ -6,13 +6,15 @@
  *
  * y is what the shared projection gave (glu_grouped_gemv, glu_fp8_linear, any other).  Each row of the batch names its
  * adapter; a row whose index is not in [0, L) has none, and its out is y.  glu_adapter_glu is the pair of gate and up
- * projections with the activation behind it: out = T(silu(g) u), g and u the sums above before any rounding.
+ * projections with the activation behind it: out = T(silu(g) u), g and u the sums above before any rounding.  As in fp32's own g / (1 + exp(-g)),
+ * silu(g) is 0 where exp(-g) passes its range, from g = -87 (2^-119) down.
  * Rows of one adapter may stand anywhere in the batch: a decode batch of many requests and a prefill, in which long
  * runs of rows share one, are the same call.  The rows that share one should be neighbours in batches of more than 1024 rows,
  * or of 16 rows per adapter of the stacks and more: others are as right, but slower.
  *
- * t stays fp32: it goes into the second product as two numbers of T, its rounding and what that left, so that no
- * bits of it are lost that a result in T could show.  Rows do not touch each other: a NaN in one request's rows or
+ * t stays fp32: it goes into the second product as two numbers of T, its rounding and the rounding of what that left, so
+ * that at most 2^-17 of it is lost (FP16: 2^-23): a result that lies so close to a border between two numbers of T may be the
+ * other one, about one in a thousand (BF16).  Rows do not touch each other: a NaN in one request's rows or
  * adapter stays there.
  *
  * T is BF16 or FP16 (GLU_DTYPE_*, glu_fp8.h) and is the type of every array but index (int32), scale and low (fp32).

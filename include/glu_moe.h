@@ -5,8 +5,9 @@
  *   p = softmax of logits[m] over them (normalize), or over all experts
  *   out[m] = T( sum_e p_e down_e T(silu(gate_e x[m]) (up_e x[m])) )
  *
- * Every matrix of an expert that some row needs is read once per 64 rows, which is what bounds the layer: it is meant for
- * the tokens of a decode step, and correct for any number of rows.  The products' sums, the activation, the softmax and the
+ * An expert's gate and up are read once per 64 rows of x in which some row needs it, and down once per 32 rows of its own (16
+ * of FP16 or E4M3 weights; 2 in calls of up to 4 rows), again from the caches mostly.  That is what bounds the layer: it is
+ * meant for the tokens of a decode step, and correct for any number of rows.  The products' sums, the activation, the softmax and the
  * sum over experts are fp32; as the operand of the second product the activation is two 16-bit numbers, its rounding and the
  * rounding of what that left, so that 2^-17 of it is lost at most (fp16 weights: 2^-23, and 2^-39 of the largest of 16
  * columns).  It has fp32's range for every T.

@@ -127,3 +127,30 @@ def spread(n, logits, gate, up, down, top):
         a = a * torch.sigmoid(a) * (n[rows].double() @ up[e].double().t())
         out[rows] += p[rows, e, None] * (a @ down[e].double().t()).abs()
     return out
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("M", [3, 20, 70])
+def test_layer_in_a_graph(M, kind):
+    """Captured once and replayed over values of very different sizes, with eager work between: nothing is left of the last."""
+    t, K, N, E, top = T[kind], 128, 100, 8, 2
+    g = torch.Generator(device=DEV).manual_seed(M)
+    rand = lambda *s: torch.randn(*s, generator=g, device=DEV)  # noqa: E731
+    router, norm = (rand(E, K) * K ** -0.5).to(t), torch.ones(K, dtype=t, device=DEV)
+    gate, up, down = ((rand(E, a, b) * b ** -0.5).to(t) for a, b in ((N, K), (N, K), (K, N)))
+    x, res = rand(M, K).to(t), rand(M, K).to(t)
+    layer = mlp.ExpertGluMlp(norm, router, gate, up, down, top)
+    layer(x, res)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y, h = layer(x, res)
+    for size in (1.0, 2.0 ** 9, 2.0 ** -9, 1.0):
+        x.copy_(rand(M, K))
+        up.copy_(rand(E, N, K) * size)
+        down.copy_(rand(E, K, N) / size / 16)
+        graph.replay()
+        eager, eager_h = layer(x, res)
+        torch.cuda.synchronize()
+        assert torch.equal(y, eager) and torch.equal(h, eager_h) and y.isfinite().all()
