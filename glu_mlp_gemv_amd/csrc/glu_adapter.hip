@@ -518,7 +518,10 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_out_kernel(OutArgs a, int
                 for (int i = threadIdx.x; i < items; i += kThreads) {
                     float v[8];
                     z8(i, v);
-                    atomicMax(&most[i / R8], abs_max8(v));  // a maximum: any order
+                    uint32_t size = 0;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) size = max(size, finite_bits(v[e]));
+                    atomicMax(&most[i / R8], size);  // a maximum: any order
                 }
                 __syncthreads();
             }

@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, RT == 4 ? 2 : 3) adapter_grad_kernel
             float z[EACH];
             z_of(row_at(i), my_rank, z);
 #pragma unroll
-            for (int e = 0; e < EACH; ++e) top[e] = max(top[e], abs_bits(z[e]));
+            for (int e = 0; e < EACH; ++e) top[e] = max(top[e], finite_bits(z[e]));
         }
 #pragma unroll
         for (int e = 0; e < EACH; ++e) {  // a wave's lanes have the same ranks

@@ -64,14 +64,21 @@ __device__ __forceinline__ void split16(float f, uint16_t& hi, uint16_t& lo)
     lo = abs_bits(w) < 0x7f800000u ? bits16<T>(f - w) : (uint16_t)0;
 }
 
-// fp16 has too small a range for any fp32 number: numbers whose largest magnitude has these bits are multiplied by a
-// power of two that brings it to 2^14 .. 2^15, and the sums by its reciprocal.  Both are normal numbers; 1 where the
-// largest is zero, infinite or NaN, and for bf16, which has fp32's range.
+// The bits of |f|, or 0 where f is not finite: what the largest of numbers is taken from that share a power of two.
+__device__ __forceinline__ uint32_t finite_bits(float f)
+{
+    const uint32_t b = abs_bits(f);
+    return b < 0x7f800000u ? b : 0u;
+}
+
+// fp16 has too small a range for any fp32 number: numbers whose largest finite magnitude has these bits are multiplied by a
+// power of two that brings it to 2^14 .. 2^15, which leaves infinities what they are, and the sums by its reciprocal.  Both are
+// normal numbers; 1 where the largest is zero, and for bf16, which has fp32's range.
 struct Pow2 { float up, down; };
 template <class T>
 __device__ __forceinline__ Pow2 pow2_for(uint32_t amax)
 {
-    if (__is_same(T, Bf16) || amax == 0 || amax >= 0x7f800000u) return Pow2{1.0f, 1.0f};
+    if (__is_same(T, Bf16) || amax == 0) return Pow2{1.0f, 1.0f};
     const int e = min(268 - (int)(amax >> 23), 253);
     return Pow2{__uint_as_float((uint32_t)e << 23), __uint_as_float((uint32_t)(254 - e) << 23)};
 }

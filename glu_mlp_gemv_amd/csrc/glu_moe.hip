@@ -388,9 +388,8 @@ __device__ __forceinline__ void gate_up(const MoeArgs& a, const int* row, const 
             u += red[k][1][t][at];
         }
         float act = silu_mul(g, u);
-        if constexpr (kScaled<T, E8>) {  // of the finite ones: infinities stay what they are
-            const uint32_t size = abs_bits(act);
-            const Pow2 f = pow2_for<T>(max16(n < a.N && size < 0x7f800000u ? size : 0u));
+        if constexpr (kScaled<T, E8>) {
+            const Pow2 f = pow2_for<T>(max16(n < a.N ? finite_bits(act) : 0u));
             act *= f.up;
             if (i == 0 && s < x.count) a.factor[(x.first + s) * a.ld_factor + (n0 >> 4)] = f.down;
         }

@@ -12,6 +12,8 @@
  * runs of rows share one, are the same call.  The rows that share one should be neighbours in batches of more than 1024 rows,
  * or of 16 rows per adapter of the stacks and more: others are as right, but slower.
  *
+ * An infinity in b (in the gradients, in dout or x) gives infinite results or NaN, as it meets two numbers of which one may be 0.
+ *
  * t stays fp32: it goes into the second product as two numbers of T, its rounding and the rounding of what that left, so
  * that at most 2^-17 of it is lost (FP16: 2^-23): a result that lies so close to a border between two numbers of T may be the
  * other one, about one in a thousand (BF16).  Rows do not touch each other: a NaN in one request's rows or
