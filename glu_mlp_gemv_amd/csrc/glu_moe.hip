@@ -470,8 +470,10 @@ __device__ __forceinline__ void down(const MoeArgs& a, const Active& x, int c0, 
     for (int t = 0; t < TT; ++t) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {  // lane ^ EACH: a turn of 16 lanes by 8, or of 4 lanes by 2
-            const int other = __builtin_amdgcn_update_dpp(0, __float_as_int(acc[0][t][e]), EACH == 8 ? 0x128 : 0x4E, 0xF, 0xF, false);
-            acc[0][t][e] += __int_as_float(other);
+            const float sum = acc[0][t][e];
+            const int other = __builtin_amdgcn_update_dpp(0, __float_as_int(sum), EACH == 8 ? 0x128 : 0x4E, 0xF, 0xF, false);
+            // an infinite sum of the first numbers is the result's: a weight's infinity meets second numbers of either sign, or 0
+            if (abs_bits(sum) != 0x7f800000u) acc[0][t][e] = sum + __int_as_float(other);
         }
         const int slot = t0 + EACH * t + at;
         // rows 4 q .. + 3 of the instruction: with 4 places, place q

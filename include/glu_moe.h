@@ -16,8 +16,6 @@
  * and out = 0.  A NaN logit ranks above all others and makes its row NaN.  Experts that a row did not choose do not
  * touch it, whatever they hold.
  *
- * An infinity in down gives infinite results or NaN, as it meets two numbers of which one may be 0.
- *
  * T, the type of x and out, is BF16 or FP16 (GLU_DTYPE_*, glu_fp8.h).  The weights are of T or block-scaled E4M3 (one
  * fp32 scale per 128 x 128 block of an expert's matrix), whose products with x are exact in fp32 sums.
  *

@@ -146,3 +146,24 @@ def test_infinite_activations_in_fp16(M):
     w[2][:, :, 37] = torch.where(torch.arange(K, device=DEV) % 2 == 0, 1.0, -1.0)
     want = (math.inf * w[2][0, :, 37].float()).expand(M, K)
     assert torch.equal(run(x, logits, w, s, 2).float(), want)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("M", [1, 2, 4, 7, 40])
+def test_infinite_weights_of_the_second_product(M, e4m3, kind):
+    """An infinite column of down, or scale of its last block: results are infinite by the activation's sign, whichever sign the
+    second of its two numbers has."""
+    K, N = 96, 200
+    x, logits, w, s = layer(M, K, N, 1, T[kind], False, M)
+    x.abs_()
+    w[0].abs_()
+    w[1].abs_()
+    sign = torch.where(torch.arange(K, device=DEV) % 2 == 0, 1.0, -1.0)
+    w[2].abs_().mul_(sign[None, :, None].to(w[2].dtype))
+    if e4m3:
+        w, s = zip(*(e4m3_of(m) for m in w))
+        s[2][..., -1] = math.inf
+    else:
+        w[2][..., 71] = (math.inf * sign).to(w[2].dtype)
+    assert torch.equal(run(x, logits, w, s, 1).float(), (math.inf * sign).expand(M, K))
